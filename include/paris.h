@@ -316,6 +316,147 @@ paris_status paris_launch_counts(const paris_ctx* ctx, int64_t* counts);
 paris_status paris_profile_begin(paris_ctx* ctx, int max_launches);
 paris_status paris_profile_end(paris_ctx* ctx, double* total_ms, int64_t* launches);
 
+/* ------------------------------------------------------------------------
+ * The prompt's own attention, and a cache in 4 bits.
+ *
+ * These calls need no context: every buffer is the caller's, sizes that
+ * vary from call to call (sequence starts and lengths) are read on the
+ * device, and nothing is allocated or kept, so they may be captured into a
+ * graph and replayed as the lengths change.  The text of their last error on
+ * the calling thread is paris_last_error(NULL).  head_dim is 128.
+ * Base addresses are 16-byte aligned and strides multiples of 8 elements.
+ * ------------------------------------------------------------------------ */
+
+/* Element strides of a tensor of heads: element c of head h of the token in
+ * row r of sequence axis entry s is at s * seq + r * token + h * head + c.   */
+typedef struct {
+  int64_t token, head, seq;
+} paris_strides;
+
+/* The sequences of a prompt call.  With starts (cu_q and cu_k), the
+ * sequences are packed along one token axis: sequence s has the query rows
+ * [cu_q[s], cu_q[s + 1]) of rows_q and the key rows [cu_k[s], cu_k[s + 1])
+ * of rows_k, and the seq strides are not used.  Without (both NULL), entry s
+ * of the sequence axis holds rows_q query rows and rows_k key rows.
+ * Starts are clamped to [0, rows] and to the start before them; rows that no
+ * sequence owns are neither read nor written.  max_q and max_k: at least
+ * the longest sequence's rows (they size the launch; query rows past max_q
+ * are left unwritten).                                                      */
+typedef struct {
+  int n_seqs, n_q_heads, n_kv_heads, head_dim;
+  int64_t rows_q, rows_k;
+  const int32_t* cu_q; /* device, n_seqs + 1 entries, or NULL */
+  const int32_t* cu_k;
+  int64_t max_q, max_k;
+  paris_strides q, k, v, out;
+} paris_prompt;
+
+/* Bytes of workspace that paris_prompt_attend needs for this call (0 when
+ * the rows alone fill the GPU).  Host only.                                  */
+paris_status paris_prompt_workspace(const paris_prompt* p, size_t* bytes);
+
+/* Causal attention over whole prompts, or over the last len_q of len_k
+ * tokens of each sequence (a prompt read in chunks, a single token):
+ *   s_ij = <q_i, k_j> / sqrt(d) for j <= i + len_k - len_q,
+ *   lse_i = log sum_j exp(s_ij),  o_i = sum_j exp(s_ij - lse_i) v_j,
+ * query head h with KV head h / (Hq / Hkv).  A query before the first key
+ * (len_q > len_k) sees nothing: o_i = 0, lse_i = -inf.  What lies in rows
+ * that a query does not see, infinities and NaN included, does not reach it.
+ * q, k, v: device, bf16 (PARIS_F32 is not supported); out: device bf16;
+ * lse: device float32 [sequence axis][Hq][rows_q] (one entry of the sequence
+ * axis when packed), or NULL.  Scores, maxima and sums are float32; the
+ * softmax weights enter the product with V as bf16.  At most 128 query heads
+ * per KV head.  workspace: device, 16-byte aligned, of at least
+ * paris_prompt_workspace bytes, used only by this call.                      */
+paris_status paris_prompt_attend(const paris_prompt* p, const void* q, const void* k, const void* v,
+                                 paris_dtype dtype, void* out_bf16, float* lse, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* The weights that the last `window` queries of each sequence give to its
+ * keys: weights[h][j] = sum over those queries i and over the query heads of
+ * KV head h of exp(s_ij - lse_i), with lse as paris_prompt_attend gives it
+ * (a query with lse = -inf adds nothing).  weights: device float32 [sequence
+ * axis][Hkv][rows_k], written for every key row of every sequence.  `v`,
+ * `out` and max_q of p are not used.                                        */
+paris_status paris_prompt_weights(const paris_prompt* p, const void* q, const void* k, paris_dtype dtype,
+                                  const float* lse, int window, float* weights, void* stream);
+
+/* A cache in 4 bits: for every (sequence, KV head) max_rows rows of a key
+ * and a value, of which the first lens[sequence] are in use, in no order.
+ * Row form: four groups of 32 channels, each with a scale S = max|x| / 7
+ * rounded up to four significant bits (and no finer than 2^-17), and codes
+ * c = rint(x / S) in [-7, 7], ties to even; a row stands for c S, which is
+ * exact in half precision and in bf16.  Values past +-1680 (7 times the
+ * largest scale, 240) become +-1680 and NaN becomes 0.  Byte j of a row's
+ * codes holds c + 8 of channel 2j in its low and of channel 2j + 1 in its
+ * high half; a scale byte is the upper byte (5 exponent bits, 3 mantissa
+ * bits) of the scale as a half without its sign bit.
+ * All arrays are device memory of the caller.  Lengths outside
+ * [0, max_rows] count as the nearest of the two.  A cache is one object: calls
+ * on it go to one stream, or are ordered by the caller.                      */
+typedef struct {
+  int batch, n_kv_heads, head_dim;
+  int64_t max_rows;
+  uint8_t *k_codes, *v_codes;   /* [batch][Hkv][max_rows][64]                  */
+  uint8_t *k_scales, *v_scales; /* [batch][Hkv][max_rows][4]                   */
+  float* weights;               /* [batch][Hkv][max_rows] accumulated weights  */
+  int32_t* positions;           /* [batch][Hkv][max_rows] each row's position  */
+  int32_t* lens;                /* [batch] rows in use                         */
+  int32_t* next_pos;            /* [batch] position of the next token          */
+  uint32_t* counters;           /* [batch] zeros; zeros again after each call  */
+  uint32_t* status;             /* [1] bits set by kernels: bit 0: no room        */
+} paris_kv4;
+
+/* Add tokens at the end of their sequences.  k, v: device, dtype, rows
+ * packed by cu (device, batch + 1 starts within [0, rows]) or, with
+ * cu = NULL, `rows` tokens for every sequence along the seq stride; max_new:
+ * at least the most tokens of a sequence.  Each new row's position counts
+ * on from next_pos, its weight comes from weights (device float32 [sequence
+ * axis][Hkv][rows]) or is 0 (NULL).  Tokens past max_rows are dropped and
+ * status bit 0 is set.  At most 2^31 - 1 tokens per sequence.                */
+paris_status paris_kv4_store(const paris_kv4* c, const void* k, const void* v, paris_dtype dtype,
+                             const paris_strides* ks, const paris_strides* vs, int64_t rows, const int32_t* cu,
+                             int64_t max_new, const float* weights, void* stream);
+
+/* Add one token to every sequence.  k, v: device, dtype, [batch][Hkv][d]
+ * contiguous.                                                               */
+paris_status paris_kv4_append(const paris_kv4* c, const void* k, const void* v, paris_dtype dtype, void* stream);
+
+/* Bytes of workspace of paris_kv4_attend.  Host only.                        */
+paris_status paris_kv4_workspace(const paris_kv4* c, int n_q_heads, int accumulate, size_t* bytes);
+
+/* Decode attention over the rows in use: p = softmax(K q / sqrt(d)),
+ * out = p V (zeros for an empty sequence), float32 throughout (queries,
+ * and softmax weights, enter the products as two half-precision parts; the rows are exact).
+ * With accumulate, weights[row] += the sum of p over the query heads of the
+ * row's KV head.  q: device, dtype, [batch][Hq][d]; out: device bf16
+ * [batch][Hq][d]; at most 16 query heads per KV head.                        */
+paris_status paris_kv4_attend(const paris_kv4* c, const void* q, paris_dtype dtype, int n_q_heads, int accumulate,
+                              void* out_bf16, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of paris_kv4_evict.  Host only.                         */
+paris_status paris_kv4_evict_workspace(const paris_kv4* c, size_t* bytes);
+
+/* Bring every sequence down to at most `keep` rows.  For each KV head of a
+ * sequence with more, rows at positions below `sink` or among the last
+ * `recent` (position >= next_pos - recent) stay, and of the others those with
+ * the largest weights (equal weights: the lowest row; NaN counts as the
+ * lowest).  Should more than `keep` rows be protected, the lowest rows of
+ * them stay.  Kept rows at index keep and above move, in ascending order,
+ * into the dropped rows below it; the others stay where they are.
+ * sink + recent <= keep.                                                     */
+paris_status paris_kv4_evict(const paris_kv4* c, int64_t keep, int64_t sink, int64_t recent, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* The values that the first min(lens, rows) rows stand for.  k_out, v_out:
+ * device bf16 [batch][Hkv][rows][d]; rows past a sequence's end are left as
+ * they were.                                                                */
+paris_status paris_kv4_read(const paris_kv4* c, void* k_out, void* v_out, int64_t rows, void* stream);
+
+/* Synchronise the device and report the status word, then clear it:
+ * PARIS_OK, or PARIS_EDEVICE if a store found no room.                       */
+paris_status paris_kv4_check(const paris_kv4* c);
+
 /* Host only, no device work: the RSQ-IP magnitude levels for subspace width
  * m, computed by float64 Lloyd-Max on the density of |x_j| for x uniform on
  * the unit sphere S^{m-1} (x_j^2 ~ Beta(1/2, (m-1)/2); ParisKV,

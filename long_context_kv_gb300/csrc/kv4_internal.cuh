@@ -1,0 +1,105 @@
+// Internal declarations of the 4-bit cache and the prompt calls
+// (include/paris.h, "The prompt's own attention, and a cache in 4 bits").
+#pragma once
+
+#include "paris_device.cuh"
+
+namespace paris {
+
+constexpr int kGroup4 = 32;            // channels that share a scale
+constexpr int kCode4 = kDim / 2;       // code bytes of a row
+constexpr int kScale4 = kDim / kGroup4;  // scale bytes of a row
+constexpr float kLimit4 = 1680.f;      // 7 x 240: the largest value a row holds
+constexpr uint32_t kStatusNoRoom = 1u;
+
+// Device view of paris_kv4.
+struct Kv4 {
+  int batch, hkv;
+  int64_t rmax;
+  uint8_t *kc, *vc, *ks, *vs;
+  float* w;
+  int32_t *pos, *lens, *next;
+  uint32_t *counters, *status;
+};
+
+struct Strides {
+  int64_t token, head, seq;
+};
+
+__device__ __forceinline__ int64_t kv4_len(const Kv4& c, int b) {
+  return min64(max64(c.lens[b], 0), c.rmax);
+}
+
+// Rows [start, start + len) of sequence s on a token axis of `rows` rows;
+// starts outside the axis, or before the start in front, are clamped.
+__device__ __forceinline__ void seq_rows(const int32_t* cu, int s, int64_t rows, int64_t& start, int64_t& len) {
+  if (cu == nullptr) {
+    start = 0;
+    len = rows;
+    return;
+  }
+  start = min64(max64(cu[s], 0), rows);
+  len = min64(max64(cu[s + 1], start), rows) - start;
+}
+
+struct StoreArgs {
+  Kv4 c;
+  const void *k, *v;
+  int dtype;
+  Strides ks, vs;
+  int64_t rows, max_new;
+  const int32_t* cu;
+  const float* weights;
+};
+cudaError_t launch_kv4_store(const StoreArgs& a, cudaStream_t st);
+
+struct Attend4Args {
+  Kv4 c;
+  const void* q;
+  int dtype, hq, g, accumulate;
+  int nsplit;              // splits of a sequence's rows
+  int64_t rows_per_split;  // a multiple of the block's tile
+  float* part;             // [batch * hq][nsplit][kPartStride]
+  float* scores;           // [batch * hq][rmax], base-2 logits (accumulate)
+  __nv_bfloat16* out;
+};
+void kv4_splits(int64_t units, int64_t rmax, int sm_count, int* nsplit, int64_t* rows_per_split);
+cudaError_t launch_kv4_attend(const Attend4Args& a, cudaStream_t st);
+
+struct EvictArgs {
+  Kv4 c;
+  int64_t keep, sink, recent;
+  int32_t* list;  // [batch * hkv][2][rmax]: dropped rows below keep, kept rows above
+};
+cudaError_t launch_kv4_evict(const EvictArgs& a, cudaStream_t st);
+
+cudaError_t launch_kv4_read(const Kv4& c, __nv_bfloat16* k_out, __nv_bfloat16* v_out, int64_t rows, cudaStream_t st);
+
+// The sequences of a prompt call (paris_prompt without its pointers' types).
+struct PromptArgs {
+  int n_seqs, hq, hkv, g;
+  int64_t rows_q, rows_k;
+  const int32_t *cu_q, *cu_k;
+  int64_t max_q, max_k;
+  Strides sq, sk, sv, so;
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16* out;
+  float* lse;  // may be null
+  float* ws;   // split partials
+  int nsplit;
+};
+cudaError_t launch_prompt_attend(const PromptArgs& a, cudaStream_t st);
+size_t prompt_workspace_bytes(PromptArgs& a, int sm_count);  // sets a.nsplit
+
+struct PromptWeightArgs {
+  PromptArgs p;
+  const float* lse;
+  int window;
+  float* weights;
+};
+cudaError_t launch_prompt_weights(const PromptWeightArgs& a, cudaStream_t st);
+
+// Text of the last error without a context (paris_last_error(NULL)).
+void set_thread_error(const char* text);
+
+}  // namespace paris

@@ -63,7 +63,7 @@ struct paris_ctx {
 
 namespace {
 
-thread_local std::string g_create_err;
+thread_local std::string g_create_err;  // also the error of the calls that have no context
 
 paris_status fail(paris_ctx* c, paris_status st, const char* fmt, ...) {
   char buf[512];
@@ -191,6 +191,8 @@ paris_status check_dtype(paris_ctx* c, int dtype) {
 }  // namespace
 
 namespace paris {
+
+void set_thread_error(const char* text) { g_create_err = text; }
 
 namespace {
 constexpr int kSmemMaxDevices = 64;

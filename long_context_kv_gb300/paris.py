@@ -53,6 +53,27 @@ _SIGNATURES = {
     "paris_launch_counts": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "paris_profile_begin": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int]),
     "paris_profile_end": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "paris_prompt_workspace": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t)]),
+    "paris_prompt_attend": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_size_t, ctypes.c_void_p]),
+    "paris_prompt_weights": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                            ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p]),
+    "paris_kv4_store": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                       ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]),
+    "paris_kv4_append": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                        ctypes.c_void_p]),
+    "paris_kv4_workspace": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int,
+                                           ctypes.POINTER(ctypes.c_size_t)]),
+    "paris_kv4_attend": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "paris_kv4_evict_workspace": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t)]),
+    "paris_kv4_evict": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                       ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "paris_kv4_read": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                      ctypes.c_void_p]),
+    "paris_kv4_check": (ctypes.c_int, [ctypes.c_void_p]),
 }
 
 KERNELS = ["place_kv", "encode", "build_index", "append", "decode", "attend", "fill", "dense", "union"]
@@ -66,6 +87,24 @@ class paris_config(ctypes.Structure):
 
 class paris_state(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("T", "N", "n_local", "n_buf", "C", "k_eff", "n_flushes")]
+
+
+class paris_strides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("token", "head", "seq")]
+
+
+class paris_prompt(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("n_seqs", "n_q_heads", "n_kv_heads", "head_dim")]
+                + [(n, ctypes.c_int64) for n in ("rows_q", "rows_k")]
+                + [(n, ctypes.c_void_p) for n in ("cu_q", "cu_k")]
+                + [(n, ctypes.c_int64) for n in ("max_q", "max_k")]
+                + [(n, paris_strides) for n in ("q", "k", "v", "out")])
+
+
+class paris_kv4(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("batch", "n_kv_heads", "head_dim")] + [("max_rows", ctypes.c_int64)]
+                + [(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scales", "v_scales", "weights", "positions",
+                                                  "lens", "next_pos", "counters", "status")])
 
 
 _lib = None
@@ -252,3 +291,240 @@ class Context:
         _check(load().paris_debug_dump(self._h, what, seq, head, out.ctypes.data_as(ctypes.c_void_p),
                                        out.nbytes), self._h)
         return out
+
+
+# -- the prompt's own attention, and the 4-bit cache ---------------------------
+HEAD_DIM = 128
+
+
+def _on(device, *tensors):
+    """Every tensor on `device`, and `device` the current one."""
+    import torch
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on different devices: {t.device} and {device}")
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device (got {device})")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _shaped(t, name, shape, dtype):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+
+
+def _heads(t, name, packed):
+    """A tensor of heads as (rows, heads, sequence axis, strides): [rows, H, d] packed, [batch, H, T, d] otherwise."""
+    if t.dim() != (3 if packed else 4) or t.shape[-1] != HEAD_DIM:
+        want = "[rows, heads, 128]" if packed else "[batch, heads, T, 128]"
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {want}")
+    if t.stride(-1) != 1 and t.numel():
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if packed:
+        return t.shape[0], t.shape[1], 1, paris_strides(t.stride(0), t.stride(1), 0)
+    return t.shape[2], t.shape[1], t.shape[0], paris_strides(t.stride(2), t.stride(1), t.stride(0))
+
+
+def _scratch(nbytes, device, stream):
+    """Scratch of one call, from the caching allocator of the call's stream."""
+    import torch
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _prompt(q, k, cu_q, cu_k, max_q, max_k, v=None, out=None):
+    import torch
+    if (cu_q is None) != (cu_k is None):
+        raise ValueError("cu_q and cu_k must both be given or both be None")
+    packed = cu_q is not None
+    for t in (q, k, v, out):
+        if t is not None and t.dtype != torch.bfloat16:
+            raise TypeError(f"the prompt calls take bfloat16 tensors (got {t.dtype})")
+    _on(q.device, q, k, v, out, cu_q, cu_k)
+    p = paris_prompt(head_dim=HEAD_DIM)
+    p.rows_q, p.n_q_heads, seqs, p.q = _heads(q, "q", packed)
+    p.rows_k, p.n_kv_heads, k_seqs, p.k = _heads(k, "k", packed)
+    if k_seqs != seqs:
+        raise ValueError(f"q and k: batches of {seqs} and {k_seqs}")
+    if packed:
+        for c, name in ((cu_q, "cu_q"), (cu_k, "cu_k")):
+            if c.dtype != torch.int32 or c.dim() != 1 or not c.is_contiguous() or c.shape != cu_q.shape or not c.numel():
+                raise ValueError(f"{name}: a contiguous int32 tensor of n + 1 starts, as many for q as for k")
+        seqs = cu_q.numel() - 1
+        p.cu_q, p.cu_k = cu_q.data_ptr(), cu_k.data_ptr()
+    p.n_seqs = seqs
+    p.max_q = p.rows_q if max_q is None else int(max_q)
+    p.max_k = p.rows_k if max_k is None else int(max_k)
+    if v is not None:
+        if v.shape != k.shape:
+            raise ValueError(f"v: shape {tuple(v.shape)}, expected {tuple(k.shape)}")
+        p.v = _heads(v, "v", packed)[3]
+    if out is not None:
+        if out.shape != q.shape:
+            raise ValueError(f"out: shape {tuple(out.shape)}, expected {tuple(q.shape)}")
+        p.out = _heads(out, "out", packed)[3]
+    return p, packed
+
+
+def _raw(t):
+    return ctypes.c_void_p(t.data_ptr()) if t is not None and t.numel() else None
+
+
+def paris_prompt_attend(q, k, v, out, cu_q=None, cu_k=None, max_q=None, max_k=None, lse=None, stream=None):
+    """Causal attention over whole prompts, or over the last queries of each sequence.
+
+    Packed: q, out [rows_q, Hq, 128], k, v [rows_k, Hkv, 128] and the int32 starts cu_q, cu_k [n + 1] on the device
+    (max_q, max_k: at least the longest sequence's rows, default all rows).  Otherwise [batch, heads, T, 128].
+    Any strides with a contiguous last dimension and 16-byte aligned rows.  lse: float32 [Hq, rows_q] or
+    [batch, Hq, T], or None.
+    """
+    import torch
+    p, packed = _prompt(q, k, cu_q, cu_k, max_q, max_k, v, out)
+    if lse is not None:
+        _on(q.device, lse)
+        _shaped(lse, "lse", (p.n_q_heads, p.rows_q) if packed else q.shape[:3], torch.float32)
+        _ptr(lse)
+    lib = load()
+    n = ctypes.c_size_t()
+    _check(lib.paris_prompt_workspace(ctypes.byref(p), ctypes.byref(n)))
+    ws = _scratch(n.value, q.device, stream) if n.value else None
+    _check(lib.paris_prompt_attend(ctypes.byref(p), _raw(q), _raw(k), _raw(v), PARIS_BF16, _raw(out), _raw(lse),
+                                   _raw(ws), n.value, _stream(stream)))
+
+
+def paris_prompt_weights(q, k, lse, weights, window, cu_q=None, cu_k=None, max_k=None, stream=None):
+    """weights[h, j]: the softmax weights that each sequence's last `window` queries give to its key j, added up over
+    them and over the query heads of KV head h.  lse as paris_prompt_attend gives it; weights: float32 [Hkv, rows_k]
+    (packed) or [batch, Hkv, T]."""
+    import torch
+    p, packed = _prompt(q, k, cu_q, cu_k, None, max_k)
+    _on(q.device, lse, weights)
+    _shaped(lse, "lse", (p.n_q_heads, p.rows_q) if packed else q.shape[:3], torch.float32)
+    _shaped(weights, "weights", (p.n_kv_heads, p.rows_k) if packed else k.shape[:3], torch.float32)
+    _ptr(lse), _ptr(weights)
+    _check(load().paris_prompt_weights(ctypes.byref(p), _raw(q), _raw(k), PARIS_BF16, _raw(lse), int(window),
+                                       _raw(weights), _stream(stream)))
+
+
+class KV4Cache:
+    """A cache in 4 bits (paris_kv4): its arrays are torch tensors, given by the caller or made by `create`.
+
+    k_codes, v_codes uint8 [batch, Hkv, max_rows, 64]; k_scales, v_scales uint8 [batch, Hkv, max_rows, 4];
+    weights float32 and positions int32 [batch, Hkv, max_rows]; lens and next_pos int32 [batch].
+    """
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, weights, positions, lens, next_pos):
+        import torch
+        if k_codes.dim() != 4 or k_codes.shape[3] != HEAD_DIM // 2:
+            raise ValueError(f"k_codes: shape {tuple(k_codes.shape)}, expected [batch, heads, max_rows, 64]")
+        b, h, r = k_codes.shape[:3]
+        want = dict(k_codes=((b, h, r, 64), torch.uint8), v_codes=((b, h, r, 64), torch.uint8),
+                    k_scales=((b, h, r, 4), torch.uint8), v_scales=((b, h, r, 4), torch.uint8),
+                    weights=((b, h, r), torch.float32), positions=((b, h, r), torch.int32),
+                    lens=((b,), torch.int32), next_pos=((b,), torch.int32))
+        given = dict(k_codes=k_codes, k_scales=k_scales, v_codes=v_codes, v_scales=v_scales, weights=weights,
+                     positions=positions, lens=lens, next_pos=next_pos)
+        for name, (shape, dtype) in want.items():
+            _shaped(given[name], name, shape, dtype)
+            if given[name].device != k_codes.device or k_codes.device.type != "cuda":
+                raise ValueError(f"{name}: on {given[name].device}; a cache is on one CUDA device")
+            if not given[name].is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            setattr(self, name, given[name])
+        self.batch, self.n_kv_heads, self.max_rows, self.device = b, h, r, k_codes.device
+        # counters and the status word, made here and zero between calls
+        self._words = torch.zeros(b + 1, dtype=torch.int32, device=k_codes.device)
+        self._c = paris_kv4(batch=b, n_kv_heads=h, head_dim=HEAD_DIM, max_rows=r,
+                            counters=self._words.data_ptr(), status=self._words.data_ptr() + 4 * b,
+                            **{n: t.data_ptr() for n, t in given.items()})
+        self._ws = {}
+
+    @classmethod
+    def create(cls, batch, n_kv_heads, max_rows, device="cuda"):
+        """An empty cache."""
+        import torch
+        z = lambda *s, dtype: torch.zeros(*s, dtype=dtype, device=device)  # noqa: E731
+        n = (batch, n_kv_heads, max_rows)
+        return cls(k_codes=z(*n, 64, dtype=torch.uint8), k_scales=z(*n, 4, dtype=torch.uint8),
+                   v_codes=z(*n, 64, dtype=torch.uint8), v_scales=z(*n, 4, dtype=torch.uint8),
+                   weights=z(*n, dtype=torch.float32), positions=z(*n, dtype=torch.int32),
+                   lens=z(batch, dtype=torch.int32), next_pos=z(batch, dtype=torch.int32))
+
+    def _bytes(self, key, call):
+        """Workspace bytes of a call, asked once per kind of call."""
+        if key not in self._ws:
+            n = ctypes.c_size_t()
+            _check(call(n))
+            self._ws[key] = n.value
+        return self._ws[key]
+
+    def paris_kv4_store(self, k, v, cu=None, max_new=None, weights=None, stream=None):
+        """Add tokens: packed [rows, Hkv, 128] with int32 starts cu [batch + 1] (max_new: at least the most tokens of
+        a sequence, default all rows), or [batch, Hkv, T, 128].  weights: float32 [Hkv, rows] or [batch, Hkv, T]."""
+        import torch
+        packed = cu is not None
+        rows, heads, seqs, ks = _heads(k, "k", packed)
+        vs = _heads(v, "v", packed)[3]
+        if v.shape != k.shape or v.dtype != k.dtype:
+            raise ValueError("k and v must have the same shape and dtype")
+        if heads != self.n_kv_heads or (not packed and seqs != self.batch):
+            raise ValueError(f"k: shape {tuple(k.shape)} for a cache of {self.batch} sequences, {self.n_kv_heads} heads")
+        _on(self.device, k, v, cu, weights)
+        if packed and (cu.dtype != torch.int32 or tuple(cu.shape) != (self.batch + 1,) or not cu.is_contiguous()):
+            raise ValueError("cu: a contiguous int32 tensor of batch + 1 starts")
+        if weights is not None:
+            _shaped(weights, "weights", (heads, rows) if packed else k.shape[:3], torch.float32)
+            _ptr(weights)
+        _check(load().paris_kv4_store(ctypes.byref(self._c), _raw(k), _raw(v), _dtype_code(k), ctypes.byref(ks),
+                                      ctypes.byref(vs), rows, _raw(cu), rows if max_new is None else int(max_new),
+                                      _raw(weights), _stream(stream)))
+
+    def paris_kv4_append(self, k, v, stream=None):
+        """Add one token to every sequence: k, v [batch, Hkv, 128]."""
+        for t, name in ((k, "k"), (v, "v")):
+            _shaped(t, name, (self.batch, self.n_kv_heads, HEAD_DIM), k.dtype)
+        _on(self.device, k, v)
+        _check(load().paris_kv4_append(ctypes.byref(self._c), _ptr(k), _ptr(v), _dtype_code(k), _stream(stream)))
+
+    def paris_kv4_attend(self, q, out, accumulate=False, stream=None):
+        """out = softmax(K q / sqrt(d)) V over the rows in use: q, out [batch, Hq, 128]; accumulate: add each row's
+        softmax weights, over its query heads, to `weights`."""
+        import torch
+        if q.dim() != 3 or q.shape[0] != self.batch or q.shape[2] != HEAD_DIM:
+            raise ValueError(f"q: shape {tuple(q.shape)}, expected [{self.batch}, heads, 128]")
+        _shaped(out, "out", q.shape, torch.bfloat16)
+        _on(self.device, q, out)
+        lib, hq, acc = load(), q.shape[1], int(bool(accumulate))
+        n = self._bytes((hq, acc), lambda b: lib.paris_kv4_workspace(ctypes.byref(self._c), hq, acc, ctypes.byref(b)))
+        ws = _scratch(n, self.device, stream)
+        _check(lib.paris_kv4_attend(ctypes.byref(self._c), _ptr(q), _dtype_code(q), hq, acc, _ptr(out), _raw(ws), n,
+                                    _stream(stream)))
+
+    def paris_kv4_evict(self, keep, sink=0, recent=0, stream=None):
+        """At most `keep` rows for each sequence: protected ones and the heaviest others."""
+        _on(self.device)
+        lib = load()
+        n = self._bytes("evict", lambda b: lib.paris_kv4_evict_workspace(ctypes.byref(self._c), ctypes.byref(b)))
+        ws = _scratch(n, self.device, stream)
+        _check(lib.paris_kv4_evict(ctypes.byref(self._c), int(keep), int(sink), int(recent), _raw(ws), n,
+                                   _stream(stream)))
+
+    def paris_kv4_read(self, k_out, v_out, stream=None):
+        """The values of the first rows: k_out, v_out bfloat16 [batch, Hkv, rows, 128]."""
+        import torch
+        if k_out.dim() != 4:
+            raise ValueError(f"k_out: shape {tuple(k_out.shape)}, expected [batch, heads, rows, 128]")
+        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+            _shaped(t, name, (self.batch, self.n_kv_heads, k_out.shape[2], HEAD_DIM), torch.bfloat16)
+        _on(self.device, k_out, v_out)
+        _ptr(k_out), _ptr(v_out)
+        _check(load().paris_kv4_read(ctypes.byref(self._c), _raw(k_out), _raw(v_out), k_out.shape[2], _stream(stream)))
+
+    def paris_kv4_check(self):
+        """Synchronise; raise if a store found no room."""
+        _check(load().paris_kv4_check(ctypes.byref(self._c)))
