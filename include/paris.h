@@ -372,6 +372,11 @@ paris_status paris_prompt_attend(const paris_prompt* p, const void* q, const voi
                                  paris_dtype dtype, void* out_bf16, float* lse, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/* Synchronise the device and report whether a prompt call on it gave up a
+ * wait since the last check (PARIS_EDEVICE, then cleared): every wait inside
+ * the kernel has a limit of seconds, past which its results are not valid.   */
+paris_status paris_prompt_check(void);
+
 /* The weights that the last `window` queries of each sequence give to its
  * keys: weights[h][j] = sum over those queries i and over the query heads of
  * KV head h of exp(s_ij - lse_i), with lse as paris_prompt_attend gives it

@@ -1,4 +1,34 @@
-// Causal attention over prompts, and the window weights: one warp per row.
+// Causal attention over prompts, and the window weights.
+//
+// k_prompt_attend, one block per 256 query rows of a KV head and a range of
+// its keys.  A query row is a (token, query head) pair with the heads
+// fastest, so the G heads of a KV head share every key and value tile and a
+// tile of rows spans only 128 / G tokens of the diagonal.  Work is split by
+// role:
+//   - a producer thread copies the query tiles and then the 128-key tiles of
+//     K and V with TMA into a ring of shared-memory stages;
+//   - an issuing thread runs the products on the tensor cores: S = Q K^T of
+//     both 128-row tiles into tensor memory, then, as soon as a tile's
+//     weights are there, O += P V (P read from tensor memory, where it
+//     replaces S) and the next S of the same tile;
+//   - two groups of four warps, one per tile, turn S into P, a thread per
+//     row: maximum, exp2, sum, all in registers.
+// While one tile is in its softmax the tensor cores work for the other.  The
+// products of a block run in the order of their issue, so S of step j being
+// complete means that O holds steps up to j - 1: a row whose maximum grew by
+// more than 2^8 rescales O right then, and the others do not touch it.
+//
+// Bound by the tensor cores (4 d flops a visible pair): per 128 keys a tile
+// takes 1024 cycles of products and as many of exponentials and conversions.
+//
+// What a row does not see has weight 0, but 0 times an infinity or NaN in V
+// is NaN: value rows past the end of a sequence are cleared in shared memory,
+// and a row whose result is not finite is computed again by prompt_row, which
+// reads only what the row sees.
+#include <cuda.h>
+
+#include <algorithm>
+
 #include "kv4_internal.cuh"
 
 namespace paris {
@@ -22,7 +52,7 @@ __device__ __forceinline__ float dot8(uint4 a, const float* q, float acc) {
 // One query row by one warp: its visible keys 32 at a time, a lane per key
 // for the scores, four channels per lane for the weighted sum.  Only rows
 // that the query sees are read.  qs: the warp's 128 floats of shared memory.
-__device__ void prompt_row(const PromptArgs& a, int s, int h, int64_t q0, int64_t i, int64_t k0, int64_t visible,
+__device__ __noinline__ void prompt_row(const PromptArgs& a, int s, int h, int64_t q0, int64_t i, int64_t k0, int64_t visible,
                            float* qs) {
   const int lane = threadIdx.x & 31;
   const int kvh = h / a.g;
@@ -74,18 +104,527 @@ __device__ void prompt_row(const PromptArgs& a, int s, int h, int64_t q0, int64_
   __syncwarp();
 }
 
-__global__ void __launch_bounds__(32 * kRowWarps) k_prompt_rows(PromptArgs a) {
+// ------------------------------------------------------------ the tensor-core kernel
+constexpr int kTile = 128;            // query rows of a tile, keys of a block
+constexpr int kTiles = 2;             // query tiles of a block
+constexpr int kStages = 4;            // K and V tiles in flight
+constexpr int kTileBytes = kTile * kDim * 2;
+constexpr int kHalfBytes = kTileBytes / 2;  // 64 channels of a tile: rows of 128 bytes, swizzled
+constexpr int kPromptThreads = 384;   // two softmax groups; a group with the issuing and the producing warp
+// Registers of a thread: 168 at launch (65536 / 384); the third group gives
+// up what the softmax groups, with a whole row of S each, need:
+// 2 x 216 + 72 = 3 x 168.
+constexpr int kSoftmaxRegs = 216, kIssueRegs = 72;
+constexpr int kPartRow = kDim + 4;    // split partial of a row: maximum, sum, -, -, o
+constexpr float kGrowth = 8.f;        // a row's maximum may lag this far (base 2): weights stay below 2^8
+constexpr size_t kPromptSmem = (size_t)(kTiles + kStages) * kTileBytes + 1024;
+constexpr uint64_t kWaitNs = 4000000000ull;  // a wait that takes this long gives up
+
+__device__ uint32_t g_prompt_error;  // set when a wait gave up
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.b32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;\n" : "=l"(t));
+  return t;
+}
+// Wait for a phase; false when it, or another wait of the block, gave up.
+__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
+  const uint64_t t0 = now_ns();
+  while (!bar_try(bar, parity)) {
+    if (*gave_up) return false;
+    if (now_ns() - t0 > kWaitNs) {
+      *gave_up = 1;
+      atomicOr(&g_prompt_error, 1u);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
+  if (bar_try(bar, parity)) return true;
+  return bar_wait_slow(bar, parity, gave_up);
+}
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+
+// Shared-memory matrix descriptor: 128-byte swizzle; lbo and sbo in bytes.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// bf16 x bf16 -> float32, M = 128, N = 128; bit 16: B has its N axis contiguous.
+constexpr uint32_t kInstr = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kTile / 8) << 17) | ((uint32_t)(kTile / 16) << 24);
+constexpr uint32_t kInstrNB = kInstr | (1u << 16);
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a),
+      "l"(b), "r"(kInstr), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a),
+      "l"(b), "r"(kInstrNB), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+#define TM32(r, o)                                                                                                     \
+  "r"(r[o + 0]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]),             \
+      "r"(r[o + 7]), "r"(r[o + 8]), "r"(r[o + 9]), "r"(r[o + 10]), "r"(r[o + 11]), "r"(r[o + 12]), "r"(r[o + 13]),     \
+      "r"(r[o + 14]), "r"(r[o + 15]), "r"(r[o + 16]), "r"(r[o + 17]), "r"(r[o + 18]), "r"(r[o + 19]), "r"(r[o + 20]),  \
+      "r"(r[o + 21]), "r"(r[o + 22]), "r"(r[o + 23]), "r"(r[o + 24]), "r"(r[o + 25]), "r"(r[o + 26]), "r"(r[o + 27]),  \
+      "r"(r[o + 28]), "r"(r[o + 29]), "r"(r[o + 30]), "r"(r[o + 31])
+#define TM32O(r, o)                                                                                                    \
+  "=r"(r[o + 0]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]),      \
+      "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]), "=r"(r[o + 10]), "=r"(r[o + 11]), "=r"(r[o + 12]),               \
+      "=r"(r[o + 13]), "=r"(r[o + 14]), "=r"(r[o + 15]), "=r"(r[o + 16]), "=r"(r[o + 17]), "=r"(r[o + 18]),            \
+      "=r"(r[o + 19]), "=r"(r[o + 20]), "=r"(r[o + 21]), "=r"(r[o + 22]), "=r"(r[o + 23]), "=r"(r[o + 24]),            \
+      "=r"(r[o + 25]), "=r"(r[o + 26]), "=r"(r[o + 27]), "=r"(r[o + 28]), "=r"(r[o + 29]), "=r"(r[o + 30]),            \
+      "=r"(r[o + 31])
+#define TM32S                                                                                                          \
+  "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, "    \
+  "%24, %25, %26, %27, %28, %29, %30, %31}"
+
+// 32 columns of the warp's 32 lanes of tensor memory: a lane's row.
+template <int N>
+__device__ __forceinline__ void tm_ld32(uint32_t (&r)[N], int o, uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 " TM32S ", [%32];\n" : TM32O(r, o) : "r"(addr) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t (&r)[N], int o) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], " TM32S ";\n" ::TM32(r, o), "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+struct PromptMaps {
+  CUtensorMap q, k, v;
+};
+
+struct PromptShared {
+  uint64_t q_full, full[kStages], empty[kStages], s_full[kTiles], p_full[kTiles], o_full[kTiles];
+  uint32_t tmem;
+  uint32_t gave_up;
+};
+
+// The block's share of the work.
+struct PromptWork {
+  int s, kvh, qb, split;
+  int64_t q0, lq, k0, lk;
+  int64_t t0;        // first token of tile 0
+  int tq;            // tokens of a tile
+  int jb, end[kTiles];  // key blocks [jb, end) of each tile
+};
+
+__device__ __forceinline__ bool prompt_work(const PromptArgs& a, int nqb, PromptWork& w) {
+  // later query blocks see more keys: they start first
+  const int per = a.n_seqs * a.hkv * a.nsplit;
+  int x = blockIdx.x;
+  w.qb = nqb - 1 - x / per;
+  x %= per;
+  w.split = x % a.nsplit;
+  x /= a.nsplit;
+  w.kvh = x % a.hkv;
+  w.s = x / a.hkv;
+  seq_rows(a.cu_q, w.s, a.rows_q, w.q0, w.lq);
+  seq_rows(a.cu_k, w.s, a.rows_k, w.k0, w.lk);
+  const int64_t lq = min64(w.lq, a.max_q);
+  w.tq = kTile / a.g;
+  w.t0 = (int64_t)w.qb * kTiles * w.tq;
+  if (w.t0 >= lq) return false;
+  // keys of each tile: up to what its last token sees
+  int n[kTiles], most = 0;
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i) {
+    const int64_t first = w.t0 + i * w.tq, last = min64(first + w.tq, lq) - 1;
+    const int64_t seen = first <= last ? min64(w.lk, last + w.lk - w.lq + 1) : 0;
+    n[i] = seen > 0 ? (int)((seen + kTile - 1) / kTile) : 0;
+    most = max(most, n[i]);
+  }
+  const int share = (most + a.nsplit - 1) / a.nsplit;
+  w.jb = min(w.split * share, most);
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i) w.end[i] = max(w.jb, min(n[i], w.jb + share));
+  return true;
+}
+
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    k_prompt_attend(const __grid_constant__ PromptArgs a, const __grid_constant__ PromptMaps maps, int nqb) {
+  extern __shared__ uint8_t dyn[];
+  __shared__ PromptShared sh;
+  pdl_wait();
+  pdl_trigger();
+  PromptWork w;
+  if (!prompt_work(a, nqb, w)) return;
+  const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int jb = w.jb, e0 = w.end[0], e1 = w.end[1], e = max(e0, e1);
+  const uint32_t q_full = smem_u32(&sh.q_full), full = smem_u32(&sh.full[0]), empty = smem_u32(&sh.empty[0]);
+  const uint32_t s_full = smem_u32(&sh.s_full[0]), p_full = smem_u32(&sh.p_full[0]), o_full = smem_u32(&sh.o_full[0]);
+  if (tid == 0) {
+    sh.gave_up = 0;
+    bar_init(q_full, 1);
+    for (int i = 0; i < kStages; ++i) {
+      bar_init(full + 8 * i, 1);
+      bar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < kTiles; ++i) {
+      bar_init(s_full + 8 * i, 1);
+      bar_init(p_full + 8 * i, kTile);
+      bar_init(o_full + 8 * i, 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&sh.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+    tm_fence_before();
+  }
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tmem = *(volatile uint32_t*)&sh.tmem;
+  volatile uint32_t* gave_up = &sh.gave_up;
+  const uint32_t ring = base + kTiles * kTileBytes;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kIssueRegs));
+  if (warp == 9) {
+    // ---- producer
+    if (lane == 0 && e > jb) {
+      const int qseq = a.cu_q ? 0 : w.s, kseq = a.cu_k ? 0 : w.s;
+      bar_expect(q_full, (uint32_t)(kTiles * 2 * w.tq * a.g * 128));
+      for (int i = 0; i < kTiles; ++i)
+        for (int h = 0; h < 2; ++h)
+          tma_load(base + i * kTileBytes + h * kHalfBytes, &maps.q, 64 * h, w.kvh * a.g, (int)(w.q0 + w.t0) + i * w.tq, qseq, q_full);
+      const int n = 2 * (e - jb);
+      int x = 0;
+      for (; x < n; ++x) {
+        const int st = x % kStages, turn = x / kStages;
+        if (turn > 0 && !bar_wait(empty + 8 * st, (turn - 1) & 1, gave_up)) break;
+        bar_expect(full + 8 * st, kTileBytes);
+        const CUtensorMap* m = (x & 1) ? &maps.v : &maps.k;
+        const int row = (int)w.k0 + (jb + (x >> 1)) * kTile;
+        for (int h = 0; h < 2; ++h) tma_load(ring + st * kTileBytes + h * kHalfBytes, m, 64 * h, row, w.kvh, kseq, full + 8 * st);
+      }
+      if (x < n) {  // given up: what was issued lands before the block ends
+        const uint64_t t0 = now_ns();
+        while (!bar_try(q_full, 0) && now_ns() - t0 < kWaitNs) {}
+        for (int y = max(0, x - kStages); y < x; ++y)
+          while (!bar_try(full + 8 * (y % kStages), (y / kStages) & 1) && now_ns() - t0 < kWaitNs) {}
+      }
+    }
+  } else if (warp == 8) {
+    // ---- products (the whole warp walks; lane 0 issues)
+    auto wait = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(kFull, bar_wait(bar, parity, gave_up)); };
+    bool ok = e > jb && wait(q_full, 0);
+    auto scores = [&](int i, int x) {  // S_i = Q_i K^T with the key tile in stage x
+      const uint32_t qa = base + i * kTileBytes, kb = ring + (x % kStages) * kTileBytes;
+      const uint64_t qd = smem_desc(qa, 16, 1024), kd = smem_desc(kb, 16, 1024);
+#pragma unroll 1
+      for (int c = 0; c < kDim / 16; ++c) {
+        const uint32_t off = (c >> 2) * (kHalfBytes >> 4) + (c & 3) * 2;
+        mma_ss(tmem + i * kTile, qd + off, kd + off, c > 0);
+      }
+      mma_commit(s_full + 8 * i);
+    };
+    const int ends[kTiles] = {e0, e1};
+    if (ok) ok = wait(full, 0);
+    if (ok && lane == 0) {
+      tm_fence_after();
+      for (int i = 0; i < kTiles; ++i)
+        if (jb < ends[i]) scores(i, 0);
+      mma_commit(empty);
+    }
+    __syncwarp();
+    const int tail = (int)(w.lk % kTile);  // keys of the sequence's last, unfilled block
+    for (int j = jb; ok && j < e; ++j) {
+      const int xv = 2 * (j - jb) + 1, xk = xv + 1;
+      ok = wait(full + 8 * (xv % kStages), (xv / kStages) & 1);
+      if (ok && j + 1 < e) ok = wait(full + 8 * (xk % kStages), (xk / kStages) & 1);
+      if (!ok) break;
+      const uint32_t vb = ring + (xv % kStages) * kTileBytes;
+      if (tail && j == (int)(w.lk / kTile)) {
+        // value rows past the sequence's end: anything times weight 0 is 0
+        for (int x = tail * 8 + lane; x < kTile * 8; x += 32)
+          for (int h = 0; h < 2; ++h)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(vb + h * kHalfBytes + x * 16), "r"(0) : "memory");
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        __syncwarp();
+      }
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) {
+        if (ok && j < ends[i]) ok = wait(p_full + 8 * i, (j - jb) & 1);
+        if (ok && lane == 0 && j < ends[i]) {
+          tm_fence_after();
+          const uint64_t vd = smem_desc(vb, kHalfBytes, 1024);
+#pragma unroll 1
+          for (int c = 0; c < kTile / 16; ++c)  // 16 keys: 8 columns of weights, 16 rows of V
+            mma_ts(tmem + (2 + i) * kTile, tmem + i * kTile + 8 * c, vd + c * 128, j > jb || c > 0);
+          if (j + 1 == ends[i]) mma_commit(o_full + 8 * i);
+          if (j + 1 < ends[i]) scores(i, xk);
+        }
+        __syncwarp();
+      }
+      if (ok && lane == 0) {
+        mma_commit(empty + 8 * (xv % kStages));
+        if (j + 1 < e) mma_commit(empty + 8 * (xk % kStages));
+      }
+      __syncwarp();
+    }
+  }
+  } else {
+    // ---- softmax of tile i, a row per thread
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
+    const int i = warp >> 2, row = tid & (kTile - 1);
+    const int end = i ? e1 : e0;
+    const int64_t tok = w.t0 + (int64_t)i * w.tq + row / a.g;
+    const int64_t lq = min64(w.lq, a.max_q);
+    const bool live = row < w.tq * a.g && tok < lq;
+    const int h = w.kvh * a.g + row % a.g;
+    // the last key the row sees; rows that are not there see what the first does
+    const int64_t first_tok = w.t0 + (int64_t)i * w.tq;
+    const int64_t last_key = min64(w.lk, (live ? tok : first_tok) + w.lk - w.lq + 1) - 1;
+    const int64_t tile_key = min64(w.lk, first_tok + w.lk - w.lq + 1) - 1;  // every row of the tile sees this far
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + i * kTile, to = tmem + lanes + (2 + i) * kTile;
+    float m = -INFINITY, l = 0.f;  // base 2
+    bool ok = true;
+    for (int j = jb; j < end; ++j) {
+      ok = bar_wait(s_full + 8 * i, (j - jb) & 1, gave_up);
+      ok = __all_sync(kFull, ok);
+      if (!ok) break;
+      tm_fence_after();
+      uint32_t s[kTile];
+      tm_ld32(s, 0, ts);
+      tm_ld32(s, 32, ts + 32);
+      tm_ld32(s, 64, ts + 64);
+      tm_ld32(s, 96, ts + 96);
+      tm_wait_ld();
+      if ((int64_t)(j + 1) * kTile - 1 > tile_key) {
+        const int left = (int)max64(-1, min64(kTile, last_key - (int64_t)j * kTile));  // last visible column
+#pragma unroll
+        for (int c = 0; c < kTile; ++c)
+          if (c > left) s[c] = 0xff800000u;  // -inf
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < kTile; c += 8)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          mx[u] = fmaxf(mx[u], fmaxf(__uint_as_float(s[c + 2 * u]), __uint_as_float(s[c + 2 * u + 1])));
+      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kScaleLog2;
+      const bool grew = mt > m + kGrowth;
+      if (j > jb && __any_sync(kFull, grew)) {
+        const float f = grew ? ex2(m - mt) : 1.f;
+        uint32_t o[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tm_ld32(o, 0, to + 32 * c);
+          tm_wait_ld();
+#pragma unroll
+          for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+          tm_st32(to + 32 * c, o, 0);
+        }
+        l *= f;
+      }
+      if (grew || m == -INFINITY) m = mt;
+      const float neg = m == -INFINITY ? 0.f : -m;
+      const uint64_t c2 = pair2(kScaleLog2, kScaleLog2), n2 = pair2(neg, neg);
+      uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+      for (int c = 0; c < kTile; c += 4) {
+        float x0, x1, x2, x3;
+        unpair2(fma2(pair2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), c2, n2), x0, x1);
+        unpair2(fma2(pair2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), c2, n2), x2, x3);
+        x0 = ex2(x0);
+        x1 = ex2(x1);
+        x2 = ex2(x2);
+        x3 = ex2(x3);
+        sum0 = add2(sum0, pair2(x0, x1));
+        sum1 = add2(sum1, pair2(x2, x3));
+        s[c / 2] = pack_bf16x2(x0, x1);
+        s[c / 2 + 1] = pack_bf16x2(x2, x3);
+      }
+      tm_st32(ts, s, 0);
+      tm_st32(ts + 32, s, 32);
+      tm_wait_st();
+      tm_fence_before();
+      bar_arrive(p_full + 8 * i);
+      float a0, a1;
+      unpair2(add2(sum0, sum1), a0, a1);
+      l += a0 + a1;
+    }
+    // ---- result
+    float* part = a.nsplit > 1
+        ? a.ws + ((((int64_t)w.s * a.hkv + w.kvh) * nqb + w.qb) * a.nsplit + w.split) * (kTiles * kTile) * kPartRow +
+              ((int64_t)i * kTile + row) * kPartRow
+        : nullptr;
+    const bool any = end > jb;
+    if (any && ok) ok = bar_wait(o_full + 8 * i, 0, gave_up);
+    ok = __all_sync(kFull, ok);
+    if (ok) {
+      if (any) tm_fence_after();
+      const float inv = l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing: 0
+      bool finite = true;
+      __nv_bfloat16* out = live ? a.out + (a.cu_q ? 0 : w.s * a.so.seq) + (w.q0 + tok) * a.so.token + h * a.so.head : nullptr;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        if (any) {
+          tm_ld32(o, 0, to + 32 * c);
+          tm_wait_ld();
+        } else {
+#pragma unroll
+          for (int u = 0; u < 32; ++u) o[u] = 0;
+        }
+        if (part != nullptr) {
+          if (live)
+#pragma unroll
+            for (int u = 0; u < 32; u += 4)
+              *reinterpret_cast<uint4*>(part + 4 + 32 * c + u) = make_uint4(o[u], o[u + 1], o[u + 2], o[u + 3]);
+          continue;
+        }
+#pragma unroll
+        for (int u = 0; u < 32; u += 8) {
+          uint32_t p[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float y0 = __uint_as_float(o[u + 2 * x]) * inv, y1 = __uint_as_float(o[u + 2 * x + 1]) * inv;
+            finite = finite && fabsf(y0) < INFINITY && fabsf(y1) < INFINITY;
+            p[x] = pack_bf16x2(y0, y1);
+          }
+          if (live) *reinterpret_cast<uint4*>(out + 32 * c + u) = make_uint4(p[0], p[1], p[2], p[3]);
+        }
+      }
+      if (part != nullptr) {
+        if (live) {
+          part[0] = m;
+          part[1] = l;
+        }
+      } else {
+        if (live && a.lse != nullptr)
+          a.lse[((int64_t)(a.cu_q ? 0 : w.s) * a.hq + h) * a.rows_q + w.q0 + tok] = last_key >= 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
+        // the tile's queries have been used: their place is the scratch
+        float* qs = reinterpret_cast<float*>(dyn + (base - smem_u32(dyn)) + i * kTileBytes) + (warp & 3) * kDim;
+        for (uint32_t again = __ballot_sync(kFull, live && !finite); again; again &= again - 1) {
+          const int src = __ffs(again) - 1;
+          const int64_t t = __shfl_sync(kFull, tok, src);
+          prompt_row(a, w.s, __shfl_sync(kFull, h, src), w.q0, t, w.k0, min64(w.lk, t + w.lk - w.lq + 1), qs);
+        }
+      }
+    }
+    tm_fence_before();
+  }
+  __syncthreads();
+  if (warp == 8) {
+    tm_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
+  }
+}
+
+// A warp per query row: join the splits' partials.
+__global__ void __launch_bounds__(32 * kRowWarps) k_prompt_join(PromptArgs a, int nqb) {
   __shared__ float qs[kRowWarps][kDim];
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5;
-  const int s = blockIdx.z, h = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.y, s = blockIdx.z, kvh = h / a.g;
   int64_t q0, lq, k0, lk;
   seq_rows(a.cu_q, s, a.rows_q, q0, lq);
   seq_rows(a.cu_k, s, a.rows_k, k0, lk);
-  const int64_t i = (int64_t)blockIdx.x * kRowWarps + warp;
-  if (i >= min64(lq, a.max_q)) return;
-  prompt_row(a, s, h, q0, i, k0, max64(0, min64(lk, i + lk - lq + 1)), qs[warp]);
+  const int64_t tok = (int64_t)blockIdx.x * kRowWarps + warp;
+  if (tok >= min64(lq, a.max_q)) return;
+  const int tq = kTile / a.g;
+  const int64_t qb = tok / (kTiles * tq);
+  const int in = (int)(tok - qb * kTiles * tq), row = in / tq * kTile + in % tq * a.g + h % a.g;
+  const float* part = a.ws + ((((int64_t)s * a.hkv + kvh) * nqb + qb) * a.nsplit * (kTiles * kTile) + row) * kPartRow;
+  const int64_t step = (int64_t)(kTiles * kTile) * kPartRow;
+  float M = -INFINITY;
+  for (int x = 0; x < a.nsplit; ++x) M = fmaxf(M, part[x * step]);
+  float L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int x = 0; x < a.nsplit; ++x) {
+    const float4 v = *reinterpret_cast<const float4*>(part + x * step + 4 + 4 * lane);
+    const float2 ml = *reinterpret_cast<const float2*>(part + x * step);
+    const float f = ml.y == 0.f ? 0.f : ml.x == M ? 1.f : exp2f(ml.x - M);
+    if (ml.y == 0.f) continue;
+    L += ml.y * f;
+    o[0] = fmaf(v.x, f, o[0]);
+    o[1] = fmaf(v.y, f, o[1]);
+    o[2] = fmaf(v.z, f, o[2]);
+    o[3] = fmaf(v.w, f, o[3]);
+  }
+  const float inv = L != 0.f ? 1.f / L : 0.f;
+  bool finite = true;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    o[c] *= inv;
+    finite = finite && fabsf(o[c]) < INFINITY;
+  }
+  const int64_t visible = max64(0, min64(lk, tok + lk - lq + 1));
+  if (!__all_sync(kFull, finite)) {
+    prompt_row(a, s, h, q0, tok, k0, visible, qs[warp]);
+    return;
+  }
+  __nv_bfloat16* out = a.out + (a.cu_q ? 0 : s * a.so.seq) + (q0 + tok) * a.so.token + h * a.so.head;
+  *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+  if (a.lse != nullptr && lane == 0)
+    a.lse[((int64_t)(a.cu_q ? 0 : s) * a.hq + h) * a.rows_q + q0 + tok] = visible > 0 ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
 // One warp per (KV head, key): the window's queries in order.
@@ -122,14 +661,91 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_prompt_weights(PromptWeightA
 
 }  // namespace
 
-size_t prompt_workspace_bytes(PromptArgs& a, int) {
-  a.nsplit = 1;
-  return 0;
+namespace {
+
+int64_t prompt_blocks(const PromptArgs& a) {  // blocks of query rows of the longest sequence
+  const int64_t tokens = kTiles * (kTile / a.g);
+  return (a.max_q + tokens - 1) / tokens;
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult st;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &st) != cudaSuccess ||
+        st != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// 64 channels x box1 x box2 of a tensor of bf16 rows of 128, 128-byte swizzle.
+bool encode(CUtensorMap* m, const void* p, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t n3, int64_t s3, int box1, int box2) {
+  EncodeTiled fn = encode_tiled();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)kDim, (cuuint64_t)n1, (cuuint64_t)n2, (cuuint64_t)n3};
+  const cuuint64_t strides[3] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2, (cuuint64_t)s3 * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box1, (cuuint32_t)box2, 1}, one[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The kernel's shared-memory limit belongs to the device and is set once on
+// each (a second thread doing the same is harmless).
+cudaError_t raise_smem() {
+  static bool done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev >= 0 && dev < 64 && done[dev])) return e;
+  e = cudaFuncSetAttribute((const void*)k_prompt_attend, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPromptSmem);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  return e;
+}
+
+}  // namespace
+
+size_t prompt_workspace_bytes(PromptArgs& a, int sm_count) {
+  // Blocks of rows that do not fill the GPU share their keys among splits,
+  // at least four key blocks each.
+  const int64_t units = prompt_blocks(a) * a.n_seqs * a.hkv;
+  const int64_t most = std::max<int64_t>(1, (a.max_k + 4 * kTile - 1) / (4 * kTile));
+  a.nsplit = (int)std::min<int64_t>({most, std::max<int64_t>(1, sm_count / units), 64});
+  return a.nsplit > 1 ? (size_t)units * a.nsplit * kTiles * kTile * kPartRow * sizeof(float) : 0;
 }
 
 cudaError_t launch_prompt_attend(const PromptArgs& a, cudaStream_t st) {
+  PromptMaps m;
+  const int64_t ns = a.cu_q ? 1 : a.n_seqs;
+  const int tq = kTile / a.g;
+  // no keys at all: nothing is loaded, and any valid address will do
+  const void* k = a.rows_k > 0 ? a.k : a.q;
+  const void* v = a.rows_k > 0 ? a.v : a.q;
+  const int64_t rows_k = std::max<int64_t>(1, a.rows_k);
+  if (!encode(&m.q, a.q, a.hq, a.sq.head, a.rows_q, a.sq.token, ns, a.sq.seq, a.g, tq) ||
+      !encode(&m.k, k, rows_k, a.sk.token, a.hkv, a.sk.head, ns, a.sk.seq, kTile, 1) ||
+      !encode(&m.v, v, rows_k, a.sv.token, a.hkv, a.sv.head, ns, a.sv.seq, kTile, 1))
+    return cudaErrorInvalidValue;
+  cudaError_t e = raise_smem();
+  if (e != cudaSuccess) return e;
+  const int64_t nqb = prompt_blocks(a), blocks = nqb * a.n_seqs * a.hkv * a.nsplit;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  e = launch_pdl(k_prompt_attend, dim3((unsigned)blocks), dim3(kPromptThreads), kPromptSmem, st, a, m, (int)nqb);
+  if (e != cudaSuccess || a.nsplit == 1) return e;
   const dim3 grid((unsigned)((a.max_q + kRowWarps - 1) / kRowWarps), a.hq, a.n_seqs);
-  return launch_pdl(k_prompt_rows, grid, dim3(32 * kRowWarps), 0, st, a);
+  return launch_pdl(k_prompt_join, grid, dim3(32 * kRowWarps), 0, st, a, (int)nqb);
+}
+
+cudaError_t prompt_error(uint32_t* bits) {
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(bits, g_prompt_error, sizeof *bits);
+  const uint32_t zero = 0;
+  if (e == cudaSuccess && *bits) e = cudaMemcpyToSymbol(g_prompt_error, &zero, sizeof zero);
+  return e;
 }
 
 cudaError_t launch_prompt_weights(const PromptWeightArgs& w, cudaStream_t st) {

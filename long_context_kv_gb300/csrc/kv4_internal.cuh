@@ -91,6 +91,8 @@ struct PromptArgs {
 cudaError_t launch_prompt_attend(const PromptArgs& a, cudaStream_t st);
 size_t prompt_workspace_bytes(PromptArgs& a, int sm_count);  // sets a.nsplit
 
+cudaError_t prompt_error(uint32_t* bits);  // synchronises; reads and clears the error word
+
 struct PromptWeightArgs {
   PromptArgs p;
   const float* lse;

@@ -161,6 +161,14 @@ paris_status paris_prompt_attend(const paris_prompt* p, const void* q, const voi
   return launched(launch_prompt_attend(a, static_cast<cudaStream_t>(stream)), "paris_prompt_attend");
 }
 
+paris_status paris_prompt_check(void) {
+  uint32_t w = 0;
+  const cudaError_t e = prompt_error(&w);
+  if (e != cudaSuccess) return launched(e, "paris_prompt_check");
+  if (w) return fail(PARIS_EDEVICE, "a prompt call gave up waiting for its copies or products: its results are not valid");
+  return PARIS_OK;
+}
+
 paris_status paris_prompt_weights(const paris_prompt* p, const void* q, const void* k, paris_dtype dtype,
                                   const float* lse, int window, float* weights, void* stream) {
   PromptWeightArgs w{};

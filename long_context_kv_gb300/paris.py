@@ -57,6 +57,7 @@ _SIGNATURES = {
     "paris_prompt_attend": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                            ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                            ctypes.c_size_t, ctypes.c_void_p]),
+    "paris_prompt_check": (ctypes.c_int, []),
     "paris_prompt_weights": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
                                             ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p]),
     "paris_kv4_store": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
@@ -395,6 +396,11 @@ def paris_prompt_attend(q, k, v, out, cu_q=None, cu_k=None, max_q=None, max_k=No
     ws = _scratch(n.value, q.device, stream) if n.value else None
     _check(lib.paris_prompt_attend(ctypes.byref(p), _raw(q), _raw(k), _raw(v), PARIS_BF16, _raw(out), _raw(lse),
                                    _raw(ws), n.value, _stream(stream)))
+
+
+def paris_prompt_check():
+    """Synchronise; raise if a prompt call gave up a wait."""
+    _check(load().paris_prompt_check())
 
 
 def paris_prompt_weights(q, k, lse, weights, window, cu_q=None, cu_k=None, max_k=None, stream=None):
