@@ -107,7 +107,7 @@ __device__ __noinline__ void prompt_row(const PromptArgs& a, int s, int h, int64
 // ------------------------------------------------------------ the tensor-core kernel
 constexpr int kTile = 128;            // query rows of a tile, keys of a block
 constexpr int kTiles = 2;             // query tiles of a block
-constexpr int kStages = 4;            // K and V tiles in flight
+constexpr int kStages = 5;            // K and V tiles in flight
 constexpr int kTileBytes = kTile * kDim * 2;
 constexpr int kHalfBytes = kTileBytes / 2;  // 64 channels of a tile: rows of 128 bytes, swizzled
 constexpr int kPromptThreads = 384;   // two softmax groups; a group with the issuing and the producing warp
@@ -193,6 +193,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "l"(b), "r"(kInstrNB), "r"(acc)
       : "memory");
 }
+// One lane of a converged warp, chosen so that the compiler keeps the
+// operands of what it issues in uniform registers.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
 }
@@ -222,6 +229,14 @@ __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sy
 template <int N>
 __device__ __forceinline__ void tm_ld32(uint32_t (&r)[N], int o, uint32_t addr) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 " TM32S ", [%32];\n" : TM32O(r, o) : "r"(addr) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[N], int o) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};\n" ::"r"(r[o]),
+      "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7]), "r"(r[o + 8]),
+      "r"(r[o + 9]), "r"(r[o + 10]), "r"(r[o + 11]), "r"(r[o + 12]), "r"(r[o + 13]), "r"(r[o + 14]), "r"(r[o + 15]), "r"(addr)
+      : "memory");
 }
 template <int N>
 __device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t (&r)[N], int o) {
@@ -257,7 +272,7 @@ struct PromptMaps {
 };
 
 struct PromptShared {
-  uint64_t q_full, full[kStages], empty[kStages], s_full[kTiles], p_full[kTiles], o_full[kTiles];
+  uint64_t q_full, full[kStages], empty[kStages], s_full[kTiles], p_full[2 * kTiles], o_full[kTiles];
   uint32_t tmem;
   uint32_t gave_up;
 };
@@ -312,7 +327,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   PromptWork w;
   if (!prompt_work(a, nqb, w)) return;
   const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same for the warp, and known to be
   const int jb = w.jb, e0 = w.end[0], e1 = w.end[1], e = max(e0, e1);
   const uint32_t q_full = smem_u32(&sh.q_full), full = smem_u32(&sh.full[0]), empty = smem_u32(&sh.empty[0]);
   const uint32_t s_full = smem_u32(&sh.s_full[0]), p_full = smem_u32(&sh.p_full[0]), o_full = smem_u32(&sh.o_full[0]);
@@ -325,7 +341,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
     for (int i = 0; i < kTiles; ++i) {
       bar_init(s_full + 8 * i, 1);
-      bar_init(p_full + 8 * i, kTile);
+      bar_init(p_full + 16 * i, kTile);
+      bar_init(p_full + 16 * i + 8, kTile);
       bar_init(o_full + 8 * i, 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -337,7 +354,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
   __syncthreads();
   tm_fence_after();
-  const uint32_t tmem = *(volatile uint32_t*)&sh.tmem;
+  const uint32_t tmem = __shfl_sync(kFull, *(volatile uint32_t*)&sh.tmem, 0);
   volatile uint32_t* gave_up = &sh.gave_up;
   const uint32_t ring = base + kTiles * kTileBytes;
 
@@ -369,13 +386,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     }
   } else if (warp == 8) {
-    // ---- products (the whole warp walks; lane 0 issues)
+    // ---- products (the whole warp walks; one lane issues)
     auto wait = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(kFull, bar_wait(bar, parity, gave_up)); };
     bool ok = e > jb && wait(q_full, 0);
     auto scores = [&](int i, int x) {  // S_i = Q_i K^T with the key tile in stage x
       const uint32_t qa = base + i * kTileBytes, kb = ring + (x % kStages) * kTileBytes;
       const uint64_t qd = smem_desc(qa, 16, 1024), kd = smem_desc(kb, 16, 1024);
-#pragma unroll 1
+#pragma unroll
       for (int c = 0; c < kDim / 16; ++c) {
         const uint32_t off = (c >> 2) * (kHalfBytes >> 4) + (c & 3) * 2;
         mma_ss(tmem + i * kTile, qd + off, kd + off, c > 0);
@@ -384,7 +401,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     };
     const int ends[kTiles] = {e0, e1};
     if (ok) ok = wait(full, 0);
-    if (ok && lane == 0) {
+    if (ok && elect()) {
       tm_fence_after();
       for (int i = 0; i < kTiles; ++i)
         if (jb < ends[i]) scores(i, 0);
@@ -408,19 +425,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
 #pragma unroll
       for (int i = 0; i < kTiles; ++i) {
-        if (ok && j < ends[i]) ok = wait(p_full + 8 * i, (j - jb) & 1);
-        if (ok && lane == 0 && j < ends[i]) {
+        // 16 keys a product: 8 columns of weights, 16 rows of V
+        const uint64_t vd = smem_desc(vb, kHalfBytes, 1024);
+        auto values = [&](int c) { mma_ts(tmem + (2 + i) * kTile, tmem + i * kTile + 8 * c, vd + c * 128, j > jb || c > 0); };
+        if (ok && j < ends[i]) ok = wait(p_full + 16 * i, (j - jb) & 1);
+        if (ok && j < ends[i] && elect()) {
           tm_fence_after();
-          const uint64_t vd = smem_desc(vb, kHalfBytes, 1024);
-#pragma unroll 1
-          for (int c = 0; c < kTile / 16; ++c)  // 16 keys: 8 columns of weights, 16 rows of V
-            mma_ts(tmem + (2 + i) * kTile, tmem + i * kTile + 8 * c, vd + c * 128, j > jb || c > 0);
+#pragma unroll
+          for (int c = 0; c < 6; ++c) values(c);
+        }
+        __syncwarp();
+        if (ok && j < ends[i]) ok = wait(p_full + 16 * i + 8, (j - jb) & 1);
+        if (ok && j < ends[i] && elect()) {
+          tm_fence_after();
+          values(6);
+          values(7);
           if (j + 1 == ends[i]) mma_commit(o_full + 8 * i);
           if (j + 1 < ends[i]) scores(i, xk);
         }
         __syncwarp();
       }
-      if (ok && lane == 0) {
+      if (ok && elect()) {
         mma_commit(empty + 8 * (xv % kStages));
         if (j + 1 < e) mma_commit(empty + 8 * (xk % kStages));
       }
@@ -461,33 +486,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         for (int c = 0; c < kTile; ++c)
           if (c > left) s[c] = 0xff800000u;  // -inf
       }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < kTile; c += 8)
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          mx[u] = fmaxf(mx[u], fmaxf(__uint_as_float(s[c + 2 * u]), __uint_as_float(s[c + 2 * u + 1])));
-      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kScaleLog2;
-      const bool grew = mt > m + kGrowth;
-      if (j > jb && __any_sync(kFull, grew)) {
-        const float f = grew ? ex2(m - mt) : 1.f;
-        uint32_t o[32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tm_ld32(o, 0, to + 32 * c);
-          tm_wait_ld();
-#pragma unroll
-          for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
-          tm_st32(to + 32 * c, o, 0);
-        }
-        l *= f;
-      }
-      if (grew || m == -INFINITY) m = mt;
-      const float neg = m == -INFINITY ? 0.f : -m;
-      const uint64_t c2 = pair2(kScaleLog2, kScaleLog2), n2 = pair2(neg, neg);
+      // The first weights are taken with the maximum so far while the block's
+      // own is found; only a row that grew past kGrowth does them again.
+      const uint64_t c2 = pair2(kScaleLog2, kScaleLog2);
       uint64_t sum0 = 0, sum1 = 0;
-#pragma unroll
-      for (int c = 0; c < kTile; c += 4) {
+      auto four = [&](int c, uint64_t n2, uint32_t& lo, uint32_t& hi) {
         float x0, x1, x2, x3;
         unpair2(fma2(pair2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), c2, n2), x0, x1);
         unpair2(fma2(pair2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), c2, n2), x2, x3);
@@ -497,14 +500,59 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         x3 = ex2(x3);
         sum0 = add2(sum0, pair2(x0, x1));
         sum1 = add2(sum1, pair2(x2, x3));
-        s[c / 2] = pack_bf16x2(x0, x1);
-        s[c / 2 + 1] = pack_bf16x2(x2, x3);
+        lo = pack_bf16x2(x0, x1);
+        hi = pack_bf16x2(x2, x3);
+      };
+      uint32_t first[16];
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      float neg = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+      for (int c = 0; c < 32; c += 4) {
+        four(c, pair2(neg, neg), first[c / 2], first[c / 2 + 1]);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          mx[u & 3] = fmaxf(mx[u & 3], fmaxf(__uint_as_float(s[4 * c + 2 * u]), __uint_as_float(s[4 * c + 2 * u + 1])));
       }
+      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kScaleLog2;
+      const bool grew = mt > m + kGrowth;
+      if (__any_sync(kFull, grew)) {
+        const float f = grew ? ex2(m - mt) : 1.f;
+        if (j > jb) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tm_ld32(o, 0, to + 32 * c);
+            tm_wait_ld();
+#pragma unroll
+            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+            tm_st32(to + 32 * c, o, 0);
+          }
+        }
+        l *= f;
+        if (grew) m = mt;
+        neg = m == -INFINITY ? 0.f : -m;
+        sum0 = sum1 = 0;
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) four(c, pair2(neg, neg), first[c / 2], first[c / 2 + 1]);
+      }
+      const uint64_t n2 = pair2(neg, neg);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) s[c] = first[c];
+#pragma unroll
+      for (int c = 32; c < 64; c += 4) four(c, n2, s[c / 2], s[c / 2 + 1]);
       tm_st32(ts, s, 0);
-      tm_st32(ts + 32, s, 32);
+#pragma unroll
+      for (int c = 64; c < 96; c += 4) four(c, n2, s[c / 2], s[c / 2 + 1]);
+      tm_st16(ts + 32, s, 32);
       tm_wait_st();
       tm_fence_before();
-      bar_arrive(p_full + 8 * i);
+      bar_arrive(p_full + 16 * i);  // the products may start on 96 keys
+#pragma unroll
+      for (int c = 96; c < 128; c += 4) four(c, n2, s[c / 2], s[c / 2 + 1]);
+      tm_st16(ts + 48, s, 48);
+      tm_wait_st();
+      tm_fence_before();
+      bar_arrive(p_full + 16 * i + 8);
       float a0, a1;
       unpair2(add2(sum0, sum1), a0, a1);
       l += a0 + a1;
