@@ -1,0 +1,243 @@
+// The weights that the last queries of each prompt give to its keys:
+// w_j = sum over the window's (query, query head) rows n of exp(s_nj - lse_n).
+//
+// The product is taken with the keys as rows, S = K Q^T, so that a key is a
+// lane of tensor memory and its sum stays in one thread: no reduction across
+// threads, no atomics.  A block holds up to 256 window rows of a KV head
+// (all of a 64-query window of four heads) in shared memory and walks a
+// range of 128-key tiles; a producing warp keeps K tiles coming by TMA, an
+// issuing warp runs a tile's product into one of two 256-column halves of
+// tensor memory, and two groups of four warps, a half each, take the
+// exponentials and add.  Longer windows go by in chunks of 256 rows, each
+// adding to the sums of the ones before.
+//
+// Bound by the read of K where the window is short, and by the products and
+// exponentials (1024 cycles each for a full tile, side by side) at 256 rows.
+#include <algorithm>
+
+#include "tc_device.cuh"
+
+namespace paris {
+namespace {
+
+constexpr int kWStages = 4;
+constexpr int kWRows = 256;            // window rows of a chunk
+constexpr int kWThreads = 384;
+constexpr int kKeyBytes = kTile * kDim * 2;
+constexpr int kQHalf = kWRows * 128;   // 64 channels of a chunk
+constexpr size_t kWSmem = (size_t)kWStages * kKeyBytes + 2 * kQHalf + 1024;
+
+struct WeightShared {
+  uint64_t q_full, q_empty, k_full[kWStages], k_empty[kWStages], s_full[2], s_empty[2];
+  uint32_t tmem, gave_up;
+  __align__(16) float lse[kWRows];  // base 2
+  int32_t lim[kWRows];  // last key that the row sees
+};
+
+struct WeightMaps {
+  CUtensorMap q, k;
+};
+
+__global__ void __launch_bounds__(kWThreads, 1)
+    k_prompt_weights(const __grid_constant__ PromptWeightArgs wa, const __grid_constant__ WeightMaps maps, int blocks_per_unit, int tiles_per_block) {
+  extern __shared__ uint8_t dyn[];
+  __shared__ __align__(16) WeightShared sh;
+  pdl_wait();
+  pdl_trigger();
+  const PromptArgs& a = wa.p;
+  const int unit = blockIdx.x / blocks_per_unit, part = blockIdx.x - unit * blocks_per_unit;
+  const int s = unit / a.hkv, kvh = unit - s * a.hkv;
+  int64_t q0, lq, k0, lk;
+  seq_rows(a.cu_q, s, a.rows_q, q0, lq);
+  seq_rows(a.cu_k, s, a.rows_k, k0, lk);
+  const int64_t lkm = min64(lk, a.max_k);
+  const int tile0 = part * tiles_per_block;
+  const int ntile = (int)min64(tiles_per_block, (lkm + kTile - 1) / kTile - tile0);
+  if (ntile <= 0) return;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(kFull, tid >> 5, 0);
+  const int win = (int)min64(wa.window, lq);      // queries of the window
+  const int tq = kWRows / a.g;                    // of a chunk
+  const int nchunk = (win + tq - 1) / tq;
+  float* out = wa.weights + ((int64_t)(a.cu_k ? 0 : s) * a.hkv + kvh) * a.rows_k + k0;
+  if (nchunk == 0) {
+    for (int64_t j = (int64_t)tile0 * kTile + tid; j < min64(lkm, (int64_t)(tile0 + ntile) * kTile); j += kWThreads) out[j] = 0.f;
+    return;
+  }
+  const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u, qb = base + kWStages * kKeyBytes;
+  const uint32_t q_full = smem_u32(&sh.q_full), q_empty = smem_u32(&sh.q_empty), k_full = smem_u32(&sh.k_full[0]),
+                 k_empty = smem_u32(&sh.k_empty[0]), s_full = smem_u32(&sh.s_full[0]), s_empty = smem_u32(&sh.s_empty[0]);
+  if (tid == 0) {
+    sh.gave_up = 0;
+    bar_init(q_full, 1);
+    bar_init(q_empty, 1);
+    for (int i = 0; i < kWStages; ++i) {
+      bar_init(k_full + 8 * i, 1);
+      bar_init(k_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(s_full + 8 * i, 1);
+      bar_init(s_empty + 8 * i, kTile);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&sh.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+    tm_fence_before();
+  }
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tmem = __shfl_sync(kFull, *(volatile uint32_t*)&sh.tmem, 0);
+  volatile uint32_t* gave_up = &sh.gave_up;
+  const int64_t first = lq - win;                 // first query of the window
+  const int total = nchunk * ntile;               // products, chunk by chunk
+  // rows of chunk c, and the product's N
+  auto rows_of = [&](int c) { return min(tq, win - c * tq) * a.g; };
+
+  if (warp == 9) {
+    if (lane == 0) {
+      int x = 0;
+      bool ok = true;
+      for (; ok && x < total; ++x) {
+        const int c = x / ntile, st = x % kWStages, turn = x / kWStages;
+        if (x % ntile == 0) {
+          if (c > 0) ok = bar_wait(q_empty, (c - 1) & 1, gave_up);
+          if (!ok) break;
+          bar_expect(q_full, (uint32_t)(2 * tq * a.g * 128));
+          for (int h = 0; h < 2; ++h)
+            tma_load(qb + h * kQHalf, &maps.q, 64 * h, kvh * a.g, (int)(q0 + first) + c * tq, a.cu_q ? 0 : s, q_full);
+        }
+        if (turn > 0) ok = bar_wait(k_empty + 8 * st, (turn - 1) & 1, gave_up);
+        if (!ok) break;
+        bar_expect(k_full + 8 * st, kKeyBytes);
+        for (int h = 0; h < 2; ++h)
+          tma_load(base + st * kKeyBytes + h * (kKeyBytes / 2), &maps.k, 64 * h, (int)k0 + (tile0 + x % ntile) * kTile, kvh, a.cu_k ? 0 : s,
+                   k_full + 8 * st);
+      }
+      if (x < total) {  // given up: what was issued lands before the block ends
+        const uint64_t t0 = now_ns();
+        for (int y = max(0, x - kWStages); y < x; ++y)
+          while (!bar_try(k_full + 8 * (y % kWStages), (y / kWStages) & 1) && now_ns() - t0 < kWaitNs) {}
+        while (x > 0 && !bar_try(q_full, ((x - 1) / ntile) & 1) && now_ns() - t0 < kWaitNs) {}
+      }
+    }
+  } else if (warp == 8) {
+    auto wait = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(kFull, bar_wait(bar, parity, gave_up)); };
+    bool ok = true;
+    for (int x = 0; ok && x < total; ++x) {
+      const int c = x / ntile, st = x % kWStages, buf = x & 1;
+      if (x % ntile == 0) ok = wait(q_full, c & 1);
+      if (ok) ok = wait(k_full + 8 * st, (x / kWStages) & 1);
+      if (ok && x > 1) ok = wait(s_empty + 8 * buf, ((x >> 1) - 1) & 1);
+      if (!ok) break;
+      if (elect()) {
+        tm_fence_after();
+        const uint32_t instr = mma_instr((uint32_t)(rows_of(c) + 15) & ~15u);
+        const uint64_t kd = smem_desc(base + st * kKeyBytes, 16, 1024), qd = smem_desc(qb, 16, 1024);
+#pragma unroll
+        for (int d = 0; d < kDim / 16; ++d)
+          mma_ss(tmem + buf * kWRows, kd + (d >> 2) * (kKeyBytes / 32) + (d & 3) * 2, qd + (d >> 2) * (kQHalf >> 4) + (d & 3) * 2, instr, d > 0);
+        mma_commit(s_full + 8 * buf);
+        mma_commit(k_empty + 8 * st);
+        if (x % ntile == ntile - 1) mma_commit(q_empty);
+      }
+      __syncwarp();
+    }
+  } else if (warp < 8) {
+    const int grp = warp >> 2, row = tid & (kTile - 1);
+    const uint32_t ts = tmem + ((uint32_t)((warp & 3) * 32) << 16) + grp * kWRows;
+    bool ok = true;
+    for (int c = 0; c < nchunk; ++c) {  // past a wait that gave up, only the barriers
+      const int n = rows_of(c);
+      // both groups are done with the last chunk's table before it changes
+      asm volatile("bar.sync 1, 256;\n" ::: "memory");
+      for (int r = tid; r < kWRows; r += 256) {
+        const int64_t i = first + (int64_t)c * tq + r / a.g;
+        const int h = kvh * a.g + r % a.g;
+        const bool in = r < n;
+        const float lse = in ? wa.lse[((int64_t)(a.cu_q ? 0 : s) * a.hq + h) * a.rows_q + q0 + i] : 0.f;
+        sh.lse[r] = lse == -INFINITY ? INFINITY : lse * kLog2e;  // adds nothing
+        sh.lim[r] = in && lse != -INFINITY ? (int32_t)min64(lk - 1, i + lk - lq) : -1;
+      }
+      asm volatile("bar.sync 1, 256;\n" ::: "memory");
+      const int whole = n & ~31;  // rows in full groups of 32
+      const int64_t least = first + (int64_t)c * tq + lk - lq;  // every row of the chunk sees this far
+      for (int t = 0; t < ntile; ++t) {
+        const int x = c * ntile + t;
+        if ((x & 1) != grp) continue;
+        if (ok) ok = __all_sync(kFull, bar_wait(s_full + 8 * grp, (x >> 1) & 1, gave_up));
+        if (!ok) break;
+        tm_fence_after();
+        const int64_t j = (int64_t)(tile0 + t) * kTile + row;
+        const bool open = (int64_t)(tile0 + t + 1) * kTile - 1 <= least;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int r0 = 0; r0 < n; r0 += 32) {
+          uint32_t v[32];
+          tm_ld32(v, 0, ts + r0);
+          tm_wait_ld();
+          if (open && r0 < whole) {
+#pragma unroll
+            for (int u = 0; u < 32; u += 4) {
+              const float4 l4 = *reinterpret_cast<const float4*>(&sh.lse[r0 + u]);
+              sum[0] += ex2(fmaf(__uint_as_float(v[u]), kScaleLog2, -l4.x));
+              sum[1] += ex2(fmaf(__uint_as_float(v[u + 1]), kScaleLog2, -l4.y));
+              sum[2] += ex2(fmaf(__uint_as_float(v[u + 2]), kScaleLog2, -l4.z));
+              sum[3] += ex2(fmaf(__uint_as_float(v[u + 3]), kScaleLog2, -l4.w));
+            }
+          } else {
+#pragma unroll
+            for (int u = 0; u < 32; ++u) {
+              const float p = ex2(fmaf(__uint_as_float(v[u]), kScaleLog2, -sh.lse[r0 + u]));
+              sum[u & 3] += j <= sh.lim[r0 + u] ? p : 0.f;
+            }
+          }
+        }
+        tm_fence_before();
+        bar_arrive(s_empty + 8 * grp);
+        const float w = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (j < lkm) out[j] = c > 0 ? out[j] + w : w;
+      }
+    }
+    tm_fence_before();
+  }
+  __syncthreads();
+  if (warp == 8) {
+    tm_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
+  }
+}
+
+cudaError_t raise_smem() {
+  static bool done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev >= 0 && dev < 64 && done[dev])) return e;
+  e = cudaFuncSetAttribute((const void*)k_prompt_weights, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWSmem);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  return e;
+}
+
+}  // namespace
+
+cudaError_t prompt_weights_error(uint32_t* bits) { return take_gave_up(bits); }
+
+cudaError_t launch_prompt_weights(const PromptWeightArgs& w, int sm_count, cudaStream_t st) {
+  const PromptArgs& a = w.p;
+  const int64_t ns = a.cu_q ? 1 : a.n_seqs;
+  WeightMaps m;
+  const void* q = a.rows_q > 0 ? a.q : a.k;  // no queries: nothing of them is loaded
+  if (!encode(&m.q, q, a.hq, a.sq.head, std::max<int64_t>(1, a.rows_q), a.sq.token, ns, a.sq.seq, a.g, kWRows / a.g) ||
+      !encode(&m.k, a.k, a.rows_k, a.sk.token, a.hkv, a.sk.head, ns, a.sk.seq, kTile, 1))
+    return cudaErrorInvalidValue;
+  cudaError_t e = raise_smem();
+  if (e != cudaSuccess) return e;
+  // a block per SM, each with an even share of the tiles
+  const int64_t units = (int64_t)a.n_seqs * a.hkv, tiles = (a.max_k + kTile - 1) / kTile;
+  const int64_t per = std::max<int64_t>(1, (units * tiles + sm_count - 1) / sm_count);
+  const int64_t blocks = (tiles + per - 1) / per;
+  if (blocks * units > 0x7fffffff) return cudaErrorInvalidValue;
+  return launch_pdl(k_prompt_weights, dim3((unsigned)(blocks * units)), dim3(kWThreads), kWSmem, st, w, m, (int)blocks, (int)per);
+}
+
+}  // namespace paris

@@ -91,7 +91,9 @@ struct PromptArgs {
 cudaError_t launch_prompt_attend(const PromptArgs& a, cudaStream_t st);
 size_t prompt_workspace_bytes(PromptArgs& a, int sm_count);  // sets a.nsplit
 
-cudaError_t prompt_error(uint32_t* bits);  // synchronises; reads and clears the error word
+// Whether a wait of the kernels gave up (read and cleared).
+cudaError_t prompt_attend_error(uint32_t* bits);
+cudaError_t prompt_weights_error(uint32_t* bits);
 
 struct PromptWeightArgs {
   PromptArgs p;
@@ -99,7 +101,7 @@ struct PromptWeightArgs {
   int window;
   float* weights;
 };
-cudaError_t launch_prompt_weights(const PromptWeightArgs& a, cudaStream_t st);
+cudaError_t launch_prompt_weights(const PromptWeightArgs& a, int sm_count, cudaStream_t st);
 
 // Text of the last error without a context (paris_last_error(NULL)).
 void set_thread_error(const char* text);

@@ -162,10 +162,12 @@ paris_status paris_prompt_attend(const paris_prompt* p, const void* q, const voi
 }
 
 paris_status paris_prompt_check(void) {
-  uint32_t w = 0;
-  const cudaError_t e = prompt_error(&w);
+  uint32_t a = 0, w = 0;
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = prompt_attend_error(&a);
+  if (e == cudaSuccess) e = prompt_weights_error(&w);
   if (e != cudaSuccess) return launched(e, "paris_prompt_check");
-  if (w) return fail(PARIS_EDEVICE, "a prompt call gave up waiting for its copies or products: its results are not valid");
+  if (a | w) return fail(PARIS_EDEVICE, "a prompt call gave up waiting for its copies or products: its results are not valid");
   return PARIS_OK;
 }
 
@@ -184,7 +186,7 @@ paris_status paris_prompt_weights(const paris_prompt* p, const void* q, const vo
   w.lse = lse;
   w.window = window;
   w.weights = weights;
-  return launched(launch_prompt_weights(w, static_cast<cudaStream_t>(stream)), "paris_prompt_weights");
+  return launched(launch_prompt_weights(w, sm_count(), static_cast<cudaStream_t>(stream)), "paris_prompt_weights");
 }
 
 paris_status paris_kv4_store(const paris_kv4* c, const void* k, const void* v, paris_dtype dtype,
