@@ -9,20 +9,24 @@
 //   Which channel a fragment slot stands for is free as long as both
 //   operands agree, so a thread's fragments are built from the 16 (keys) or
 //   8 (values) contiguous code bytes that it loads itself.
-// - A code word x becomes pairs of halves with one shift for two pairs, one
-//   logic operation and one fma each: the nibble lands in the mantissa of 256 (bits
-//   2-5) or 16 (bits 6-9), giving 256 + u or 16 + u, and the fma with S and
-//   -264 S or -24 S gives S (u - 8) exactly (S has four significant bits, so
-//   every term fits a half's eleven).
-// - The M side of the mma has 16 rows for at most 8 query heads, so rows
-//   0-7 hold the upper and rows 8-15 the lower half-precision part of the
-//   queries, and then of the softmax weights: 22 bits for the cost of 11.
-// - The score fragments are already the weight fragments of the second
-//   product (rows: heads; columns: tokens), as in any m16n8k16 chain.
+// - A code word becomes pairs of halves with half a shift, one logic
+//   operation and one fma a pair: a nibble or-ed into the mantissa of 64
+//   gives 64 + u / 16 (bits 0-3) or 64 + u (bits 4-7), and the fma with S and
+//   -64.5 S or -72 S gives S (u - 8) / 16 or S (u - 8).  S has four
+//   significant bits, so 129 S and 9 S fit a half's eleven and every term is
+//   exact; the 1/16 of the even channels is made good in the queries and in
+//   the result.
+// - Both products have the cache's rows on their M side, S^T = K Q^T and
+//   O^T = V^T P^T, so that the eight columns are what there are few of: for up
+//   to four query heads their upper and lower half-precision parts (22 bits
+//   of a query or weight for the cost of 11), for up to eight two products.
+//   The weights go from the one's result to the other's operand by 8x8
+//   transposes in registers.
 //
 // A warp walks its rows 32 at a time with a running maximum and sum per
-// head; the next 32 rows' loads are in flight meanwhile.  Partials of (split, head)
-// are merged by k_kv4_finish, which also turns the scores into weights.
+// head, its next steps' rows on the way to its own ring in shared memory; no
+// warp waits for another until the end.  Partials of (split, head) are merged
+// by k_kv4_finish, which also turns the scores into weights.
 #include <float.h>
 
 #include <cuda_fp16.h>
@@ -39,6 +43,9 @@ constexpr int kThreads4 = 32 * kWarps4;
 constexpr int kRows4 = 32;                     // rows per warp and step
 constexpr int kTile4 = kRows4 * kWarps4;       // rows per block and step
 constexpr int kHeads4 = 8;                     // query heads per block
+constexpr int kDepth4 = 3;                     // steps of a warp's ring
+constexpr float kGrowth4 = 8.f;                // how far a running maximum may lag, base 2
+constexpr float kLowUp = 4096.f;               // the weights' lower parts are kept this much larger
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -52,79 +59,124 @@ __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<ui
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 
 // The four nibbles of each half of x (two words' or one word's) as four
-// pairs of halves, times their scales: v[i] = S (nibble i - 8).
-__device__ __forceinline__ void unpack4(uint32_t x, __half2 S, __half2 m264, __half2 m24, uint32_t (&v)[4]) {
-  const uint32_t z = x << 2, y = x >> 6;
-  v[0] = h2u(__hfma2(u2h((z & 0x003C003Cu) | 0x5C005C00u), S, m264));
-  v[1] = h2u(__hfma2(u2h((z & 0x03C003C0u) | 0x4C004C00u), S, m24));
-  v[2] = h2u(__hfma2(u2h((y & 0x003C003Cu) | 0x5C005C00u), S, m264));
-  v[3] = h2u(__hfma2(u2h((y & 0x03C003C0u) | 0x4C004C00u), S, m24));
+// pairs of halves, times their scales: v[i] = S (nibble i - 8), the even ones
+// over 16.  y: x shifted right by 8.
+__device__ __forceinline__ void unpack2(uint32_t x, __half2 S, __half2 even, __half2 odd, uint32_t& v0, uint32_t& v1) {
+  v0 = h2u(__hfma2(u2h((x & 0x000F000Fu) | 0x54005400u), S, even));
+  v1 = h2u(__hfma2(u2h((x & 0x00F000F0u) | 0x54005400u), S, odd));
 }
 
-struct Step4 {  // one 32-row step of a warp as loaded
-  uint4 k[4];        // rows 8 i + lane / 4, bytes 16 (lane % 4) ...
-  uint32_t ks[4];    // their scale byte
-  uint2 v[4][2];     // rows 8 i + 2 (lane % 4) + {0, 1}, bytes 8 (lane / 4) ...
-  uint32_t vs[4][2];
+// A warp's ring: kDepth4 steps of 32 rows as they are in memory.
+struct Step4 {
+  uint4 k[kRows4 * kCode4 / 16], v[kRows4 * kCode4 / 16];
+  uint32_t ks[kRows4], vs[kRows4];
 };
 
-__device__ __forceinline__ void load_step(Step4& s, const uint8_t* kc, const uint8_t* ks, const uint8_t* vc,
-                                          const uint8_t* vs, int64_t row0, int64_t last, int g, int t) {
-  // rows past the end read the last row again; their weights become zero
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t r = min64(row0 + 8 * i + g, last);
-    s.k[i] = __ldg(reinterpret_cast<const uint4*>(kc + r * kCode4 + 16 * t));
-    s.ks[i] = __ldg(ks + r * kScale4 + t);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t rv = min64(row0 + 8 * i + 2 * t + j, last);
-      s.v[i][j] = __ldg(reinterpret_cast<const uint2*>(vc + rv * kCode4 + 8 * g));
-      s.vs[i][j] = __ldg(vs + rv * kScale4 + (g >> 1));
-    }
-  }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
 }
 
-__global__ void __launch_bounds__(kThreads4) k_kv4_attend(Attend4Args a) {
-  __shared__ float so[kWarps4][kHeads4][kDim];
-  __shared__ float sml[kWarps4][kHeads4][2];
+struct Rows4 {  // a split's rows
+  const uint8_t *kc, *vc, *ks, *vs;
+};
+
+// Start the copy of rows [row0, row0 + 32); past `last` the last row again
+// (its weights are set to zero).
+__device__ __forceinline__ void copy_step(uint32_t dst, const Rows4& p, int row0, int last, int lane) {
+  if (row0 + kRows4 - 1 <= last) {
+    const uint8_t *k = p.kc + (int64_t)row0 * kCode4 + 16 * lane, *v = p.vc + (int64_t)row0 * kCode4 + 16 * lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      copy16(dst + 16 * lane + 512 * i, k + 512 * i);
+      copy16(dst + 2048 + 16 * lane + 512 * i, v + 512 * i);
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = min(row0 + 8 * i + (lane >> 2), last);
+      copy16(dst + 16 * lane + 512 * i, p.kc + r * kCode4 + 16 * (lane & 3));
+      copy16(dst + 2048 + 16 * lane + 512 * i, p.vc + r * kCode4 + 16 * (lane & 3));
+    }
+  }
+  const int64_t r = min(row0 + lane, last);
+  copy4(dst + 4096 + 4 * lane, p.ks + r * kScale4);
+  copy4(dst + 4224 + 4 * lane, p.vs + r * kScale4);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+
+struct Shared4 {
+  uint2 q[8][2][32];           // query fragments: step, column tile, lane
+  float qscale[kHeads4];
+  float ml[kWarps4][kHeads4][2];
+};
+
+// NT column tiles: 1 for up to four query heads (columns 0-3 their upper,
+// 4-7 their lower parts), 2 for up to eight (a tile of each).
+template <int NT>
+__global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Attend4Args a) {
+  extern __shared__ __align__(16) uint8_t ring_mem[];
+  __shared__ Shared4 sh;
+  constexpr int kHeads = 4 * NT;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int split = blockIdx.x, bh = blockIdx.y, h0 = blockIdx.z * kHeads4;
+  const int split = blockIdx.x, bh = blockIdx.y, h0 = blockIdx.z * kHeads;
   const int b = bh / a.c.hkv, kvh = bh - b * a.c.hkv;
-  const int nh = min(kHeads4, a.g - h0);
+  const int nh = min(kHeads, a.g - h0);
   const int qh0 = kvh * a.g + h0;  // first query head of the block
   const int64_t len = kv4_len(a.c, b);
-  const int64_t r_begin = (int64_t)split * a.rows_per_split, r_end = min64(len, r_begin + a.rows_per_split);
+  const int64_t r_begin = (int64_t)split * a.rows_per_split;
   float* part = a.part + (((int64_t)b * a.hq + qh0) * a.nsplit + split) * kPartStride;
-  if (r_begin >= r_end) {
+  if (r_begin >= len) {
     if (tid < nh) {
       part[(int64_t)tid * a.nsplit * kPartStride] = -INFINITY;
       part[(int64_t)tid * a.nsplit * kPartStride + 1] = 0.f;
     }
     return;
   }
-  const int64_t base = (int64_t)bh * a.c.rmax;
-  const uint8_t *kc = a.c.kc + base * kCode4, *ks = a.c.ks + base * kScale4;
-  const uint8_t *vc = a.c.vc + base * kCode4, *vs = a.c.vs + base * kScale4;
+  // rows of this split from its first on, and of the sequence
+  const int n = (int)min64(len - r_begin, a.rows_per_split);
+  const int64_t base = (int64_t)bh * a.c.rmax + r_begin;
+  const Rows4 rows{a.c.kc + base * kCode4, a.c.vc + base * kCode4, a.c.ks + base * kScale4, a.c.vs + base * kScale4};
+  const Step4* ring = reinterpret_cast<const Step4*>(ring_mem) + warp * kDepth4;
+  const uint32_t ring_u32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  int row0 = warp * kRows4;
+#pragma unroll
+  for (int i = 0; i < kDepth4 - 1; ++i) {
+    if (row0 + i * kTile4 < n) copy_step(ring_u32 + i * (int)sizeof(Step4), rows, row0 + i * kTile4, n - 1, lane);
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  }
 
-  // the query of head g as two half parts, scaled by a power of two to at
-  // most 1 (its scores are scaled back, with log2(e) / sqrt(d))
-  uint32_t qa[8][4];
-  float qscale;
+  // The query of column g's head as two half parts, scaled by a power of two
+  // to at most 1 (its scores are scaled back, with log2(e) / sqrt(d)); each
+  // warp makes two of the eight steps' fragments.
   {
-    float x[32];
+    const int h = NT == 1 ? g & 3 : g;
     float amax = 0.f;
-    const int64_t qe = ((int64_t)b * a.hq + qh0 + g) * kDim + 32 * t;
+    const int64_t qe = ((int64_t)b * a.hq + qh0 + h) * kDim + 32 * t;
+    float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float y[4] = {0.f, 0.f, 0.f, 0.f};
-      if (g < nh) load4(a.q, a.dtype, qe + 4 * i, y);
+      if (h < nh) load4(a.q, a.dtype, qe + 4 * i, y);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        x[4 * i + j] = y[j];
         amax = fmaxf(amax, fabsf(y[j]));
+        if (i >> 1 == warp) x[4 * (i & 1) + j] = y[j];
       }
     }
     amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
@@ -133,134 +185,229 @@ __global__ void __launch_bounds__(kThreads4) k_kv4_attend(Attend4Args a) {
     // infinities that such queries' scores are anyway
     const int e = min(max((int)((__float_as_uint(amax) >> 23) & 255u) - 126, -100), 100);
     const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-    qscale = __uint_as_float((uint32_t)(127 + e) << 23) * (1.4426950408889634f * 0.08838834764831845f);
+    if (warp == 0 && t == 0) sh.qscale[h] = __uint_as_float((uint32_t)(127 + e) << 23) * (1.4426950408889634f * 0.08838834764831845f);
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
+    for (int s = 0; s < 2; ++s) {
+      uint32_t hi[2], lo[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        // fragment slots of step s: channels c and c + 4, c = 8 (s / 2) + 2 (s % 2) + j
-        const int c = 8 * (s >> 1) + 2 * (s & 1) + j;
-        const float y0 = x[c] * down, y1 = x[c + 4] * down;
-        const __half2 hi = __floats2half2_rn(y0, y1);
-        const float2 f = __half22float2(hi);
-        qa[s][2 * j] = h2u(hi);
-        qa[s][2 * j + 1] = h2u(__floats2half2_rn(y0 - f.x, y1 - f.y));
+        // fragment slots of step 2 warp + s: channels c and c + 4 of the
+        // warp's eight, c = 2 s + j; even channels' rows come over 16
+        const float up = j == 0 ? 16.f * down : down;
+        const float y0 = x[2 * s + j] * up, y1 = x[2 * s + j + 4] * up;
+        const __half2 u = __floats2half2_rn(y0, y1);
+        const float2 r = __half22float2(u);
+        hi[j] = h2u(u);
+        lo[j] = h2u(__floats2half2_rn(y0 - r.x, y1 - r.y));
       }
+      const bool low = NT == 1 && g >= 4;
+      sh.q[2 * warp + s][0][lane] = low ? make_uint2(lo[0], lo[1]) : make_uint2(hi[0], hi[1]);
+      if (NT == 2) sh.q[2 * warp + s][1][lane] = make_uint2(lo[0], lo[1]);
     }
   }
-  const __half2 c264 = __float2half2_rn(-264.f), c24 = __float2half2_rn(-24.f);
-
-  float o[16][4];
+  __syncthreads();
+  uint2 qf[8][NT];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  float* sc = a.accumulate ? a.scores + ((int64_t)b * a.hq + qh0 + g) * a.c.rmax : nullptr;
-
-  Step4 cur;
-  int64_t row0 = r_begin + warp * kRows4;
-  if (row0 < r_end) load_step(cur, kc, ks, vc, vs, row0, len - 1, g, t);
-  for (; row0 < r_end; row0 += kTile4) {
-    Step4 s = cur;
-    if (row0 + kTile4 < r_end) load_step(cur, kc, ks, vc, vs, row0 + kTile4, len - 1, g, t);
-    float p[4][2];
+  for (int s = 0; s < 8; ++s)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-      const __half2 S = u2h((s.ks[i] << 7) * 0x10001u);
-      const __half2 m264 = __hmul2(S, c264), m24 = __hmul2(S, c24);
-      const uint32_t w[4] = {s.k[i].x, s.k[i].y, s.k[i].z, s.k[i].w};
+    for (int c = 0; c < NT; ++c) qf[s][c] = sh.q[s][c][lane];
+  // a thread's columns: heads hc and hc + 1
+  const int hc = NT == 1 ? 2 * (t & 1) : 2 * t;
+  const float qs[2] = {sh.qscale[hc], sh.qscale[hc + 1]};
+  const __half2 c_even = __float2half2_rn(-64.5f), c_odd = __float2half2_rn(-72.f);
+
+  float o[8][NT][4];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int c = 0; c < NT; ++c) o[j][c][0] = o[j][c][1] = o[j][c][2] = o[j][c][3] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float* sc = a.accumulate ? a.scores + ((int64_t)b * a.hq + qh0 + hc) * a.c.rmax + r_begin : nullptr;
+
+  // Index 2x + y of an 8-row product stands for row 2x + (y ^ (x & 1)): the
+  // rows of a key fragment's quarter warp then lie in different halves of
+  // the banks, and of a value fragment's half warp in two.
+  const int krow = (g & 6) + ((g & 1) ^ ((g >> 1) & 1));
+  const int vrow[2] = {2 * t + (t & 1), 2 * t + ((t & 1) ^ 1)};
+  int stage = 0;
+#pragma unroll 1
+  for (; row0 < n; row0 += kTile4) {
+    {
+      const int next = row0 + (kDepth4 - 1) * kTile4;
+      const int to = stage == 0 ? kDepth4 - 1 : stage - 1;
+      if (next < n) copy_step(ring_u32 + to * (int)sizeof(Step4), rows, next, n - 1, lane);
+      asm volatile("cp.async.commit_group;\n" ::: "memory");
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(kDepth4 - 1) : "memory");
+      __syncwarp();
+    }
+    const Step4& st = ring[stage];
+    // p[u][r][c]: row krow + 8 r + 16 u, head hc + c
+    float p[2][2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float d[NT][4];
+      uint4 kw[2];
+      __half2 S[2], even[2], odd[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 16 * u + 8 * i + krow;
+        kw[i] = st.k[4 * r + t];
+        S[i] = u2h(((uint32_t) reinterpret_cast<const uint8_t*>(st.ks)[4 * r + t] << 7) * 0x10001u);
+        even[i] = __hmul2(S[i], c_even);
+        odd[i] = __hmul2(S[i], c_odd);
+      }
+#pragma unroll
+      for (int c = 0; c < NT; ++c) d[c][0] = d[c][1] = d[c][2] = d[c][3] = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        uint32_t v[4];
-        unpack4(w[j], S, m264, m24, v);
-        mma_f16(d, qa[2 * j][0], qa[2 * j][1], qa[2 * j][2], qa[2 * j][3], v[0], v[1]);
-        mma_f16(d, qa[2 * j + 1][0], qa[2 * j + 1][1], qa[2 * j + 1][2], qa[2 * j + 1][3], v[2], v[3]);
+        const uint32_t w0 = j == 0 ? kw[0].x : j == 1 ? kw[0].y : j == 2 ? kw[0].z : kw[0].w;
+        const uint32_t w1 = j == 0 ? kw[1].x : j == 1 ? kw[1].y : j == 2 ? kw[1].z : kw[1].w;
+        uint32_t a0, a1, a2, a3;
+        unpack2(w0, S[0], even[0], odd[0], a0, a2);
+        unpack2(w1, S[1], even[1], odd[1], a1, a3);
+#pragma unroll
+        for (int c = 0; c < NT; ++c) mma_f16(d[c], a0, a1, a2, a3, qf[2 * j][c].x, qf[2 * j][c].y);
+        unpack2(w0 >> 8, S[0], even[0], odd[0], a0, a2);
+        unpack2(w1 >> 8, S[1], even[1], odd[1], a1, a3);
+#pragma unroll
+        for (int c = 0; c < NT; ++c) mma_f16(d[c], a0, a1, a2, a3, qf[2 * j + 1][c].x, qf[2 * j + 1][c].y);
       }
-      const int64_t r = row0 + 8 * i + 2 * t;
-      p[i][0] = r < r_end ? (d[0] + d[2]) * qscale : -INFINITY;
-      p[i][1] = r + 1 < r_end ? (d[1] + d[3]) * qscale : -INFINITY;
-      if (sc != nullptr && g < nh) {
-        if (r < r_end) sc[r] = p[i][0];
-        if (r + 1 < r_end) sc[r + 1] = p[i][1];
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          // the upper and the lower part's share
+          const float x = d[0][2 * r + c];
+          p[u][r][c] = (NT == 1 ? x + __shfl_xor_sync(kFull, x, 2) : x + d[NT - 1][2 * r + c]) * qs[c];
+        }
+    }
+    if (row0 + kRows4 > n) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          if (row0 + 16 * u + 8 * r + krow >= n) p[u][r][0] = p[u][r][1] = -INFINITY;
+    }
+    if (sc != nullptr && (NT == 2 || t < 2)) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int x = row0 + 16 * u + 8 * r + krow;
+          if (x < n) {
+            if (hc < nh) sc[x] = p[u][r][0];
+            if (hc + 1 < nh) sc[a.c.rmax + x] = p[u][r][1];
+          }
+        }
+    }
+    float mx[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) mx[c] = fmaxf(fmaxf(p[0][0][c], p[0][1][c]), fmaxf(p[1][0][c], p[1][1][c]));
+    // a maximum may lag by kGrowth4: weights stay below 2^8, and the sums are
+    // scaled again a few times at most
+    if (__any_sync(kFull, mx[0] > m[0] + kGrowth4 || mx[1] > m[1] + kGrowth4)) {
+      float f[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(kFull, mx[c], off));
+        const float mn = fmaxf(m[c], mx[c]);
+        f[c] = mn == -INFINITY ? 1.f : exp2_fast(m[c] - mn);
+        m[c] = mn;
+        l[c] *= f[c];
       }
+      // a thread's columns of O^T are the same heads
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[j][c][i] *= f[i & 1];
     }
-    float mx = p[0][0];
+    // the lower part is kept 2^12 up, so that weights down to 2^-37 count
+    uint32_t pb[2][2][NT];  // rows 8 r + 16 u, column tile
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(p[i][0], p[i][1]));
-    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-    if (__any_sync(kFull, mx > m)) {
-      const float mn = fmaxf(m, mx);
-      const float f = mn == -INFINITY ? 1.f : exp2f(m - mn);
-      m = mn;
-      l *= f;
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        o[j][0] *= f;
-        o[j][1] *= f;
-        o[j][2] *= f;
-        o[j][3] *= f;
+      for (int r = 0; r < 2; ++r) {
+        const float p0 = exp2_fast(p[u][r][0] - m[0]), p1 = exp2_fast(p[u][r][1] - m[1]);
+        l[0] += p0;
+        l[1] += p1;
+        const __half2 hi = __floats2half2_rn(p0, p1);
+        const float2 f = __half22float2(hi);
+        const __half2 lo = __floats2half2_rn((p0 - f.x) * kLowUp, (p1 - f.y) * kLowUp);
+        if (NT == 1) {
+          pb[u][r][0] = transpose8(t < 2 ? h2u(hi) : h2u(lo));
+        } else {
+          pb[u][r][0] = transpose8(h2u(hi));
+          pb[u][r][NT - 1] = transpose8(h2u(lo));
+        }
       }
-    }
-    uint32_t ph[4], pl[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float p0 = exp2f(p[i][0] - m), p1 = exp2f(p[i][1] - m);
-      l += p0 + p1;
-      const __half2 hi = __floats2half2_rn(p0, p1);
-      const float2 f = __half22float2(hi);
-      ph[i] = h2u(hi);
-      pl[i] = h2u(__floats2half2_rn(p0 - f.x, p1 - f.y));
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {  // 16 rows: row pairs of 8-row groups 2u and 2u + 1
-      const __half2 S0 = u2h((s.vs[2 * u][0] << 7) | (s.vs[2 * u][1] << 23));
-      const __half2 S1 = u2h((s.vs[2 * u + 1][0] << 7) | (s.vs[2 * u + 1][1] << 23));
-      const __half2 a0 = __hmul2(S0, c264), b0 = __hmul2(S0, c24), a1 = __hmul2(S1, c264), b1 = __hmul2(S1, c24);
+    for (int u = 0; u < 2; ++u) {
+      const uint8_t* vs = reinterpret_cast<const uint8_t*>(st.vs) + (g >> 1);
+      const uint2* vc = reinterpret_cast<const uint2*>(st.v) + g;
+      const int r0 = 16 * u + vrow[0], r1 = 16 * u + vrow[1];
+      const uint2 xa = vc[8 * r0], xb = vc[8 * r1], ya = vc[8 * (r0 + 8)], yb = vc[8 * (r1 + 8)];
+      const __half2 S0 = u2h((uint32_t)vs[4 * r0] << 7 | (uint32_t)vs[4 * r1] << 23);
+      const __half2 S1 = u2h((uint32_t)vs[4 * (r0 + 8)] << 7 | (uint32_t)vs[4 * (r1 + 8)] << 23);
+      const __half2 e0 = __hmul2(S0, c_even), d0 = __hmul2(S0, c_odd), e1 = __hmul2(S1, c_even), d1 = __hmul2(S1, c_odd);
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        const uint32_t x0 = w ? s.v[2 * u][0].y : s.v[2 * u][0].x, x1 = w ? s.v[2 * u][1].y : s.v[2 * u][1].x;
-        const uint32_t y0 = w ? s.v[2 * u + 1][0].y : s.v[2 * u + 1][0].x,
-                       y1 = w ? s.v[2 * u + 1][1].y : s.v[2 * u + 1][1].x;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t v0[4], v1[4];
-          unpack4(__byte_perm(x0, x1, half ? 0x7632 : 0x5410), S0, a0, b0, v0);
-          unpack4(__byte_perm(y0, y1, half ? 0x7632 : 0x5410), S1, a1, b1, v1);
+        for (int i = 0; i < 4; ++i) {  // byte i of the word: channels 16 g + 8 w + 2 i and the next
+          const uint32_t sel = (uint32_t)(i | (i << 4) | ((4 + i) << 8) | ((4 + i) << 12));
+          uint32_t a0, a1, a2, a3;
+          unpack2(__byte_perm(w ? xa.y : xa.x, w ? xb.y : xb.x, sel), S0, e0, d0, a0, a1);
+          unpack2(__byte_perm(w ? ya.y : ya.x, w ? yb.y : yb.x, sel), S1, e1, d1, a2, a3);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_f16(o[8 * w + 4 * half + j], ph[2 * u], pl[2 * u], ph[2 * u + 1], pl[2 * u + 1], v0[j], v1[j]);
+          for (int c = 0; c < NT; ++c) mma_f16(o[4 * w + i][c], a0, a1, a2, a3, pb[u][0][c], pb[u][1][c]);
         }
       }
     }
+    stage = stage + 1 == kDepth4 ? 0 : stage + 1;
+    __syncwarp();  // the stage may be filled again
   }
-  l += __shfl_xor_sync(kFull, l, 1);
-  l += __shfl_xor_sync(kFull, l, 2);
+  asm volatile("cp.async.wait_all;\n" ::: "memory");
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {  // columns 2t, 2t + 1 of tile j are channels 16 (2t) + j and 16 (2t + 1) + j
-    so[warp][g][32 * t + j] = o[j][0] + o[j][2];
-    so[warp][g][32 * t + 16 + j] = o[j][1] + o[j][3];
-  }
-  if (t == 0) {
-    sml[warp][g][0] = m;
-    sml[warp][g][1] = l;
+  for (int c = 0; c < 2; ++c) {
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) l[c] += __shfl_xor_sync(kFull, l[c], off);
+    if (g == 0 && (NT == 2 || t < 2)) {
+      sh.ml[warp][hc + c][0] = m[c];
+      sh.ml[warp][hc + c][1] = l[c];
+    }
   }
   __syncthreads();
-  for (int e = tid; e < nh * kDim; e += kThreads4) {
-    const int h = e / kDim, d = e - h * kDim;
-    float M = sml[0][h][0];
+  // every warp's result in the rings' place: [warp][head][channel]; rows g and
+  // g + 8 of tile j are channels 16 g + 2 j and the next
+  float* so = reinterpret_cast<float*>(ring_mem);
 #pragma unroll
-    for (int w = 1; w < kWarps4; ++w) M = fmaxf(M, sml[w][h][0]);
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = o[j][0][i], low = NT == 1 ? __shfl_xor_sync(kFull, x, 2) : o[j][NT - 1][i];
+      if (NT == 2 || t < 2)
+        so[(warp * kHeads4 + hc + (i & 1)) * kDim + 16 * g + 2 * j + (i >> 1)] = fmaf(low, 1.f / kLowUp, x) * (i < 2 ? 16.f : 1.f);
+    }
+  __syncthreads();
+  for (int e = tid; e < nh * kDim; e += kThreads4) {
+    const int h = e / kDim, dd = e - h * kDim;
+    float M = sh.ml[0][h][0];
+#pragma unroll
+    for (int w = 1; w < kWarps4; ++w) M = fmaxf(M, sh.ml[w][h][0]);
     float L = 0.f, O = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps4; ++w) {
-      const float mw = sml[w][h][0], f = mw == -INFINITY ? 0.f : exp2f(mw - M);
-      L += sml[w][h][1] * f;
-      O += so[w][h][d] * f;
+      // a warp without rows has the sum 0; one whose scores are all NaN has
+      // m = -inf too, and a NaN sum
+      const float mw = sh.ml[w][h][0], lw = sh.ml[w][h][1], f = lw == 0.f ? 0.f : exp2f(mw - M);
+      L += lw * f;
+      O += so[(w * kHeads4 + h) * kDim + dd] * f;
     }
     float* ph = part + (int64_t)h * a.nsplit * kPartStride;
-    ph[4 + d] = O;
-    if (d == 0) {
+    ph[4 + dd] = O;
+    if (dd == 0) {
       ph[0] = M;
       ph[1] = L;
     }
@@ -335,19 +482,38 @@ __global__ void __launch_bounds__(kFinishThreads) k_kv4_finish(Attend4Args a) {
 
 }  // namespace
 
-void kv4_splits(int64_t units, int64_t rmax, int sm_count, int* nsplit, int64_t* rows_per_split) {
-  // about three blocks per SM over all (sequence, KV head, head group)s, at
-  // least two steps of a block each
-  const int64_t want = std::max<int64_t>(1, (3 * sm_count + units - 1) / units);
+void kv4_splits(int64_t heads, int g, int64_t rmax, int sm_count, int* nsplit, int64_t* rows_per_split) {
+  // one wave of blocks over all (sequence, KV head, head group)s, at least
+  // two steps of a block each
+  const int64_t units = heads * ((g + 7) / 8), slots = (g <= 4 ? 4 : 3) * (int64_t)sm_count;
+  const int64_t want = std::max<int64_t>(1, slots / units);
   const int64_t most = std::max<int64_t>(1, (rmax + 2 * kTile4 - 1) / (2 * kTile4));
   const int64_t n = std::min<int64_t>({want, most, 512});
   *rows_per_split = std::max<int64_t>(kTile4, ((rmax + n - 1) / n + kTile4 - 1) / kTile4 * kTile4);
   *nsplit = (int)std::max<int64_t>(1, (rmax + *rows_per_split - 1) / *rows_per_split);
 }
 
+namespace {
+
+template <int NT>
+cudaError_t launch_attend4(const Attend4Args& a, cudaStream_t st) {
+  constexpr int smem = kWarps4 * kDepth4 * (int)sizeof(Step4);
+  static bool done[64];  // the limit belongs to the device; setting it twice is harmless
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && !(dev >= 0 && dev < 64 && done[dev])) {
+    e = cudaFuncSetAttribute((const void*)k_kv4_attend<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  }
+  if (e != cudaSuccess) return e;
+  const dim3 grid(a.nsplit, a.c.batch * a.c.hkv, (a.g + 4 * NT - 1) / (4 * NT));
+  return launch_pdl(k_kv4_attend<NT>, grid, dim3(kThreads4), smem, st, a);
+}
+
+}  // namespace
+
 cudaError_t launch_kv4_attend(const Attend4Args& a, cudaStream_t st) {
-  const dim3 grid(a.nsplit, a.c.batch * a.c.hkv, (a.g + kHeads4 - 1) / kHeads4);
-  cudaError_t e = launch_pdl(k_kv4_attend, grid, dim3(kThreads4), 0, st, a);
+  cudaError_t e = a.g <= 4 ? launch_attend4<1>(a, st) : launch_attend4<2>(a, st);
   if (e != cudaSuccess) return e;
   const int64_t rows = a.accumulate ? (a.c.rmax + kFinishRows - 1) / kFinishRows : 0;
   return launch_pdl(k_kv4_finish, dim3((unsigned)(a.g + rows), a.c.batch * a.c.hkv), dim3(kFinishThreads), 0, st, a);

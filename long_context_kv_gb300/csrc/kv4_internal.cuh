@@ -63,7 +63,7 @@ struct Attend4Args {
   float* scores;           // [batch * hq][rmax], base-2 logits (accumulate)
   __nv_bfloat16* out;
 };
-void kv4_splits(int64_t units, int64_t rmax, int sm_count, int* nsplit, int64_t* rows_per_split);
+void kv4_splits(int64_t heads, int g, int64_t rmax, int sm_count, int* nsplit, int64_t* rows_per_split);
 cudaError_t launch_kv4_attend(const Attend4Args& a, cudaStream_t st);
 
 struct EvictArgs {

@@ -113,7 +113,7 @@ paris_status check_dtype(paris_dtype t) {
 
 size_t attend4_workspace(const Kv4& k, int hq, bool accumulate, int* nsplit, int64_t* rows_per_split) {
   const int g = hq / k.hkv;
-  kv4_splits((int64_t)k.batch * k.hkv * ((g + 7) / 8), k.rmax, sm_count(), nsplit, rows_per_split);
+  kv4_splits((int64_t)k.batch * k.hkv, g, k.rmax, sm_count(), nsplit, rows_per_split);
   const size_t heads = (size_t)k.batch * hq;
   return heads * *nsplit * kPartStride * sizeof(float) + (accumulate ? heads * k.rmax * sizeof(float) : 0);
 }
