@@ -45,7 +45,7 @@ constexpr int kTile4 = kRows4 * kWarps4;       // rows per block and step
 constexpr int kHeads4 = 8;                     // query heads per block
 constexpr int kDepth4 = 3;                     // steps of a warp's ring
 constexpr float kGrowth4 = 8.f;                // how far a running maximum may lag, base 2
-constexpr float kLowUp = 4096.f;               // the weights' lower parts are kept this much larger
+constexpr float kUp4 = 7.f, kDown4 = 1.f / 128.f;  // weights are kept 2^7 up
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -58,12 +58,18 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 
-// The four nibbles of each half of x (two words' or one word's) as four
-// pairs of halves, times their scales: v[i] = S (nibble i - 8), the even ones
-// over 16.  y: x shifted right by 8.
-__device__ __forceinline__ void unpack2(uint32_t x, __half2 S, __half2 even, __half2 odd, uint32_t& v0, uint32_t& v1) {
-  v0 = h2u(__hfma2(u2h((x & 0x000F000Fu) | 0x54005400u), S, even));
-  v1 = h2u(__hfma2(u2h((x & 0x00F000F0u) | 0x54005400u), S, odd));
+// The two lower nibbles of each half of x as pairs of halves, times their
+// scales: v0 = S (first - 8) / 16, v1 = S (second - 8).  magic: 64 in each
+// half.  It comes as a kernel argument because as a constant it is or-ed in
+// by an instruction of its own (an instruction holds one immediate, the
+// mask): twice the logic, 259 against 131 of them for 32 rows.
+constexpr uint32_t kMagic4 = 0x54005400u;
+__device__ __forceinline__ void unpack2(uint32_t x, uint32_t magic, __half2 S, __half2 even, __half2 odd, uint32_t& v0, uint32_t& v1) {
+  uint32_t y0, y1;
+  asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;\n" : "=r"(y0) : "r"(x), "r"(magic));
+  asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;\n" : "=r"(y1) : "r"(x), "r"(magic));
+  v0 = h2u(__hfma2(u2h(y0), S, even));
+  v1 = h2u(__hfma2(u2h(y1), S, odd));
 }
 
 // A warp's ring: kDepth4 steps of 32 rows as they are in memory.
@@ -127,13 +133,14 @@ struct Shared4 {
 // NT column tiles: 1 for up to four query heads (columns 0-3 their upper,
 // 4-7 their lower parts), 2 for up to eight (a tile of each).
 template <int NT>
-__global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Attend4Args a) {
+__global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Attend4Args a, uint32_t magic) {
   extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ Shared4 sh;
   constexpr int kHeads = 4 * NT;
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int warp = __shfl_sync(kFull, tid >> 5, 0);
   const int split = blockIdx.x, bh = blockIdx.y, h0 = blockIdx.z * kHeads;
   const int b = bh / a.c.hkv, kvh = bh - b * a.c.hkv;
   const int nh = min(kHeads, a.g - h0);
@@ -252,7 +259,7 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
       for (int i = 0; i < 2; ++i) {
         const int r = 16 * u + 8 * i + krow;
         kw[i] = st.k[4 * r + t];
-        S[i] = u2h(((uint32_t) reinterpret_cast<const uint8_t*>(st.ks)[4 * r + t] << 7) * 0x10001u);
+        S[i] = u2h((uint32_t) reinterpret_cast<const uint8_t*>(st.ks)[4 * r + t] * 0x00800080u);
         even[i] = __hmul2(S[i], c_even);
         odd[i] = __hmul2(S[i], c_odd);
       }
@@ -263,12 +270,12 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
         const uint32_t w0 = j == 0 ? kw[0].x : j == 1 ? kw[0].y : j == 2 ? kw[0].z : kw[0].w;
         const uint32_t w1 = j == 0 ? kw[1].x : j == 1 ? kw[1].y : j == 2 ? kw[1].z : kw[1].w;
         uint32_t a0, a1, a2, a3;
-        unpack2(w0, S[0], even[0], odd[0], a0, a2);
-        unpack2(w1, S[1], even[1], odd[1], a1, a3);
+        unpack2(w0, magic, S[0], even[0], odd[0], a0, a2);
+        unpack2(w1, magic, S[1], even[1], odd[1], a1, a3);
 #pragma unroll
         for (int c = 0; c < NT; ++c) mma_f16(d[c], a0, a1, a2, a3, qf[2 * j][c].x, qf[2 * j][c].y);
-        unpack2(w0 >> 8, S[0], even[0], odd[0], a0, a2);
-        unpack2(w1 >> 8, S[1], even[1], odd[1], a1, a3);
+        unpack2(w0 >> 8, magic, S[0], even[0], odd[0], a0, a2);
+        unpack2(w1 >> 8, magic, S[1], even[1], odd[1], a1, a3);
 #pragma unroll
         for (int c = 0; c < NT; ++c) mma_f16(d[c], a0, a1, a2, a3, qf[2 * j + 1][c].x, qf[2 * j + 1][c].y);
       }
@@ -278,7 +285,7 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
         for (int c = 0; c < 2; ++c) {
           // the upper and the lower part's share
           const float x = d[0][2 * r + c];
-          p[u][r][c] = (NT == 1 ? x + __shfl_xor_sync(kFull, x, 2) : x + d[NT - 1][2 * r + c]) * qs[c];
+          p[u][r][c] = NT == 1 ? x + __shfl_xor_sync(kFull, x, 2) : x + d[NT - 1][2 * r + c];
         }
     }
     if (row0 + kRows4 > n) {
@@ -295,14 +302,14 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
         for (int r = 0; r < 2; ++r) {
           const int x = row0 + 16 * u + 8 * r + krow;
           if (x < n) {
-            if (hc < nh) sc[x] = p[u][r][0];
-            if (hc + 1 < nh) sc[a.c.rmax + x] = p[u][r][1];
+            if (hc < nh) sc[x] = p[u][r][0] * qs[0];
+            if (hc + 1 < nh) sc[a.c.rmax + x] = p[u][r][1] * qs[1];
           }
         }
     }
     float mx[2];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) mx[c] = fmaxf(fmaxf(p[0][0][c], p[0][1][c]), fmaxf(p[1][0][c], p[1][1][c]));
+    for (int c = 0; c < 2; ++c) mx[c] = fmaxf(fmaxf(p[0][0][c], p[0][1][c]), fmaxf(p[1][0][c], p[1][1][c])) * qs[c];
     // a maximum may lag by kGrowth4: weights stay below 2^8, and the sums are
     // scaled again a few times at most
     if (__any_sync(kFull, mx[0] > m[0] + kGrowth4 || mx[1] > m[1] + kGrowth4)) {
@@ -324,18 +331,20 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[j][c][i] *= f[i & 1];
     }
-    // the lower part is kept 2^12 up, so that weights down to 2^-37 count
+    // weights are kept 2^kUp4 up, at most 2^15: down to 2^-32 of the largest
+    // they still count in a half's subnormals
+    const float neg[2] = {kUp4 - m[0], kUp4 - m[1]};
     uint32_t pb[2][2][NT];  // rows 8 r + 16 u, column tile
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float p0 = exp2_fast(p[u][r][0] - m[0]), p1 = exp2_fast(p[u][r][1] - m[1]);
+        const float p0 = exp2_fast(fmaf(p[u][r][0], qs[0], neg[0])), p1 = exp2_fast(fmaf(p[u][r][1], qs[1], neg[1]));
         l[0] += p0;
         l[1] += p1;
         const __half2 hi = __floats2half2_rn(p0, p1);
         const float2 f = __half22float2(hi);
-        const __half2 lo = __floats2half2_rn((p0 - f.x) * kLowUp, (p1 - f.y) * kLowUp);
+        const __half2 lo = __floats2half2_rn(p0 - f.x, p1 - f.y);
         if (NT == 1) {
           pb[u][r][0] = transpose8(t < 2 ? h2u(hi) : h2u(lo));
         } else {
@@ -358,8 +367,8 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
         for (int i = 0; i < 4; ++i) {  // byte i of the word: channels 16 g + 8 w + 2 i and the next
           const uint32_t sel = (uint32_t)(i | (i << 4) | ((4 + i) << 8) | ((4 + i) << 12));
           uint32_t a0, a1, a2, a3;
-          unpack2(__byte_perm(w ? xa.y : xa.x, w ? xb.y : xb.x, sel), S0, e0, d0, a0, a1);
-          unpack2(__byte_perm(w ? ya.y : ya.x, w ? yb.y : yb.x, sel), S1, e1, d1, a2, a3);
+          unpack2(__byte_perm(w ? xa.y : xa.x, w ? xb.y : xb.x, sel), magic, S0, e0, d0, a0, a1);
+          unpack2(__byte_perm(w ? ya.y : ya.x, w ? yb.y : yb.x, sel), magic, S1, e1, d1, a2, a3);
 #pragma unroll
           for (int c = 0; c < NT; ++c) mma_f16(o[4 * w + i][c], a0, a1, a2, a3, pb[u][0][c], pb[u][1][c]);
         }
@@ -375,7 +384,7 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
     for (int off = 4; off < 32; off <<= 1) l[c] += __shfl_xor_sync(kFull, l[c], off);
     if (g == 0 && (NT == 2 || t < 2)) {
       sh.ml[warp][hc + c][0] = m[c];
-      sh.ml[warp][hc + c][1] = l[c];
+      sh.ml[warp][hc + c][1] = l[c] * kDown4;
     }
   }
   __syncthreads();
@@ -388,7 +397,7 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
     for (int i = 0; i < 4; ++i) {
       const float x = o[j][0][i], low = NT == 1 ? __shfl_xor_sync(kFull, x, 2) : o[j][NT - 1][i];
       if (NT == 2 || t < 2)
-        so[(warp * kHeads4 + hc + (i & 1)) * kDim + 16 * g + 2 * j + (i >> 1)] = fmaf(low, 1.f / kLowUp, x) * (i < 2 ? 16.f : 1.f);
+        so[(warp * kHeads4 + hc + (i & 1)) * kDim + 16 * g + 2 * j + (i >> 1)] = (x + low) * (i < 2 ? 16.f * kDown4 : kDown4);
     }
   __syncthreads();
   for (int e = tid; e < nh * kDim; e += kThreads4) {
@@ -507,7 +516,7 @@ cudaError_t launch_attend4(const Attend4Args& a, cudaStream_t st) {
   }
   if (e != cudaSuccess) return e;
   const dim3 grid(a.nsplit, a.c.batch * a.c.hkv, (a.g + 4 * NT - 1) / (4 * NT));
-  return launch_pdl(k_kv4_attend<NT>, grid, dim3(kThreads4), smem, st, a);
+  return launch_pdl(k_kv4_attend<NT>, grid, dim3(kThreads4), smem, st, a, kMagic4);
 }
 
 }  // namespace
