@@ -423,68 +423,97 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
   }
 }
 
-constexpr int kFinishThreads = 256;
+constexpr int kFinishThreads = 512;
+constexpr int kFinishWarps = kFinishThreads / 32;
 constexpr int kFinishRows = 2048;  // rows whose weights a block adds up
+constexpr int kMaxSplit4 = 512;
 
-// Blocks [0, G): merge the splits of one query head.  Blocks from G on: add
-// a range of rows' weights, head by head in ascending order.
+// A warp: the maximum and the sum of one head over its splits.
+__device__ __forceinline__ float2 merge_ml(const float* ph, int nsplit, int lane) {
+  float M = -INFINITY, L = 0.f;
+#pragma unroll 4
+  for (int s = lane; s < nsplit; s += 32) {
+    const float2 ml = *reinterpret_cast<const float2*>(ph + (int64_t)s * kPartStride);
+    if (ml.y == 0.f) continue;  // no rows
+    const float mn = fmaxf(M, ml.x);
+    L = (L != 0.f ? L * exp2f(M - mn) : 0.f) + ml.y * exp2f(ml.x - mn);
+    M = mn;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    const float om = __shfl_xor_sync(kFull, M, off), ol = __shfl_xor_sync(kFull, L, off);
+    const float mn = fmaxf(M, om);
+    L = (L != 0.f ? L * exp2f(M - mn) : 0.f) + (ol != 0.f ? ol * exp2f(om - mn) : 0.f);
+    M = mn;
+  }
+  return make_float2(M, L);
+}
+
+// Blocks [0, G): merge the splits of one query head, a warp taking every
+// 16th split with all its loads in flight at once.  Blocks from G on: add a
+// range of rows' weights, head by head in ascending order.
 __global__ void __launch_bounds__(kFinishThreads) k_kv4_finish(Attend4Args a) {
-  __shared__ float sM[16], sI[16];
-  __shared__ float half_o[kDim];
+  __shared__ float2 sml[16];  // maximum, 1 / sum
+  __shared__ float4 so[kFinishWarps][32];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.y / a.c.hkv, kvh = blockIdx.y - b * a.c.hkv;
-  const int64_t len = kv4_len(a.c, b);
   const int64_t q0 = (int64_t)b * a.hq + kvh * a.g;
-  const bool merge = (int)blockIdx.x < a.g;
-  const int64_t r0 = ((int64_t)blockIdx.x - a.g) * kFinishRows;
-  if (!merge && r0 >= len) return;
-  for (int h = warp; h < a.g; h += kFinishThreads / 32) {
-    if (merge && h != (int)blockIdx.x) continue;
-    const float* ph = a.part + (q0 + h) * a.nsplit * kPartStride;
-    float M = -INFINITY;
-    for (int s = lane; s < a.nsplit; s += 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(ph + (int64_t)s * kPartStride);
-      M = fmaxf(M, ml.x);
-    }
+  if ((int)blockIdx.x < a.g) {
+    const float* ph = a.part + (q0 + blockIdx.x) * a.nsplit * kPartStride;
+    constexpr int kAhead = 8;
+    float4 x[kAhead];
+    float2 ml[kAhead];
+    auto load = [&](int s0) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
-    float L = 0.f;
-    for (int s = lane; s < a.nsplit; s += 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(ph + (int64_t)s * kPartStride);
-      if (ml.y != 0.f) L += ml.y * exp2f(ml.x - M);
-    }
+      for (int i = 0; i < kAhead; ++i) {
+        const int s = s0 + warp + i * kFinishWarps;
+        ml[i] = make_float2(-INFINITY, 0.f);
+        if (s >= a.nsplit) continue;
+        ml[i] = *reinterpret_cast<const float2*>(ph + (int64_t)s * kPartStride);
+        x[i] = *reinterpret_cast<const float4*>(ph + (int64_t)s * kPartStride + 4 + 4 * lane);  // not written without rows
+      }
+    };
+    load(0);
+    const float2 all = merge_ml(ph, a.nsplit, lane);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < a.nsplit; s0 += kAhead * kFinishWarps) {
+      if (s0 > 0) load(s0);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(kFull, L, off);
-    if (lane == 0) {
-      sM[h] = M;
-      sI[h] = L != 0.f ? 1.f / L : 0.f;
+      for (int i = 0; i < kAhead; ++i) {
+        if (ml[i].y == 0.f) continue;
+        const float f = exp2f(ml[i].x - all.x);
+        o.x = fmaf(x[i].x, f, o.x);
+        o.y = fmaf(x[i].y, f, o.y);
+        o.z = fmaf(x[i].z, f, o.z);
+        o.w = fmaf(x[i].w, f, o.w);
+      }
     }
-  }
-  __syncthreads();
-  if (merge) {
-    const int h = blockIdx.x, d = tid & (kDim - 1), part = tid >> 7;
-    const float* ph = a.part + (q0 + h) * a.nsplit * kPartStride;
-    const float M = sM[h];
-    float o = 0.f;
-#pragma unroll 8
-    for (int s = part; s < a.nsplit; s += 2) {
-      const float2 ml = *reinterpret_cast<const float2*>(ph + (int64_t)s * kPartStride);
-      const float x = ph[(int64_t)s * kPartStride + 4 + d];  // not written by a split without rows
-      if (ml.y != 0.f) o += x * exp2f(ml.x - M);
-    }
-    if (part == 1) half_o[d] = o;
+    so[warp][lane] = o;
     __syncthreads();
-    if (part == 0) a.out[(q0 + h) * kDim + d] = __float2bfloat16_rn((o + half_o[d]) * sI[h]);
+    if (tid < kDim) {
+      float r = 0.f;
+#pragma unroll
+      for (int w = 0; w < kFinishWarps; ++w) r += reinterpret_cast<const float*>(so[w])[tid];
+      a.out[(q0 + blockIdx.x) * kDim + tid] = __float2bfloat16_rn(all.y != 0.f ? r / all.y : 0.f);
+    }
     return;
   }
-  const int64_t r1 = min64(len, r0 + kFinishRows);
+  const int64_t len = kv4_len(a.c, b);
+  const int64_t r0 = ((int64_t)blockIdx.x - a.g) * kFinishRows, r1 = min64(len, r0 + kFinishRows);
+  if (r0 >= len) return;
+  if (warp < a.g) {
+    const float2 all = merge_ml(a.part + (q0 + warp) * a.nsplit * kPartStride, a.nsplit, lane);
+    if (lane == 0) sml[warp] = make_float2(all.x, all.y != 0.f ? 1.f / all.y : 0.f);
+  }
   float* w = a.c.w + (int64_t)blockIdx.y * a.c.rmax;
   const float* sc = a.scores + q0 * a.c.rmax;
+  __syncthreads();
   for (int64_t r = r0 + tid; r < r1; r += kFinishThreads) {
     float p = 0.f;
-    for (int h = 0; h < a.g; ++h) p += exp2f(sc[h * a.c.rmax + r] - sM[h]) * sI[h];
+#pragma unroll 4
+    for (int h = 0; h < a.g; ++h) p += exp2f(sc[h * a.c.rmax + r] - sml[h].x) * sml[h].y;
     w[r] += p;
   }
 }
@@ -497,7 +526,7 @@ void kv4_splits(int64_t heads, int g, int64_t rmax, int sm_count, int* nsplit, i
   const int64_t units = heads * ((g + 7) / 8), slots = (g <= 4 ? 4 : 3) * (int64_t)sm_count;
   const int64_t want = std::max<int64_t>(1, slots / units);
   const int64_t most = std::max<int64_t>(1, (rmax + 2 * kTile4 - 1) / (2 * kTile4));
-  const int64_t n = std::min<int64_t>({want, most, 512});
+  const int64_t n = std::min<int64_t>({want, most, kMaxSplit4});
   *rows_per_split = std::max<int64_t>(kTile4, ((rmax + n - 1) / n + kTile4 - 1) / kTile4 * kTile4);
   *nsplit = (int)std::max<int64_t>(1, (rmax + *rows_per_split - 1) / *rows_per_split);
 }
