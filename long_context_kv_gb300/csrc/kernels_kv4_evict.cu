@@ -1,9 +1,9 @@
 // Eviction from the 4-bit cache by accumulated weight.
 //
 // One block per (sequence, KV head), or a cluster of up to eight for more
-// than 16384 rows; a thread keeps its rows' keys in registers (bits ordered
-// like the weights), a warp has a contiguous piece of the rows.  Protected
-// rows are counted apart.  The smallest kept key is found by narrowing a
+// than 16384 rows; the rows' keys (bits ordered like the weights) are kept in
+// shared memory, a warp has a contiguous piece of them.  Protected rows are
+// counted apart.  The smallest kept key is found by narrowing a
 // range of keys: the range's rows are counted in 2048 equal bins (a
 // cluster's counts are read through distributed shared memory), and the bin
 // in which the wanted row falls is the next range; once it holds at most 32
@@ -18,7 +18,9 @@
 //
 // Bound by latency: a row costs 8 bytes, and the rounds are barriers.  A
 // cluster costs some 2000 cycles a barrier and round of remote reads, which
-// is why it starts only where a thread's keys would no longer fit.
+// is why it starts only where the keys would no longer fit.  The code is kept
+// short for the same reason: it runs once, and with the keys in registers and
+// every loop unrolled (46 KB) it waited for its instructions longest.
 #include <cooperative_groups.h>
 
 #include "kv4_internal.cuh"
@@ -32,8 +34,8 @@ constexpr int kEvictThreads = 1024;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictMaxBlocks = 8;
 constexpr int kBins = 2048;
-constexpr int kHeldKeys = 16;  // keys of a thread in registers; further ones are read again
-constexpr int kMoves = 4;      // moves of 16 threads in flight
+constexpr int kHeldRows = 16384;  // rows of a block whose keys are in shared memory; further ones are read again
+constexpr int kMoves = 8;      // rows that a warp moves at once
 
 struct EvictShared {
   uint32_t hist[3][kBins];
@@ -46,15 +48,16 @@ struct EvictShared {
   uint32_t count[3];            // this block's rows with the threshold key; its holes; its tails
   uint32_t blocks[3][kEvictMaxBlocks];
 };
+constexpr uint32_t kProtected = 0xFFFFFFFFu;  // above every weight's key
 
-// Key of an unprotected row (protected: false).
-__device__ __forceinline__ bool evict_key(float w, int32_t pos, int64_t sink, int64_t recent_from, uint32_t& key) {
-  key = w == w ? order_key(w) : 0u;
-  return !(pos < sink || pos >= recent_from);
+__device__ __forceinline__ uint32_t evict_key(float w, int32_t pos, int64_t sink, int64_t recent_from) {
+  if (pos < sink || pos >= recent_from) return kProtected;
+  return w == w ? order_key(w) : 0u;
 }
 
 template <bool kCluster>
 __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(EvictArgs a) {
+  extern __shared__ uint32_t keys[];
   __shared__ __align__(16) EvictShared sh;
   cg::cluster_group cluster = cg::this_cluster();
   auto sync_all = [&]() {
@@ -73,56 +76,66 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(EvictArgs a) {
   const int bh = blockIdx.x / nb;
   const int b = bh / a.c.hkv;
   const int32_t next = a.c.next[b];
-  const int64_t n = kv4_len(a.c, b);
+  const int n = (int)kv4_len(a.c, b), keep = (int)a.keep;
   const int64_t base = (int64_t)bh * a.c.rmax;
-  if (n > a.keep) {  // the same for the whole cluster
+  if (n > keep) {  // the same for the whole cluster
     const int64_t recent_from = (int64_t)next - a.recent;
-    const int64_t slice = (n + nb - 1) / nb;
-    const int64_t r0 = min64(n, rank * slice), r1 = min64(n, r0 + slice);
+    const int slice = kCluster ? (int)(((int64_t)n + nb - 1) / nb) : n;
+    const int r0 = kCluster ? (int)min64(n, (int64_t)rank * slice) : 0, r1 = r0 + min(n - r0, slice);
     const float* w = a.c.w + base;
     const int32_t* pos = a.c.pos + base;
     // the warp's rows: 32 x [0, mine) from first on
-    const int mine = (int)((r1 - r0 + kEvictThreads - 1) / kEvictThreads);
+    const int mine = (int)(((uint32_t)(r1 - r0) + kEvictThreads - 1) / kEvictThreads);
     const int64_t first = r0 + (int64_t)warp * mine * 32;
-    const int64_t left = r1 - first - lane;  // row i of the lane is there if 32 i < left
-    uint32_t held[kHeldKeys];
-    uint32_t flags = 0;  // bit 2i: row i is there; bit 2i + 1: and not protected
-    {
-      float wv[kHeldKeys];
-      int32_t pv[kHeldKeys];
-#pragma unroll
-      for (int i = 0; i < kHeldKeys; ++i)
-        if (i < mine && 32 * i < left) {
-          wv[i] = w[first + 32 * i + lane];
-          pv[i] = pos[first + 32 * i + lane];
-        }
-#pragma unroll
-      for (int i = 0; i < kHeldKeys; ++i) {
-        held[i] = 0;
-        if (i < mine && 32 * i < left) flags |= (evict_key(wv[i], pv[i], a.sink, recent_from, held[i]) ? 3u : 1u) << (2 * i);
-      }
-    }
-    auto each = [&](auto&& f) {  // f(i, key, state): 0 not there, 1 protected, 3 neither; whole warps, rows ascending
-#pragma unroll
-      for (int i = 0; i < kHeldKeys; ++i) {
-        if (i >= mine) break;
-        f(i, held[i], (flags >> (2 * i)) & 3u);
-      }
-      for (int i = kHeldKeys; i < mine; ++i) {
-        uint32_t key = 0, st = 0;
-        if (32 * (int64_t)i < left)
-          st = evict_key(w[first + 32 * (int64_t)i + lane], pos[first + 32 * (int64_t)i + lane], a.sink, recent_from, key) ? 3u : 1u;
-        f(i, key, st);
-      }
-    };
+    const int end = (int)max64(min64(r1 - first, (int64_t)mine * 32), 0);  // the warp's rows that are there: < end
+    const int room = (int)max64(min64(keep - first, (int64_t)mine * 32), 0);  // and below keep: < room
+    const int heldi = min(mine, kHeldRows / kEvictThreads);
+    uint32_t* mykeys = keys + warp * heldi * 32;
     uint32_t lo = 0xFFFFFFFFu, hi = 0, prot = 0;
-    each([&](int, uint32_t key, uint32_t st) {
-      if (st == 3u) {
+    auto take = [&](uint32_t key) {
+      if (key == kProtected) ++prot;
+      else {
         lo = min(lo, key);
         hi = max(hi, key);
       }
-      prot += st == 1u;
-    });
+    };
+    constexpr int kAhead = 8;  // rows of a thread on their way at once
+#pragma unroll 1
+    for (int i0 = 0; i0 < heldi; i0 += kAhead) {
+      float wv[kAhead];
+      int32_t pv[kAhead];
+      const float* wp = w + first + 32 * i0 + lane;
+      const int32_t* pp = pos + first + 32 * i0 + lane;
+      const int here = min(min(heldi - i0, kAhead), (end - 32 * i0 - lane + 31) >> 5);  // the thread's rows of these
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (u < here) {
+          wv[u] = __ldcg(wp + 32 * u);
+          pv[u] = __ldcg(pp + 32 * u);
+        }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (u < here) {
+          const uint32_t key = evict_key(wv[u], pv[u], a.sink, recent_from);
+          mykeys[32 * (i0 + u) + lane] = key;
+          take(key);
+        }
+    }
+    auto each = [&](auto&& f) {  // f(i, key, whether the row is there): whole warps, rows ascending
+#pragma unroll 1
+      for (int i = 0; i < mine; ++i) {
+        const int x = 32 * i + lane;
+        const bool in = x < end;
+        uint32_t key = 0;
+        if (in) key = i < heldi ? mykeys[x] : evict_key(w[first + x], pos[first + x], a.sink, recent_from);
+        f(i, key, in);
+      }
+    };
+#pragma unroll 1
+    for (int i = heldi; i < mine; ++i) {
+      const int x = 32 * i + lane;
+      if (x < end) take(evict_key(w[first + x], pos[first + x], a.sink, recent_from));
+    }
     lo = __reduce_min_sync(kFull, lo);
     hi = __reduce_max_sync(kFull, hi);
     prot = __reduce_add_sync(kFull, prot);
@@ -154,40 +167,46 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(EvictArgs a) {
     }
     lo = kCluster ? sh.all_lo : sh.lo;
     hi = kCluster ? sh.all_hi : sh.hi;
-    const int64_t protected_rows = kCluster ? sh.all_held : sh.held;
+    const uint32_t protected_rows = kCluster ? sh.all_held : sh.held;
     // Rows stay whose key is above `least`, and the first `want` of those
     // with it.  With more protected rows than room, the protected ones are
     // the rows with the threshold key and no other stays.
-    const bool crowded = protected_rows >= a.keep;
-    int64_t want = crowded ? a.keep : a.keep - protected_rows;
-    int64_t equal = crowded ? protected_rows : n - protected_rows;  // rows in the range
+    const bool crowded = protected_rows >= (uint32_t)keep;
+    uint32_t want = crowded ? keep : keep - protected_rows;
+    uint32_t equal = crowded ? protected_rows : n - protected_rows;  // rows in the range
 #pragma unroll 1
     for (int d = 0; d < 3 && !crowded && lo < hi; ++d) {
       if (!kCluster && equal <= 32) {
         // few rows in the range: a warp ranks them
-        each([&](int, uint32_t key, uint32_t st) {
-          if (st == 3u && key >= lo && key <= hi) sh.few[atomicAdd(&sh.nfew, 1u)] = key;
+        each([&](int, uint32_t key, bool in) {
+          if (in && key >= lo && key <= hi) sh.few[atomicAdd(&sh.nfew, 1u)] = key;
         });
         __syncthreads();
-        const uint32_t mine_key = lane < equal ? sh.few[lane] : 0u;
-        uint32_t larger = 0, same = 0;
-        for (int i = 0; i < equal; ++i) {
-          const uint32_t k = __shfl_sync(kFull, mine_key, i);
-          larger += k > mine_key;
-          same += k == mine_key;
+        if (warp == 0) {
+          const uint32_t own = lane < equal ? sh.few[lane] : 0u;
+          uint32_t larger = 0, same = 0;
+          for (uint32_t i = 0; i < equal; ++i) {
+            const uint32_t k = __shfl_sync(kFull, own, i);
+            larger += k > own;
+            same += k == own;
+          }
+          // the key that the wanted row has
+          if (lane < equal && larger < want && larger + same >= want) {
+            sh.bin = own;
+            sh.above = larger;
+            sh.in_bin = same;
+          }
         }
-        // the key that the wanted row has
-        const uint32_t hit = __ballot_sync(kFull, lane < equal && larger < want && larger + same >= want);
-        const int src = __ffs(hit) - 1;
-        lo = hi = __shfl_sync(kFull, mine_key, src);
-        want -= __shfl_sync(kFull, larger, src);
-        equal = __shfl_sync(kFull, same, src);
+        __syncthreads();
+        lo = hi = sh.bin;
+        want -= sh.above;
+        equal = sh.in_bin;
         break;
       }
       // keys lo .. hi in bins of 2^shift
       const int shift = max(0, 32 - __clz(hi - lo) - 11);
-      each([&](int, uint32_t key, uint32_t st) {
-        if (st == 3u && key >= lo && key <= hi) atomicAdd(&sh.hist[d][(key - lo) >> shift], 1u);
+      each([&](int, uint32_t key, bool in) {
+        if (in && key >= lo && key <= hi) atomicAdd(&sh.hist[d][(key - lo) >> shift], 1u);
       });
       sync_all();
       // four bins a thread of the first half, from the top
@@ -234,15 +253,14 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(EvictArgs a) {
       want -= sh.above;
       equal = sh.in_bin;
     }
-    const uint32_t least = lo;
-    const uint32_t tied = crowded ? 1u : 3u;  // state of the rows that share the last places
-    auto is_tied = [&](uint32_t key, uint32_t st) { return st == tied && (crowded || key == least); };
+    // the threshold: rows above it stay, and the first `want` of those on it
+    const uint32_t least = crowded ? kProtected : lo;
     const uint32_t below = (1u << lane) - 1u;
     uint32_t eq_at = 0;
     const bool split_tie = equal > want;  // not all of them stay: the first by row
     if (split_tie) {
       uint32_t eq = 0;
-      each([&](int, uint32_t key, uint32_t st) { eq += __popc(__ballot_sync(kFull, is_tied(key, st))); });
+      each([&](int, uint32_t key, bool in) { eq += __popc(__ballot_sync(kFull, in && key == least)); });
       __syncthreads();
       if (lane == 0) sh.warp_a[warp] = eq;
       __syncthreads();
@@ -256,25 +274,22 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(EvictArgs a) {
       }
     }
     // holes and tails of 32 rows as bits
-    auto sort_out = [&](int i, uint32_t key, uint32_t st, uint32_t& hs, uint32_t& ts) {
-      bool k;
-      const bool tie = is_tied(key, st);
+    auto sort_out = [&](int i, uint32_t key, bool in, uint32_t& hs, uint32_t& ts) {
+      bool k = key >= least;
       if (split_tie) {
-        const uint32_t eqs = __ballot_sync(kFull, tie);
-        k = (tie && eq_at + __popc(eqs & below) < want) || (!crowded && (st == 1u || (st == 3u && key > least)));
+        const uint32_t eqs = __ballot_sync(kFull, in && key == least);
+        k = key > least || (key == least && eq_at + __popc(eqs & below) < want);
         eq_at += __popc(eqs);
-      } else {
-        k = tie || (!crowded && (st == 1u || (st == 3u && key > least)));
       }
-      const bool low = first + 32 * (int64_t)i + lane < a.keep;
-      hs = __ballot_sync(kFull, st != 0u && !k && low);
-      ts = __ballot_sync(kFull, k && !low);
+      const bool low = 32 * i + lane < room;
+      hs = __ballot_sync(kFull, in && !k && low);
+      ts = __ballot_sync(kFull, in && k && !low);
     };
     uint32_t holes = 0, tails = 0;
     const uint32_t eq_start = eq_at;
-    each([&](int i, uint32_t key, uint32_t st) {
+    each([&](int i, uint32_t key, bool in) {
       uint32_t hs, ts;
-      sort_out(i, key, st, hs, ts);
+      sort_out(i, key, in, hs, ts);
       holes += __popc(hs);
       tails += __popc(ts);
     });
@@ -293,11 +308,11 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(EvictArgs a) {
     }
     int32_t* list = a.list + (int64_t)bh * 2 * a.c.rmax;
     eq_at = eq_start;
-    if (block_holes + block_tails > 0)
-      each([&](int i, uint32_t key, uint32_t st) {
+    if (holes + tails > 0)  // of the warp
+      each([&](int i, uint32_t key, bool in) {
         uint32_t hs, ts;
-        sort_out(i, key, st, hs, ts);
-        const int32_t r = (int32_t)(first + 32 * (int64_t)i + lane);
+        sort_out(i, key, in, hs, ts);
+        const int32_t r = (int32_t)first + 32 * i + lane;
         if (hs >> lane & 1u) list[r0 + hole_at + __popc(hs & below)] = r;
         if (ts >> lane & 1u) list[a.c.rmax + r0 + tail_at + __popc(ts & below)] = r;
         hole_at += __popc(hs);
@@ -317,39 +332,42 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(EvictArgs a) {
       for (int i = 0; i < nb; ++i) moves += sh.blocks[1][i];
     }
     // entry i of a list whose pieces start at the blocks' slices
-    auto entry = [&](int which, uint32_t i) -> int64_t {
+    auto entry = [&](int which, uint32_t i) -> int32_t {
       const int32_t* l = list + (which == 2 ? a.c.rmax : 0);
       if (kCluster) {
         int blk = 0;
         for (; blk + 1 < nb && i >= sh.blocks[which][blk]; ++blk) i -= sh.blocks[which][blk];
-        l += min64(n, blk * slice);
+        l += min64(n, (int64_t)blk * slice);
       }
-      return base + __ldcg(l + i);
+      return __ldcg(l + i);
     };
-    const int l16 = tid & 15;
-    const uint32_t stride = nb * (kEvictThreads / 16);
-    for (uint32_t i0 = rank * (kEvictThreads / 16) + (tid >> 4); i0 < moves; i0 += kMoves * stride) {
-      int64_t dst[kMoves], src[kMoves];
-      uint4 v[kMoves];
-#pragma unroll
-      for (int u = 0; u < kMoves; ++u)
-        if (i0 + u * stride < moves) {
-          dst[u] = entry(1, i0 + u * stride);
-          src[u] = entry(2, i0 + u * stride);
-        }
+    // a warp moves a row in four bytes a lane: its codes, then the rest
+    uint8_t* const codes_at = (lane < 16 ? a.c.kc : a.c.vc) + base * kCode4 + 4 * (lane & 15);
+    uint32_t* const rest_at = (lane == 0 ? reinterpret_cast<uint32_t*>(a.c.ks) : lane == 1 ? reinterpret_cast<uint32_t*>(a.c.vs)
+                               : lane == 2 ? reinterpret_cast<uint32_t*>(a.c.w) : reinterpret_cast<uint32_t*>(a.c.pos)) + base;
+#pragma unroll 1
+    for (uint32_t i0 = (rank * kEvictWarps + warp) * kMoves; i0 < moves; i0 += nb * kEvictWarps * kMoves) {
+      int32_t to = 0, from = 0;
+      if (lane < kMoves && i0 + lane < moves) {
+        to = entry(1, i0 + lane);
+        from = entry(2, i0 + lane);
+      }
+      uint32_t x[kMoves], y[kMoves];
 #pragma unroll
       for (int u = 0; u < kMoves; ++u) {
-        if (i0 + u * stride >= moves) continue;
-        if (l16 < 8) v[u] = reinterpret_cast<const uint4*>((l16 < 4 ? a.c.kc : a.c.vc) + src[u] * kCode4)[l16 & 3];
-        else if (l16 < 12) v[u].x = (l16 == 8 ? reinterpret_cast<const uint32_t*>(a.c.ks) : l16 == 9 ? reinterpret_cast<const uint32_t*>(a.c.vs)
-                                     : l16 == 10 ? reinterpret_cast<const uint32_t*>(a.c.w) : reinterpret_cast<const uint32_t*>(a.c.pos))[src[u]];
+        const int32_t src = __shfl_sync(kFull, from, u);
+        if (i0 + u < moves) {
+          x[u] = *reinterpret_cast<const uint32_t*>(codes_at + (int64_t)src * kCode4);
+          if (lane < 4) y[u] = rest_at[src];
+        }
       }
 #pragma unroll
       for (int u = 0; u < kMoves; ++u) {
-        if (i0 + u * stride >= moves) continue;
-        if (l16 < 8) reinterpret_cast<uint4*>((l16 < 4 ? a.c.kc : a.c.vc) + dst[u] * kCode4)[l16 & 3] = v[u];
-        else if (l16 < 12) (l16 == 8 ? reinterpret_cast<uint32_t*>(a.c.ks) : l16 == 9 ? reinterpret_cast<uint32_t*>(a.c.vs)
-                            : l16 == 10 ? reinterpret_cast<uint32_t*>(a.c.w) : reinterpret_cast<uint32_t*>(a.c.pos))[dst[u]] = v[u].x;
+        const int32_t dst = __shfl_sync(kFull, to, u);
+        if (i0 + u < moves) {
+          *reinterpret_cast<uint32_t*>(codes_at + (int64_t)dst * kCode4) = x[u];
+          if (lane < 4) rest_at[dst] = y[u];
+        }
       }
     }
   }
@@ -357,7 +375,7 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(EvictArgs a) {
   // the last KV head of the sequence to finish shortens it
   if (rank == 0 && tid == 0) {
     __threadfence();
-    if (atomicInc(&a.c.counters[b], (uint32_t)(a.c.hkv - 1)) == (uint32_t)(a.c.hkv - 1) && n > a.keep)
+    if (atomicInc(&a.c.counters[b], (uint32_t)(a.c.hkv - 1)) == (uint32_t)(a.c.hkv - 1) && n > keep)
       a.c.lens[b] = (int32_t)a.keep;
   }
 }
@@ -366,11 +384,23 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(EvictArgs a) {
 
 cudaError_t launch_kv4_evict(const EvictArgs& a, cudaStream_t st) {
   int nb = 1;
-  while (nb < kEvictMaxBlocks && nb * kHeldKeys * kEvictThreads < a.c.rmax) nb *= 2;
-  if (nb == 1) return launch_pdl(k_kv4_evict<false>, dim3(a.c.batch * a.c.hkv), dim3(kEvictThreads), 0, st, a);
+  while (nb < kEvictMaxBlocks && (int64_t)nb * kHeldRows < a.c.rmax) nb *= 2;
+  const int64_t per_block = min64(kHeldRows, (a.c.rmax + nb - 1) / nb + kEvictThreads);
+  const size_t smem = (size_t)min64(kHeldRows, (per_block + kEvictThreads - 1) / kEvictThreads * kEvictThreads) * sizeof(uint32_t);
+  static bool done[64];  // the limit belongs to the device; setting it twice is harmless
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && !(dev >= 0 && dev < 64 && done[dev])) {
+    e = cudaFuncSetAttribute((const void*)k_kv4_evict<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldRows * 4);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute((const void*)k_kv4_evict<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldRows * 4);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  }
+  if (e != cudaSuccess) return e;
+  if (nb == 1) return launch_pdl(k_kv4_evict<false>, dim3(a.c.batch * a.c.hkv), dim3(kEvictThreads), smem, st, a);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.c.batch * a.c.hkv * nb);
   cfg.blockDim = dim3(kEvictThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
