@@ -324,7 +324,8 @@ paris_status paris_profile_end(paris_ctx* ctx, double* total_ms, int64_t* launch
  * device, and nothing is allocated or kept, so they may be captured into a
  * graph and replayed as the lengths change.  The text of their last error on
  * the calling thread is paris_last_error(NULL).  head_dim is 128.
- * Base addresses are 16-byte aligned and strides multiples of 8 elements.
+ * Base addresses are 16-byte aligned; strides are multiples of 8 elements, at
+ * least 128, token and head strides below 2^31 and seq strides below 2^38.
  * ------------------------------------------------------------------------ */
 
 /* Element strides of a tensor of heads: element c of head h of the token in

@@ -29,91 +29,113 @@ __device__ __forceinline__ float group_scale(float amax, uint32_t& byte) {
   return n * 7.62939453125e-06f;
 }
 
-// Codes and scale byte of a thread's 8 channels (a group is 4 threads), any
-// values.
-__device__ __forceinline__ uint32_t quantise8(float (&x)[8], uint32_t& byte) {
-  float amax = 0.f;
+// A thread's 16 channels of a row; a group is two threads.
+struct RowF32 {
+  float x[16];
+};
+struct RowBf16 {
+  uint32_t w[8];
+};
+
+__device__ __forceinline__ void load_row(const void* p, int64_t e, RowF32& r) {
+  const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + e);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] = clean4(x[i]);
-    amax = fmaxf(amax, fabsf(x[i]));
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = __ldg(q + i);
+    r.x[4 * i] = v.x; r.x[4 * i + 1] = v.y; r.x[4 * i + 2] = v.z; r.x[4 * i + 3] = v.w;
   }
-  amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
-  amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
-  const float S = group_scale(amax, byte);
-  uint32_t word = 0;
+}
+__device__ __forceinline__ void load_row(const void* p, int64_t e, RowBf16& r) {
+  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + e);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float c = S > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x[i], S)), -7.f), 7.f) : 0.f;
-    word |= (uint32_t)((int)c + 8) << (4 * i);
+  for (int i = 0; i < 2; ++i) {
+    const uint4 v = __ldg(q + i);
+    r.w[4 * i] = v.x; r.w[4 * i + 1] = v.y; r.w[4 * i + 2] = v.z; r.w[4 * i + 3] = v.w;
   }
-  return word;
 }
 
-// The same of 8 bf16 values, five operations each.  With X the value's 8-bit
-// and s the scale's 4-bit integer, x / S = X 2^e / s is a tie or at least
-// 2^-10 from one where it could round to 1..7; so x times an approximate 1 / S
-// (off by 2^-20 at most), rounded to multiples of 2^-13 by an addition of
-// 1536, is the tie exactly where x / S is, and on its side of it elsewhere.
-// The second addition rounds it to the integer c + 8 (8 is even: ties still
-// go to even c) in the low bits of 1.5 2^23 + 8 + c; the shifted sum of the
-// eight words, less the sum of what is above those bits, is the code word.
-__device__ __forceinline__ uint32_t quantise8(uint4 v, uint32_t& byte) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t top = w[0] & 0x7fff7fffu;
+// Codes and scale byte, any values.
+__device__ __forceinline__ uint2 quantise(RowF32& r, uint32_t& byte) {
+  float amax = 0.f;
 #pragma unroll
-  for (int i = 1; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+  for (int i = 0; i < 16; ++i) {
+    r.x[i] = clean4(r.x[i]);
+    amax = fmaxf(amax, fabsf(r.x[i]));
+  }
+  amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+  const float S = group_scale(amax, byte);
+  uint32_t word[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float c = S > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(r.x[i], S)), -7.f), 7.f) : 0.f;
+    word[i >> 3] |= (uint32_t)((int)c + 8) << (4 * (i & 7));
+  }
+  return make_uint2(word[0], word[1]);
+}
+
+// The same of bf16 values, without divisions and in five operations a value.
+//
+// With A the largest value's 8-bit integer, A 2^e / 7 is on the grid of
+// four-bit scales or at least 2^-11 of itself from it, so its product with an
+// approximate 1 / 7, taken down by 2^-17, rounds up to the same scale.
+//
+// With X a value's 8-bit and s the scale's 4-bit integer, x / S = X 2^e / s is
+// a tie or at least 2^-10 from one where it could round to 1..7; so x times an
+// approximate 1 / S (off by 2^-20 at most), rounded to multiples of 2^-13 by
+// an addition of 1536, is the tie exactly where x / S is, and on its side of it
+// elsewhere.  The second addition rounds it to the integer c + 8 (8 is even:
+// ties still go to even c) in the low bits of 1.5 2^23 + 8 + c; the shifted sum
+// of eight of these, less the sum of what is above those bits, is a code word.
+__device__ __forceinline__ uint2 quantise(RowBf16& r, uint32_t& byte) {
+  uint32_t top = r.w[0] & 0x7fff7fffu;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) top = __vmaxu2(top, r.w[i] & 0x7fff7fffu);
   uint32_t amax = max(top & 0xffffu, top >> 16);
   amax = max(amax, __shfl_xor_sync(kFull, amax, 1));
-  amax = max(amax, __shfl_xor_sync(kFull, amax, 2));
   if (__any_sync(kFull, amax > 0x44D2u)) {  // past 1680, infinities, NaN
-    float x[8];
+    RowF32 f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = bf16_bits_to_float(w[i] & 0xffffu);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < 8; ++i) {
+      f.x[2 * i] = bf16_bits_to_float(r.w[i] & 0xffffu);
+      f.x[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
     }
-    return quantise8(x, byte);
+    return quantise(f, byte);
   }
-  const float S = group_scale(bf16_bits_to_float(amax), byte);
+  const float t = bf16_bits_to_float(amax) * (1.f / 7.f);
+  const uint32_t up = (__float_as_uint(t) - 64u + 0xFFFFFu) & ~0xFFFFFu;
+  const float small = ceilf(t * (131072.f * (1.f - 7.62939453125e-06f)));  // multiples of 2^-17
+  const bool is_small = t < 6.1e-05f;  // below 2^-14, whose neighbours the 64 steps leave on its side
+  byte = is_small ? (uint32_t)small : (up >> 20) - 896u;
+  const float S = is_small ? small * 7.62939453125e-06f : __uint_as_float(up);
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(inv) : "f"(S));
   if (S == 0.f) inv = 0.f;
-  uint32_t word = 0;
+  uint32_t word[2];
 #pragma unroll
-  for (int i = 3; i >= 0; --i) {
-    const float hi = fmaf(__uint_as_float(w[i] & 0xffff0000u), inv, 1536.f) + (12582920.f - 1536.f);
-    const float lo = fmaf(__uint_as_float(w[i] << 16), inv, 1536.f) + (12582920.f - 1536.f);
-    word = (word << 4) + __float_as_uint(hi);
-    word = (word << 4) + __float_as_uint(lo);
+  for (int h = 0; h < 2; ++h) {
+    uint32_t x = 0;
+#pragma unroll
+    for (int i = 4 * h + 3; i >= 4 * h; --i) {
+      const float hi = fmaf(__uint_as_float(r.w[i] & 0xffff0000u), inv, 1536.f) + (12582920.f - 1536.f);
+      const float lo = fmaf(__uint_as_float(r.w[i] << 16), inv, 1536.f) + (12582920.f - 1536.f);
+      x = (x << 4) + __float_as_uint(hi);
+      x = (x << 4) + __float_as_uint(lo);
+    }
+    word[h] = x - (0x4B400000u + 0xB4000000u + 0x40000000u);
   }
-  return word - (0x4B400000u + 0xB4000000u + 0x40000000u);
+  return make_uint2(word[0], word[1]);
 }
 
-__device__ __forceinline__ void load8(const void* p, int64_t e, uint4& v) {
-  v = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + e));
-}
-struct Eight {
-  float x[8];
-};
-__device__ __forceinline__ void load8(const void* p, int64_t e, Eight& v) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(p) + e));
-  const float4 b = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(p) + e + 4));
-  v.x[0] = a.x; v.x[1] = a.y; v.x[2] = a.z; v.x[3] = a.w;
-  v.x[4] = b.x; v.x[5] = b.y; v.x[6] = b.z; v.x[7] = b.w;
-}
-__device__ __forceinline__ uint32_t quantise8(Eight& v, uint32_t& byte) { return quantise8(v.x, byte); }
-
-// Block: up to `tokens` tokens of one sequence.  16 threads take the key and
-// the value row of a (token, KV head), 8 channels each, two such pairs at a
-// time.  Bound by the read of k and v: four 16-byte loads a thread are in
-// flight, and the arithmetic is kept below the memory's time.
-template <typename V>
+// Block: up to `tokens` tokens of one sequence.  Eight threads take the key
+// and the value row of a (token, KV head), 16 channels each.  Bound by the
+// read of k and v: the arithmetic (35 operations of a warp a row) stays below
+// the memory's time.
+template <typename Row>
 __global__ void __launch_bounds__(kStoreThreads) k_kv4_store(StoreArgs a, int nblk, int tokens, uint32_t hkv_inv) {
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.x / nblk, blk = blockIdx.x - b * nblk;
-  const int tid = threadIdx.x, lane = tid & 31, l16 = tid & 15;
+  const int tid = threadIdx.x, l8 = tid & 7;
   const int hkv = a.c.hkv;
   int64_t start, len;
   seq_rows(a.cu, b, a.rows, start, len);
@@ -123,45 +145,34 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv4_store(StoreArgs a, int nb
   const int64_t t0 = (int64_t)blk * tokens;
   const int n = (int)max64(0, min64(tokens, stored - t0));
   const int32_t pos0 = a.c.next[b];
-  const int items = n * hkv;
-  const int64_t seq_k = a.cu ? 0 : b * a.ks.seq, seq_v = a.cu ? 0 : b * a.vs.seq;
-  for (int it0 = (tid >> 5) * 2; it0 < items; it0 += 2 * (kStoreThreads / 16)) {
-    V x[2][2];
-    int tok[2], h[2];
-    bool active[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int it = it0 + u * (kStoreThreads / 16) + (lane >> 4);
-      active[u] = it < items;
-      tok[u] = hkv == 1 ? it : (int)__umulhi((uint32_t)it, hkv_inv);
-      h[u] = it - tok[u] * hkv;
-      if (!active[u]) tok[u] = h[u] = 0;  // read again, and dropped
-      const int64_t r = start + t0 + tok[u];
-      load8(a.k, seq_k + r * a.ks.token + h[u] * a.ks.head + 8 * l16, x[u][0]);
-      load8(a.v, seq_v + r * a.vs.token + h[u] * a.vs.head + 8 * l16, x[u][1]);
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t row = ((int64_t)b * hkv + h[u]) * a.c.rmax + old_len + t0 + tok[u];
-      uint32_t sw[2];
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        uint32_t byte;
-        const uint32_t word = quantise8(x[u][kv], byte);
-        sw[kv] = byte << (8 * (l16 >> 2));
-        sw[kv] |= __shfl_xor_sync(kFull, sw[kv], 4);
-        sw[kv] |= __shfl_xor_sync(kFull, sw[kv], 8);
-        if (active[u]) *reinterpret_cast<uint32_t*>((kv ? a.c.vc : a.c.kc) + row * kCode4 + 4 * l16) = word;
-      }
-      if (!active[u]) continue;
-      if (l16 == 0) *reinterpret_cast<uint32_t*>(a.c.ks + row * kScale4) = sw[0];
-      if (l16 == 4) *reinterpret_cast<uint32_t*>(a.c.vs + row * kScale4) = sw[1];
-      if (l16 == 8) a.c.pos[row] = pos0 + (int32_t)(t0 + tok[u]);
-      if (l16 == 12) {
-        const int64_t wrow = (a.cu ? (int64_t)h[u] * a.rows + start : ((int64_t)b * hkv + h[u]) * a.rows) + t0 + tok[u];
-        a.c.w[row] = a.weights ? a.weights[wrow] : 0.f;
-      }
-    }
+  const uint32_t items = n * hkv;
+  const int64_t k0 = (a.cu ? 0 : b * a.ks.seq) + (start + t0) * a.ks.token + 16 * l8;
+  const int64_t v0 = (a.cu ? 0 : b * a.vs.seq) + (start + t0) * a.vs.token + 16 * l8;
+  const int64_t row0 = (int64_t)b * hkv * a.c.rmax + old_len + t0;
+  // strides and max_rows fit 32 bits: offsets are one wide product each
+  const uint32_t kt = (uint32_t)a.ks.token, kh = (uint32_t)a.ks.head, vt = (uint32_t)a.vs.token, vh = (uint32_t)a.vs.head;
+  const uint32_t rmax = (uint32_t)a.c.rmax;
+  for (uint32_t it0 = (tid >> 5) * 4; it0 < items; it0 += kStoreThreads / 8) {
+    const uint32_t it = min(it0 + ((tid >> 3) & 3), items - 1);  // past the end the last again: the same is written twice
+    const uint32_t tok = hkv == 1 ? it : __umulhi(it, hkv_inv), h = it - tok * hkv;
+    Row k, v;
+    load_row(a.k, k0 + (uint64_t)tok * kt + (uint64_t)h * kh, k);
+    load_row(a.v, v0 + (uint64_t)tok * vt + (uint64_t)h * vh, v);
+    float wt = 0.f;
+    if (a.weights != nullptr && l8 == 2) wt = a.weights[(a.cu ? (int64_t)h * a.rows + start : ((int64_t)b * hkv + h) * a.rows) + t0 + tok];
+    const int64_t row = row0 + (uint64_t)h * rmax + tok;
+    uint32_t kb, vb;
+    const uint2 kw = quantise(k, kb), vw = quantise(v, vb);
+    reinterpret_cast<uint2*>(a.c.kc + row * kCode4)[l8] = kw;
+    reinterpret_cast<uint2*>(a.c.vc + row * kCode4)[l8] = vw;
+    // a row's four scale bytes: the even threads hold one of each
+    uint32_t sw = (kb | vb << 16) << (l8 & 2 ? 8 : 0);
+    sw |= __shfl_xor_sync(kFull, sw, 2);                    // k 0, 1 and v 0, 1; k 2, 3 and v 2, 3
+    const uint32_t other = __shfl_xor_sync(kFull, sw, 4);
+    if (l8 == 0) *reinterpret_cast<uint32_t*>(a.c.ks + row * kScale4) = (sw & 0xffffu) | other << 16;
+    if (l8 == 4) *reinterpret_cast<uint32_t*>(a.c.vs + row * kScale4) = other >> 16 | (sw & 0xffff0000u);
+    if (l8 == 6) a.c.pos[row] = pos0 + (int32_t)(t0 + tok);
+    if (l8 == 2) a.c.w[row] = wt;
   }
   // the last block of the sequence to finish moves its length on: every
   // block has read the old one (and the counter wraps back to zero)
@@ -214,16 +225,16 @@ __global__ void __launch_bounds__(256) k_kv4_read(Kv4 c, __nv_bfloat16* k_out, _
 }  // namespace
 
 cudaError_t launch_kv4_store(const StoreArgs& a, cudaStream_t st) {
-  // 16 tokens a block, fewer where that leaves SMs without four blocks
+  // 16 tokens a block, fewer where that leaves SMs without two blocks
   int tokens = 16;
-  while (tokens > 1 && a.c.batch * ((a.max_new + tokens - 1) / tokens) < 4 * 152) tokens /= 2;
+  while (tokens > 1 && a.c.batch * ((a.max_new + tokens - 1) / tokens) < 2 * 152) tokens /= 2;
   const int64_t nblk = max64(1, (a.max_new + tokens - 1) / tokens);
   if (nblk * a.c.batch > 0x7fffffff) return cudaErrorInvalidValue;
   // exact for the at most 16 hkv items of a block
   const uint32_t inv = (uint32_t)(((uint64_t)1 << 32) / a.c.hkv + 1);
   const dim3 grid((unsigned)(nblk * a.c.batch));
-  if (a.dtype == 1) return launch_pdl(k_kv4_store<uint4>, grid, dim3(kStoreThreads), 0, st, a, (int)nblk, tokens, inv);
-  return launch_pdl(k_kv4_store<Eight>, grid, dim3(kStoreThreads), 0, st, a, (int)nblk, tokens, inv);
+  if (a.dtype == 1) return launch_pdl(k_kv4_store<RowBf16>, grid, dim3(kStoreThreads), 0, st, a, (int)nblk, tokens, inv);
+  return launch_pdl(k_kv4_store<RowF32>, grid, dim3(kStoreThreads), 0, st, a, (int)nblk, tokens, inv);
 }
 
 cudaError_t launch_kv4_read(const Kv4& c, __nv_bfloat16* k_out, __nv_bfloat16* v_out, int64_t rows, cudaStream_t st) {

@@ -52,9 +52,11 @@ paris_status take_strides(const paris_strides& s, int64_t tokens, int heads, int
       *x.to = kDim;
       continue;
     }
-    if (x.stride < kDim || x.stride % 8 || x.stride >= ((int64_t)1 << 38))
-      return fail(PARIS_EINVAL, "%s: the %s stride must be a multiple of 8 elements, at least %d (got %lld)", name, x.axis,
-                  kDim, (long long)x.stride);
+    // sequences may be further apart: tensor maps take 2^40 bytes
+    const int64_t most = x.to == &out->seq ? (int64_t)1 << 38 : (int64_t)1 << 31;
+    if (x.stride < kDim || x.stride % 8 || x.stride >= most)
+      return fail(PARIS_EINVAL, "%s: the %s stride must be a multiple of 8 elements, from %d to below %lld (got %lld)", name,
+                  x.axis, kDim, (long long)most, (long long)x.stride);
     *x.to = x.stride;
   }
   return PARIS_OK;
