@@ -85,31 +85,38 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
 }
 
-struct Rows4 {  // a split's rows
-  const uint8_t *kc, *vc, *ks, *vs;
+// What a lane copies of the warp's next step: a code piece (and those 512, 1024
+// and 1536 bytes on) and a row's scales, of keys and values.
+struct Next4 {
+  const uint8_t *k, *v, *ks, *vs;
 };
 
-// Start the copy of rows [row0, row0 + 32); past `last` the last row again
-// (its weights are set to zero).
-__device__ __forceinline__ void copy_step(uint32_t dst, const Rows4& p, int row0, int last, int lane) {
-  if (row0 + kRows4 - 1 <= last) {
-    const uint8_t *k = p.kc + (int64_t)row0 * kCode4 + 16 * lane, *v = p.vc + (int64_t)row0 * kCode4 + 16 * lane;
+// Start the copy of a step of which `left` rows are there; past them the last
+// one again (its weights are set to zero).
+__device__ __forceinline__ void copy_step(uint32_t dst, Next4& p, int left, int lane) {
+  if (left >= kRows4) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      copy16(dst + 16 * lane + 512 * i, k + 512 * i);
-      copy16(dst + 2048 + 16 * lane + 512 * i, v + 512 * i);
+      copy16(dst + 16 * lane + 512 * i, p.k + 512 * i);
+      copy16(dst + 2048 + 16 * lane + 512 * i, p.v + 512 * i);
     }
+    copy4(dst + 4096 + 4 * lane, p.ks);
+    copy4(dst + 4224 + 4 * lane, p.vs);
   } else {
 #pragma unroll 1
     for (int i = 0; i < 4; ++i) {
-      const int64_t r = min(row0 + 8 * i + (lane >> 2), last);
-      copy16(dst + 16 * lane + 512 * i, p.kc + r * kCode4 + 16 * (lane & 3));
-      copy16(dst + 2048 + 16 * lane + 512 * i, p.vc + r * kCode4 + 16 * (lane & 3));
+      const int row = 8 * i + (lane >> 2), back = max(row - left + 1, 0) * kCode4 - 512 * i;
+      copy16(dst + 16 * lane + 512 * i, p.k - back);
+      copy16(dst + 2048 + 16 * lane + 512 * i, p.v - back);
     }
+    const int back = max(lane - left + 1, 0) * kScale4;
+    copy4(dst + 4096 + 4 * lane, p.ks - back);
+    copy4(dst + 4224 + 4 * lane, p.vs - back);
   }
-  const int64_t r = min(row0 + lane, last);
-  copy4(dst + 4096 + 4 * lane, p.ks + r * kScale4);
-  copy4(dst + 4224 + 4 * lane, p.vs + r * kScale4);
+  p.k += kTile4 * kCode4;
+  p.v += kTile4 * kCode4;
+  p.ks += kTile4 * kScale4;
+  p.vs += kTile4 * kScale4;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -124,10 +131,59 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
+// The rows of a batch are cut into chunks, a block each (per KV head and head
+// group), a sequence's into equal ones.  Their size comes from the lengths as
+// they are on the device, so that nblocks chunks hold every row however the
+// lengths differ: C tiles, C = ceil(sum of tiles / (nblocks - batch)), leaves
+// sum of ceil(tiles / C) <= nblocks.  Batches of more than 128 sequences (a
+// thread each) fill the GPU anyway, and are cut evenly.
+struct ChunkShared {
+  uint32_t warp_sum[4], warp_n[4];
+  int b, first, n;
+};
+
+// The block's sequence (-1: none), the first of its chunks and their number.
+__device__ __forceinline__ int3 chunk_of(const Attend4Args& a, ChunkShared& sh, int x) {
+  if (a.c.batch > 128) {
+    const int n = a.nblocks / a.c.batch;
+    return make_int3(x / n, x / n * n, n);
+  }
+  // tiles fit 31 bits: 128 x 2^31 / 128
+  if (a.c.batch == 1) {
+    const uint32_t all = ((uint32_t)kv4_len(a.c, 0) + kTile4 - 1) / kTile4;
+    const uint32_t size = max(2u, (all + a.nblocks - 1) / a.nblocks), n = (all + size - 1) / size;
+    return make_int3((uint32_t)x < n ? 0 : -1, 0, n);
+  }
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const uint32_t tiles = t < a.c.batch ? ((uint32_t)kv4_len(a.c, t) + kTile4 - 1) / kTile4 : 0u;
+  const uint32_t sum = __reduce_add_sync(kFull, tiles);
+  if (lane == 0) sh.warp_sum[warp] = sum;
+  if (t == 0) sh.b = -1;
+  __syncthreads();
+  const uint32_t all = sh.warp_sum[0] + sh.warp_sum[1] + sh.warp_sum[2] + sh.warp_sum[3];
+  const uint32_t spare = (uint32_t)(a.nblocks - a.c.batch);
+  const uint32_t size = max(2u, (all + spare - 1) / spare), n = (tiles + size - 1) / size;
+  const uint32_t inc = warp_incl_scan(n, lane);
+  if (lane == 31) sh.warp_n[warp] = inc;
+  __syncthreads();
+  uint32_t first = inc - n;
+#pragma unroll
+  for (int w = 0; w < 3; ++w)
+    if (w < warp) first += sh.warp_n[w];
+  if ((uint32_t)x >= first && (uint32_t)x < first + n) {
+    sh.b = t;
+    sh.first = (int)first;
+    sh.n = (int)n;
+  }
+  __syncthreads();
+  return make_int3(sh.b, sh.first, sh.n);
+}
+
 struct Shared4 {
   uint2 q[8][2][32];           // query fragments: step, column tile, lane
   float qscale[kHeads4];
   float ml[kWarps4][kHeads4][2];
+  ChunkShared chunks;
 };
 
 // NT column tiles: 1 for up to four query heads (columns 0-3 their upper,
@@ -141,30 +197,40 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int warp = __shfl_sync(kFull, tid >> 5, 0);
-  const int split = blockIdx.x, bh = blockIdx.y, h0 = blockIdx.z * kHeads;
-  const int b = bh / a.c.hkv, kvh = bh - b * a.c.hkv;
+  const int kvh = blockIdx.y, h0 = blockIdx.z * kHeads;
+  int3 chunk = chunk_of(a, sh.chunks, blockIdx.x);
+  // the same in every lane: a reduction tells the compiler, and the addresses
+  // stay in uniform registers (36.4 against 33.4 us at 128K rows)
+  chunk = make_int3(__reduce_max_sync(kFull, chunk.x), __reduce_max_sync(kFull, chunk.y), __reduce_max_sync(kFull, chunk.z));
+  const int b = chunk.x;
+  if (b < 0) return;
+  const int split = (int)blockIdx.x - chunk.y, bh = b * a.c.hkv + kvh;
+  // for the merging kernel; a sequence without rows has no chunk, or empty ones
+  if (split == 0 && kvh == 0 && blockIdx.z == 0 && tid == 0) a.chunks[b] = make_int2(chunk.y, chunk.z);
   const int nh = min(kHeads, a.g - h0);
   const int qh0 = kvh * a.g + h0;  // first query head of the block
   const int64_t len = kv4_len(a.c, b);
-  const int64_t r_begin = (int64_t)split * a.rows_per_split;
-  float* part = a.part + (((int64_t)b * a.hq + qh0) * a.nsplit + split) * kPartStride;
+  const uint32_t chunk_rows = (((uint32_t)len + kTile4 - 1) / kTile4 + chunk.z - 1) / chunk.z * kTile4;
+  const int64_t r_begin = (int64_t)split * chunk_rows;
+  float* part = a.part + ((int64_t)qh0 * a.nblocks + blockIdx.x) * kPartStride;
   if (r_begin >= len) {
     if (tid < nh) {
-      part[(int64_t)tid * a.nsplit * kPartStride] = -INFINITY;
-      part[(int64_t)tid * a.nsplit * kPartStride + 1] = 0.f;
+      part[(int64_t)tid * a.nblocks * kPartStride] = -INFINITY;
+      part[(int64_t)tid * a.nblocks * kPartStride + 1] = 0.f;
     }
     return;
   }
   // rows of this split from its first on, and of the sequence
-  const int n = (int)min64(len - r_begin, a.rows_per_split);
+  const int n = __reduce_max_sync(kFull, (int)min64(len - r_begin, chunk_rows));
   const int64_t base = (int64_t)bh * a.c.rmax + r_begin;
-  const Rows4 rows{a.c.kc + base * kCode4, a.c.vc + base * kCode4, a.c.ks + base * kScale4, a.c.vs + base * kScale4};
   const Step4* ring = reinterpret_cast<const Step4*>(ring_mem) + warp * kDepth4;
   const uint32_t ring_u32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   int row0 = warp * kRows4;
+  Next4 ahead{a.c.kc + (base + row0) * kCode4 + 16 * lane, a.c.vc + (base + row0) * kCode4 + 16 * lane,
+              a.c.ks + (base + row0 + lane) * kScale4, a.c.vs + (base + row0 + lane) * kScale4};
 #pragma unroll
   for (int i = 0; i < kDepth4 - 1; ++i) {
-    if (row0 + i * kTile4 < n) copy_step(ring_u32 + i * (int)sizeof(Step4), rows, row0 + i * kTile4, n - 1, lane);
+    if (row0 + i * kTile4 < n) copy_step(ring_u32 + i * (int)sizeof(Step4), ahead, n - row0 - i * kTile4, lane);
     asm volatile("cp.async.commit_group;\n" ::: "memory");
   }
 
@@ -242,7 +308,7 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
     {
       const int next = row0 + (kDepth4 - 1) * kTile4;
       const int to = stage == 0 ? kDepth4 - 1 : stage - 1;
-      if (next < n) copy_step(ring_u32 + to * (int)sizeof(Step4), rows, next, n - 1, lane);
+      if (next < n) copy_step(ring_u32 + to * (int)sizeof(Step4), ahead, n - next, lane);
       asm volatile("cp.async.commit_group;\n" ::: "memory");
       asm volatile("cp.async.wait_group %0;\n" ::"n"(kDepth4 - 1) : "memory");
       __syncwarp();
@@ -414,7 +480,7 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
       L += lw * f;
       O += so[(w * kHeads4 + h) * kDim + dd] * f;
     }
-    float* ph = part + (int64_t)h * a.nsplit * kPartStride;
+    float* ph = part + (int64_t)h * a.nblocks * kPartStride;
     ph[4 + dd] = O;
     if (dd == 0) {
       ph[0] = M;
@@ -423,36 +489,30 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
   }
 }
 
-constexpr int kFinishThreads = 512;
-constexpr int kFinishWarps = kFinishThreads / 32;
-constexpr int kFinishRows = 2048;  // rows whose weights a block adds up
-constexpr int kMaxSplit4 = 512;
-
 // A warp: the maximum and the sum of one head over its splits.
 __device__ __forceinline__ float2 merge_ml(const float* ph, int nsplit, int lane) {
-  float M = -INFINITY, L = 0.f;
-#pragma unroll 4
-  for (int s = lane; s < nsplit; s += 32) {
-    const float2 ml = *reinterpret_cast<const float2*>(ph + (int64_t)s * kPartStride);
-    if (ml.y == 0.f) continue;  // no rows
-    const float mn = fmaxf(M, ml.x);
-    L = (L != 0.f ? L * exp2f(M - mn) : 0.f) + ml.y * exp2f(ml.x - mn);
-    M = mn;
+  auto ml_of = [&](int s) { return *reinterpret_cast<const float2*>(ph + (int64_t)s * kPartStride); };
+  const float2 first = lane < nsplit ? ml_of(lane) : make_float2(-INFINITY, 0.f);
+  float M = first.x;
+  for (int s = lane + 32; s < nsplit; s += 32) M = fmaxf(M, ml_of(s).x);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
+  float L = first.y != 0.f ? first.y * exp2_fast(first.x - M) : 0.f;  // the sum 0: no rows
+  for (int s = lane + 32; s < nsplit; s += 32) {
+    const float2 ml = ml_of(s);
+    if (ml.y != 0.f) L += ml.y * exp2_fast(ml.x - M);
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    const float om = __shfl_xor_sync(kFull, M, off), ol = __shfl_xor_sync(kFull, L, off);
-    const float mn = fmaxf(M, om);
-    L = (L != 0.f ? L * exp2f(M - mn) : 0.f) + (ol != 0.f ? ol * exp2f(om - mn) : 0.f);
-    M = mn;
-  }
+  for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(kFull, L, off);
   return make_float2(M, L);
 }
 
-// Blocks [0, G): merge the splits of one query head, a warp taking every
-// 16th split with all its loads in flight at once.  Blocks from G on: add a
-// range of rows' weights, head by head in ascending order.
-__global__ void __launch_bounds__(kFinishThreads) k_kv4_finish(Attend4Args a) {
+// The first blocks merge the splits of `per_block` query heads each, with
+// all of a warp's loads in flight at once; the others add the weights of four
+// rows a thread, head by head in ascending order.
+template <int kFinishThreads>
+__global__ void __launch_bounds__(kFinishThreads, kFinishThreads == 256 ? 3 : 1) k_kv4_finish(Attend4Args a, int per_block) {
+  constexpr int kFinishWarps = kFinishThreads / 32, kFinishRows = 4 * kFinishThreads;
   __shared__ float2 sml[16];  // maximum, 1 / sum
   __shared__ float4 so[kFinishWarps][32];
   pdl_wait();
@@ -460,75 +520,119 @@ __global__ void __launch_bounds__(kFinishThreads) k_kv4_finish(Attend4Args a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.y / a.c.hkv, kvh = blockIdx.y - b * a.c.hkv;
   const int64_t q0 = (int64_t)b * a.hq + kvh * a.g;
-  if ((int)blockIdx.x < a.g) {
-    const float* ph = a.part + (q0 + blockIdx.x) * a.nsplit * kPartStride;
+  const int2 chunk = a.chunks[b];
+  const int64_t len = kv4_len(a.c, b);
+  const int merging = (a.g + per_block - 1) / per_block;
+  const int nsplit = len > 0 ? chunk.y : 0;
+  const float* part = a.part + ((int64_t)kvh * a.g * a.nblocks + chunk.x) * kPartStride;
+  if ((int)blockIdx.x < merging) {
+    const int each = kFinishWarps / per_block, sub = warp % each;
+    const int h = blockIdx.x * per_block + warp / each;
+    const bool live = h < a.g;
+    const float* ph = part + (int64_t)h * a.nblocks * kPartStride;
     constexpr int kAhead = 8;
     float4 x[kAhead];
     float2 ml[kAhead];
+    const int n = live ? nsplit : 0;
     auto load = [&](int s0) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const int s = s0 + warp + i * kFinishWarps;
+        const int s = s0 + sub + i * each;
         ml[i] = make_float2(-INFINITY, 0.f);
-        if (s >= a.nsplit) continue;
+        if (s >= n) continue;
         ml[i] = *reinterpret_cast<const float2*>(ph + (int64_t)s * kPartStride);
         x[i] = *reinterpret_cast<const float4*>(ph + (int64_t)s * kPartStride + 4 + 4 * lane);  // not written without rows
       }
     };
     load(0);
-    const float2 all = merge_ml(ph, a.nsplit, lane);
+    const float2 all = merge_ml(ph, n, lane);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < a.nsplit; s0 += kAhead * kFinishWarps) {
+    for (int s0 = 0; s0 < n; s0 += kAhead * each) {
       if (s0 > 0) load(s0);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         if (ml[i].y == 0.f) continue;
-        const float f = exp2f(ml[i].x - all.x);
+        const float f = exp2_fast(ml[i].x - all.x);
         o.x = fmaf(x[i].x, f, o.x);
         o.y = fmaf(x[i].y, f, o.y);
         o.z = fmaf(x[i].z, f, o.z);
         o.w = fmaf(x[i].w, f, o.w);
       }
     }
-    so[warp][lane] = o;
-    __syncthreads();
-    if (tid < kDim) {
-      float r = 0.f;
-#pragma unroll
-      for (int w = 0; w < kFinishWarps; ++w) r += reinterpret_cast<const float*>(so[w])[tid];
-      a.out[(q0 + blockIdx.x) * kDim + tid] = __float2bfloat16_rn(all.y != 0.f ? r / all.y : 0.f);
+    if (each > 1) {
+      so[warp][lane] = o;
+      __syncthreads();
+      if (sub > 0 || !live) return;
+      for (int w = 1; w < each; ++w) {
+        const float4 y = so[warp + w][lane];
+        o.x += y.x;
+        o.y += y.y;
+        o.z += y.z;
+        o.w += y.w;
+      }
     }
+    if (!live) return;
+    const float inv = all.y != 0.f ? 1.f / all.y : 0.f;
+    *reinterpret_cast<uint2*>(a.out + (q0 + h) * kDim + 4 * lane) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     return;
   }
-  const int64_t len = kv4_len(a.c, b);
-  const int64_t r0 = ((int64_t)blockIdx.x - a.g) * kFinishRows, r1 = min64(len, r0 + kFinishRows);
+  const int64_t r0 = ((int64_t)blockIdx.x - merging) * kFinishRows, r1 = min64(len, r0 + kFinishRows);
   if (r0 >= len) return;
-  if (warp < a.g) {
-    const float2 all = merge_ml(a.part + (q0 + warp) * a.nsplit * kPartStride, a.nsplit, lane);
-    if (lane == 0) sml[warp] = make_float2(all.x, all.y != 0.f ? 1.f / all.y : 0.f);
-  }
   float* w = a.c.w + (int64_t)blockIdx.y * a.c.rmax;
   const float* sc = a.scores + q0 * a.c.rmax;
+  // rows of whole heads are 16-byte aligned: four a thread, on their way
+  // while the splits are merged
+  constexpr int kHeadsAhead = 8;
+  const bool vec = a.c.rmax % 4 == 0 && r0 + kFinishRows <= len;
+  const int64_t rv = r0 + 4 * tid;
+  float4 x[kHeadsAhead], old = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (vec) {
+    old = *reinterpret_cast<const float4*>(w + rv);
+#pragma unroll
+    for (int h = 0; h < kHeadsAhead; ++h)
+      if (h < a.g) x[h] = *reinterpret_cast<const float4*>(sc + h * a.c.rmax + rv);
+  }
+  for (int h = warp; h < a.g; h += kFinishWarps) {
+    const float2 all = merge_ml(part + (int64_t)h * a.nblocks * kPartStride, nsplit, lane);
+    if (lane == 0) sml[h] = make_float2(all.x, all.y != 0.f ? 1.f / all.y : 0.f);
+  }
   __syncthreads();
+  if (vec) {
+    float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4& v, int h) {
+      const float2 ml = sml[h];
+      p.x += exp2_fast(v.x - ml.x) * ml.y;
+      p.y += exp2_fast(v.y - ml.x) * ml.y;
+      p.z += exp2_fast(v.z - ml.x) * ml.y;
+      p.w += exp2_fast(v.w - ml.x) * ml.y;
+    };
+#pragma unroll
+    for (int h = 0; h < kHeadsAhead; ++h)
+      if (h < a.g) add(x[h], h);
+    for (int h = kHeadsAhead; h < a.g; ++h) add(*reinterpret_cast<const float4*>(sc + h * a.c.rmax + rv), h);
+    *reinterpret_cast<float4*>(w + rv) = make_float4(old.x + p.x, old.y + p.y, old.z + p.z, old.w + p.w);
+    return;
+  }
   for (int64_t r = r0 + tid; r < r1; r += kFinishThreads) {
     float p = 0.f;
 #pragma unroll 4
-    for (int h = 0; h < a.g; ++h) p += exp2f(sc[h * a.c.rmax + r] - sml[h].x) * sml[h].y;
+    for (int h = 0; h < a.g; ++h) p += exp2_fast(sc[h * a.c.rmax + r] - sml[h].x) * sml[h].y;
     w[r] += p;
   }
 }
 
 }  // namespace
 
-void kv4_splits(int64_t heads, int g, int64_t rmax, int sm_count, int* nsplit, int64_t* rows_per_split) {
-  // one wave of blocks over all (sequence, KV head, head group)s, at least
-  // two steps of a block each
-  const int64_t units = heads * ((g + 7) / 8), slots = (g <= 4 ? 4 : 3) * (int64_t)sm_count;
-  const int64_t want = std::max<int64_t>(1, slots / units);
-  const int64_t most = std::max<int64_t>(1, (rmax + 2 * kTile4 - 1) / (2 * kTile4));
-  const int64_t n = std::min<int64_t>({want, most, kMaxSplit4});
-  *rows_per_split = std::max<int64_t>(kTile4, ((rmax + n - 1) / n + kTile4 - 1) / kTile4 * kTile4);
-  *nsplit = (int)std::max<int64_t>(1, (rmax + *rows_per_split - 1) / *rows_per_split);
+int kv4_blocks(int batch, int hkv, int g, int64_t rmax, int sm_count) {
+  // one wave of blocks for each KV head and head group, as long as a block
+  // has two tiles; a batch that is cut by its lengths needs more blocks than
+  // sequences, and one that is cut evenly a multiple of its sequences
+  const int64_t wave = std::max<int64_t>(1, (g <= 4 ? 4 : 3) * (int64_t)sm_count / ((int64_t)hkv * ((g + 7) / 8)));
+  const int64_t tiles = (rmax + kTile4 - 1) / kTile4;
+  if (batch > 128) return (int)(batch * std::max<int64_t>(1, std::min(wave / batch, (tiles + 1) / 2)));
+  const int64_t most = batch * ((tiles + 1) / 2) + (batch > 1 ? batch : 0);
+  return (int)std::max<int64_t>(std::min(wave, most), batch > 1 ? batch + 1 : 1);
 }
 
 namespace {
@@ -544,7 +648,7 @@ cudaError_t launch_attend4(const Attend4Args& a, cudaStream_t st) {
     if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
   }
   if (e != cudaSuccess) return e;
-  const dim3 grid(a.nsplit, a.c.batch * a.c.hkv, (a.g + 4 * NT - 1) / (4 * NT));
+  const dim3 grid(a.nblocks, a.c.hkv, (a.g + 4 * NT - 1) / (4 * NT));
   return launch_pdl(k_kv4_attend<NT>, grid, dim3(kThreads4), smem, st, a, kMagic4);
 }
 
@@ -553,8 +657,13 @@ cudaError_t launch_attend4(const Attend4Args& a, cudaStream_t st) {
 cudaError_t launch_kv4_attend(const Attend4Args& a, cudaStream_t st) {
   cudaError_t e = a.g <= 4 ? launch_attend4<1>(a, st) : launch_attend4<2>(a, st);
   if (e != cudaSuccess) return e;
-  const int64_t rows = a.accumulate ? (a.c.rmax + kFinishRows - 1) / kFinishRows : 0;
-  return launch_pdl(k_kv4_finish, dim3((unsigned)(a.g + rows), a.c.batch * a.c.hkv), dim3(kFinishThreads), 0, st, a);
+  // few splits a sequence: a warp merges a head; many: a block, of 16 warps
+  // where it is all that there is to do (76 splits: 5.9 -> 3.5 us)
+  const int per_block = a.nblocks <= 16 * a.c.batch ? 8 : 1;
+  const unsigned heads = (unsigned)(a.g + per_block - 1) / per_block, units = a.c.batch * a.c.hkv;
+  if (per_block == 1 && !a.accumulate) return launch_pdl(k_kv4_finish<512>, dim3(heads, units), dim3(512), 0, st, a, 1);
+  const unsigned rows = a.accumulate ? (unsigned)((a.c.rmax + 1023) / 1024) : 0u;
+  return launch_pdl(k_kv4_finish<256>, dim3(heads + rows, units), dim3(256), 0, st, a, per_block);
 }
 
 }  // namespace paris

@@ -57,13 +57,13 @@ struct Attend4Args {
   Kv4 c;
   const void* q;
   int dtype, hq, g, accumulate;
-  int nsplit;              // splits of a sequence's rows
-  int64_t rows_per_split;  // a multiple of the block's tile
-  float* part;             // [batch * hq][nsplit][kPartStride]
+  int nblocks;             // chunks of the batch's rows, at most
+  float* part;             // [hq][nblocks][kPartStride]
+  int2* chunks;            // [batch] first chunk and number of chunks
   float* scores;           // [batch * hq][rmax], base-2 logits (accumulate)
   __nv_bfloat16* out;
 };
-void kv4_splits(int64_t heads, int g, int64_t rmax, int sm_count, int* nsplit, int64_t* rows_per_split);
+int kv4_blocks(int batch, int hkv, int g, int64_t rmax, int sm_count);
 cudaError_t launch_kv4_attend(const Attend4Args& a, cudaStream_t st);
 
 struct EvictArgs {

@@ -113,11 +113,9 @@ paris_status check_dtype(paris_dtype t) {
   return t == PARIS_F32 || t == PARIS_BF16 ? PARIS_OK : fail(PARIS_EINVAL, "dtype must be PARIS_F32 or PARIS_BF16");
 }
 
-size_t attend4_workspace(const Kv4& k, int hq, bool accumulate, int* nsplit, int64_t* rows_per_split) {
-  const int g = hq / k.hkv;
-  kv4_splits((int64_t)k.batch * k.hkv, g, k.rmax, sm_count(), nsplit, rows_per_split);
-  const size_t heads = (size_t)k.batch * hq;
-  return heads * *nsplit * kPartStride * sizeof(float) + (accumulate ? heads * k.rmax * sizeof(float) : 0);
+size_t attend4_workspace(const Kv4& k, int hq, bool accumulate, int* nblocks) {
+  *nblocks = kv4_blocks(k.batch, k.hkv, hq / k.hkv, k.rmax, sm_count());
+  return (size_t)hq * *nblocks * kPartStride * sizeof(float) + ((size_t)k.batch * sizeof(int2) + 15) / 16 * 16 + (accumulate ? (size_t)k.batch * hq * k.rmax * sizeof(float) : 0);
 }
 
 paris_status check_heads(const Kv4& k, int hq) {
@@ -229,9 +227,8 @@ paris_status paris_kv4_workspace(const paris_kv4* c, int n_q_heads, int accumula
   paris_status st = take_cache(c, &k);
   if (st == PARIS_OK) st = check_heads(k, n_q_heads);
   if (st != PARIS_OK) return st;
-  int nsplit;
-  int64_t rows;
-  *bytes = attend4_workspace(k, n_q_heads, accumulate != 0, &nsplit, &rows);
+  int nblocks;
+  *bytes = attend4_workspace(k, n_q_heads, accumulate != 0, &nblocks);
   return PARIS_OK;
 }
 
@@ -244,7 +241,7 @@ paris_status paris_kv4_attend(const paris_kv4* c, const void* q, paris_dtype dty
   if (st != PARIS_OK) return st;
   if (!q || !out_bf16) return fail(PARIS_EINVAL, "q and out must not be NULL");
   if (!aligned16(q) || !aligned16(out_bf16)) return fail(PARIS_EINVAL, "q and out must be 16-byte aligned");
-  const size_t need = attend4_workspace(a.c, n_q_heads, accumulate != 0, &a.nsplit, &a.rows_per_split);
+  const size_t need = attend4_workspace(a.c, n_q_heads, accumulate != 0, &a.nblocks);
   if (!workspace || workspace_bytes < need || !aligned16(workspace))
     return fail(PARIS_EINVAL, "paris_kv4_attend: needs %zu bytes of 16-byte aligned workspace (got %zu)", need,
                 workspace ? workspace_bytes : (size_t)0);
@@ -254,7 +251,8 @@ paris_status paris_kv4_attend(const paris_kv4* c, const void* q, paris_dtype dty
   a.g = n_q_heads / a.c.hkv;
   a.accumulate = accumulate != 0;
   a.part = static_cast<float*>(workspace);
-  a.scores = a.part + (size_t)a.c.batch * a.hq * a.nsplit * kPartStride;
+  a.chunks = reinterpret_cast<int2*>(a.part + (size_t)a.hq * a.nblocks * kPartStride);
+  a.scores = reinterpret_cast<float*>(a.chunks) + ((size_t)a.c.batch * 2 + 3) / 4 * 4;
   a.out = static_cast<__nv_bfloat16*>(out_bf16);
   return launched(launch_kv4_attend(a, static_cast<cudaStream_t>(stream)), "paris_kv4_attend");
 }

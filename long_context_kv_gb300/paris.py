@@ -295,23 +295,44 @@ class Context:
 
 
 # -- the prompt's own attention, and the 4-bit cache ---------------------------
+# These calls are made once or more for every token: what they check is
+# checked with as few calls into torch as it takes, and pointers go to the
+# library as plain integers.
 HEAD_DIM = 128
 
 
-def _on(device, *tensors):
-    """Every tensor on `device`, and `device` the current one."""
+def _on(index, *tensors):
+    """Every tensor on CUDA device `index`, and that the current one."""
     import torch
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on different devices: {t.device} and {device}")
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device (got {device})")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors on different devices: {t.device} and cuda:{index}")
+    if index < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if torch._C._cuda_getDevice() != index:
+        raise ValueError(f"the tensors are on cuda:{index}, the current device is cuda:{torch._C._cuda_getDevice()}")
+
+
+def _raw_stream(index, stream):
+    """The stream's handle: the one given, or the device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _flat(t):
+    """Address of a contiguous, 16-byte aligned tensor (None: no address)."""
+    if t is None:
+        return None
+    p = t.data_ptr()
+    if p % 16 or not t.is_contiguous():
+        raise ValueError("tensors must be contiguous, their data 16-byte aligned")
+    return p or None
 
 
 def _shaped(t, name, shape, dtype):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
@@ -319,14 +340,15 @@ def _shaped(t, name, shape, dtype):
 
 def _heads(t, name, packed):
     """A tensor of heads as (rows, heads, sequence axis, strides): [rows, H, d] packed, [batch, H, T, d] otherwise."""
-    if t.dim() != (3 if packed else 4) or t.shape[-1] != HEAD_DIM:
+    shape, st = t.shape, t.stride()
+    if len(shape) != (3 if packed else 4) or shape[-1] != HEAD_DIM:
         want = "[rows, heads, 128]" if packed else "[batch, heads, T, 128]"
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {want}")
-    if t.stride(-1) != 1 and t.numel():
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected {want}")
+    if st[-1] != 1 and t.numel():
         raise ValueError(f"{name}: the last dimension must be contiguous")
     if packed:
-        return t.shape[0], t.shape[1], 1, paris_strides(t.stride(0), t.stride(1), 0)
-    return t.shape[2], t.shape[1], t.shape[0], paris_strides(t.stride(2), t.stride(1), t.stride(0))
+        return shape[0], shape[1], 1, (st[0], st[1], 0)
+    return shape[2], shape[1], shape[0], (st[2], st[1], st[0])
 
 
 def _scratch(nbytes, device, stream):
@@ -340,40 +362,39 @@ def _scratch(nbytes, device, stream):
 
 def _prompt(q, k, cu_q, cu_k, max_q, max_k, v=None, out=None):
     import torch
+    bf16 = torch.bfloat16
     if (cu_q is None) != (cu_k is None):
         raise ValueError("cu_q and cu_k must both be given or both be None")
     packed = cu_q is not None
     for t in (q, k, v, out):
-        if t is not None and t.dtype != torch.bfloat16:
+        if t is not None and t.dtype != bf16:
             raise TypeError(f"the prompt calls take bfloat16 tensors (got {t.dtype})")
-    _on(q.device, q, k, v, out, cu_q, cu_k)
-    p = paris_prompt(head_dim=HEAD_DIM)
-    p.rows_q, p.n_q_heads, seqs, p.q = _heads(q, "q", packed)
-    p.rows_k, p.n_kv_heads, k_seqs, p.k = _heads(k, "k", packed)
+    _on(q.get_device(), q, k, v, out, cu_q, cu_k)
+    rows_q, hq, seqs, qs = _heads(q, "q", packed)
+    rows_k, hkv, k_seqs, ks = _heads(k, "k", packed)
     if k_seqs != seqs:
         raise ValueError(f"q and k: batches of {seqs} and {k_seqs}")
+    starts_q = starts_k = None
     if packed:
         for c, name in ((cu_q, "cu_q"), (cu_k, "cu_k")):
             if c.dtype != torch.int32 or c.dim() != 1 or not c.is_contiguous() or c.shape != cu_q.shape or not c.numel():
                 raise ValueError(f"{name}: a contiguous int32 tensor of n + 1 starts, as many for q as for k")
-        seqs = cu_q.numel() - 1
-        p.cu_q, p.cu_k = cu_q.data_ptr(), cu_k.data_ptr()
-    p.n_seqs = seqs
-    p.max_q = p.rows_q if max_q is None else int(max_q)
-    p.max_k = p.rows_k if max_k is None else int(max_k)
+        seqs, starts_q, starts_k = cu_q.numel() - 1, cu_q.data_ptr(), cu_k.data_ptr()
+    vs = os_ = (0, 0, 0)
     if v is not None:
         if v.shape != k.shape:
             raise ValueError(f"v: shape {tuple(v.shape)}, expected {tuple(k.shape)}")
-        p.v = _heads(v, "v", packed)[3]
+        vs = _heads(v, "v", packed)[3]
     if out is not None:
         if out.shape != q.shape:
             raise ValueError(f"out: shape {tuple(out.shape)}, expected {tuple(q.shape)}")
-        p.out = _heads(out, "out", packed)[3]
-    return p, packed
+        os_ = _heads(out, "out", packed)[3]
+    return paris_prompt(seqs, hq, hkv, HEAD_DIM, rows_q, rows_k, starts_q, starts_k,
+                        rows_q if max_q is None else max_q, rows_k if max_k is None else max_k, qs, ks, vs, os_), packed
 
 
 def _raw(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None and t.numel() else None
+    return t.data_ptr() or None if t is not None else None
 
 
 def paris_prompt_attend(q, k, v, out, cu_q=None, cu_k=None, max_q=None, max_k=None, lse=None, stream=None):
@@ -386,16 +407,17 @@ def paris_prompt_attend(q, k, v, out, cu_q=None, cu_k=None, max_q=None, max_k=No
     """
     import torch
     p, packed = _prompt(q, k, cu_q, cu_k, max_q, max_k, v, out)
+    index = q.get_device()
     if lse is not None:
-        _on(q.device, lse)
+        _on(index, lse)
         _shaped(lse, "lse", (p.n_q_heads, p.rows_q) if packed else q.shape[:3], torch.float32)
-        _ptr(lse)
-    lib = load()
+    lib = _lib or load()
+    ref = ctypes.byref(p)
     n = ctypes.c_size_t()
-    _check(lib.paris_prompt_workspace(ctypes.byref(p), ctypes.byref(n)))
+    _check(lib.paris_prompt_workspace(ref, ctypes.byref(n)))
     ws = _scratch(n.value, q.device, stream) if n.value else None
-    _check(lib.paris_prompt_attend(ctypes.byref(p), _raw(q), _raw(k), _raw(v), PARIS_BF16, _raw(out), _raw(lse),
-                                   _raw(ws), n.value, _stream(stream)))
+    _check(lib.paris_prompt_attend(ref, _raw(q), _raw(k), _raw(v), PARIS_BF16, _raw(out), _flat(lse), _raw(ws), n.value,
+                                   _raw_stream(index, stream)))
 
 
 def paris_prompt_check():
@@ -409,12 +431,12 @@ def paris_prompt_weights(q, k, lse, weights, window, cu_q=None, cu_k=None, max_k
     (packed) or [batch, Hkv, T]."""
     import torch
     p, packed = _prompt(q, k, cu_q, cu_k, None, max_k)
-    _on(q.device, lse, weights)
+    index = q.get_device()
+    _on(index, lse, weights)
     _shaped(lse, "lse", (p.n_q_heads, p.rows_q) if packed else q.shape[:3], torch.float32)
     _shaped(weights, "weights", (p.n_kv_heads, p.rows_k) if packed else k.shape[:3], torch.float32)
-    _ptr(lse), _ptr(weights)
-    _check(load().paris_prompt_weights(ctypes.byref(p), _raw(q), _raw(k), PARIS_BF16, _raw(lse), int(window),
-                                       _raw(weights), _stream(stream)))
+    _check((_lib or load()).paris_prompt_weights(ctypes.byref(p), _raw(q), _raw(k), PARIS_BF16, _flat(lse), int(window),
+                                                 _flat(weights), _raw_stream(index, stream)))
 
 
 class KV4Cache:
@@ -443,11 +465,13 @@ class KV4Cache:
                 raise ValueError(f"{name} must be contiguous")
             setattr(self, name, given[name])
         self.batch, self.n_kv_heads, self.max_rows, self.device = b, h, r, k_codes.device
+        self._index, self._token_shape = k_codes.get_device(), (b, h, HEAD_DIM)
         # counters and the status word, made here and zero between calls
         self._words = torch.zeros(b + 1, dtype=torch.int32, device=k_codes.device)
         self._c = paris_kv4(batch=b, n_kv_heads=h, head_dim=HEAD_DIM, max_rows=r,
                             counters=self._words.data_ptr(), status=self._words.data_ptr() + 4 * b,
                             **{n: t.data_ptr() for n, t in given.items()})
+        self._ref = ctypes.byref(self._c)
         self._ws = {}
 
     @classmethod
@@ -480,45 +504,46 @@ class KV4Cache:
             raise ValueError("k and v must have the same shape and dtype")
         if heads != self.n_kv_heads or (not packed and seqs != self.batch):
             raise ValueError(f"k: shape {tuple(k.shape)} for a cache of {self.batch} sequences, {self.n_kv_heads} heads")
-        _on(self.device, k, v, cu, weights)
-        if packed and (cu.dtype != torch.int32 or tuple(cu.shape) != (self.batch + 1,) or not cu.is_contiguous()):
+        _on(self._index, k, v, cu, weights)
+        if packed and (cu.dtype != torch.int32 or cu.shape != (self.batch + 1,) or not cu.is_contiguous()):
             raise ValueError("cu: a contiguous int32 tensor of batch + 1 starts")
         if weights is not None:
             _shaped(weights, "weights", (heads, rows) if packed else k.shape[:3], torch.float32)
-            _ptr(weights)
-        _check(load().paris_kv4_store(ctypes.byref(self._c), _raw(k), _raw(v), _dtype_code(k), ctypes.byref(ks),
-                                      ctypes.byref(vs), rows, _raw(cu), rows if max_new is None else int(max_new),
-                                      _raw(weights), _stream(stream)))
+        _check((_lib or load()).paris_kv4_store(
+            self._ref, _raw(k), _raw(v), _dtype_code(k), ctypes.byref(paris_strides(*ks)), ctypes.byref(paris_strides(*vs)),
+            rows, _raw(cu), rows if max_new is None else int(max_new), _flat(weights), _raw_stream(self._index, stream)))
 
     def paris_kv4_append(self, k, v, stream=None):
         """Add one token to every sequence: k, v [batch, Hkv, 128]."""
-        for t, name in ((k, "k"), (v, "v")):
-            _shaped(t, name, (self.batch, self.n_kv_heads, HEAD_DIM), k.dtype)
-        _on(self.device, k, v)
-        _check(load().paris_kv4_append(ctypes.byref(self._c), _ptr(k), _ptr(v), _dtype_code(k), _stream(stream)))
+        _shaped(k, "k", self._token_shape, k.dtype)
+        _shaped(v, "v", self._token_shape, k.dtype)
+        _on(self._index, k, v)
+        _check((_lib or load()).paris_kv4_append(self._ref, _flat(k), _flat(v), _dtype_code(k),
+                                                 _raw_stream(self._index, stream)))
 
     def paris_kv4_attend(self, q, out, accumulate=False, stream=None):
         """out = softmax(K q / sqrt(d)) V over the rows in use: q, out [batch, Hq, 128]; accumulate: add each row's
         softmax weights, over its query heads, to `weights`."""
         import torch
-        if q.dim() != 3 or q.shape[0] != self.batch or q.shape[2] != HEAD_DIM:
-            raise ValueError(f"q: shape {tuple(q.shape)}, expected [{self.batch}, heads, 128]")
-        _shaped(out, "out", q.shape, torch.bfloat16)
-        _on(self.device, q, out)
-        lib, hq, acc = load(), q.shape[1], int(bool(accumulate))
-        n = self._bytes((hq, acc), lambda b: lib.paris_kv4_workspace(ctypes.byref(self._c), hq, acc, ctypes.byref(b)))
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != self.batch or shape[2] != HEAD_DIM:
+            raise ValueError(f"q: shape {tuple(shape)}, expected [{self.batch}, heads, 128]")
+        _shaped(out, "out", shape, torch.bfloat16)
+        _on(self._index, q, out)
+        lib, hq, acc = _lib or load(), shape[1], 1 if accumulate else 0
+        n = self._bytes((hq, acc), lambda b: lib.paris_kv4_workspace(self._ref, hq, acc, ctypes.byref(b)))
         ws = _scratch(n, self.device, stream)
-        _check(lib.paris_kv4_attend(ctypes.byref(self._c), _ptr(q), _dtype_code(q), hq, acc, _ptr(out), _raw(ws), n,
-                                    _stream(stream)))
+        _check(lib.paris_kv4_attend(self._ref, _flat(q), _dtype_code(q), hq, acc, _flat(out), ws.data_ptr(), n,
+                                    _raw_stream(self._index, stream)))
 
     def paris_kv4_evict(self, keep, sink=0, recent=0, stream=None):
         """At most `keep` rows for each sequence: protected ones and the heaviest others."""
-        _on(self.device)
-        lib = load()
-        n = self._bytes("evict", lambda b: lib.paris_kv4_evict_workspace(ctypes.byref(self._c), ctypes.byref(b)))
+        _on(self._index)
+        lib = _lib or load()
+        n = self._bytes("evict", lambda b: lib.paris_kv4_evict_workspace(self._ref, ctypes.byref(b)))
         ws = _scratch(n, self.device, stream)
-        _check(lib.paris_kv4_evict(ctypes.byref(self._c), int(keep), int(sink), int(recent), _raw(ws), n,
-                                   _stream(stream)))
+        _check(lib.paris_kv4_evict(self._ref, int(keep), int(sink), int(recent), ws.data_ptr(), n,
+                                   _raw_stream(self._index, stream)))
 
     def paris_kv4_read(self, k_out, v_out, stream=None):
         """The values of the first rows: k_out, v_out bfloat16 [batch, Hkv, rows, 128]."""
@@ -527,10 +552,10 @@ class KV4Cache:
             raise ValueError(f"k_out: shape {tuple(k_out.shape)}, expected [batch, heads, rows, 128]")
         for t, name in ((k_out, "k_out"), (v_out, "v_out")):
             _shaped(t, name, (self.batch, self.n_kv_heads, k_out.shape[2], HEAD_DIM), torch.bfloat16)
-        _on(self.device, k_out, v_out)
-        _ptr(k_out), _ptr(v_out)
-        _check(load().paris_kv4_read(ctypes.byref(self._c), _raw(k_out), _raw(v_out), k_out.shape[2], _stream(stream)))
+        _on(self._index, k_out, v_out)
+        _check((_lib or load()).paris_kv4_read(self._ref, _flat(k_out), _flat(v_out), k_out.shape[2],
+                                               _raw_stream(self._index, stream)))
 
     def paris_kv4_check(self):
         """Synchronise; raise if a store found no room."""
-        _check(load().paris_kv4_check(ctypes.byref(self._c)))
+        _check(load().paris_kv4_check(self._ref))
