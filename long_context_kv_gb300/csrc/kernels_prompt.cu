@@ -34,31 +34,25 @@ namespace {
 
 constexpr int kRowWarps = 8;
 
-__device__ __forceinline__ float dot8(uint4 a, const float* q, float acc) {
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ float dot8(uint4 a, uint4 b, float acc) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    acc = fmaf(bf16_bits_to_float(w[i] & 0xffffu), q[2 * i], acc);
-    acc = fmaf(bf16_bits_to_float(w[i] >> 16), q[2 * i + 1], acc);
+    acc = fmaf(bf16_bits_to_float(x[i] & 0xffffu), bf16_bits_to_float(y[i] & 0xffffu), acc);
+    acc = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), acc);
   }
   return acc;
 }
 
 // One query row by one warp: its visible keys 32 at a time, a lane per key
 // for the scores, four channels per lane for the weighted sum.  Only rows
-// that the query sees are read.  qs: the warp's 128 floats of shared memory.
-__device__ __noinline__ void prompt_row(const PromptArgs& a, int s, int h, int64_t q0, int64_t i, int64_t k0, int64_t visible,
-                           float* qs) {
+// that the query sees are read.
+__device__ __noinline__ void prompt_row(const PromptArgs& a, int s, int h, int64_t q0, int64_t i, int64_t k0, int64_t visible) {
   const int lane = threadIdx.x & 31;
   const int kvh = h / a.g;
-  const __nv_bfloat16* q = a.q + (a.cu_q ? 0 : s * a.sq.seq) + (q0 + i) * a.sq.token + h * a.sq.head;
+  const uint4* q = reinterpret_cast<const uint4*>(a.q + (a.cu_q ? 0 : s * a.sq.seq) + (q0 + i) * a.sq.token + h * a.sq.head);
   const __nv_bfloat16* k = a.k + (a.cu_k ? 0 : s * a.sk.seq) + k0 * a.sk.token + kvh * a.sk.head;
   const __nv_bfloat16* v = a.v + (a.cu_k ? 0 : s * a.sv.seq) + k0 * a.sv.token + kvh * a.sv.head;
-  float y[4];
-  load4(q, 1, 4 * lane, y);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) qs[4 * lane + c] = y[c];
-  __syncwarp();
   float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
   for (int64_t j0 = 0; j0 < visible; j0 += 32) {
     const int n = (int)min64(32, visible - j0);
@@ -66,8 +60,8 @@ __device__ __noinline__ void prompt_row(const PromptArgs& a, int s, int h, int64
     if (lane < n) {
       const uint4* kr = reinterpret_cast<const uint4*>(k + (j0 + lane) * a.sk.token);
       float acc = 0.f;
-#pragma unroll
-      for (int c = 0; c < 16; ++c) acc = dot8(kr[c], qs + 8 * c, acc);
+#pragma unroll 4
+      for (int c = 0; c < 16; ++c) acc = dot8(kr[c], __ldg(q + c), acc);
       sc = acc * kScaleLog2;
     }
     float mx = sc;
@@ -96,7 +90,6 @@ __device__ __noinline__ void prompt_row(const PromptArgs& a, int s, int h, int64
   *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
   if (a.lse != nullptr && lane == 0)
     a.lse[((int64_t)(a.cu_q ? 0 : s) * a.hq + h) * a.rows_q + q0 + i] = visible > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
-  __syncwarp();
 }
 
 // ------------------------------------------------------------ the tensor-core kernel
@@ -117,43 +110,92 @@ struct PromptMaps {
   CUtensorMap q, k, v;
 };
 
+// A block's piece of work: 256 query rows of a KV head and a range of keys.
+struct PromptItem {
+  int s, kvh, qb, split;
+  int q0, lq, k0, lk;
+  int t0;               // first token of tile 0
+  int jb, end[kTiles];  // key blocks [jb, end) of each tile
+};
+
+constexpr int kItems = 4;
+
 struct PromptShared {
-  uint64_t q_full, full[kStages], empty[kStages], s_full[kTiles], p_full[2 * kTiles], o_full[kTiles];
+  uint64_t q_full, q_empty, full[kStages], empty[kStages], s_full[kTiles], p_full[2 * kTiles], o_full[kTiles], o_empty[kTiles];
+  uint64_t item_full[kItems], item_empty[kItems];
+  PromptItem items[kItems];  // s < 0: no more
   uint32_t tmem;
   uint32_t gave_up;
 };
 
-// The block's share of the work.
-struct PromptWork {
-  int s, kvh, qb, split;
-  int64_t q0, lq, k0, lk;
-  int64_t t0;        // first token of tile 0
-  int tq;            // tokens of a tile
-  int jb, end[kTiles];  // key blocks [jb, end) of each tile
-};
+__device__ __forceinline__ int blocks_of(int64_t lq, int tokens) { return (int)((lq + tokens - 1) / tokens); }
 
-__device__ __forceinline__ bool prompt_work(const PromptArgs& a, int nqb, PromptWork& w) {
-  // later query blocks see more keys: they start first
-  const int per = a.n_seqs * a.hkv * a.nsplit;
-  int x = blockIdx.x;
-  w.qb = nqb - 1 - x / per;
-  x %= per;
-  w.split = x % a.nsplit;
-  x /= a.nsplit;
-  w.kvh = x % a.hkv;
-  w.s = x / a.hkv;
-  seq_rows(a.cu_q, w.s, a.rows_q, w.q0, w.lq);
-  seq_rows(a.cu_k, w.s, a.rows_k, w.k0, w.lk);
-  const int64_t lq = min64(w.lq, a.max_q);
-  w.tq = kTile / a.g;
-  w.t0 = (int64_t)w.qb * kTiles * w.tq;
-  if (w.t0 >= lq) return false;
+// Item x of the call (a warp computes it): query blocks in descending order,
+// so that those that see most keys come first, and for each the sequences
+// that have it, KV heads and splits.  False: there is no such item.
+__device__ __forceinline__ bool prompt_item(const PromptArgs& a, int64_t x, PromptItem& w) {
+  const int lane = threadIdx.x & 31;
+  const int tq = kTile / a.g, tokens = kTiles * tq;
+  const int per = a.hkv * a.nsplit;
+  int64_t y = x / per;  // (query block, sequence)
+  int z = (int)(x - y * per);
+  w.split = z % a.nsplit;
+  w.kvh = z / a.nsplit;
+  if (a.cu_q == nullptr) {
+    const int nqb = blocks_of(a.max_q, tokens);
+    if (y >= (int64_t)nqb * a.n_seqs) return false;
+    w.qb = nqb - 1 - (int)(y / a.n_seqs);
+    w.s = (int)(y % a.n_seqs);
+  } else {
+    auto blocks = [&](int s) -> int {  // of sequence s
+      if (s >= a.n_seqs) return 0;
+      int64_t q0, lq;
+      seq_rows(a.cu_q, s, a.rows_q, q0, lq);
+      return blocks_of(min64(lq, a.max_q), tokens);
+    };
+    // number of (block, sequence) pairs with block >= level
+    auto from = [&](int level) -> int64_t {
+      int64_t n = 0;
+      for (int s0 = 0; s0 < a.n_seqs; s0 += 32) n += __reduce_add_sync(kFull, (uint32_t)max(0, blocks(s0 + lane) - level));
+      return n;
+    };
+    if (y >= from(0)) return false;
+    int lo = 0, hi = blocks_of(a.max_q, tokens);  // from(lo) > y >= from(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (from(mid) > y) lo = mid;
+      else hi = mid;
+    }
+    int64_t j = y - from(lo + 1);  // among the sequences that have block lo
+    w.qb = lo;
+    w.s = 0;
+    for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
+      const uint32_t has = __ballot_sync(kFull, blocks(s0 + lane) > lo);
+      const int n = __popc(has);
+      if (j < n) {
+        uint32_t m = has;
+        for (int i = 0; i < j; ++i) m &= m - 1;
+        w.s = s0 + __ffs(m) - 1;
+        break;
+      }
+      j -= n;
+    }
+  }
+  int64_t q0, lq, k0, lk;
+  seq_rows(a.cu_q, w.s, a.rows_q, q0, lq);
+  seq_rows(a.cu_k, w.s, a.rows_k, k0, lk);
+  w.q0 = (int)q0;
+  w.lq = (int)lq;
+  w.k0 = (int)k0;
+  w.lk = (int)lk;
+  w.t0 = w.qb * tokens;
+  const int64_t rows = min64(lq, a.max_q);
   // keys of each tile: up to what its last token sees
   int n[kTiles], most = 0;
 #pragma unroll
   for (int i = 0; i < kTiles; ++i) {
-    const int64_t first = w.t0 + i * w.tq, last = min64(first + w.tq, lq) - 1;
-    const int64_t seen = first <= last ? min64(w.lk, last + w.lk - w.lq + 1) : 0;
+    const int64_t first = w.t0 + i * tq, last = min64(first + tq, rows) - 1;
+    const int64_t seen = first <= last ? min64(lk, last + lk - lq + 1) : 0;
     n[i] = seen > 0 ? (int)((seen + kTile - 1) / kTile) : 0;
     most = max(most, n[i]);
   }
@@ -165,22 +207,19 @@ __device__ __forceinline__ bool prompt_work(const PromptArgs& a, int nqb, Prompt
 }
 
 __global__ void __launch_bounds__(kPromptThreads, 1)
-    k_prompt_attend(const __grid_constant__ PromptArgs a, const __grid_constant__ PromptMaps maps, int nqb) {
+    k_prompt_attend(const __grid_constant__ PromptArgs a, const __grid_constant__ PromptMaps maps) {
   extern __shared__ uint8_t dyn[];
   __shared__ PromptShared sh;
-  pdl_wait();
-  pdl_trigger();
-  PromptWork w;
-  if (!prompt_work(a, nqb, w)) return;
   const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same for the warp, and known to be
-  const int jb = w.jb, e0 = w.end[0], e1 = w.end[1], e = max(e0, e1);
-  const uint32_t q_full = smem_u32(&sh.q_full), full = smem_u32(&sh.full[0]), empty = smem_u32(&sh.empty[0]);
-  const uint32_t s_full = smem_u32(&sh.s_full[0]), p_full = smem_u32(&sh.p_full[0]), o_full = smem_u32(&sh.o_full[0]);
+  const uint32_t q_full = smem_u32(&sh.q_full), q_empty = smem_u32(&sh.q_empty), full = smem_u32(&sh.full[0]), empty = smem_u32(&sh.empty[0]);
+  const uint32_t s_full = smem_u32(&sh.s_full[0]), p_full = smem_u32(&sh.p_full[0]), o_full = smem_u32(&sh.o_full[0]),
+                 o_empty = smem_u32(&sh.o_empty[0]), item_full = smem_u32(&sh.item_full[0]), item_empty = smem_u32(&sh.item_empty[0]);
   if (tid == 0) {
     sh.gave_up = 0;
     bar_init(q_full, 1);
+    bar_init(q_empty, 1);
     for (int i = 0; i < kStages; ++i) {
       bar_init(full + 8 * i, 1);
       bar_init(empty + 8 * i, 1);
@@ -190,6 +229,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       bar_init(p_full + 16 * i, kTile);
       bar_init(p_full + 16 * i + 8, kTile);
       bar_init(o_full + 8 * i, 1);
+      bar_init(o_empty + 8 * i, kTile);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      bar_init(item_full + 8 * i, 1);
+      bar_init(item_empty + 8 * i, 9);  // the issuing warp and eight softmax warps
     }
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -200,228 +244,301 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
   __syncthreads();
   tm_fence_after();
+  pdl_wait();
+  pdl_trigger();
   const uint32_t tmem = __shfl_sync(kFull, *(volatile uint32_t*)&sh.tmem, 0);
   volatile uint32_t* gave_up = &sh.gave_up;
   const uint32_t ring = base + kTiles * kTileBytes;
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kIssueRegs));
-  if (warp == 9) {
-    // ---- producer
-    if (lane == 0 && e > jb) {
-      const int qseq = a.cu_q ? 0 : w.s, kseq = a.cu_k ? 0 : w.s;
-      bar_expect(q_full, (uint32_t)(kTiles * 2 * w.tq * a.g * 128));
-      for (int i = 0; i < kTiles; ++i)
-        for (int h = 0; h < 2; ++h)
-          tma_load(base + i * kTileBytes + h * kHalfBytes, &maps.q, 64 * h, w.kvh * a.g, (int)(w.q0 + w.t0) + i * w.tq, qseq, q_full);
-      const int n = 2 * (e - jb);
-      int x = 0;
-      for (; x < n; ++x) {
-        const int st = x % kStages, turn = x / kStages;
-        if (turn > 0 && !bar_wait(empty + 8 * st, (turn - 1) & 1, gave_up)) break;
-        bar_expect(full + 8 * st, kTileBytes);
-        const CUtensorMap* m = (x & 1) ? &maps.v : &maps.k;
-        const int row = (int)w.k0 + (jb + (x >> 1)) * kTile;
-        for (int h = 0; h < 2; ++h) tma_load(ring + st * kTileBytes + h * kHalfBytes, m, 64 * h, row, w.kvh, kseq, full + 8 * st);
+    auto wait = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(kFull, bar_wait(bar, parity, gave_up)); };
+    if (warp == 9) {
+      // ---- producer: items, queries, keys and values
+      const int tq = kTile / a.g;
+      int nq = 0, x = 0;  // query loads, ring loads so far
+      bool ok = true;
+      for (int it = 0; ok; ++it) {
+        // items in turns of the grid, every other turn backwards: who had the
+        // longest of one turn has the shortest of the next
+        const int64_t at = (int64_t)it * gridDim.x + (it & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+        PromptItem w;
+        const bool more = prompt_item(a, at, w);
+        if (!more) w.s = -1;
+        if (it >= kItems) ok = wait(item_empty + 8 * (it % kItems), (it / kItems - 1) & 1);
+        if (!ok) break;
+        if (lane == 0) {
+          sh.items[it % kItems] = w;
+          bar_arrive(item_full + 8 * (it % kItems));
+        }
+        if (!more) break;
+        const int jb = w.jb, e = max(w.end[0], w.end[1]);
+        if (e == jb) continue;
+        if (nq > 0) ok = wait(q_empty, (nq - 1) & 1);
+        if (!ok) break;
+        const int qseq = a.cu_q ? 0 : w.s, kseq = a.cu_k ? 0 : w.s;
+        if (lane == 0) {
+          bar_expect(q_full, (uint32_t)(kTiles * 2 * tq * a.g * 128));
+          for (int i = 0; i < kTiles; ++i)
+            for (int h = 0; h < 2; ++h)
+              tma_load(base + i * kTileBytes + h * kHalfBytes, &maps.q, 64 * h, w.kvh * a.g, w.q0 + w.t0 + i * tq, qseq, q_full);
+        }
+        ++nq;
+        for (int j = 0; ok && j < 2 * (e - jb); ++j) {
+          const int st = x % kStages, turn = x / kStages;
+          if (turn > 0) ok = wait(empty + 8 * st, (turn - 1) & 1);
+          if (!ok) break;
+          if (lane == 0) {
+            bar_expect(full + 8 * st, kTileBytes);
+            const CUtensorMap* m = (j & 1) ? &maps.v : &maps.k;
+            const int row = w.k0 + (jb + (j >> 1)) * kTile;
+            for (int h = 0; h < 2; ++h) tma_load(ring + st * kTileBytes + h * kHalfBytes, m, 64 * h, row, w.kvh, kseq, full + 8 * st);
+          }
+          ++x;
+        }
       }
-      if (x < n) {  // given up: what was issued lands before the block ends
+      if (!ok && lane == 0) {  // given up: what was issued lands before the block ends
         const uint64_t t0 = now_ns();
-        while (!bar_try(q_full, 0) && now_ns() - t0 < kWaitNs) {}
+        while (nq > 0 && !bar_try(q_full, (nq - 1) & 1) && now_ns() - t0 < kWaitNs) {}
         for (int y = max(0, x - kStages); y < x; ++y)
           while (!bar_try(full + 8 * (y % kStages), (y / kStages) & 1) && now_ns() - t0 < kWaitNs) {}
       }
-    }
-  } else if (warp == 8) {
-    // ---- products (the whole warp walks; one lane issues)
-    auto wait = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(kFull, bar_wait(bar, parity, gave_up)); };
-    bool ok = e > jb && wait(q_full, 0);
-    auto scores = [&](int i, int x) {  // S_i = Q_i K^T with the key tile in stage x
-      const uint32_t qa = base + i * kTileBytes, kb = ring + (x % kStages) * kTileBytes;
-      const uint64_t qd = smem_desc(qa, 16, 1024), kd = smem_desc(kb, 16, 1024);
+    } else if (warp == 8) {
+      // ---- products (the whole warp walks; one lane issues)
+      bool ok = true;
+      int nq = 0, x = 0;              // items with keys, ring stages so far
+      int ns[kTiles] = {0, 0};        // steps of each tile so far
+      int no[kTiles] = {0, 0};        // results of each tile so far
+      auto scores = [&](int i, int xs) {  // S_i = Q_i K^T with the key tile in stage xs
+        const uint32_t qa = base + i * kTileBytes, kb = ring + (xs % kStages) * kTileBytes;
+        const uint64_t qd = smem_desc(qa, 16, 1024), kd = smem_desc(kb, 16, 1024);
 #pragma unroll
-      for (int c = 0; c < kDim / 16; ++c) {
-        const uint32_t off = (c >> 2) * (kHalfBytes >> 4) + (c & 3) * 2;
-        mma_ss(tmem + i * kTile, qd + off, kd + off, mma_instr(kTile), c > 0);
-      }
-      mma_commit(s_full + 8 * i);
-    };
-    const int ends[kTiles] = {e0, e1};
-    if (ok) ok = wait(full, 0);
-    if (ok && elect()) {
-      tm_fence_after();
-      for (int i = 0; i < kTiles; ++i)
-        if (jb < ends[i]) scores(i, 0);
-      mma_commit(empty);
-    }
-    __syncwarp();
-    const int tail = (int)(w.lk % kTile);  // keys of the sequence's last, unfilled block
-    for (int j = jb; ok && j < e; ++j) {
-      const int xv = 2 * (j - jb) + 1, xk = xv + 1;
-      ok = wait(full + 8 * (xv % kStages), (xv / kStages) & 1);
-      if (ok && j + 1 < e) ok = wait(full + 8 * (xk % kStages), (xk / kStages) & 1);
-      if (!ok) break;
-      const uint32_t vb = ring + (xv % kStages) * kTileBytes;
-      if (tail && j == (int)(w.lk / kTile)) {
-        // value rows past the sequence's end: anything times weight 0 is 0
-        for (int x = tail * 8 + lane; x < kTile * 8; x += 32)
-          for (int h = 0; h < 2; ++h)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(vb + h * kHalfBytes + x * 16), "r"(0) : "memory");
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-        __syncwarp();
-      }
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        // 16 keys a product: 8 columns of weights, 16 rows of V
-        const uint64_t vd = smem_desc(vb, kHalfBytes, 1024);
-        auto values = [&](int c) { mma_ts(tmem + (2 + i) * kTile, tmem + i * kTile + 8 * c, vd + c * 128, mma_instr(kTile) | kMmaBN, j > jb || c > 0); };
-        if (ok && j < ends[i]) ok = wait(p_full + 16 * i, (j - jb) & 1);
-        if (ok && j < ends[i] && elect()) {
+        for (int c = 0; c < kDim / 16; ++c) {
+          const uint32_t off = (c >> 2) * (kHalfBytes >> 4) + (c & 3) * 2;
+          mma_ss(tmem + i * kTile, qd + off, kd + off, mma_instr(kTile), c > 0);
+        }
+        mma_commit(s_full + 8 * i);
+      };
+      for (int it = 0; ok; ++it) {
+        ok = wait(item_full + 8 * (it % kItems), (it / kItems) & 1);
+        if (!ok) break;
+        const volatile PromptItem& w = sh.items[it % kItems];
+        if (__shfl_sync(kFull, w.s, 0) < 0) break;
+        const int jb = __shfl_sync(kFull, w.jb, 0), lk = __shfl_sync(kFull, w.lk, 0);  // every lane has read it
+        const int ends[kTiles] = {__shfl_sync(kFull, w.end[0], 0), __shfl_sync(kFull, w.end[1], 0)};
+        const int e = max(ends[0], ends[1]);
+        if (lane == 0) bar_arrive(item_empty + 8 * (it % kItems));
+        if (e == jb) continue;
+        ok = wait(q_full, nq & 1);
+        ++nq;
+        if (ok) ok = wait(full + 8 * (x % kStages), (x / kStages) & 1);
+        if (ok && elect()) {
           tm_fence_after();
-#pragma unroll
-          for (int c = 0; c < 6; ++c) values(c);
+          for (int i = 0; i < kTiles; ++i)
+            if (jb < ends[i]) scores(i, x);
+          mma_commit(empty + 8 * (x % kStages));
+          if (e == jb + 1) mma_commit(q_empty);
         }
         __syncwarp();
-        if (ok && j < ends[i]) ok = wait(p_full + 16 * i + 8, (j - jb) & 1);
-        if (ok && j < ends[i] && elect()) {
-          tm_fence_after();
-          values(6);
-          values(7);
-          if (j + 1 == ends[i]) mma_commit(o_full + 8 * i);
-          if (j + 1 < ends[i]) scores(i, xk);
+        const int tail = lk % kTile;  // keys of the sequence's last, unfilled block
+        for (int j = jb; ok && j < e; ++j) {
+          const int xv = x + 1, xk = x + 2;
+          ok = wait(full + 8 * (xv % kStages), (xv / kStages) & 1);
+          if (ok && j + 1 < e) ok = wait(full + 8 * (xk % kStages), (xk / kStages) & 1);
+          if (!ok) break;
+          const uint32_t vb = ring + (xv % kStages) * kTileBytes;
+          if (tail && j == lk / kTile) {
+            // value rows past the sequence's end: anything times weight 0 is 0
+            for (int y = tail * 8 + lane; y < kTile * 8; y += 32)
+              for (int h = 0; h < 2; ++h)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(vb + h * kHalfBytes + y * 16), "r"(0) : "memory");
+            asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+            __syncwarp();
+          }
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i) {
+            const bool mine = j < ends[i];
+            // 16 keys a product: 8 columns of weights, 16 rows of V
+            const uint64_t vd = smem_desc(vb, kHalfBytes, 1024);
+            auto values = [&](int c) {
+              mma_ts(tmem + (2 + i) * kTile, tmem + i * kTile + 8 * c, vd + c * 128, mma_instr(kTile) | kMmaBN, j > jb || c > 0);
+            };
+            // the last result has been read before the first product replaces it
+            if (ok && mine && j == jb && no[i] > 0) ok = wait(o_empty + 8 * i, (no[i] - 1) & 1);
+            if (ok && mine) ok = wait(p_full + 16 * i, ns[i] & 1);
+            if (ok && mine && elect()) {
+              tm_fence_after();
+#pragma unroll
+              for (int c = 0; c < 6; ++c) values(c);
+            }
+            __syncwarp();
+            if (ok && mine) ok = wait(p_full + 16 * i + 8, ns[i] & 1);
+            if (ok && mine && elect()) {
+              tm_fence_after();
+              values(6);
+              values(7);
+              if (j + 1 == ends[i]) mma_commit(o_full + 8 * i);
+              if (j + 1 < ends[i]) scores(i, xk);
+            }
+            __syncwarp();
+            if (mine) ++ns[i];
+            if (mine && j + 1 == ends[i]) ++no[i];
+          }
+          if (ok && elect()) {
+            mma_commit(empty + 8 * (xv % kStages));
+            if (j + 1 < e) mma_commit(empty + 8 * (xk % kStages));
+            if (j + 2 == e) mma_commit(q_empty);  // the item's last scores
+          }
+          __syncwarp();
+          x += 2;
         }
-        __syncwarp();
       }
-      if (ok && elect()) {
-        mma_commit(empty + 8 * (xv % kStages));
-        if (j + 1 < e) mma_commit(empty + 8 * (xk % kStages));
-      }
-      __syncwarp();
+      // the last products and their signals have arrived before the block ends
+      if (ok && x > 0) wait(empty + 8 * ((x - 1) % kStages), ((x - 1) / kStages) & 1);
     }
-  }
   } else {
     // ---- softmax of tile i, a row per thread
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
     const int i = warp >> 2, row = tid & (kTile - 1);
-    const int end = i ? e1 : e0;
-    const int64_t tok = w.t0 + (int64_t)i * w.tq + row / a.g;
-    const int64_t lq = min64(w.lq, a.max_q);
-    const bool live = row < w.tq * a.g && tok < lq;
-    const int h = w.kvh * a.g + row % a.g;
-    // the last key the row sees; rows that are not there see what the first does
-    const int64_t first_tok = w.t0 + (int64_t)i * w.tq;
-    const int64_t last_key = min64(w.lk, (live ? tok : first_tok) + w.lk - w.lq + 1) - 1;
-    const int64_t tile_key = min64(w.lk, first_tok + w.lk - w.lq + 1) - 1;  // every row of the tile sees this far
+    const int tq = kTile / a.g;
+    const int row_tok = row / a.g, row_head = row % a.g;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + i * kTile, to = tmem + lanes + (2 + i) * kTile;
-    float m = -INFINITY, l = 0.f;  // base 2
     bool ok = true;
-    for (int j = jb; j < end; ++j) {
-      ok = bar_wait(s_full + 8 * i, (j - jb) & 1, gave_up);
+    uint32_t ns = 0, no = 0;  // steps and results of the tile so far
+    for (int it = 0; ok; ++it) {
+      ok = __all_sync(kFull, bar_wait(item_full + 8 * (it % kItems), (it / kItems) & 1, gave_up));
+      if (!ok) break;
+      const volatile PromptItem& w = sh.items[it % kItems];
+      const int ws = __shfl_sync(kFull, w.s, 0);
+      if (ws < 0) break;
+      const int jb = __shfl_sync(kFull, w.jb, 0), end = __shfl_sync(kFull, w.end[i], 0);
+      const int lq = w.lq, lk = w.lk, q0 = w.q0;
+      const int first_tok = w.t0 + i * tq, tok = first_tok + row_tok;
+      const bool live = row < tq * a.g && tok < (int)min64(lq, a.max_q);
+      const int h = w.kvh * a.g + row_head;
+      // the last key the row sees; rows that are not there see what the first does
+      const int last_key = min(lk, (live ? tok : first_tok) + lk - lq + 1) - 1;
+      const int tile_key = min(lk, first_tok + lk - lq + 1) - 1;  // every row of the tile sees this far
+      float* part = nullptr;
+      if (a.nsplit > 1) {
+        const int64_t nqb = (a.max_q + kTiles * tq - 1) / (kTiles * tq);
+        part = a.ws + (((((int64_t)ws * a.hkv + w.kvh) * nqb + w.qb) * a.nsplit + w.split) * (kTiles * kTile) + i * kTile + row) * kPartRow;
+      }
+      const int k0 = w.k0;
+      __syncwarp();
+      if (lane == 0) bar_arrive(item_empty + 8 * (it % kItems));
+      float m = -INFINITY, l = 0.f;  // base 2
+      for (int j = jb; j < end; ++j) {
+        ok = __all_sync(kFull, bar_wait(s_full + 8 * i, ns & 1, gave_up));
+        if (!ok) break;
+        ++ns;
+        tm_fence_after();
+        uint32_t s[kTile];
+        tm_ld32(s, 0, ts);
+        tm_ld32(s, 32, ts + 32);
+        tm_ld32(s, 64, ts + 64);
+        tm_ld32(s, 96, ts + 96);
+        tm_wait_ld();
+        if ((j + 1) * kTile - 1 > tile_key) {
+          const int left = last_key - j * kTile;  // last visible column
+#pragma unroll
+          for (int c = 0; c < kTile; ++c)
+            if (c > left) s[c] = 0xff800000u;  // -inf
+        }
+        // The first weights are taken with the maximum so far while the block's
+        // own is found; only a row that grew past kGrowth does them again.
+        const uint64_t c2 = pair2(kScaleLog2, kScaleLog2);
+        uint64_t sum0 = 0, sum1 = 0;
+        auto four = [&](int c, uint64_t n2, uint32_t& lo, uint32_t& hi) {
+          float x0, x1, x2, x3;
+          unpair2(fma2(pair2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), c2, n2), x0, x1);
+          unpair2(fma2(pair2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), c2, n2), x2, x3);
+          x0 = ex2(x0);
+          x1 = ex2(x1);
+          x2 = ex2(x2);
+          x3 = ex2(x3);
+          sum0 = add2(sum0, pair2(x0, x1));
+          sum1 = add2(sum1, pair2(x2, x3));
+          lo = pack_bf16x2(x0, x1);
+          hi = pack_bf16x2(x2, x3);
+        };
+        uint32_t first[16];
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float neg = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          four(c, pair2(neg, neg), first[c / 2], first[c / 2 + 1]);
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            mx[u & 3] = fmaxf(mx[u & 3], fmaxf(__uint_as_float(s[4 * c + 2 * u]), __uint_as_float(s[4 * c + 2 * u + 1])));
+        }
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kScaleLog2;
+        const bool grew = mt > m + kGrowth;
+        if (__any_sync(kFull, grew)) {
+          const float f = grew ? ex2(m - mt) : 1.f;
+          if (j > jb) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tm_ld32(o, 0, to + 32 * c);
+              tm_wait_ld();
+#pragma unroll
+              for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+              tm_st32(to + 32 * c, o, 0);
+            }
+          }
+          l *= f;
+          if (grew) m = mt;
+          neg = m == -INFINITY ? 0.f : -m;
+          sum0 = sum1 = 0;
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) four(c, pair2(neg, neg), first[c / 2], first[c / 2 + 1]);
+        }
+        const uint64_t n2 = pair2(neg, neg);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) s[c] = first[c];
+#pragma unroll
+        for (int c = 32; c < 64; c += 4) four(c, n2, s[c / 2], s[c / 2 + 1]);
+        tm_st32(ts, s, 0);
+#pragma unroll
+        for (int c = 64; c < 96; c += 4) four(c, n2, s[c / 2], s[c / 2 + 1]);
+        tm_st16(ts + 32, s, 32);
+        tm_wait_st();
+        tm_fence_before();
+        bar_arrive(p_full + 16 * i);  // the products may start on 96 keys
+#pragma unroll
+        for (int c = 96; c < 128; c += 4) four(c, n2, s[c / 2], s[c / 2 + 1]);
+        tm_st16(ts + 48, s, 48);
+        tm_wait_st();
+        tm_fence_before();
+        bar_arrive(p_full + 16 * i + 8);
+        float a0, a1;
+        unpair2(add2(sum0, sum1), a0, a1);
+        l += a0 + a1;
+      }
+      // ---- result
+      const bool any = end > jb;
+      if (any && ok) ok = bar_wait(o_full + 8 * i, no & 1, gave_up);
       ok = __all_sync(kFull, ok);
       if (!ok) break;
-      tm_fence_after();
-      uint32_t s[kTile];
-      tm_ld32(s, 0, ts);
-      tm_ld32(s, 32, ts + 32);
-      tm_ld32(s, 64, ts + 64);
-      tm_ld32(s, 96, ts + 96);
-      tm_wait_ld();
-      if ((int64_t)(j + 1) * kTile - 1 > tile_key) {
-        const int left = (int)max64(-1, min64(kTile, last_key - (int64_t)j * kTile));  // last visible column
-#pragma unroll
-        for (int c = 0; c < kTile; ++c)
-          if (c > left) s[c] = 0xff800000u;  // -inf
+      if (any) {
+        ++no;
+        tm_fence_after();
       }
-      // The first weights are taken with the maximum so far while the block's
-      // own is found; only a row that grew past kGrowth does them again.
-      const uint64_t c2 = pair2(kScaleLog2, kScaleLog2);
-      uint64_t sum0 = 0, sum1 = 0;
-      auto four = [&](int c, uint64_t n2, uint32_t& lo, uint32_t& hi) {
-        float x0, x1, x2, x3;
-        unpair2(fma2(pair2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), c2, n2), x0, x1);
-        unpair2(fma2(pair2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), c2, n2), x2, x3);
-        x0 = ex2(x0);
-        x1 = ex2(x1);
-        x2 = ex2(x2);
-        x3 = ex2(x3);
-        sum0 = add2(sum0, pair2(x0, x1));
-        sum1 = add2(sum1, pair2(x2, x3));
-        lo = pack_bf16x2(x0, x1);
-        hi = pack_bf16x2(x2, x3);
-      };
-      uint32_t first[16];
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      float neg = m == -INFINITY ? 0.f : -m;
-#pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        four(c, pair2(neg, neg), first[c / 2], first[c / 2 + 1]);
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          mx[u & 3] = fmaxf(mx[u & 3], fmaxf(__uint_as_float(s[4 * c + 2 * u]), __uint_as_float(s[4 * c + 2 * u + 1])));
-      }
-      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kScaleLog2;
-      const bool grew = mt > m + kGrowth;
-      if (__any_sync(kFull, grew)) {
-        const float f = grew ? ex2(m - mt) : 1.f;
-        if (j > jb) {
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tm_ld32(o, 0, to + 32 * c);
-            tm_wait_ld();
-#pragma unroll
-            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
-            tm_st32(to + 32 * c, o, 0);
-          }
-        }
-        l *= f;
-        if (grew) m = mt;
-        neg = m == -INFINITY ? 0.f : -m;
-        sum0 = sum1 = 0;
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) four(c, pair2(neg, neg), first[c / 2], first[c / 2 + 1]);
-      }
-      const uint64_t n2 = pair2(neg, neg);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) s[c] = first[c];
-#pragma unroll
-      for (int c = 32; c < 64; c += 4) four(c, n2, s[c / 2], s[c / 2 + 1]);
-      tm_st32(ts, s, 0);
-#pragma unroll
-      for (int c = 64; c < 96; c += 4) four(c, n2, s[c / 2], s[c / 2 + 1]);
-      tm_st16(ts + 32, s, 32);
-      tm_wait_st();
-      tm_fence_before();
-      bar_arrive(p_full + 16 * i);  // the products may start on 96 keys
-#pragma unroll
-      for (int c = 96; c < 128; c += 4) four(c, n2, s[c / 2], s[c / 2 + 1]);
-      tm_st16(ts + 48, s, 48);
-      tm_wait_st();
-      tm_fence_before();
-      bar_arrive(p_full + 16 * i + 8);
-      float a0, a1;
-      unpair2(add2(sum0, sum1), a0, a1);
-      l += a0 + a1;
-    }
-    // ---- result
-    float* part = a.nsplit > 1
-        ? a.ws + ((((int64_t)w.s * a.hkv + w.kvh) * nqb + w.qb) * a.nsplit + w.split) * (kTiles * kTile) * kPartRow +
-              ((int64_t)i * kTile + row) * kPartRow
-        : nullptr;
-    const bool any = end > jb;
-    if (any && ok) ok = bar_wait(o_full + 8 * i, 0, gave_up);
-    ok = __all_sync(kFull, ok);
-    if (ok) {
-      if (any) tm_fence_after();
       const float inv = l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing: 0
       bool finite = true;
-      __nv_bfloat16* out = live ? a.out + (a.cu_q ? 0 : w.s * a.so.seq) + (w.q0 + tok) * a.so.token + h * a.so.head : nullptr;
+      __nv_bfloat16* out = live ? a.out + (a.cu_q ? 0 : ws * a.so.seq) + (int64_t)(q0 + tok) * a.so.token + h * a.so.head : nullptr;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
         if (any) {
           tm_ld32(o, 0, to + 32 * c);
           tm_wait_ld();
+          if (c == 3) {  // the next item's products may replace it
+            tm_fence_before();
+            bar_arrive(o_empty + 8 * i);
+          }
         } else {
 #pragma unroll
           for (int u = 0; u < 32; ++u) o[u] = 0;
@@ -452,13 +569,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
       } else {
         if (live && a.lse != nullptr)
-          a.lse[((int64_t)(a.cu_q ? 0 : w.s) * a.hq + h) * a.rows_q + w.q0 + tok] = last_key >= 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
-        // the tile's queries have been used: their place is the scratch
-        float* qs = reinterpret_cast<float*>(dyn + (base - smem_u32(dyn)) + i * kTileBytes) + (warp & 3) * kDim;
+          a.lse[((int64_t)(a.cu_q ? 0 : ws) * a.hq + h) * a.rows_q + q0 + tok] = last_key >= 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
         for (uint32_t again = __ballot_sync(kFull, live && !finite); again; again &= again - 1) {
           const int src = __ffs(again) - 1;
-          const int64_t t = __shfl_sync(kFull, tok, src);
-          prompt_row(a, w.s, __shfl_sync(kFull, h, src), w.q0, t, w.k0, min64(w.lk, t + w.lk - w.lq + 1), qs);
+          const int t = __shfl_sync(kFull, tok, src);
+          prompt_row(a, ws, __shfl_sync(kFull, h, src), q0, t, k0, min(lk, t + lk - lq + 1));
         }
       }
     }
@@ -473,7 +588,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
 // A warp per query row: join the splits' partials.
 __global__ void __launch_bounds__(32 * kRowWarps) k_prompt_join(PromptArgs a, int nqb) {
-  __shared__ float qs[kRowWarps][kDim];
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -512,7 +626,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_prompt_join(PromptArgs a, in
   }
   const int64_t visible = max64(0, min64(lk, tok + lk - lq + 1));
   if (!__all_sync(kFull, finite)) {
-    prompt_row(a, s, h, q0, tok, k0, visible, qs[warp]);
+    prompt_row(a, s, h, q0, tok, k0, visible);
     return;
   }
   __nv_bfloat16* out = a.out + (a.cu_q ? 0 : s * a.so.seq) + (q0 + tok) * a.so.token + h * a.so.head;
@@ -553,7 +667,7 @@ size_t prompt_workspace_bytes(PromptArgs& a, int sm_count) {
   return a.nsplit > 1 ? (size_t)units * a.nsplit * kTiles * kTile * kPartRow * sizeof(float) : 0;
 }
 
-cudaError_t launch_prompt_attend(const PromptArgs& a, cudaStream_t st) {
+cudaError_t launch_prompt_attend(const PromptArgs& a, int sm_count, cudaStream_t st) {
   PromptMaps m;
   const int64_t ns = a.cu_q ? 1 : a.n_seqs;
   const int tq = kTile / a.g;
@@ -567,9 +681,11 @@ cudaError_t launch_prompt_attend(const PromptArgs& a, cudaStream_t st) {
     return cudaErrorInvalidValue;
   cudaError_t e = raise_smem();
   if (e != cudaSuccess) return e;
-  const int64_t nqb = prompt_blocks(a), blocks = nqb * a.n_seqs * a.hkv * a.nsplit;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  e = launch_pdl(k_prompt_attend, dim3((unsigned)blocks), dim3(kPromptThreads), kPromptSmem, st, a, m, (int)nqb);
+  // a block per SM walks the items; no more blocks than there can be items
+  const int64_t nqb = prompt_blocks(a), tokens = kTiles * (kTile / a.g);
+  const int64_t pairs = a.cu_q ? std::min(nqb * a.n_seqs, a.rows_q / tokens + a.n_seqs) : nqb * a.n_seqs;
+  const int64_t blocks = std::min<int64_t>(sm_count, pairs * a.hkv * a.nsplit);
+  e = launch_pdl(k_prompt_attend, dim3((unsigned)blocks), dim3(kPromptThreads), kPromptSmem, st, a, m);
   if (e != cudaSuccess || a.nsplit == 1) return e;
   const dim3 grid((unsigned)((a.max_q + kRowWarps - 1) / kRowWarps), a.hq, a.n_seqs);
   return launch_pdl(k_prompt_join, grid, dim3(32 * kRowWarps), 0, st, a, (int)nqb);

@@ -88,7 +88,7 @@ struct PromptArgs {
   float* ws;   // split partials
   int nsplit;
 };
-cudaError_t launch_prompt_attend(const PromptArgs& a, cudaStream_t st);
+cudaError_t launch_prompt_attend(const PromptArgs& a, int sm_count, cudaStream_t st);
 size_t prompt_workspace_bytes(PromptArgs& a, int sm_count);  // sets a.nsplit
 
 // Whether a wait of the kernels gave up (read and cleared).

@@ -158,7 +158,7 @@ paris_status paris_prompt_attend(const paris_prompt* p, const void* q, const voi
   a.out = static_cast<__nv_bfloat16*>(out_bf16);
   a.lse = lse;
   a.ws = static_cast<float*>(workspace);
-  return launched(launch_prompt_attend(a, static_cast<cudaStream_t>(stream)), "paris_prompt_attend");
+  return launched(launch_prompt_attend(a, sm_count(), static_cast<cudaStream_t>(stream)), "paris_prompt_attend");
 }
 
 paris_status paris_prompt_check(void) {
