@@ -228,28 +228,54 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
   int row0 = warp * kRows4;
   Next4 ahead{a.c.kc + (base + row0) * kCode4 + 16 * lane, a.c.vc + (base + row0) * kCode4 + 16 * lane,
               a.c.ks + (base + row0 + lane) * kScale4, a.c.vs + (base + row0 + lane) * kScale4};
-#pragma unroll
-  for (int i = 0; i < kDepth4 - 1; ++i) {
+  auto start_copy = [&](int i) {
     if (row0 + i * kTile4 < n) copy_step(ring_u32 + i * (int)sizeof(Step4), ahead, n - row0 - i * kTile4, lane);
     asm volatile("cp.async.commit_group;\n" ::: "memory");
-  }
+  };
 
   // The query of column g's head as two half parts, scaled by a power of two
   // to at most 1 (its scores are scaled back, with log2(e) / sqrt(d)); each
-  // warp makes two of the eight steps' fragments.
+  // warp makes two of the eight steps' fragments.  Its loads go out first,
+  // then the first step's; the further ones, which the memory takes a while to
+  // deliver to all blocks at once, do not hold up the query's.
   {
     const int h = NT == 1 ? g & 3 : g;
-    float amax = 0.f;
     const int64_t qe = ((int64_t)b * a.hq + qh0 + h) * kDim + 32 * t;
-    float x[8];
+    uint4 raw[8];
+    if (a.dtype == 1) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float y[4] = {0.f, 0.f, 0.f, 0.f};
-      if (h < nh) load4(a.q, a.dtype, qe + 4 * i, y);
+      for (int i = 0; i < 4; ++i)
+        raw[i] = h < nh ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + qe) + i) : make_uint4(0, 0, 0, 0);
+    } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        amax = fmaxf(amax, fabsf(y[j]));
-        if (i >> 1 == warp) x[4 * (i & 1) + j] = y[j];
+      for (int i = 0; i < 8; ++i)
+        raw[i] = h < nh ? __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + qe) + i) : make_uint4(0, 0, 0, 0);
+    }
+    start_copy(0);
+    float x[8], amax = 0.f;
+    if (a.dtype == 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float lo = bf16_bits_to_float(w[j] & 0xffffu), hi = __uint_as_float(w[j] & 0xffff0000u);
+          amax = fmaxf(amax, fmaxf(fabsf(lo), fabsf(hi)));
+          if (i == warp) {
+            x[2 * j] = lo;
+            x[2 * j + 1] = hi;
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          amax = fmaxf(amax, fabsf(__uint_as_float(w[j])));
+          if (i >> 1 == warp) x[4 * (i & 1) + j] = __uint_as_float(w[j]);
+        }
       }
     }
     amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
@@ -278,6 +304,8 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
       if (NT == 2) sh.q[2 * warp + s][1][lane] = make_uint2(lo[0], lo[1]);
     }
   }
+#pragma unroll
+  for (int i = 1; i < kDepth4 - 1; ++i) start_copy(i);
   __syncthreads();
   uint2 qf[8][NT];
 #pragma unroll
