@@ -5,6 +5,8 @@
 // come out the same in any precision that holds the inputs: S has 4 bits and
 // (c + 1/2) S at most 8, so which code a value gets is decided by an exact
 // comparison except within float32's last bit.
+#include <cuda_fp16.h>
+
 #include "kv4_internal.cuh"
 
 namespace paris {
@@ -131,7 +133,7 @@ __device__ __forceinline__ uint2 quantise(RowBf16& r, uint32_t& byte) {
 // read of k and v: the arithmetic (35 operations of a warp a row) stays below
 // the memory's time.
 template <typename Row>
-__global__ void __launch_bounds__(kStoreThreads) k_kv4_store(StoreArgs a, int nblk, int tokens, uint32_t hkv_inv) {
+__global__ void __launch_bounds__(kStoreThreads, 5) k_kv4_store(StoreArgs a, int nblk, int tokens, uint32_t hkv_inv) {
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.x / nblk, blk = blockIdx.x - b * nblk;
@@ -187,38 +189,47 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv4_store(StoreArgs a, int nb
   }
 }
 
-// Eight values of a code word as bf16: c S has at most 7 significant bits.
-__device__ __forceinline__ uint4 word_values(uint32_t w, float S) {
+// Eight values of a code word as bf16, c S having at most 7 significant bits.
+// A byte's two nibbles go into the mantissas of two halves 64 (64 + u / 16 and
+// 64 + u), which a subtraction and a product with 16 S and S make exact.
+__device__ __forceinline__ uint4 word_values(uint32_t w, uint32_t byte) {
+  const __half S = __ushort_as_half((unsigned short)(byte << 7));
+  const __half2 scale = __halves2half2(__hmul(S, __float2half(16.f)), S), off = __floats2half2_rn(64.5f, 72.f);
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float lo = (float)((int)((w >> (8 * i)) & 15u) - 8) * S;
-    const float hi = (float)((int)((w >> (8 * i + 4)) & 15u) - 8) * S;
-    o[i] = pack_bf16x2(lo, hi);
+    const uint32_t x = (__byte_perm(w, 0, 0x4040 | i | i << 8) & 0x00F0000Fu) | 0x54005400u;
+    const float2 f = __half22float2(__hmul2(__hsub2(*reinterpret_cast<const __half2*>(&x), off), scale));
+    o[i] = pack_bf16x2(f.x, f.y);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-__device__ __forceinline__ float scale_value(uint32_t byte) {
-  return __half2float(__ushort_as_half((unsigned short)(byte << 7)));
-}
-
-// 16 threads per row, 8 channels each; row index over [batch * Hkv][rows].
-__global__ void __launch_bounds__(256) k_kv4_read(Kv4 c, __nv_bfloat16* k_out, __nv_bfloat16* v_out, int64_t rows,
-                                                  int64_t total) {
+// 16 threads per row, 8 channels each, four rows at a time; blocks (rows,
+// sequence x KV head).  Bound by the write of the values.
+constexpr int kReadRows = 64;
+__global__ void __launch_bounds__(256) k_kv4_read(Kv4 c, __nv_bfloat16* k_out, __nv_bfloat16* v_out, int64_t rows) {
   pdl_wait();
   pdl_trigger();
   const int l16 = threadIdx.x & 15;
-  const int64_t step = (int64_t)gridDim.x * (blockDim.x / 16);
-  for (int64_t r = (int64_t)blockIdx.x * (blockDim.x / 16) + (threadIdx.x >> 4); r < total; r += step) {
-    const int64_t bh = r / rows, i = r - bh * rows;
-    if (i >= kv4_len(c, (int)(bh / c.hkv))) continue;
-    const int64_t src = bh * c.rmax + i;
-    const uint32_t kw = *reinterpret_cast<const uint32_t*>(c.kc + src * kCode4 + 4 * l16);
-    const uint32_t vw = *reinterpret_cast<const uint32_t*>(c.vc + src * kCode4 + 4 * l16);
-    const float sk = scale_value(c.ks[src * kScale4 + (l16 >> 2)]), sv = scale_value(c.vs[src * kScale4 + (l16 >> 2)]);
-    __stcs(reinterpret_cast<uint4*>(k_out + r * kDim + 8 * l16), word_values(kw, sk));
-    __stcs(reinterpret_cast<uint4*>(v_out + r * kDim + 8 * l16), word_values(vw, sv));
+  const int64_t bh = blockIdx.y, i0 = (int64_t)blockIdx.x * kReadRows + (threadIdx.x >> 4);
+  const int64_t n = min64(rows, kv4_len(c, (int)(bh / c.hkv)));
+  uint32_t kw[4], vw[4], ks[4], vs[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int64_t i = i0 + 16 * u, src = bh * c.rmax + i;
+    if (i >= n) continue;
+    kw[u] = *reinterpret_cast<const uint32_t*>(c.kc + src * kCode4 + 4 * l16);
+    vw[u] = *reinterpret_cast<const uint32_t*>(c.vc + src * kCode4 + 4 * l16);
+    ks[u] = c.ks[src * kScale4 + (l16 >> 2)];
+    vs[u] = c.vs[src * kScale4 + (l16 >> 2)];
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int64_t i = i0 + 16 * u, dst = (bh * rows + i) * kDim + 8 * l16;
+    if (i >= n) continue;
+    __stcs(reinterpret_cast<uint4*>(k_out + dst), word_values(kw[u], ks[u]));
+    __stcs(reinterpret_cast<uint4*>(v_out + dst), word_values(vw[u], vs[u]));
   }
 }
 
@@ -238,9 +249,8 @@ cudaError_t launch_kv4_store(const StoreArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_kv4_read(const Kv4& c, __nv_bfloat16* k_out, __nv_bfloat16* v_out, int64_t rows, cudaStream_t st) {
-  const int64_t total = (int64_t)c.batch * c.hkv * rows;
-  const int64_t blocks = min64((total + 15) / 16, 152 * 16);
-  return launch_pdl(k_kv4_read, dim3((unsigned)max64(1, blocks)), dim3(256), 0, st, c, k_out, v_out, rows, total);
+  const dim3 grid((unsigned)((rows + kReadRows - 1) / kReadRows), c.batch * c.hkv);
+  return launch_pdl(k_kv4_read, grid, dim3(256), 0, st, c, k_out, v_out, rows);
 }
 
 }  // namespace paris

@@ -30,8 +30,7 @@ namespace cg = cooperative_groups;
 namespace paris {
 namespace {
 
-constexpr int kEvictThreads = 1024;
-constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kMaxWarps = 32;
 constexpr int kEvictMaxBlocks = 8;
 constexpr int kBins = 2048;
 constexpr int kHeldRows = 16384;  // rows of a block whose keys are in shared memory; further ones are read again
@@ -39,7 +38,7 @@ constexpr int kMoves = 8;      // rows that a warp moves at once
 
 struct EvictShared {
   uint32_t hist[3][kBins];
-  uint32_t warp_a[kEvictWarps], warp_b[kEvictWarps];
+  uint32_t warp_a[kMaxWarps], warp_b[kMaxWarps];
   uint32_t few[32];
   uint32_t nfew;
   uint32_t lo, hi, held;        // this block's least and greatest key, its protected rows
@@ -55,8 +54,10 @@ __device__ __forceinline__ uint32_t evict_key(float w, int32_t pos, int64_t sink
   return w == w ? order_key(w) : 0u;
 }
 
-template <bool kCluster>
-__global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(EvictArgs a) {
+template <bool kCluster, int kThreads>
+__global__ void __launch_bounds__(kThreads) k_kv4_evict(EvictArgs a) {
+  constexpr int kWarps = kThreads / 32;
+  constexpr int kBinsPer = kBins / kThreads < 4 ? 4 : kBins / kThreads;  // bins of a thread
   extern __shared__ uint32_t keys[];
   __shared__ __align__(16) EvictShared sh;
   cg::cluster_group cluster = cg::this_cluster();
@@ -66,11 +67,12 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(EvictArgs a) {
   };
   const int nb = kCluster ? (int)cluster.num_blocks() : 1, rank = kCluster ? (int)cluster.block_rank() : 0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < 3 * kBins; i += kEvictThreads) (&sh.hist[0][0])[i] = 0;
+  for (int i = tid; i < 3 * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
   if (tid == 0) {
     sh.lo = 0xFFFFFFFFu;
     sh.hi = sh.held = sh.nfew = 0;
   }
+  if (tid < kMaxWarps) sh.warp_a[tid] = sh.warp_b[tid] = 0;  // what warps that are not there count
   pdl_wait();
   pdl_trigger();
   const int bh = blockIdx.x / nb;
@@ -85,11 +87,11 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(EvictArgs a) {
     const float* w = a.c.w + base;
     const int32_t* pos = a.c.pos + base;
     // the warp's rows: 32 x [0, mine) from first on
-    const int mine = (int)(((uint32_t)(r1 - r0) + kEvictThreads - 1) / kEvictThreads);
+    const int mine = (int)(((uint32_t)(r1 - r0) + kThreads - 1) / kThreads);
     const int64_t first = r0 + (int64_t)warp * mine * 32;
     const int end = (int)max64(min64(r1 - first, (int64_t)mine * 32), 0);  // the warp's rows that are there: < end
     const int room = (int)max64(min64(keep - first, (int64_t)mine * 32), 0);  // and below keep: < room
-    const int heldi = min(mine, kHeldRows / kEvictThreads);
+    const int heldi = min(mine, kHeldRows / kThreads);
     uint32_t* mykeys = keys + warp * heldi * 32;
     uint32_t lo = 0xFFFFFFFFu, hi = 0, prot = 0;
     auto take = [&](uint32_t key) {
@@ -209,38 +211,40 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(EvictArgs a) {
         if (in && key >= lo && key <= hi) atomicAdd(&sh.hist[d][(key - lo) >> shift], 1u);
       });
       sync_all();
-      // four bins a thread of the first half, from the top
-      uint32_t c[4] = {0, 0, 0, 0};
-      const int b0 = kBins - 4 - 4 * tid;
-      if (tid < kBins / 4) {
-        if (kCluster) {
-          uint4 v[kEvictMaxBlocks];
+      // a thread's bins, from the top
+      uint32_t c[kBinsPer];
 #pragma unroll
-          for (int i = 0; i < kEvictMaxBlocks; ++i)
-            v[i] = i < nb ? *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&sh.hist[d][b0], i)) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < kBinsPer; ++i) c[i] = 0;
+      const int b0 = kBins - kBinsPer - kBinsPer * tid;
+      if (tid < kBins / kBinsPer) {
 #pragma unroll
-          for (int i = 0; i < kEvictMaxBlocks; ++i) {
-            c[0] += v[i].w;
-            c[1] += v[i].z;
-            c[2] += v[i].y;
-            c[3] += v[i].x;
+        for (int q = 0; q < kBinsPer; q += 4) {
+          const uint32_t* bins = &sh.hist[d][b0 + kBinsPer - 4 - q];
+          uint4 v[kCluster ? kEvictMaxBlocks : 1];
+#pragma unroll
+          for (int i = 0; i < (kCluster ? kEvictMaxBlocks : 1); ++i)
+            v[i] = !kCluster ? *reinterpret_cast<const uint4*>(bins)
+                   : i < nb ? *reinterpret_cast<const uint4*>(cluster.map_shared_rank(bins, i)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < (kCluster ? kEvictMaxBlocks : 1); ++i) {
+            c[q] += v[i].w;
+            c[q + 1] += v[i].z;
+            c[q + 2] += v[i].y;
+            c[q + 3] += v[i].x;
           }
-        } else {
-          const uint4 v = *reinterpret_cast<const uint4*>(&sh.hist[d][b0]);
-          c[0] = v.w;
-          c[1] = v.z;
-          c[2] = v.y;
-          c[3] = v.x;
         }
       }
-      const uint32_t sum = c[0] + c[1] + c[2] + c[3], inc = warp_incl_scan(sum, lane);
+      uint32_t sum = 0;
+#pragma unroll
+      for (int i = 0; i < kBinsPer; ++i) sum += c[i];
+      const uint32_t inc = warp_incl_scan(sum, lane);
       if (lane == 31) sh.warp_a[warp] = inc;
       __syncthreads();
       uint32_t before = __reduce_add_sync(kFull, lane < warp ? sh.warp_a[lane] : 0u) + inc - sum;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kBinsPer; ++i) {
         if (before < want && before + c[i] >= want) {
-          sh.bin = b0 + 3 - i;
+          sh.bin = b0 + kBinsPer - 1 - i;
           sh.above = before;
           sh.in_bin = c[i];
         }
@@ -346,7 +350,7 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(EvictArgs a) {
     uint32_t* const rest_at = (lane == 0 ? reinterpret_cast<uint32_t*>(a.c.ks) : lane == 1 ? reinterpret_cast<uint32_t*>(a.c.vs)
                                : lane == 2 ? reinterpret_cast<uint32_t*>(a.c.w) : reinterpret_cast<uint32_t*>(a.c.pos)) + base;
 #pragma unroll 1
-    for (uint32_t i0 = (rank * kEvictWarps + warp) * kMoves; i0 < moves; i0 += nb * kEvictWarps * kMoves) {
+    for (uint32_t i0 = (rank * kWarps + warp) * kMoves; i0 < moves; i0 += nb * kWarps * kMoves) {
       int32_t to = 0, from = 0;
       if (lane < kMoves && i0 + lane < moves) {
         to = entry(1, i0 + lane);
@@ -382,24 +386,23 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(EvictArgs a) {
 
 }  // namespace
 
-cudaError_t launch_kv4_evict(const EvictArgs& a, cudaStream_t st) {
-  int nb = 1;
-  while (nb < kEvictMaxBlocks && (int64_t)nb * kHeldRows < a.c.rmax) nb *= 2;
-  const int64_t per_block = min64(kHeldRows, (a.c.rmax + nb - 1) / nb + kEvictThreads);
-  const size_t smem = (size_t)min64(kHeldRows, (per_block + kEvictThreads - 1) / kEvictThreads * kEvictThreads) * sizeof(uint32_t);
+namespace {
+
+template <bool kCluster, int kThreads>
+cudaError_t launch_evict(const EvictArgs& a, int nb, cudaStream_t st) {
+  const int64_t per_block = ((a.c.rmax + nb - 1) / nb + kThreads - 1) / kThreads * kThreads;
+  const size_t smem = (size_t)min64(kHeldRows, per_block) * sizeof(uint32_t);
   static bool done[64];  // the limit belongs to the device; setting it twice is harmless
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && !(dev >= 0 && dev < 64 && done[dev])) {
-    e = cudaFuncSetAttribute((const void*)k_kv4_evict<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldRows * 4);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute((const void*)k_kv4_evict<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldRows * 4);
+    e = cudaFuncSetAttribute((const void*)k_kv4_evict<kCluster, kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldRows * 4);
     if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
   }
   if (e != cudaSuccess) return e;
-  if (nb == 1) return launch_pdl(k_kv4_evict<false>, dim3(a.c.batch * a.c.hkv), dim3(kEvictThreads), smem, st, a);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.c.batch * a.c.hkv * nb);
-  cfg.blockDim = dim3(kEvictThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -409,8 +412,17 @@ cudaError_t launch_kv4_evict(const EvictArgs& a, cudaStream_t st) {
   attr[1].val.clusterDim.x = nb;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_kv4_evict<true>, a);
+  cfg.numAttrs = kCluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k_kv4_evict<kCluster, kThreads>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_evict(const EvictArgs& a, cudaStream_t st) {
+  if (a.c.rmax <= 6144) return launch_evict<false, 512>(a, 1, st);
+  int nb = 1;
+  while (nb < kEvictMaxBlocks && (int64_t)nb * kHeldRows < a.c.rmax) nb *= 2;
+  return nb == 1 ? launch_evict<false, 1024>(a, 1, st) : launch_evict<true, 1024>(a, nb, st);
 }
 
 }  // namespace paris

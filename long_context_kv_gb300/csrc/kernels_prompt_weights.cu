@@ -30,7 +30,7 @@ constexpr size_t kWSmem = (size_t)kWStages * kKeyBytes + 2 * kQHalf + 1024;
 struct WeightShared {
   uint64_t q_full, q_empty, k_full[kWStages], k_empty[kWStages], s_full[2], s_empty[2];
   uint32_t tmem, gave_up;
-  __align__(16) float lse[kWRows];  // base 2
+  __align__(16) float lse[kWRows];  // base 2, negative
   int32_t lim[kWRows];  // last key that the row sees
 };
 
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const int h = kvh * a.g + r % a.g;
         const bool in = r < n;
         const float lse = in ? wa.lse[((int64_t)(a.cu_q ? 0 : s) * a.hq + h) * a.rows_q + q0 + i] : 0.f;
-        sh.lse[r] = lse == -INFINITY ? INFINITY : lse * kLog2e;  // adds nothing
+        sh.lse[r] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;  // adds nothing
         sh.lim[r] = in && lse != -INFINITY ? (int32_t)min64(lk - 1, i + lk - lq) : -1;
       }
       asm volatile("bar.sync 1, 256;\n" ::: "memory");
@@ -171,32 +171,55 @@ __global__ void __launch_bounds__(kWThreads, 1)
         tm_fence_after();
         const int64_t j = (int64_t)(tile0 + t) * kTile + row;
         const bool open = (int64_t)(tile0 + t + 1) * kTile - 1 <= least;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int r0 = 0; r0 < n; r0 += 32) {
-          uint32_t v[32];
-          tm_ld32(v, 0, ts + r0);
-          tm_wait_ld();
-          if (open && r0 < whole) {
+        float sum = 0.f;
+        if (open && n == whole) {
+          // 32 columns at a time, the next 32 on their way meanwhile
+          uint32_t v[2][32];
+          uint64_t sum2[2] = {0, 0};
+          const uint64_t c2 = pair2(kScaleLog2, kScaleLog2);
+          auto add32 = [&](const uint32_t (&x)[32], int r0) {
 #pragma unroll
             for (int u = 0; u < 32; u += 4) {
-              const float4 l4 = *reinterpret_cast<const float4*>(&sh.lse[r0 + u]);
-              sum[0] += ex2(fmaf(__uint_as_float(v[u]), kScaleLog2, -l4.x));
-              sum[1] += ex2(fmaf(__uint_as_float(v[u + 1]), kScaleLog2, -l4.y));
-              sum[2] += ex2(fmaf(__uint_as_float(v[u + 2]), kScaleLog2, -l4.z));
-              sum[3] += ex2(fmaf(__uint_as_float(v[u + 3]), kScaleLog2, -l4.w));
+              const ulonglong2 l4 = *reinterpret_cast<const ulonglong2*>(&sh.lse[r0 + u]);
+              float p[4];
+              unpair2(fma2(pair2(__uint_as_float(x[u]), __uint_as_float(x[u + 1])), c2, l4.x), p[0], p[1]);
+              unpair2(fma2(pair2(__uint_as_float(x[u + 2]), __uint_as_float(x[u + 3])), c2, l4.y), p[2], p[3]);
+              sum2[0] = add2(sum2[0], pair2(ex2(p[0]), ex2(p[1])));
+              sum2[1] = add2(sum2[1], pair2(ex2(p[2]), ex2(p[3])));
             }
-          } else {
-#pragma unroll
-            for (int u = 0; u < 32; ++u) {
-              const float p = ex2(fmaf(__uint_as_float(v[u]), kScaleLog2, -sh.lse[r0 + u]));
-              sum[u & 3] += j <= sh.lim[r0 + u] ? p : 0.f;
+          };
+          tm_ld32(v[0], 0, ts);
+          tm_wait_ld();
+          for (int r0 = 0; r0 < n; r0 += 64) {
+            if (r0 + 32 < n) tm_ld32(v[1], 0, ts + r0 + 32);
+            add32(v[0], r0);
+            tm_wait_ld();
+            if (r0 + 32 < n) {
+              if (r0 + 64 < n) tm_ld32(v[0], 0, ts + r0 + 64);
+              add32(v[1], r0 + 32);
+              tm_wait_ld();
             }
           }
+          float p0, p1;
+          unpair2(add2(sum2[0], sum2[1]), p0, p1);
+          sum = p0 + p1;
+        } else {
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int r0 = 0; r0 < n; r0 += 32) {
+            uint32_t v[32];
+            tm_ld32(v, 0, ts + r0);
+            tm_wait_ld();
+#pragma unroll
+            for (int u = 0; u < 32; ++u) {
+              const float p = ex2(fmaf(__uint_as_float(v[u]), kScaleLog2, sh.lse[r0 + u]));
+              part[u & 3] += j <= sh.lim[r0 + u] ? p : 0.f;
+            }
+          }
+          sum = (part[0] + part[1]) + (part[2] + part[3]);
         }
         tm_fence_before();
         bar_arrive(s_empty + 8 * grp);
-        const float w = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        if (j < lkm) out[j] = c > 0 ? out[j] + w : w;
+        if (j < lkm) out[j] = c > 0 ? out[j] + sum : sum;
       }
     }
     tm_fence_before();
