@@ -7,12 +7,15 @@
 // (all of a 64-query window of four heads) in shared memory and walks a
 // range of 128-key tiles; a producing warp keeps K tiles coming by TMA, an
 // issuing warp runs a tile's product into one of two 256-column halves of
-// tensor memory, and two groups of four warps, a half each, take the
-// exponentials and add.  Longer windows go by in chunks of 256 rows, each
-// adding to the sums of the ones before.
+// tensor memory, and two groups of four warps take the exponentials of half of
+// the columns each and add, while the tensor cores fill the other half of
+// tensor memory.  Longer windows go by in chunks of 256 rows, each adding to
+// the sums before.
 //
-// Bound by the read of K where the window is short, and by the products and
-// exponentials (1024 cycles each for a full tile, side by side) at 256 rows.
+// Bound by the read of K where the window is short, and at 256 rows by the
+// exponentials and by shared memory, which the products read at 96 of its 128
+// bytes a cycle (with a product of 128 columns a time it was all 128, and the
+// copies of K waited for it: 23.3 us for 32K keys of 8 KV heads, against 21.3).
 #include <algorithm>
 
 #include "tc_device.cuh"
@@ -28,10 +31,11 @@ constexpr int kQHalf = kWRows * 128;   // 64 channels of a chunk
 constexpr size_t kWSmem = (size_t)kWStages * kKeyBytes + 2 * kQHalf + 1024;
 
 struct WeightShared {
-  uint64_t q_full, q_empty, k_full[kWStages], k_empty[kWStages], s_full[2], s_empty[2];
+  uint64_t q_full, q_empty, k_full[kWStages], k_empty[kWStages], s_full[2], s_empty[2], part_full[4];
   uint32_t tmem, gave_up;
+  float part[4][kTile];  // the second group's sums
   __align__(16) float lse[kWRows];  // base 2, negative
-  int32_t lim[kWRows];  // last key that the row sees
+  uint8_t tok[kWRows];  // the row's query, counted from the chunk's first
 };
 
 struct WeightMaps {
@@ -66,7 +70,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
   }
   const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u, qb = base + kWStages * kKeyBytes;
   const uint32_t q_full = smem_u32(&sh.q_full), q_empty = smem_u32(&sh.q_empty), k_full = smem_u32(&sh.k_full[0]),
-                 k_empty = smem_u32(&sh.k_empty[0]), s_full = smem_u32(&sh.s_full[0]), s_empty = smem_u32(&sh.s_empty[0]);
+                 k_empty = smem_u32(&sh.k_empty[0]), s_full = smem_u32(&sh.s_full[0]), s_empty = smem_u32(&sh.s_empty[0]), part_full = smem_u32(&sh.part_full[0]);
   if (tid == 0) {
     sh.gave_up = 0;
     bar_init(q_full, 1);
@@ -77,8 +81,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(s_full + 8 * i, 1);
-      bar_init(s_empty + 8 * i, kTile);
+      bar_init(s_empty + 8 * i, 2 * kTile);
     }
+    for (int i = 0; i < 4; ++i) bar_init(part_full + 8 * i, kTile);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == 8) {
@@ -144,9 +149,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
       }
       __syncwarp();
     }
+    // the last signals have arrived before the block ends
+    if (ok) wait(q_empty, (nchunk - 1) & 1);
   } else if (warp < 8) {
     const int grp = warp >> 2, row = tid & (kTile - 1);
-    const uint32_t ts = tmem + ((uint32_t)((warp & 3) * 32) << 16) + grp * kWRows;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     bool ok = true;
     for (int c = 0; c < nchunk; ++c) {  // past a wait that gave up, only the barriers
       const int n = rows_of(c);
@@ -156,47 +163,48 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const int64_t i = first + (int64_t)c * tq + r / a.g;
         const int h = kvh * a.g + r % a.g;
         const bool in = r < n;
-        const float lse = in ? wa.lse[((int64_t)(a.cu_q ? 0 : s) * a.hq + h) * a.rows_q + q0 + i] : 0.f;
+        const float lse = in ? wa.lse[((int64_t)(a.cu_q ? 0 : s) * a.hq + h) * a.rows_q + q0 + i] : -INFINITY;
         sh.lse[r] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;  // adds nothing
-        sh.lim[r] = in && lse != -INFINITY ? (int32_t)min64(lk - 1, i + lk - lq) : -1;
+        sh.tok[r] = (uint8_t)(r / a.g);
       }
       asm volatile("bar.sync 1, 256;\n" ::: "memory");
-      const int whole = n & ~31;  // rows in full groups of 32
+      // this group's columns: whole groups of 32 but for the last
+      const int half = ((n + 1) / 2 + 31) & ~31, c0 = grp ? min(half, n) : 0, c1 = grp ? n : min(half, n);
       const int64_t least = first + (int64_t)c * tq + lk - lq;  // every row of the chunk sees this far
       for (int t = 0; t < ntile; ++t) {
-        const int x = c * ntile + t;
-        if ((x & 1) != grp) continue;
-        if (ok) ok = __all_sync(kFull, bar_wait(s_full + 8 * grp, (x >> 1) & 1, gave_up));
+        const int x = c * ntile + t, buf = x & 1;
+        if (ok) ok = __all_sync(kFull, bar_wait(s_full + 8 * buf, (x >> 1) & 1, gave_up));
         if (!ok) break;
         tm_fence_after();
+        const uint32_t ts = tmem + lanes + buf * kWRows;
         const int64_t j = (int64_t)(tile0 + t) * kTile + row;
-        const bool open = (int64_t)(tile0 + t + 1) * kTile - 1 <= least;
         float sum = 0.f;
-        if (open && n == whole) {
+        if ((int64_t)(tile0 + t + 1) * kTile - 1 <= least && (c1 - c0) % 32 == 0) {
           // 32 columns at a time, the next 32 on their way meanwhile
           uint32_t v[2][32];
           uint64_t sum2[2] = {0, 0};
           const uint64_t c2 = pair2(kScaleLog2, kScaleLog2);
-          auto add32 = [&](const uint32_t (&x)[32], int r0) {
+          auto add32 = [&](const uint32_t (&y)[32], int r) {
 #pragma unroll
             for (int u = 0; u < 32; u += 4) {
-              const ulonglong2 l4 = *reinterpret_cast<const ulonglong2*>(&sh.lse[r0 + u]);
+              const ulonglong2 l4 = *reinterpret_cast<const ulonglong2*>(&sh.lse[r + u]);
               float p[4];
-              unpair2(fma2(pair2(__uint_as_float(x[u]), __uint_as_float(x[u + 1])), c2, l4.x), p[0], p[1]);
-              unpair2(fma2(pair2(__uint_as_float(x[u + 2]), __uint_as_float(x[u + 3])), c2, l4.y), p[2], p[3]);
+              unpair2(fma2(pair2(__uint_as_float(y[u]), __uint_as_float(y[u + 1])), c2, l4.x), p[0], p[1]);
+              unpair2(fma2(pair2(__uint_as_float(y[u + 2]), __uint_as_float(y[u + 3])), c2, l4.y), p[2], p[3]);
               sum2[0] = add2(sum2[0], pair2(ex2(p[0]), ex2(p[1])));
               sum2[1] = add2(sum2[1], pair2(ex2(p[2]), ex2(p[3])));
             }
           };
-          tm_ld32(v[0], 0, ts);
+          if (c0 < c1) tm_ld32(v[0], 0, ts + c0);
           tm_wait_ld();
-          for (int r0 = 0; r0 < n; r0 += 64) {
-            if (r0 + 32 < n) tm_ld32(v[1], 0, ts + r0 + 32);
-            add32(v[0], r0);
+          for (int r = c0; r < c1; r += 64) {
+            const bool second = r + 32 < c1, third = r + 64 < c1;
+            if (second) tm_ld32(v[1], 0, ts + r + 32);
+            add32(v[0], r);
             tm_wait_ld();
-            if (r0 + 32 < n) {
-              if (r0 + 64 < n) tm_ld32(v[0], 0, ts + r0 + 64);
-              add32(v[1], r0 + 32);
+            if (second) {
+              if (third) tm_ld32(v[0], 0, ts + r + 64);
+              add32(v[1], r + 32);
               tm_wait_ld();
             }
           }
@@ -205,21 +213,33 @@ __global__ void __launch_bounds__(kWThreads, 1)
           sum = p0 + p1;
         } else {
           float part[4] = {0.f, 0.f, 0.f, 0.f};
-          for (int r0 = 0; r0 < n; r0 += 32) {
+          for (int r = c0; r < c1; r += 32) {
             uint32_t v[32];
-            tm_ld32(v, 0, ts + r0);
+            tm_ld32(v, 0, ts + r);
             tm_wait_ld();
 #pragma unroll
             for (int u = 0; u < 32; ++u) {
-              const float p = ex2(fmaf(__uint_as_float(v[u]), kScaleLog2, sh.lse[r0 + u]));
-              part[u & 3] += j <= sh.lim[r0 + u] ? p : 0.f;
+              const float p = ex2(fmaf(__uint_as_float(v[u]), kScaleLog2, sh.lse[r + u]));
+              // rows that see nothing, or are not there, have -inf: their
+              // products may be anything
+              part[u & 3] += j <= least + sh.tok[r + u] && sh.lse[r + u] != -INFINITY ? p : 0.f;
             }
           }
           sum = (part[0] + part[1]) + (part[2] + part[3]);
         }
         tm_fence_before();
-        bar_arrive(s_empty + 8 * grp);
-        if (j < lkm) out[j] = c > 0 ? out[j] + sum : sum;
+        bar_arrive(s_empty + 8 * buf);
+        // the first group adds the second's sum; a place is written again four
+        // tiles later, when the first group has given back two more
+        if (grp) {
+          sh.part[x & 3][row] = sum;
+          bar_arrive(part_full + 8 * (x & 3));
+        } else {
+          ok = __all_sync(kFull, bar_wait(part_full + 8 * (x & 3), (x >> 2) & 1, gave_up));
+          if (!ok) break;
+          sum += sh.part[x & 3][row];
+          if (j < lkm) out[j] = c > 0 ? out[j] + sum : sum;
+        }
       }
     }
     tm_fence_before();
