@@ -381,7 +381,7 @@ paris_status paris_prompt_check(void);
 /* The weights that the last `window` queries of each sequence give to its
  * keys: weights[h][j] = sum over those queries i and over the query heads of
  * KV head h of exp(s_ij - lse_i), with lse as paris_prompt_attend gives it
- * (a query with lse = -inf adds nothing).  weights: device float32 [sequence
+ * (a query with lse = -inf adds nothing); window <= 2^24.  weights: device float32 [sequence
  * axis][Hkv][rows_k], written for every key row of every sequence.  `v`,
  * `out` and max_q of p are not used.                                        */
 paris_status paris_prompt_weights(const paris_prompt* p, const void* q, const void* k, paris_dtype dtype,
@@ -397,7 +397,8 @@ paris_status paris_prompt_weights(const paris_prompt* p, const void* q, const vo
  * codes holds c + 8 of channel 2j in its low and of channel 2j + 1 in its
  * high half; a scale byte is the upper byte (5 exponent bits, 3 mantissa
  * bits) of the scale as a half without its sign bit.
- * All arrays are device memory of the caller.  Lengths outside
+ * All arrays are device memory of the caller; codes, scales and weights are
+ * 16-byte aligned.  Lengths outside
  * [0, max_rows] count as the nearest of the two.  A cache is one object: calls
  * on it go to one stream, or are ordered by the caller.                      */
 typedef struct {

@@ -239,9 +239,10 @@ cudaError_t launch_kv4_store(const StoreArgs& a, cudaStream_t st) {
   // 16 tokens a block, fewer where that leaves SMs without two blocks
   int tokens = 16;
   while (tokens > 1 && a.c.batch * ((a.max_new + tokens - 1) / tokens) < 2 * 152) tokens /= 2;
+  // the division by hkv is a product: exact below 2^32 / hkv items
+  while (tokens > 1 && (int64_t)tokens * a.c.hkv * a.c.hkv >= (int64_t)1 << 32) tokens /= 2;
   const int64_t nblk = max64(1, (a.max_new + tokens - 1) / tokens);
   if (nblk * a.c.batch > 0x7fffffff) return cudaErrorInvalidValue;
-  // exact for the at most 16 hkv items of a block
   const uint32_t inv = (uint32_t)(((uint64_t)1 << 32) / a.c.hkv + 1);
   const dim3 grid((unsigned)(nblk * a.c.batch));
   if (a.dtype == 1) return launch_pdl(k_kv4_store<RowBf16>, grid, dim3(kStoreThreads), 0, st, a, (int)nblk, tokens, inv);

@@ -130,10 +130,22 @@ struct PromptShared {
 
 __device__ __forceinline__ int blocks_of(int64_t lq, int tokens) { return (int)((lq + tokens - 1) / tokens); }
 
+// Up to this many packed sequences are walked by query block, with a few
+// looks at every length for each item; more of them one after the other.
+constexpr int kFewSeqs = 64;
+
+// Where a walk over the sequences has come to: those before s0 have `before`
+// query blocks.
+struct PromptCursor {
+  int s0;
+  int64_t before;
+};
+
 // Item x of the call (a warp computes it): query blocks in descending order,
 // so that those that see most keys come first, and for each the sequences
-// that have it, KV heads and splits.  False: there is no such item.
-__device__ __forceinline__ bool prompt_item(const PromptArgs& a, int64_t x, PromptItem& w) {
+// that have it, KV heads and splits.  Of more than kFewSeqs sequences, their
+// query blocks in turn; x must not decrease then.  False: there is no such item.
+__device__ __forceinline__ bool prompt_item(const PromptArgs& a, int64_t x, PromptCursor& cur, PromptItem& w) {
   const int lane = threadIdx.x & 31;
   const int tq = kTile / a.g, tokens = kTiles * tq;
   const int per = a.hkv * a.nsplit;
@@ -153,32 +165,49 @@ __device__ __forceinline__ bool prompt_item(const PromptArgs& a, int64_t x, Prom
       seq_rows(a.cu_q, s, a.rows_q, q0, lq);
       return blocks_of(min64(lq, a.max_q), tokens);
     };
-    // number of (block, sequence) pairs with block >= level
-    auto from = [&](int level) -> int64_t {
-      int64_t n = 0;
-      for (int s0 = 0; s0 < a.n_seqs; s0 += 32) n += __reduce_add_sync(kFull, (uint32_t)max(0, blocks(s0 + lane) - level));
-      return n;
-    };
-    if (y >= from(0)) return false;
-    int lo = 0, hi = blocks_of(a.max_q, tokens);  // from(lo) > y >= from(hi)
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (from(mid) > y) lo = mid;
-      else hi = mid;
-    }
-    int64_t j = y - from(lo + 1);  // among the sequences that have block lo
-    w.qb = lo;
-    w.s = 0;
-    for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
-      const uint32_t has = __ballot_sync(kFull, blocks(s0 + lane) > lo);
-      const int n = __popc(has);
-      if (j < n) {
-        uint32_t m = has;
-        for (int i = 0; i < j; ++i) m &= m - 1;
-        w.s = s0 + __ffs(m) - 1;
-        break;
+    if (a.n_seqs > kFewSeqs) {
+      for (;; cur.s0 += 32) {
+        if (cur.s0 >= a.n_seqs) return false;
+        const int n = blocks(cur.s0 + lane);
+        const uint32_t inc = warp_incl_scan((uint32_t)n, lane), all = __shfl_sync(kFull, inc, 31);
+        const int64_t j = y - cur.before;
+        if (j < all) {
+          const int src = __popc(__ballot_sync(kFull, inc <= j));  // the lanes before it
+          w.s = cur.s0 + src;
+          // the longest of a sequence's blocks first
+          w.qb = (int)(__shfl_sync(kFull, inc, src) - 1 - j);
+          break;
+        }
+        cur.before += all;
       }
-      j -= n;
+    } else {
+      // number of (block, sequence) pairs with block >= level
+      auto from = [&](int level) -> int64_t {
+        int64_t n = 0;
+        for (int s0 = 0; s0 < a.n_seqs; s0 += 32) n += __reduce_add_sync(kFull, (uint32_t)max(0, blocks(s0 + lane) - level));
+        return n;
+      };
+      if (y >= from(0)) return false;
+      int lo = 0, hi = blocks_of(a.max_q, tokens);  // from(lo) > y >= from(hi)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (from(mid) > y) lo = mid;
+        else hi = mid;
+      }
+      int64_t j = y - from(lo + 1);  // among the sequences that have block lo
+      w.qb = lo;
+      w.s = 0;
+      for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
+        const uint32_t has = __ballot_sync(kFull, blocks(s0 + lane) > lo);
+        const int n = __popc(has);
+        if (j < n) {
+          uint32_t m = has;
+          for (int i = 0; i < j; ++i) m &= m - 1;
+          w.s = s0 + __ffs(m) - 1;
+          break;
+        }
+        j -= n;
+      }
     }
   }
   int64_t q0, lq, k0, lk;
@@ -258,12 +287,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int tq = kTile / a.g;
       int nq = 0, x = 0;  // query loads, ring loads so far
       bool ok = true;
+      PromptCursor cur{0, 0};
       for (int it = 0; ok; ++it) {
         // items in turns of the grid, every other turn backwards: who had the
         // longest of one turn has the shortest of the next
         const int64_t at = (int64_t)it * gridDim.x + (it & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
         PromptItem w;
-        const bool more = prompt_item(a, at, w);
+        const bool more = prompt_item(a, at, cur, w);
         if (!more) w.s = -1;
         if (it >= kItems) ok = wait(item_empty + 8 * (it % kItems), (it / kItems - 1) & 1);
         if (!ok) break;

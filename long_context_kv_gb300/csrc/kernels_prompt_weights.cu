@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
   const uint32_t tmem = __shfl_sync(kFull, *(volatile uint32_t*)&sh.tmem, 0);
   volatile uint32_t* gave_up = &sh.gave_up;
   const int64_t first = lq - win;                 // first query of the window
-  const int total = nchunk * ntile;               // products, chunk by chunk
+  const int total = nchunk * ntile;               // products, chunk by chunk (the launch keeps it below 2^31)
   // rows of chunk c, and the product's N
   auto rows_of = [&](int c) { return min(tq, win - c * tq) * a.g; };
 
@@ -278,6 +278,8 @@ cudaError_t launch_prompt_weights(const PromptWeightArgs& w, int sm_count, cudaS
   // a block per SM, each with an even share of the tiles
   const int64_t units = (int64_t)a.n_seqs * a.hkv, tiles = (a.max_k + kTile - 1) / kTile;
   const int64_t per = std::max<int64_t>(1, (units * tiles + sm_count - 1) / sm_count);
+  const int64_t chunk = kWRows / a.g, chunks = (std::min<int64_t>(w.window, a.rows_q) + chunk - 1) / chunk;
+  if (chunks * per > 0x7fffffff) return cudaErrorInvalidValue;
   const int64_t blocks = (tiles + per - 1) / per;
   if (blocks * units > 0x7fffffff) return cudaErrorInvalidValue;
   return launch_pdl(k_prompt_weights, dim3((unsigned)(blocks * units)), dim3(kWThreads), kWSmem, st, w, m, (int)blocks, (int)per);

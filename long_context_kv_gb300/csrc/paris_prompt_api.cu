@@ -102,8 +102,8 @@ paris_status take_cache(const paris_kv4* c, Kv4* k) {
   if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales || !c->weights || !c->positions || !c->lens ||
       !c->next_pos || !c->counters || !c->status)
     return fail(PARIS_EINVAL, "the cache's arrays must not be NULL");
-  if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_scales) || !aligned16(c->v_scales))
-    return fail(PARIS_EINVAL, "the cache's codes and scales must be 16-byte aligned");
+  if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_scales) || !aligned16(c->v_scales) || !aligned16(c->weights))
+    return fail(PARIS_EINVAL, "the cache's codes, scales and weights must be 16-byte aligned");
   *k = Kv4{c->batch, c->n_kv_heads, c->max_rows, c->k_codes, c->v_codes, c->k_scales, c->v_scales,
            c->weights, c->positions, c->lens, c->next_pos, c->counters, c->status};
   return PARIS_OK;
@@ -177,7 +177,7 @@ paris_status paris_prompt_weights(const paris_prompt* p, const void* q, const vo
   paris_status st = take_prompt(p, &w.p, false);
   if (st != PARIS_OK) return st;
   if (dtype != PARIS_BF16) return fail(PARIS_EINVAL, "paris_prompt_weights: q and k must be PARIS_BF16");
-  if (window < 0) return fail(PARIS_EINVAL, "window must be >= 0");
+  if (window < 0 || window > 1 << 24) return fail(PARIS_EINVAL, "window must be in [0, 2^24]");
   if (w.p.n_seqs == 0 || w.p.max_k == 0) return PARIS_OK;
   if (!k || !weights || (w.p.rows_q > 0 && (!q || !lse))) return fail(PARIS_EINVAL, "q, k, lse and weights must not be NULL");
   if (!aligned16(q) || !aligned16(k)) return fail(PARIS_EINVAL, "q and k must be 16-byte aligned");

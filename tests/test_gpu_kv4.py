@@ -211,6 +211,34 @@ def test_queries_of_any_size(amp):
     check_attend(c, q, out)
 
 
+@pytest.mark.parametrize("batch", [2, 33, 128, 129, 300])
+def test_batches_of_very_different_lengths(batch):
+    gen = torch.Generator().manual_seed(batch)
+    lens = torch.randint(0, 40, (batch,), generator=gen).tolist()
+    lens[batch // 2] = 700
+    c = filled(lens, 1, 704, seed=61)
+    q = rand(batch, 4, R.D, seed=62, amp=2.0).to(BF)
+    out = torch.full_like(q, 9.0)
+    before = c.weights.clone()
+    c.paris_kv4_attend(q, out, accumulate=True)
+    check_attend(c, q, out, before)
+    check_evict(c, 20, 1, 4)
+
+
+def test_many_kv_heads():
+    h = 300
+    c = P.KV4Cache.create(2, h, 24)
+    k, v = rand(30, h, R.D, seed=63).to(BF), rand(30, h, R.D, seed=64).to(BF)
+    c.paris_kv4_store(k, v, cu=R.starts([11, 19]))
+    assert torch.equal(c.k_codes[0, :, :11], R.quantise(k[:11])[0].transpose(0, 1))
+    assert torch.equal(c.v_codes[1, :, :19], R.quantise(v[11:])[0].transpose(0, 1))
+    assert torch.equal(c.v_scales[1, :, :19], R.quantise(v[11:])[1].transpose(0, 1))
+    q = rand(2, h, R.D, seed=65).to(BF)
+    out = torch.zeros_like(q)
+    c.paris_kv4_attend(q, out)
+    check_attend(c, q, out)
+
+
 def test_a_query_that_is_not_finite_spoils_only_its_own_head():
     c = filled([100], 1, 128, seed=54)
     q = rand(1, 4, R.D, seed=55).to(BF)

@@ -92,6 +92,22 @@ def test_a_longer_prompt_with_a_running_maximum_that_grows():
     check_seq(q, k, v, out, None, 4)
 
 
+@pytest.mark.parametrize("hq,hkv", [(128, 1), (100, 1), (66, 2)])
+def test_many_query_heads_share_a_kv_head(hq, hkv):
+    check([3, 150], [3, 150], hq, hkv, seed=16)
+    check([2], [700], hq, hkv, seed=17)
+
+
+def test_many_sequences():
+    # more than are walked by query block; some empty, one long
+    gen = torch.Generator().manual_seed(18)
+    lens = torch.randint(0, 50, (150,), generator=gen).tolist()
+    lens[70] = 900
+    check(lens, lens, 8, 2, seed=18)
+    lens_q = [min(n, 3) for n in lens]
+    check(lens_q, lens, 4, 4, seed=19)
+
+
 def test_padded_layout_and_strided_views():
     b, hq, hkv, t = 3, 6, 2, 190
     gen = torch.Generator(device="cuda").manual_seed(6)
@@ -131,6 +147,23 @@ def test_what_a_query_does_not_see_does_not_reach_it(bad):
         P.paris_prompt_attend(q2, k2, v2, out, cu_q=cu, cu_k=cu, max_q=150, max_k=150)
         check_seq(q[:first], k[:first], v[:first], out[:first], None, 2)
         assert torch.all(out[150:] == 7.0)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_what_a_chunk_does_not_see_does_not_reach_it(bad):
+    # few queries over many keys: the keys are split among blocks
+    q, k, v = make([20], [3100], 4, 2, seed=20)
+    k[3000:], v[3000:] = bad, bad                       # past the sequence's end
+    cq, ck = R.starts([20]), torch.tensor([0, 3000], dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 7.0)
+    P.paris_prompt_attend(q, k, v, out, cu_q=cq, cu_k=ck, max_q=20, max_k=3100)
+    check_seq(q, k[:3000], v[:3000], out, None, 2)
+    v[2990:3000] = bad                                  # seen by the last ten queries only
+    P.paris_prompt_attend(q, k, v, out, cu_q=cq, cu_k=ck, max_q=20, max_k=3100)
+    want, _, mass, size = R.attend_rows(q[:10, 0].double(), k[:2990, 0].double(), v[:2990, 0].double())
+    tol = R.HALF_BF16 * want.abs() + ((1 + R.HALF_BF16) * (R.HALF_BF16 + R.score_error(size, 2990)))[:, None] * mass
+    assert torch.all((out[:10, 0].double() - want).abs() <= tol)
+    assert not torch.isfinite(out[10:]).any()
 
 
 def test_non_finite_values_that_a_query_sees_reach_it():
@@ -265,6 +298,21 @@ def test_window_weights_of_chunks_padded_layout_and_queries_that_see_nothing():
         assert torch.all((got[i].double() - want).abs() <= tol + 1e-30)
 
 
+def test_window_weights_of_many_query_heads_and_sequences():
+    for lens, hq, hkv, window in (([40, 300], 128, 1, 7), ([5] * 70 + [400], 6, 2, 4)):
+        q, k, v = make(lens, lens, hq, hkv, seed=21)
+        cu = R.starts(lens)
+        lse = torch.zeros(hq, q.shape[0], device="cuda")
+        P.paris_prompt_attend(q, k, v, torch.empty_like(q), cu_q=cu, cu_k=cu, lse=lse)
+        got = torch.full((hkv, k.shape[0]), 9.0, device="cuda")
+        P.paris_prompt_weights(q, k, lse, got, window=window, cu_q=cu, cu_k=cu, max_k=max(lens))
+        a = 0
+        for n in lens:
+            want, tol = weights_ref(q[a:a + n], k[a:a + n], lse[:, a:a + n], hq // hkv, window)
+            assert torch.all((got[:, a:a + n].double() - want).abs() <= tol + 1e-30)
+            a += n
+
+
 def test_window_weights_do_not_see_other_rows():
     q, k, v = make([100], [100], 4, 2, seed=15)
     cu = torch.tensor([0, 60], dtype=torch.int32, device="cuda")
@@ -276,3 +324,21 @@ def test_window_weights_do_not_see_other_rows():
     want, tol = weights_ref(q[:60], k[:60], lse[:, :60], 2, 16)
     assert torch.all((got[:, :60].double() - want).abs() <= tol + 1e-30)
     assert torch.all(got[:, 60:] == 9.0)
+
+
+def test_two_calls_at_once_on_two_streams():
+    q, k, v = make([500, 900], [500, 900], 8, 2, seed=22)
+    cu = R.starts([500, 900])
+    want, lse = torch.zeros_like(q), torch.zeros(8, 1400, device="cuda")
+    P.paris_prompt_attend(q, k, v, want, cu_q=cu, cu_k=cu, lse=lse)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [torch.zeros_like(q) for _ in range(6)]
+    ws = [torch.zeros(2, 1400, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        P.paris_prompt_attend(q, k, v, o, cu_q=cu, cu_k=cu, stream=streams[i % 3])
+        P.paris_prompt_weights(q, k, lse, ws[i % 3], window=16, cu_q=cu, cu_k=cu, stream=streams[i % 3])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs) and all(torch.equal(w, ws[0]) for w in ws)
+    P.paris_prompt_check()

@@ -36,6 +36,7 @@ def prompt(**kw):
     (dict(v=P.paris_strides(0, 128, 0)), "v: the token stride"),
     (dict(out=P.paris_strides(-1024, 128, 0)), "out: the token stride"),
     (dict(cu_q=None, cu_k=None, q=P.paris_strides(1024, 128, 4)), "q: the seq stride"),
+    (dict(k=P.paris_strides(1 << 31, 128, 0)), "k: the token stride"),
 ])
 def test_prompt_descriptions(lib, bad, text):
     n = ctypes.c_size_t(5)
@@ -63,6 +64,7 @@ def test_prompt_pointers_types_and_workspace(lib):
     assert call(prompt(n_seqs=0), None, None, None, P.PARIS_BF16, None) == P.PARIS_OK  # nothing to do
     w = lambda p, window: lib.paris_prompt_weights(ctypes.byref(p), a, a, P.PARIS_BF16, a, window, a, None)  # noqa: E731
     assert w(prompt(), -1) == P.PARIS_EINVAL
+    assert w(prompt(), (1 << 24) + 1) == P.PARIS_EINVAL
     assert w(prompt(n_seqs=0), 4) == P.PARIS_OK
     assert lib.paris_prompt_weights(ctypes.byref(prompt()), a, a, P.PARIS_F32, a, 1, a, None) == P.PARIS_EINVAL
     assert lib.paris_prompt_weights(ctypes.byref(prompt()), a, a, P.PARIS_BF16, None, 1, a, None) == P.PARIS_EINVAL
@@ -80,6 +82,7 @@ def cache(**kw):
     (dict(head_dim=64), "head_dim"), (dict(batch=0), "batch"), (dict(n_kv_heads=0), "n_kv_heads"),
     (dict(batch=40000), "65535"), (dict(max_rows=0), "max_rows"), (dict(max_rows=1 << 31), "max_rows"),
     (dict(lens=None), "NULL"), (dict(k_codes=None), "NULL"), (dict(status=None), "NULL"), (dict(v_scales=4104), "aligned"),
+    (dict(weights=4104), "aligned"),
 ])
 def test_cache_descriptions(lib, bad, text):
     c, n, a = ctypes.byref(cache(**bad)), ctypes.c_size_t(), ctypes.c_void_p(4096)
