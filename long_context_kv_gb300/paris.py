@@ -367,7 +367,7 @@ def _prompt(q, k, cu_q, cu_k, max_q, max_k, v=None, out=None):
         raise ValueError("cu_q and cu_k must both be given or both be None")
     packed = cu_q is not None
     for t in (q, k, v, out):
-        if t is not None and t.dtype != bf16:
+        if t is not None and t.dtype is not bf16:
             raise TypeError(f"the prompt calls take bfloat16 tensors (got {t.dtype})")
     _on(q.get_device(), q, k, v, out, cu_q, cu_k)
     rows_q, hq, seqs, qs = _heads(q, "q", packed)
@@ -472,7 +472,7 @@ class KV4Cache:
                             counters=self._words.data_ptr(), status=self._words.data_ptr() + 4 * b,
                             **{n: t.data_ptr() for n, t in given.items()})
         self._ref = ctypes.byref(self._c)
-        self._ws = {}
+        self._ws, self._spaces = {}, {}
 
     @classmethod
     def create(cls, batch, n_kv_heads, max_rows, device="cuda"):
@@ -487,11 +487,26 @@ class KV4Cache:
 
     def _bytes(self, key, call):
         """Workspace bytes of a call, asked once per kind of call."""
-        if key not in self._ws:
-            n = ctypes.c_size_t()
-            _check(call(n))
-            self._ws[key] = n.value
-        return self._ws[key]
+        n = ctypes.c_size_t()
+        _check(call(ctypes.byref(n)))
+        self._ws[key] = n.value
+        return n.value
+
+    def _space(self, nbytes, stream, handle):
+        """Address of the workspace of a call: kept for each stream, whose calls take turns with it; during a capture
+        one of the graph's own."""
+        import torch
+        if stream is None:
+            capturing = torch.cuda.is_current_stream_capturing()
+        else:
+            with torch.cuda.stream(stream):
+                capturing = torch.cuda.is_current_stream_capturing()
+        if capturing:
+            return _scratch(nbytes, self.device, stream).data_ptr()
+        t = self._spaces.get(handle)
+        if t is None or t.numel() < nbytes:
+            t = self._spaces[handle] = _scratch(nbytes, self.device, stream)
+        return t.data_ptr()
 
     def paris_kv4_store(self, k, v, cu=None, max_new=None, weights=None, stream=None):
         """Add tokens: packed [rows, Hkv, 128] with int32 starts cu [batch + 1] (max_new: at least the most tokens of
@@ -531,19 +546,18 @@ class KV4Cache:
         _shaped(out, "out", shape, torch.bfloat16)
         _on(self._index, q, out)
         lib, hq, acc = _lib or load(), shape[1], 1 if accumulate else 0
-        n = self._bytes((hq, acc), lambda b: lib.paris_kv4_workspace(self._ref, hq, acc, ctypes.byref(b)))
-        ws = _scratch(n, self.device, stream)
-        _check(lib.paris_kv4_attend(self._ref, _flat(q), _dtype_code(q), hq, acc, _flat(out), ws.data_ptr(), n,
-                                    _raw_stream(self._index, stream)))
+        n = self._ws.get((hq, acc)) or self._bytes((hq, acc), lambda b: lib.paris_kv4_workspace(self._ref, hq, acc, b))
+        handle = _raw_stream(self._index, stream)
+        _check(lib.paris_kv4_attend(self._ref, _flat(q), _dtype_code(q), hq, acc, _flat(out),
+                                    self._space(n, stream, handle), n, handle))
 
     def paris_kv4_evict(self, keep, sink=0, recent=0, stream=None):
         """At most `keep` rows for each sequence: protected ones and the heaviest others."""
         _on(self._index)
         lib = _lib or load()
-        n = self._bytes("evict", lambda b: lib.paris_kv4_evict_workspace(self._ref, ctypes.byref(b)))
-        ws = _scratch(n, self.device, stream)
-        _check(lib.paris_kv4_evict(self._ref, int(keep), int(sink), int(recent), ws.data_ptr(), n,
-                                   _raw_stream(self._index, stream)))
+        n = self._ws.get("evict") or self._bytes("evict", lambda b: lib.paris_kv4_evict_workspace(self._ref, b))
+        handle = _raw_stream(self._index, stream)
+        _check(lib.paris_kv4_evict(self._ref, int(keep), int(sink), int(recent), self._space(n, stream, handle), n, handle))
 
     def paris_kv4_read(self, k_out, v_out, stream=None):
         """The values of the first rows: k_out, v_out bfloat16 [batch, Hkv, rows, 128]."""
