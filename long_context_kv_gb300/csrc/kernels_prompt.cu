@@ -557,7 +557,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tm_fence_after();
       }
       const float inv = l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing: 0
-      bool finite = true;
+      // 0 times every value, added up: 0 but for infinities and NaN
+      uint64_t none = 0;
+      const uint64_t inv2 = pair2(inv, inv);
       __nv_bfloat16* out = live ? a.out + (a.cu_q ? 0 : ws * a.so.seq) + (int64_t)(q0 + tok) * a.so.token + h * a.so.head : nullptr;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -585,8 +587,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           uint32_t p[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const float y0 = __uint_as_float(o[u + 2 * x]) * inv, y1 = __uint_as_float(o[u + 2 * x + 1]) * inv;
-            finite = finite && fabsf(y0) < INFINITY && fabsf(y1) < INFINITY;
+            const uint64_t y = mul2(pair2(__uint_as_float(o[u + 2 * x]), __uint_as_float(o[u + 2 * x + 1])), inv2);
+            none = fma2(y, 0, none);
+            float y0, y1;
+            unpair2(y, y0, y1);
             p[x] = pack_bf16x2(y0, y1);
           }
           if (live) *reinterpret_cast<uint4*>(out + 32 * c + u) = make_uint4(p[0], p[1], p[2], p[3]);
@@ -600,7 +604,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       } else {
         if (live && a.lse != nullptr)
           a.lse[((int64_t)(a.cu_q ? 0 : ws) * a.hq + h) * a.rows_q + q0 + tok] = last_key >= 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
-        for (uint32_t again = __ballot_sync(kFull, live && !finite); again; again &= again - 1) {
+        float z0, z1;
+        unpair2(none, z0, z1);
+        for (uint32_t again = __ballot_sync(kFull, live && !(z0 + z1 == 0.f)); again; again &= again - 1) {
           const int src = __ffs(again) - 1;
           const int t = __shfl_sync(kFull, tok, src);
           prompt_row(a, ws, __shfl_sync(kFull, h, src), q0, t, k0, min(lk, t + lk - lq + 1));
