@@ -134,12 +134,22 @@ __device__ __forceinline__ int blocks_of(int64_t lq, int tokens) { return (int)(
 // looks at every length for each item; more of them one after the other.
 constexpr int kFewSeqs = 64;
 
-// Where a walk over the sequences has come to: those before s0 have `before`
-// query blocks.
+// What a producing warp keeps from item to item: of few sequences a lane's
+// two numbers of query blocks; of many, where the walk over them has come to
+// (those before s0 have `before` query blocks).
 struct PromptCursor {
+  int few[kFewSeqs / 32];
   int s0;
   int64_t before;
 };
+
+// Query blocks of sequence s (0: there is no such sequence).
+__device__ __forceinline__ int seq_blocks(const PromptArgs& a, int s, int tokens) {
+  if (s >= a.n_seqs) return 0;
+  int64_t q0, lq;
+  seq_rows(a.cu_q, s, a.rows_q, q0, lq);
+  return blocks_of(min64(lq, a.max_q), tokens);
+}
 
 // Item x of the call (a warp computes it): query blocks in descending order,
 // so that those that see most keys come first, and for each the sequences
@@ -159,16 +169,10 @@ __device__ __forceinline__ bool prompt_item(const PromptArgs& a, int64_t x, Prom
     w.qb = nqb - 1 - (int)(y / a.n_seqs);
     w.s = (int)(y % a.n_seqs);
   } else {
-    auto blocks = [&](int s) -> int {  // of sequence s
-      if (s >= a.n_seqs) return 0;
-      int64_t q0, lq;
-      seq_rows(a.cu_q, s, a.rows_q, q0, lq);
-      return blocks_of(min64(lq, a.max_q), tokens);
-    };
     if (a.n_seqs > kFewSeqs) {
       for (;; cur.s0 += 32) {
         if (cur.s0 >= a.n_seqs) return false;
-        const int n = blocks(cur.s0 + lane);
+        const int n = seq_blocks(a, cur.s0 + lane, tokens);
         const uint32_t inc = warp_incl_scan((uint32_t)n, lane), all = __shfl_sync(kFull, inc, 31);
         const int64_t j = y - cur.before;
         if (j < all) {
@@ -184,7 +188,8 @@ __device__ __forceinline__ bool prompt_item(const PromptArgs& a, int64_t x, Prom
       // number of (block, sequence) pairs with block >= level
       auto from = [&](int level) -> int64_t {
         int64_t n = 0;
-        for (int s0 = 0; s0 < a.n_seqs; s0 += 32) n += __reduce_add_sync(kFull, (uint32_t)max(0, blocks(s0 + lane) - level));
+#pragma unroll
+        for (int i = 0; i < kFewSeqs / 32; ++i) n += __reduce_add_sync(kFull, (uint32_t)max(0, cur.few[i] - level));
         return n;
       };
       if (y >= from(0)) return false;
@@ -197,13 +202,14 @@ __device__ __forceinline__ bool prompt_item(const PromptArgs& a, int64_t x, Prom
       int64_t j = y - from(lo + 1);  // among the sequences that have block lo
       w.qb = lo;
       w.s = 0;
-      for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
-        const uint32_t has = __ballot_sync(kFull, blocks(s0 + lane) > lo);
+#pragma unroll
+      for (int i = 0; i < kFewSeqs / 32; ++i) {
+        const uint32_t has = __ballot_sync(kFull, cur.few[i] > lo);
         const int n = __popc(has);
         if (j < n) {
           uint32_t m = has;
-          for (int i = 0; i < j; ++i) m &= m - 1;
-          w.s = s0 + __ffs(m) - 1;
+          for (int x = 0; x < j; ++x) m &= m - 1;
+          w.s = 32 * i + __ffs(m) - 1;
           break;
         }
         j -= n;
@@ -287,13 +293,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int tq = kTile / a.g;
       int nq = 0, x = 0;  // query loads, ring loads so far
       bool ok = true;
-      PromptCursor cur{0, 0};
+      PromptCursor cur{};
+#pragma unroll
+      for (int i = 0; i < kFewSeqs / 32; ++i)
+        if (a.cu_q != nullptr && a.n_seqs <= kFewSeqs) cur.few[i] = seq_blocks(a, 32 * i + lane, kTiles * tq);
+      // items in turns of the grid, every other turn backwards: who had the
+      // longest of one turn has the shortest of the next
+      auto item = [&](int it, PromptItem& w) {
+        return prompt_item(a, (int64_t)it * gridDim.x + (it & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x), cur, w);
+      };
+      PromptItem w, next;
+      bool more = item(0, next);
       for (int it = 0; ok; ++it) {
-        // items in turns of the grid, every other turn backwards: who had the
-        // longest of one turn has the shortest of the next
-        const int64_t at = (int64_t)it * gridDim.x + (it & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
-        PromptItem w;
-        const bool more = prompt_item(a, at, cur, w);
+        w = next;
         if (!more) w.s = -1;
         if (it >= kItems) ok = wait(item_empty + 8 * (it % kItems), (it / kItems - 1) & 1);
         if (!ok) break;
@@ -302,8 +314,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           bar_arrive(item_full + 8 * (it % kItems));
         }
         if (!more) break;
-        const int jb = w.jb, e = max(w.end[0], w.end[1]);
-        if (e == jb) continue;
+        const int jb = w.jb, e = max(w.end[0], w.end[1]), loads = 2 * (e - jb);
+        if (loads == 0) {
+          more = item(it + 1, next);
+          continue;
+        }
         if (nq > 0) ok = wait(q_empty, (nq - 1) & 1);
         if (!ok) break;
         const int qseq = a.cu_q ? 0 : w.s, kseq = a.cu_k ? 0 : w.s;
@@ -314,7 +329,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               tma_load(base + i * kTileBytes + h * kHalfBytes, &maps.q, 64 * h, w.kvh * a.g, w.q0 + w.t0 + i * tq, qseq, q_full);
         }
         ++nq;
-        for (int j = 0; ok && j < 2 * (e - jb); ++j) {
+        for (int j = 0; ok && j < loads; ++j) {
           const int st = x % kStages, turn = x / kStages;
           if (turn > 0) ok = wait(empty + 8 * st, (turn - 1) & 1);
           if (!ok) break;
@@ -325,6 +340,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             for (int h = 0; h < 2; ++h) tma_load(ring + st * kTileBytes + h * kHalfBytes, m, 64 * h, row, w.kvh, kseq, full + 8 * st);
           }
           ++x;
+          // the ring is full for now: time to find the next item
+          if (j == min(loads, kStages) - 1) more = item(it + 1, next);
         }
       }
       if (!ok && lane == 0) {  // given up: what was issued lands before the block ends
@@ -560,41 +577,66 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       // 0 times every value, added up: 0 but for infinities and NaN
       uint64_t none = 0;
       const uint64_t inv2 = pair2(inv, inv);
-      __nv_bfloat16* out = live ? a.out + (a.cu_q ? 0 : ws * a.so.seq) + (int64_t)(q0 + tok) * a.so.token + h * a.so.head : nullptr;
+      // A lane has a row; stored like that, a warp's 16-byte pieces lie in 32
+      // lines (4500 cycles an item).  So eight lanes exchange 128 bytes of
+      // their eight rows at a time, and four whole lines are stored at once.
+      char* to_row = nullptr;
+      if (live) to_row = part != nullptr ? reinterpret_cast<char*>(part + 4)
+                                         : reinterpret_cast<char*>(a.out + (a.cu_q ? 0 : ws * a.so.seq) + (int64_t)(q0 + tok) * a.so.token + h * a.so.head);
+      auto store_lines = [&](uint32_t (&v)[32], int at) {  // 128 bytes of every row, `at` bytes into it
+        // eight by eight pieces: (lane, piece) and (piece, lane) change places
+        // where bit b of the two differs, for one b after the other
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
+        for (int b = 1; b < 8; b <<= 1) {
+          const bool up = lane & b;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            if (c & b) continue;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t &p = v[4 * c + x], &q = v[4 * (c | b) + x];
+              const uint32_t got = __shfl_xor_sync(kFull, up ? p : q, b);
+              if (up) p = got;
+              else q = got;
+            }
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          char* to = reinterpret_cast<char*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(to_row), (lane & ~7) + c));
+          if (to != nullptr) *reinterpret_cast<uint4*>(to + at + 16 * (lane & 7)) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+        }
+      };
+#pragma unroll 1
+      for (int c = 0; c < 4; c += 2) {
+        uint32_t o[2][32];
         if (any) {
-          tm_ld32(o, 0, to + 32 * c);
+          tm_ld32(o[0], 0, to + 32 * c);
+          tm_ld32(o[1], 0, to + 32 * c + 32);
           tm_wait_ld();
-          if (c == 3) {  // the next item's products may replace it
+          if (c == 2) {  // the next item's products may replace it
             tm_fence_before();
             bar_arrive(o_empty + 8 * i);
           }
         } else {
 #pragma unroll
-          for (int u = 0; u < 32; ++u) o[u] = 0;
+          for (int u = 0; u < 32; ++u) o[0][u] = o[1][u] = 0;
         }
         if (part != nullptr) {
-          if (live)
-#pragma unroll
-            for (int u = 0; u < 32; u += 4)
-              *reinterpret_cast<uint4*>(part + 4 + 32 * c + u) = make_uint4(o[u], o[u + 1], o[u + 2], o[u + 3]);
+          store_lines(o[0], 128 * c);
+          store_lines(o[1], 128 * c + 128);
           continue;
         }
+        uint32_t v[32];
 #pragma unroll
-        for (int u = 0; u < 32; u += 8) {
-          uint32_t p[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint64_t y = mul2(pair2(__uint_as_float(o[u + 2 * x]), __uint_as_float(o[u + 2 * x + 1])), inv2);
-            none = fma2(y, 0, none);
-            float y0, y1;
-            unpair2(y, y0, y1);
-            p[x] = pack_bf16x2(y0, y1);
-          }
-          if (live) *reinterpret_cast<uint4*>(out + 32 * c + u) = make_uint4(p[0], p[1], p[2], p[3]);
+        for (int u = 0; u < 64; u += 2) {
+          const uint64_t y = mul2(pair2(__uint_as_float(o[u >> 5][u & 31]), __uint_as_float(o[u >> 5][(u & 31) + 1])), inv2);
+          none = fma2(y, 0, none);
+          float y0, y1;
+          unpair2(y, y0, y1);
+          v[u / 2] = pack_bf16x2(y0, y1);
         }
+        store_lines(v, 64 * c);
       }
       if (part != nullptr) {
         if (live) {
