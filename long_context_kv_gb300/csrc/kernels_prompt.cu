@@ -607,36 +607,36 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (to != nullptr) *reinterpret_cast<uint4*>(to + at + 16 * (lane & 7)) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
         }
       };
+      // one copy of the code: it runs once an item and is fetched anew
+      const int cols = part != nullptr ? 32 : 64;  // columns in 128 bytes
 #pragma unroll 1
-      for (int c = 0; c < 4; c += 2) {
-        uint32_t o[2][32];
-        if (any) {
-          tm_ld32(o[0], 0, to + 32 * c);
-          tm_ld32(o[1], 0, to + 32 * c + 32);
-          tm_wait_ld();
-          if (c == 2) {  // the next item's products may replace it
-            tm_fence_before();
-            bar_arrive(o_empty + 8 * i);
-          }
-        } else {
-#pragma unroll
-          for (int u = 0; u < 32; ++u) o[0][u] = o[1][u] = 0;
-        }
-        if (part != nullptr) {
-          store_lines(o[0], 128 * c);
-          store_lines(o[1], 128 * c + 128);
-          continue;
-        }
+      for (int c = 0; c < kDim; c += cols) {
         uint32_t v[32];
+        if (!any) {
 #pragma unroll
-        for (int u = 0; u < 64; u += 2) {
-          const uint64_t y = mul2(pair2(__uint_as_float(o[u >> 5][u & 31]), __uint_as_float(o[u >> 5][(u & 31) + 1])), inv2);
-          none = fma2(y, 0, none);
-          float y0, y1;
-          unpair2(y, y0, y1);
-          v[u / 2] = pack_bf16x2(y0, y1);
+          for (int u = 0; u < 32; ++u) v[u] = 0;
+        } else if (part != nullptr) {
+          tm_ld32(v, 0, to + c);
+          tm_wait_ld();
+        } else {
+          uint32_t o[64];
+          tm_ld32(o, 0, to + c);
+          tm_ld32(o, 32, to + c + 32);
+          tm_wait_ld();
+#pragma unroll
+          for (int u = 0; u < 64; u += 2) {
+            const uint64_t y = mul2(pair2(__uint_as_float(o[u]), __uint_as_float(o[u + 1])), inv2);
+            none = fma2(y, 0, none);
+            float y0, y1;
+            unpair2(y, y0, y1);
+            v[u / 2] = pack_bf16x2(y0, y1);
+          }
         }
-        store_lines(v, 64 * c);
+        if (any && c + cols == kDim) {  // the next item's products may replace it
+          tm_fence_before();
+          bar_arrive(o_empty + 8 * i);
+        }
+        store_lines(v, c / cols * 128);
       }
       if (part != nullptr) {
         if (live) {
