@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
     for (int w = 0; w < kWarps4; ++w) {
       // a warp without rows has the sum 0; one whose scores are all NaN has
       // m = -inf too, and a NaN sum
-      const float mw = sh.ml[w][h][0], lw = sh.ml[w][h][1], f = lw == 0.f ? 0.f : exp2f(mw - M);
+      const float mw = sh.ml[w][h][0], lw = sh.ml[w][h][1], f = lw == 0.f ? 0.f : exp2_fast(mw - M);
       L += lw * f;
       O += so[(w * kHeads4 + h) * kDim + dd] * f;
     }
@@ -517,10 +517,11 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
   }
 }
 
-// A warp: the maximum and the sum of one head over its splits.
-__device__ __forceinline__ float2 merge_ml(const float* ph, int nsplit, int lane) {
+// A warp: the maximum and the sum of one head over its splits; `first`: those
+// of split `lane`, which may be anything where there is none.
+__device__ __forceinline__ float2 merge_ml(const float* ph, int nsplit, int lane, float2 first) {
   auto ml_of = [&](int s) { return *reinterpret_cast<const float2*>(ph + (int64_t)s * kPartStride); };
-  const float2 first = lane < nsplit ? ml_of(lane) : make_float2(-INFINITY, 0.f);
+  if (lane >= nsplit) first = make_float2(-INFINITY, 0.f);
   float M = first.x;
   for (int s = lane + 32; s < nsplit; s += 32) M = fmaxf(M, ml_of(s).x);
 #pragma unroll
@@ -552,7 +553,12 @@ __global__ void __launch_bounds__(kFinishThreads, kFinishThreads == 256 ? 3 : 1)
   const int64_t len = kv4_len(a.c, b);
   const int merging = (a.g + per_block - 1) / per_block;
   const int nsplit = len > 0 ? chunk.y : 0;
-  const float* part = a.part + ((int64_t)kvh * a.g * a.nblocks + chunk.x) * kPartStride;
+  // of one sequence the first chunk is known, and its partials are loaded
+  // before their number is: one round trip to memory less
+  const bool one = a.c.batch == 1;
+  const float* part = a.part + (int64_t)kvh * a.g * a.nblocks * kPartStride;
+  if (!one) part += (int64_t)chunk.x * kPartStride;
+  const int limit = one ? a.nblocks : nsplit;
   if ((int)blockIdx.x < merging) {
     const int each = kFinishWarps / per_block, sub = warp % each;
     const int h = blockIdx.x * per_block + warp / each;
@@ -561,25 +567,25 @@ __global__ void __launch_bounds__(kFinishThreads, kFinishThreads == 256 ? 3 : 1)
     constexpr int kAhead = 8;
     float4 x[kAhead];
     float2 ml[kAhead];
-    const int n = live ? nsplit : 0;
+    const int most = live ? limit : 0, n = live ? nsplit : 0;
     auto load = [&](int s0) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int s = s0 + sub + i * each;
-        ml[i] = make_float2(-INFINITY, 0.f);
-        if (s >= n) continue;
+        if (s >= most) continue;
         ml[i] = *reinterpret_cast<const float2*>(ph + (int64_t)s * kPartStride);
         x[i] = *reinterpret_cast<const float4*>(ph + (int64_t)s * kPartStride + 4 + 4 * lane);  // not written without rows
       }
     };
     load(0);
-    const float2 all = merge_ml(ph, n, lane);
+    const float2 first = lane < most ? *reinterpret_cast<const float2*>(ph + (int64_t)lane * kPartStride) : make_float2(0.f, 0.f);
+    const float2 all = merge_ml(ph, n, lane, first);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s0 = 0; s0 < n; s0 += kAhead * each) {
       if (s0 > 0) load(s0);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        if (ml[i].y == 0.f) continue;
+        if (s0 + sub + i * each >= n || ml[i].y == 0.f) continue;
         const float f = exp2_fast(ml[i].x - all.x);
         o.x = fmaf(x[i].x, f, o.x);
         o.y = fmaf(x[i].y, f, o.y);
@@ -622,7 +628,9 @@ __global__ void __launch_bounds__(kFinishThreads, kFinishThreads == 256 ? 3 : 1)
       if (h < a.g) x[h] = *reinterpret_cast<const float4*>(sc + h * a.c.rmax + rv);
   }
   for (int h = warp; h < a.g; h += kFinishWarps) {
-    const float2 all = merge_ml(part + (int64_t)h * a.nblocks * kPartStride, nsplit, lane);
+    const float* ph = part + (int64_t)h * a.nblocks * kPartStride;
+    const float2 first = lane < limit ? *reinterpret_cast<const float2*>(ph + (int64_t)lane * kPartStride) : make_float2(0.f, 0.f);
+    const float2 all = merge_ml(ph, nsplit, lane, first);
     if (lane == 0) sml[h] = make_float2(all.x, all.y != 0.f ? 1.f / all.y : 0.f);
   }
   __syncthreads();
