@@ -34,7 +34,7 @@ constexpr int kMaxWarps = 32;
 constexpr int kEvictMaxBlocks = 8;
 constexpr int kBins = 2048;
 constexpr int kHeldRows = 16384;  // rows of a block whose keys are in shared memory; further ones are read again
-constexpr int kMoves = 8;      // rows that a warp moves at once
+constexpr int kMoves = 16;     // rows that a warp moves at once
 
 struct EvictShared {
   uint32_t hist[3][kBins];
@@ -345,33 +345,40 @@ __global__ void __launch_bounds__(kThreads) k_kv4_evict(EvictArgs a) {
       }
       return __ldcg(l + i);
     };
-    // a warp moves a row in four bytes a lane: its codes, then the rest
+    // a warp moves kMoves rows at once: of each its codes, four bytes a lane,
+    // and of eight together their scales, weights and positions
     uint8_t* const codes_at = (lane < 16 ? a.c.kc : a.c.vc) + base * kCode4 + 4 * (lane & 15);
-    uint32_t* const rest_at = (lane == 0 ? reinterpret_cast<uint32_t*>(a.c.ks) : lane == 1 ? reinterpret_cast<uint32_t*>(a.c.vs)
-                               : lane == 2 ? reinterpret_cast<uint32_t*>(a.c.w) : reinterpret_cast<uint32_t*>(a.c.pos)) + base;
+    const int what = lane & 3;
+    uint32_t* const rest_at = (what == 0 ? reinterpret_cast<uint32_t*>(a.c.ks) : what == 1 ? reinterpret_cast<uint32_t*>(a.c.vs)
+                               : what == 2 ? reinterpret_cast<uint32_t*>(a.c.w) : reinterpret_cast<uint32_t*>(a.c.pos)) + base;
 #pragma unroll 1
     for (uint32_t i0 = (rank * kWarps + warp) * kMoves; i0 < moves; i0 += nb * kWarps * kMoves) {
+      const int here = (int)min(moves - i0, (uint32_t)kMoves);
       int32_t to = 0, from = 0;
-      if (lane < kMoves && i0 + lane < moves) {
+      if (lane < here) {
         to = entry(1, i0 + lane);
         from = entry(2, i0 + lane);
       }
-      uint32_t x[kMoves], y[kMoves];
+      uint32_t x[kMoves], y[kMoves / 8];
 #pragma unroll
       for (int u = 0; u < kMoves; ++u) {
         const int32_t src = __shfl_sync(kFull, from, u);
-        if (i0 + u < moves) {
-          x[u] = *reinterpret_cast<const uint32_t*>(codes_at + (int64_t)src * kCode4);
-          if (lane < 4) y[u] = rest_at[src];
-        }
+        if (u < here) x[u] = *reinterpret_cast<const uint32_t*>(codes_at + (int64_t)src * kCode4);
+      }
+#pragma unroll
+      for (int u = 0; u < kMoves / 8; ++u) {
+        const int32_t src = __shfl_sync(kFull, from, 8 * u + (lane >> 2));
+        if (8 * u + (lane >> 2) < here) y[u] = rest_at[src];
       }
 #pragma unroll
       for (int u = 0; u < kMoves; ++u) {
         const int32_t dst = __shfl_sync(kFull, to, u);
-        if (i0 + u < moves) {
-          *reinterpret_cast<uint32_t*>(codes_at + (int64_t)dst * kCode4) = x[u];
-          if (lane < 4) rest_at[dst] = y[u];
-        }
+        if (u < here) *reinterpret_cast<uint32_t*>(codes_at + (int64_t)dst * kCode4) = x[u];
+      }
+#pragma unroll
+      for (int u = 0; u < kMoves / 8; ++u) {
+        const int32_t dst = __shfl_sync(kFull, to, 8 * u + (lane >> 2));
+        if (8 * u + (lane >> 2) < here) rest_at[dst] = y[u];
       }
     }
   }
