@@ -1,25 +1,36 @@
-// Causal attention over prompts, and the window weights.
+// Causal attention over prompts.
 //
-// k_prompt_attend, one block per 256 query rows of a KV head and a range of
-// its keys.  A query row is a (token, query head) pair with the heads
-// fastest, so the G heads of a KV head share every key and value tile and a
-// tile of rows spans only 128 / G tokens of the diagonal.  Work is split by
-// role:
-//   - a producer thread copies the query tiles and then the 128-key tiles of
-//     K and V with TMA into a ring of shared-memory stages;
-//   - an issuing thread runs the products on the tensor cores: S = Q K^T of
-//     both 128-row tiles into tensor memory, then, as soon as a tile's
-//     weights are there, O += P V (P read from tensor memory, where it
-//     replaces S) and the next S of the same tile;
-//   - two groups of four warps, one per tile, turn S into P, a thread per
-//     row: maximum, exp2, sum, all in registers.
+//   s_ij = <q_i, k_j> / sqrt(d),  j <= i + len_k - len_q,
+//   o_i = sum_j exp(s_ij - m_i) v_j / sum_j exp(s_ij - m_i)
+//
+// with the running maximum m_i of one pass over the keys.  k_prompt_attend has
+// a block per SM that walks items: 256 query rows of a KV head and a range of
+// its keys.  A query row is a (token, query head) pair with the heads fastest,
+// so the G heads of a KV head share every key and value tile and a tile of
+// rows spans only 128 / G tokens of the diagonal.  Work is split by role:
+//   - a producing warp finds the items, longest first, and copies the query
+//     tiles and then the 128-key tiles of K and V with TMA into a ring of
+//     shared-memory stages, the next item's while this one still computes;
+//   - an issuing warp runs the products on the tensor cores: S = Q K^T of both
+//     128-row tiles into tensor memory, then, as soon as a tile's weights are
+//     there, O += P V (P read from tensor memory, where it replaces S) and the
+//     next S of the same tile;
+//   - two groups of four warps, one per tile, turn S into P, a thread per row:
+//     maximum, exp2, sum, all in registers.
 // While one tile is in its softmax the tensor cores work for the other.  The
 // products of a block run in the order of their issue, so S of step j being
 // complete means that O holds steps up to j - 1: a row whose maximum grew by
 // more than 2^8 rescales O right then, and the others do not touch it.
 //
-// Bound by the tensor cores (4 d flops a visible pair): per 128 keys a tile
-// takes 1024 cycles of products and as many of exponentials and conversions.
+// Bound by the tensor cores (4 d flops a visible pair), and right under them
+// by shared memory: a step of both tiles and 128 keys is 2048 cycles of
+// products, whose operands and copies are 256 KB at 128 bytes a cycle, again
+// 2048; it takes 2900 to 3050 (32768 tokens of 8 query heads: 1.36 ms,
+// 1617 TFLOP/s, 0.83 of the measured bf16 rate).  What the steps measured:
+// operands kept in uniform registers by electing the issuing lane, 2474 ->
+// 1446 us there; a block per item instead of per SM, 1468 against 1364 us.  An
+// item's result takes 4000 cycles more, in which its tile's group does nothing
+// else; that is 15 % of a batch of short prompts.
 //
 // What a row does not see has weight 0, but 0 times an infinity or NaN in V
 // is NaN: value rows past the end of a sequence are cleared in shared memory,
