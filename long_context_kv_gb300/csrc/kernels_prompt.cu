@@ -113,7 +113,7 @@ constexpr int kPromptThreads = 384;   // two softmax groups; a group with the is
 // up what the softmax groups, with a whole row of S each, need:
 // 2 x 216 + 72 = 3 x 168.
 constexpr int kSoftmaxRegs = 216, kIssueRegs = 72;
-constexpr int kPartRow = kDim + 4;    // split partial of a row: maximum, sum, -, -, o
+constexpr int kPartRow = kDim + 4;    // partial of a row: maximum, sum, number of its parts, -, o
 constexpr float kGrowth = 8.f;        // a row's maximum may lag this far (base 2): weights stay below 2^8
 constexpr size_t kPromptSmem = (size_t)(kTiles + kStages) * kTileBytes + 1024;
 
@@ -123,7 +123,8 @@ struct PromptMaps {
 
 // A block's piece of work: 256 query rows of a KV head and a range of keys.
 struct PromptItem {
-  int s, kvh, qb, split;
+  int s, kvh, qb;
+  int part, parts;      // of the keys, where several blocks share them
   int q0, lq, k0, lk;
   int t0;               // first token of tile 0
   int jb, end[kTiles];  // key blocks [jb, end) of each tile
@@ -149,6 +150,7 @@ constexpr int kFewSeqs = 64;
 // two numbers of query blocks; of many, where the walk over them has come to
 // (those before s0 have `before` query blocks).
 struct PromptCursor {
+  int64_t units;  // (query block, sequence, KV head)s in all
   int few[kFewSeqs / 32];
   int s0;
   int64_t before;
@@ -162,27 +164,48 @@ __device__ __forceinline__ int seq_blocks(const PromptArgs& a, int s, int tokens
   return blocks_of(min64(lq, a.max_q), tokens);
 }
 
-// Item x of the call (a warp computes it): query blocks in descending order,
-// so that those that see most keys come first, and for each the sequences
-// that have it, KV heads and splits.  Of more than kFewSeqs sequences, their
-// query blocks in turn; x must not decrease then.  False: there is no such item.
-__device__ __forceinline__ bool prompt_item(const PromptArgs& a, int64_t x, PromptCursor& cur, PromptItem& w) {
+// Item `it` of this block (a warp computes it).  False: there is no such item.
+//
+// Units are numbered by query block in descending order, so that those that
+// see most keys come first, and for each the sequences that have it and the KV
+// heads; of more than kFewSeqs sequences, their query blocks in turn.  Where
+// there are units for all blocks, a block takes one of every turn of the grid,
+// every other turn backwards: who had the longest of one turn has the
+// shortest of the next.  Where there are fewer (nsplit > 1), block c of G
+// takes the c-th G-th part of all the units' keys, taken to be equally many:
+// the end of one unit, maybe whole ones, and the beginning of another.
+__device__ __forceinline__ bool prompt_item(const PromptArgs& a, int it, PromptCursor& cur, PromptItem& w) {
   const int lane = threadIdx.x & 31;
   const int tq = kTile / a.g, tokens = kTiles * tq;
-  const int per = a.hkv * a.nsplit;
-  int64_t y = x / per;  // (query block, sequence)
-  int z = (int)(x - y * per);
-  w.split = z % a.nsplit;
-  w.kvh = z / a.nsplit;
+  int64_t x, from_part = 0, to_part = 1, blocks = 1;  // the unit; its keys from from_part / blocks to to_part / blocks
+  w.part = 0;
+  w.parts = 1;
+  if (a.nsplit > 1) {
+    const int64_t c = blockIdx.x, u = cur.units;
+    blocks = min64(gridDim.x, u * (a.nsplit - 1));
+    if (c >= blocks) return false;
+    const int64_t lo = c * u, hi = lo + u;  // in blocks-ths of a unit
+    x = lo / blocks + it;
+    if (x * blocks >= hi) return false;
+    from_part = max64(lo - x * blocks, 0);
+    to_part = min64(hi - x * blocks, blocks);
+    const int64_t first = x * blocks / u, last = ((x + 1) * blocks - 1) / u;
+    w.part = (int)(c - first);
+    w.parts = (int)(last - first + 1);
+  } else {
+    x = (int64_t)it * gridDim.x + (it & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    if (x >= cur.units) return false;
+  }
+  const int64_t y = x / a.hkv;  // (query block, sequence)
+  w.kvh = (int)(x - y * a.hkv);
   if (a.cu_q == nullptr) {
     const int nqb = blocks_of(a.max_q, tokens);
-    if (y >= (int64_t)nqb * a.n_seqs) return false;
     w.qb = nqb - 1 - (int)(y / a.n_seqs);
     w.s = (int)(y % a.n_seqs);
   } else {
     if (a.n_seqs > kFewSeqs) {
       for (;; cur.s0 += 32) {
-        if (cur.s0 >= a.n_seqs) return false;
+        if (cur.s0 >= a.n_seqs) return false;  // not for a unit
         const int n = seq_blocks(a, cur.s0 + lane, tokens);
         const uint32_t inc = warp_incl_scan((uint32_t)n, lane), all = __shfl_sync(kFull, inc, 31);
         const int64_t j = y - cur.before;
@@ -203,7 +226,6 @@ __device__ __forceinline__ bool prompt_item(const PromptArgs& a, int64_t x, Prom
         for (int i = 0; i < kFewSeqs / 32; ++i) n += __reduce_add_sync(kFull, (uint32_t)max(0, cur.few[i] - level));
         return n;
       };
-      if (y >= from(0)) return false;
       int lo = 0, hi = blocks_of(a.max_q, tokens);  // from(lo) > y >= from(hi)
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -245,10 +267,10 @@ __device__ __forceinline__ bool prompt_item(const PromptArgs& a, int64_t x, Prom
     n[i] = seen > 0 ? (int)((seen + kTile - 1) / kTile) : 0;
     most = max(most, n[i]);
   }
-  const int share = (most + a.nsplit - 1) / a.nsplit;
-  w.jb = min(w.split * share, most);
+  w.jb = (int)(most * from_part / blocks);
+  const int to = (int)(most * to_part / blocks);
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i) w.end[i] = max(w.jb, min(n[i], w.jb + share));
+  for (int i = 0; i < kTiles; ++i) w.end[i] = max(w.jb, min(n[i], to));
   return true;
 }
 
@@ -305,14 +327,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       int nq = 0, x = 0;  // query loads, ring loads so far
       bool ok = true;
       PromptCursor cur{};
+      const int tokens = kTiles * tq;
+      if (a.cu_q == nullptr) {
+        cur.units = (int64_t)blocks_of(a.max_q, tokens) * a.n_seqs;
+      } else {
 #pragma unroll
-      for (int i = 0; i < kFewSeqs / 32; ++i)
-        if (a.cu_q != nullptr && a.n_seqs <= kFewSeqs) cur.few[i] = seq_blocks(a, 32 * i + lane, kTiles * tq);
-      // items in turns of the grid, every other turn backwards: who had the
-      // longest of one turn has the shortest of the next
-      auto item = [&](int it, PromptItem& w) {
-        return prompt_item(a, (int64_t)it * gridDim.x + (it & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x), cur, w);
-      };
+        for (int i = 0; i < kFewSeqs / 32; ++i) {
+          cur.few[i] = seq_blocks(a, 32 * i + lane, tokens);
+          cur.units += __reduce_add_sync(kFull, (uint32_t)cur.few[i]);
+        }
+        for (int s0 = kFewSeqs; s0 < a.n_seqs; s0 += 32) cur.units += __reduce_add_sync(kFull, (uint32_t)seq_blocks(a, s0 + lane, tokens));
+      }
+      cur.units *= a.hkv;
+      auto item = [&](int it, PromptItem& w) { return prompt_item(a, it, cur, w); };
       PromptItem w, next;
       bool more = item(0, next);
       for (int it = 0; ok; ++it) {
@@ -481,9 +508,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       float* part = nullptr;
       if (a.nsplit > 1) {
         const int64_t nqb = (a.max_q + kTiles * tq - 1) / (kTiles * tq);
-        part = a.ws + (((((int64_t)ws * a.hkv + w.kvh) * nqb + w.qb) * a.nsplit + w.split) * (kTiles * kTile) + i * kTile + row) * kPartRow;
+        part = a.ws + (((((int64_t)ws * a.hkv + w.kvh) * nqb + w.qb) * a.nsplit + w.part) * (kTiles * kTile) + i * kTile + row) * kPartRow;
       }
       const int k0 = w.k0;
+      if (part != nullptr && live) part[2] = __int_as_float(w.parts);
       __syncwarp();
       if (lane == 0) bar_arrive(item_empty + 8 * (it % kItems));
       float m = -INFINITY, l = 0.f;  // base 2
@@ -675,7 +703,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
 }
 
-// A warp per query row: join the splits' partials.
+// A warp per query row: join the partials.
 __global__ void __launch_bounds__(32 * kRowWarps) k_prompt_join(PromptArgs a, int nqb) {
   pdl_wait();
   pdl_trigger();
@@ -691,11 +719,12 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_prompt_join(PromptArgs a, in
   const int in = (int)(tok - qb * kTiles * tq), row = in / tq * kTile + in % tq * a.g + h % a.g;
   const float* part = a.ws + ((((int64_t)s * a.hkv + kvh) * nqb + qb) * a.nsplit * (kTiles * kTile) + row) * kPartRow;
   const int64_t step = (int64_t)(kTiles * kTile) * kPartRow;
+  const int parts = __float_as_int(part[2]);  // at most nsplit
   float M = -INFINITY;
-  for (int x = 0; x < a.nsplit; ++x) M = fmaxf(M, part[x * step]);
+  for (int x = 0; x < parts; ++x) M = fmaxf(M, part[x * step]);
   float L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-  for (int x = 0; x < a.nsplit; ++x) {
+  for (int x = 0; x < parts; ++x) {
     const float4 v = *reinterpret_cast<const float4*>(part + x * step + 4 + 4 * lane);
     const float2 ml = *reinterpret_cast<const float2*>(part + x * step);
     const float f = ml.y == 0.f ? 0.f : ml.x == M ? 1.f : exp2f(ml.x - M);
@@ -748,11 +777,12 @@ cudaError_t raise_smem() {
 }  // namespace
 
 size_t prompt_workspace_bytes(PromptArgs& a, int sm_count) {
-  // Blocks of rows that do not fill the GPU share their keys among splits,
-  // at least four key blocks each.
+  // Units that do not fill the GPU are shared among blocks, at least four key
+  // blocks to each; a unit's keys then lie in up to nsplit blocks.
   const int64_t units = prompt_blocks(a) * a.n_seqs * a.hkv;
   const int64_t most = std::max<int64_t>(1, (a.max_k + 4 * kTile - 1) / (4 * kTile));
-  a.nsplit = (int)std::min<int64_t>({most, std::max<int64_t>(1, sm_count / units), 64});
+  const int64_t share = std::min<int64_t>({most, (sm_count + units - 1) / units, 63});
+  a.nsplit = units < sm_count && share > 1 ? (int)share + 1 : 1;
   return a.nsplit > 1 ? (size_t)units * a.nsplit * kTiles * kTile * kPartRow * sizeof(float) : 0;
 }
 
@@ -773,7 +803,7 @@ cudaError_t launch_prompt_attend(const PromptArgs& a, int sm_count, cudaStream_t
   // a block per SM walks the items; no more blocks than there can be items
   const int64_t nqb = prompt_blocks(a), tokens = kTiles * (kTile / a.g);
   const int64_t pairs = a.cu_q ? std::min(nqb * a.n_seqs, a.rows_q / tokens + a.n_seqs) : nqb * a.n_seqs;
-  const int64_t blocks = std::min<int64_t>(sm_count, pairs * a.hkv * a.nsplit);
+  const int64_t blocks = std::min<int64_t>(sm_count, pairs * a.hkv * std::max(1, a.nsplit - 1));
   e = launch_pdl(k_prompt_attend, dim3((unsigned)blocks), dim3(kPromptThreads), kPromptSmem, st, a, m);
   if (e != cudaSuccess || a.nsplit == 1) return e;
   const dim3 grid((unsigned)((a.max_q + kRowWarps - 1) / kRowWarps), a.hq, a.n_seqs);

@@ -85,8 +85,8 @@ struct PromptArgs {
   const __nv_bfloat16 *q, *k, *v;
   __nv_bfloat16* out;
   float* lse;  // may be null
-  float* ws;   // split partials
-  int nsplit;
+  float* ws;   // partials of shared units
+  int nsplit;  // blocks that may share a unit of rows; 1: none do
 };
 cudaError_t launch_prompt_attend(const PromptArgs& a, int sm_count, cudaStream_t st);
 size_t prompt_workspace_bytes(PromptArgs& a, int sm_count);  // sets a.nsplit
