@@ -118,10 +118,14 @@ __device__ __forceinline__ uint2 quantise(RowBf16& r, uint32_t& byte) {
     uint32_t x = 0;
 #pragma unroll
     for (int i = 4 * h + 3; i >= 4 * h; --i) {
-      const float hi = fmaf(__uint_as_float(r.w[i] & 0xffff0000u), inv, 1536.f) + (12582920.f - 1536.f);
-      const float lo = fmaf(__uint_as_float(r.w[i] << 16), inv, 1536.f) + (12582920.f - 1536.f);
-      x = (x << 4) + __float_as_uint(hi);
-      x = (x << 4) + __float_as_uint(lo);
+      // both values of the word at once
+      uint32_t lo, hi;
+      asm("{\n .reg .b64 v, f, m, a;\n mov.b64 v, {%2, %3};\n mov.b64 f, {%4, %4};\n mov.b64 m, {%5, %5};\n mov.b64 a, {%6, %6};\n"
+          " fma.rn.f32x2 v, v, f, m;\n add.rn.f32x2 v, v, a;\n mov.b64 {%0, %1}, v;\n}\n"
+          : "=r"(lo), "=r"(hi)
+          : "r"(r.w[i] << 16), "r"(r.w[i] & 0xffff0000u), "f"(inv), "f"(1536.f), "f"(12582920.f - 1536.f));
+      x = (x << 4) + hi;
+      x = (x << 4) + lo;
     }
     word[h] = x - (0x4B400000u + 0xB4000000u + 0x40000000u);
   }
