@@ -34,6 +34,7 @@
 // 6 TB/s and 7 for the start, the first rows' way and the end.  Fewer
 // instructions no longer tell (HFMA2 halved by keys as subnormals: the same),
 // nor do more or fewer warps (12, 16, 20 an SM: within 2 us).
+#include <atomic>
 #include <float.h>
 
 #include <cuda_fp16.h>
@@ -683,7 +684,7 @@ namespace {
 template <int NT>
 cudaError_t launch_attend4(const Attend4Args& a, cudaStream_t st) {
   constexpr int smem = kWarps4 * kDepth4 * (int)sizeof(Step4);
-  static bool done[64];  // the limit belongs to the device; setting it twice is harmless
+  static std::atomic<bool> done[64];  // the limit belongs to the device; setting it twice is harmless
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && !(dev >= 0 && dev < 64 && done[dev])) {

@@ -21,6 +21,7 @@
 // is why it starts only where the keys would no longer fit.  The code is kept
 // short for the same reason: it runs once, and with the keys in registers and
 // every loop unrolled (46 KB) it waited for its instructions longest.
+#include <atomic>
 #include <cooperative_groups.h>
 
 #include "kv4_internal.cuh"
@@ -176,8 +177,11 @@ __global__ void __launch_bounds__(kThreads) k_kv4_evict(EvictArgs a) {
     const bool crowded = protected_rows >= (uint32_t)keep;
     uint32_t want = crowded ? keep : keep - protected_rows;
     uint32_t equal = crowded ? protected_rows : n - protected_rows;  // rows in the range
+    // a decode step drops one row: the last of those with the least key, which
+    // is known without a round (2049 rows: the rounds were 4000 of 12000 cycles)
+    const bool one = n - keep == 1 && !crowded;
 #pragma unroll 1
-    for (int d = 0; d < 3 && !crowded && lo < hi; ++d) {
+    for (int d = 0; d < 3 && !crowded && !one && lo < hi; ++d) {
       if (!kCluster && equal <= 32) {
         // few rows in the range: a warp ranks them
         each([&](int, uint32_t key, bool in) {
@@ -261,7 +265,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_evict(EvictArgs a) {
     const uint32_t least = crowded ? kProtected : lo;
     const uint32_t below = (1u << lane) - 1u;
     uint32_t eq_at = 0;
-    const bool split_tie = equal > want;  // not all of them stay: the first by row
+    const bool split_tie = one || equal > want;  // not all of them stay: the first by row
     if (split_tie) {
       uint32_t eq = 0;
       each([&](int, uint32_t key, bool in) { eq += __popc(__ballot_sync(kFull, in && key == least)); });
@@ -270,12 +274,15 @@ __global__ void __launch_bounds__(kThreads) k_kv4_evict(EvictArgs a) {
       __syncthreads();
       const uint32_t v = sh.warp_a[lane];
       eq_at = __reduce_add_sync(kFull, lane < warp ? v : 0u);
+      uint32_t all = __reduce_add_sync(kFull, v);
       if (kCluster) {
-        const uint32_t all = __reduce_add_sync(kFull, v);
         if (tid == 0) sh.count[0] = all;
         cluster.sync();
-        eq_at += __reduce_add_sync(kFull, lane < rank ? *cluster.map_shared_rank(&sh.count[0], min(lane, nb - 1)) : 0u);
+        const uint32_t of = lane < nb ? *cluster.map_shared_rank(&sh.count[0], min(lane, nb - 1)) : 0u;
+        eq_at += __reduce_add_sync(kFull, lane < rank ? of : 0u);
+        all = __reduce_add_sync(kFull, of);
       }
+      if (one) want = all - 1;
     }
     // holes and tails of 32 rows as bits
     auto sort_out = [&](int i, uint32_t key, bool in, uint32_t& hs, uint32_t& ts) {
@@ -399,7 +406,7 @@ template <bool kCluster, int kThreads>
 cudaError_t launch_evict(const EvictArgs& a, int nb, cudaStream_t st) {
   const int64_t per_block = ((a.c.rmax + nb - 1) / nb + kThreads - 1) / kThreads * kThreads;
   const size_t smem = (size_t)min64(kHeldRows, per_block) * sizeof(uint32_t);
-  static bool done[64];  // the limit belongs to the device; setting it twice is harmless
+  static std::atomic<bool> done[64];  // the limit belongs to the device; setting it twice is harmless
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && !(dev >= 0 && dev < 64 && done[dev])) {

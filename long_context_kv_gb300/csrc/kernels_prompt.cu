@@ -36,6 +36,7 @@
 // is NaN: value rows past the end of a sequence are cleared in shared memory,
 // and a row whose result is not finite is computed again by prompt_row, which
 // reads only what the row sees.
+#include <atomic>
 #include <algorithm>
 
 #include "tc_device.cuh"
@@ -765,7 +766,7 @@ int64_t prompt_blocks(const PromptArgs& a) {  // blocks of query rows of the lon
 // The kernel's shared-memory limit belongs to the device and is set once on
 // each (a second thread doing the same is harmless).
 cudaError_t raise_smem() {
-  static bool done[64];
+  static std::atomic<bool> done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || (dev >= 0 && dev < 64 && done[dev])) return e;

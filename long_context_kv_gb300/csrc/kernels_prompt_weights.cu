@@ -16,6 +16,7 @@
 // exponentials and by shared memory, which the products read at 96 of its 128
 // bytes a cycle (with a product of 128 columns a time it was all 128, and the
 // copies of K waited for it: 23.3 us for 32K keys of 8 KV heads, against 21.3).
+#include <atomic>
 #include <algorithm>
 
 #include "tc_device.cuh"
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
 }
 
 cudaError_t raise_smem() {
-  static bool done[64];
+  static std::atomic<bool> done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || (dev >= 0 && dev < 64 && done[dev])) return e;

@@ -2,6 +2,7 @@
 // checks and launches.  These calls hold no state: sizes that vary live on
 // the device, buffers are the caller's.
 #include <algorithm>
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 
@@ -30,7 +31,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 int sm_count() {
   // asked once per device: the attribute cannot change
-  static int cached[64];
+  static std::atomic<int> cached[64];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 148;
   if (dev < 64 && cached[dev] > 0) return cached[dev];

@@ -315,6 +315,14 @@ def test_eviction_of_one_row_at_a_time():
         c.weights[:, :, 40] = torch.rand(2, 2, device="cuda")
 
 
+@pytest.mark.parametrize("rows", [2, 33, 1500, 9000, 20000])
+def test_eviction_of_one_row_among_equal_ones(rows):
+    c = filled([rows, rows], 2, rows, seed=75)
+    c.weights.fill_(0.25)
+    c.weights[1, 1, rows // 2:] = 0.5
+    check_evict(c, rows - 1, 1 if rows > 2 else 0, 0)
+
+
 def test_eviction_with_odd_weights_and_many_protected_rows():
     c = filled([100], 1, 100, seed=73)
     c.weights.copy_(torch.randn(1, 1, 100, device="cuda"))
