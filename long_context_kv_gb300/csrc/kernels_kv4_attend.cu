@@ -29,11 +29,11 @@
 // by k_kv4_finish, which also turns the scores into weights.  More than eight
 // query heads per KV head are two blocks, each reading the rows.
 //
-// At 131072 rows of 8 KV heads, 4 query heads each (142.6 MB): 35.4 us and 3.5
-// to merge.  The copies alone, with nothing computed, take 30.6: 23.5 at
-// 6 TB/s and 7 for the start, the first rows' way and the end.  Fewer
-// instructions no longer tell (HFMA2 halved by keys as subnormals: the same),
-// nor do more or fewer warps (12, 16, 20 an SM: within 2 us).
+// At 131072 rows of 8 KV heads, 4 query heads each (142.6 MB): 37.6 us with the
+// merge.  The copies alone, with nothing computed, take 30.6: 23.5 at 6 TB/s and
+// 7 for the start, the first rows' way and the end.  Fewer instructions no
+// longer tell (HFMA2 halved by keys as subnormals: the same), nor do more or
+// fewer warps (12, 16, 20 an SM: within 2 us).
 #include <atomic>
 #include <float.h>
 
@@ -51,7 +51,10 @@ constexpr int kThreads4 = 32 * kWarps4;
 constexpr int kRows4 = 32;                     // rows per warp and step
 constexpr int kTile4 = kRows4 * kWarps4;       // rows per block and step
 constexpr int kHeads4 = 8;                     // query heads per block
-constexpr int kDepth4 = 3;                     // steps of a warp's ring
+// Steps of a warp's ring.  Two are enough to keep the rows coming (16 warps an
+// SM, 4.4 KB each on the way) and leave shared memory for the blocks of the
+// kernel that follows: 37.6 us at 131072 rows, 39.5 with three.
+constexpr int kDepth4 = 2;
 constexpr float kGrowth4 = 8.f;                // how far a running maximum may lag, base 2
 constexpr float kUp4 = 7.f, kDown4 = 1.f / 128.f;  // weights are kept 2^7 up
 
@@ -315,11 +318,25 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
 #pragma unroll
   for (int i = 1; i < kDepth4 - 1; ++i) start_copy(i);
   __syncthreads();
-  uint2 qf[8][NT];
+  // Eight heads' fragments are read again at each use, as they would take 32 of
+  // the registers that keep the loads and the unpacking apart (16 ragged
+  // sequences of up to 16384 rows: 40.5 -> 38.2 us).  Four heads' stay in
+  // registers (read again: 38.1 -> 39.2 us at 131072 rows).
+  const uint32_t q_u32 = static_cast<uint32_t>(__cvta_generic_to_shared(&sh.q[0][0][lane]));
+  uint2 q1[8];
+  if constexpr (NT == 1) {
 #pragma unroll
-  for (int s = 0; s < 8; ++s)
-#pragma unroll
-    for (int c = 0; c < NT; ++c) qf[s][c] = sh.q[s][c][lane];
+    for (int s = 0; s < 8; ++s) q1[s] = sh.q[s][0][lane];
+  }
+  auto qf = [&](int s, int c) {
+    if constexpr (NT == 1) {
+      return q1[s];
+    } else {
+      uint2 r;
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(q_u32 + (s * NT + c) * (int)sizeof(sh.q[0][0])));
+      return r;
+    }
+  };
   // a thread's columns: heads hc and hc + 1
   const int hc = NT == 1 ? 2 * (t & 1) : 2 * t;
   const float qs[2] = {sh.qscale[hc], sh.qscale[hc + 1]};
@@ -375,11 +392,17 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
         unpack2(w0, magic, S[0], even[0], odd[0], a0, a2);
         unpack2(w1, magic, S[1], even[1], odd[1], a1, a3);
 #pragma unroll
-        for (int c = 0; c < NT; ++c) mma_f16(d[c], a0, a1, a2, a3, qf[2 * j][c].x, qf[2 * j][c].y);
+        for (int c = 0; c < NT; ++c) {
+          const uint2 q = qf(2 * j, c);
+          mma_f16(d[c], a0, a1, a2, a3, q.x, q.y);
+        }
         unpack2(w0 >> 8, magic, S[0], even[0], odd[0], a0, a2);
         unpack2(w1 >> 8, magic, S[1], even[1], odd[1], a1, a3);
 #pragma unroll
-        for (int c = 0; c < NT; ++c) mma_f16(d[c], a0, a1, a2, a3, qf[2 * j + 1][c].x, qf[2 * j + 1][c].y);
+        for (int c = 0; c < NT; ++c) {
+          const uint2 q = qf(2 * j + 1, c);
+          mma_f16(d[c], a0, a1, a2, a3, q.x, q.y);
+        }
       }
 #pragma unroll
       for (int r = 0; r < 2; ++r)
