@@ -571,7 +571,7 @@ __device__ __forceinline__ float2 merge_ml(const float* ph, int nsplit, int lane
 // all of a warp's loads in flight at once; the others add the weights of four
 // rows a thread, head by head in ascending order.
 template <int kFinishThreads>
-__global__ void __launch_bounds__(kFinishThreads, kFinishThreads == 256 ? 3 : 1) k_kv4_finish(Attend4Args a, int per_block) {
+__global__ void __launch_bounds__(kFinishThreads, kFinishThreads == 256 ? 4 : 1) k_kv4_finish(Attend4Args a, int per_block) {
   constexpr int kFinishWarps = kFinishThreads / 32, kFinishRows = 4 * kFinishThreads;
   __shared__ float2 sml[16];  // maximum, 1 / sum
   __shared__ float4 so[kFinishWarps][32];
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kFinishThreads, kFinishThreads == 256 ? 3 : 1)
     const int h = blockIdx.x * per_block + warp / each;
     const bool live = h < a.g;
     const float* ph = part + (int64_t)h * a.nblocks * kPartStride;
-    constexpr int kAhead = 8;
+    constexpr int kAhead = kFinishThreads == 256 ? 4 : 8;
     float4 x[kAhead];
     float2 ml[kAhead];
     const int most = live ? limit : 0, n = live ? nsplit : 0;
@@ -646,13 +646,14 @@ __global__ void __launch_bounds__(kFinishThreads, kFinishThreads == 256 ? 3 : 1)
   if (r0 >= len) return;
   float* w = a.c.w + (int64_t)blockIdx.y * a.c.rmax;
   const float* sc = a.scores + q0 * a.c.rmax;
-  // rows of whole heads are 16-byte aligned: four a thread, on their way
-  // while the splits are merged
+  // where heads are 16-byte aligned, four rows a thread, on their way while the
+  // splits are merged; of those behind the last, which lie within the same
+  // head, nothing is written
   constexpr int kHeadsAhead = 8;
-  const bool vec = a.c.rmax % 4 == 0 && r0 + kFinishRows <= len;
+  const bool vec = a.c.rmax % 4 == 0;
   const int64_t rv = r0 + 4 * tid;
   float4 x[kHeadsAhead], old = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (vec) {
+  if (vec && rv < len) {
     old = *reinterpret_cast<const float4*>(w + rv);
 #pragma unroll
     for (int h = 0; h < kHeadsAhead; ++h)
@@ -666,6 +667,7 @@ __global__ void __launch_bounds__(kFinishThreads, kFinishThreads == 256 ? 3 : 1)
   }
   __syncthreads();
   if (vec) {
+    if (rv >= len) return;
     float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](const float4& v, int h) {
       const float2 ml = sml[h];
@@ -678,7 +680,14 @@ __global__ void __launch_bounds__(kFinishThreads, kFinishThreads == 256 ? 3 : 1)
     for (int h = 0; h < kHeadsAhead; ++h)
       if (h < a.g) add(x[h], h);
     for (int h = kHeadsAhead; h < a.g; ++h) add(*reinterpret_cast<const float4*>(sc + h * a.c.rmax + rv), h);
-    *reinterpret_cast<float4*>(w + rv) = make_float4(old.x + p.x, old.y + p.y, old.z + p.z, old.w + p.w);
+    p = make_float4(old.x + p.x, old.y + p.y, old.z + p.z, old.w + p.w);
+    if (rv + 4 <= len) {
+      *reinterpret_cast<float4*>(w + rv) = p;
+      return;
+    }
+    w[rv] = p.x;
+    if (rv + 1 < len) w[rv + 1] = p.y;
+    if (rv + 2 < len) w[rv + 2] = p.z;
     return;
   }
   for (int64_t r = r0 + tid; r < r1; r += kFinishThreads) {
