@@ -44,6 +44,7 @@ struct EvictShared {
   uint32_t nfew;
   uint32_t lo, hi, held;        // this block's least and greatest key, its protected rows
   uint32_t all_lo, all_hi, all_held;
+  uint32_t drop;                // one row to drop: its index + 1, if it may be in this block
   uint32_t bin, above, in_bin;
   uint32_t count[3];            // this block's rows with the threshold key; its holes; its tails
   uint32_t blocks[3][kEvictMaxBlocks];
@@ -56,7 +57,7 @@ __device__ __forceinline__ uint32_t evict_key(float w, int32_t pos, int64_t sink
 }
 
 template <bool kCluster, int kThreads>
-__global__ void __launch_bounds__(kThreads) k_kv4_evict(EvictArgs a) {
+__global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 1) k_kv4_evict(EvictArgs a) {
   constexpr int kWarps = kThreads / 32;
   constexpr int kBinsPer = kBins / kThreads < 4 ? 4 : kBins / kThreads;  // bins of a thread
   extern __shared__ uint32_t keys[];
@@ -71,7 +72,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_evict(EvictArgs a) {
   for (int i = tid; i < 3 * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
   if (tid == 0) {
     sh.lo = 0xFFFFFFFFu;
-    sh.hi = sh.held = sh.nfew = 0;
+    sh.hi = sh.held = sh.nfew = sh.drop = 0;
   }
   if (tid < kMaxWarps) sh.warp_a[tid] = sh.warp_b[tid] = 0;  // what warps that are not there count
   pdl_wait();
@@ -94,10 +95,11 @@ __global__ void __launch_bounds__(kThreads) k_kv4_evict(EvictArgs a) {
     const int room = (int)max64(min64(keep - first, (int64_t)mine * 32), 0);  // and below keep: < room
     const int heldi = min(mine, kHeldRows / kThreads);
     uint32_t* mykeys = keys + warp * heldi * 32;
-    uint32_t lo = 0xFFFFFFFFu, hi = 0, prot = 0;
-    auto take = [&](uint32_t key) {
+    uint32_t lo = 0xFFFFFFFFu, hi = 0, prot = 0, lo_at = 0;  // lo_at: the last row with the key lo
+    auto take = [&](uint32_t key, uint32_t row) {  // a thread's rows ascend
       if (key == kProtected) ++prot;
       else {
+        if (key <= lo) lo_at = row;
         lo = min(lo, key);
         hi = max(hi, key);
       }
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_evict(EvictArgs a) {
         if (u < here) {
           const uint32_t key = evict_key(wv[u], pv[u], a.sink, recent_from);
           mykeys[32 * (i0 + u) + lane] = key;
-          take(key);
+          take(key, (uint32_t)first + 32 * (i0 + u) + lane);
         }
     }
     auto each = [&](auto&& f) {  // f(i, key, whether the row is there): whole warps, rows ascending
@@ -137,14 +139,17 @@ __global__ void __launch_bounds__(kThreads) k_kv4_evict(EvictArgs a) {
 #pragma unroll 1
     for (int i = heldi; i < mine; ++i) {
       const int x = 32 * i + lane;
-      if (x < end) take(evict_key(w[first + x], pos[first + x], a.sink, recent_from));
+      if (x < end) take(evict_key(w[first + x], pos[first + x], a.sink, recent_from), (uint32_t)first + x);
     }
-    lo = __reduce_min_sync(kFull, lo);
+    const uint32_t warp_lo = __reduce_min_sync(kFull, lo);
+    lo_at = __reduce_max_sync(kFull, lo == warp_lo ? lo_at : 0u);
     hi = __reduce_max_sync(kFull, hi);
     prot = __reduce_add_sync(kFull, prot);
     __syncthreads();
     if (lane == 0) {
-      atomicMin(&sh.lo, lo);
+      sh.warp_a[warp] = warp_lo;
+      sh.warp_b[warp] = lo_at;
+      atomicMin(&sh.lo, warp_lo);
       atomicMax(&sh.hi, hi);
       atomicAdd(&sh.held, prot);
     }
@@ -177,174 +182,180 @@ __global__ void __launch_bounds__(kThreads) k_kv4_evict(EvictArgs a) {
     const bool crowded = protected_rows >= (uint32_t)keep;
     uint32_t want = crowded ? keep : keep - protected_rows;
     uint32_t equal = crowded ? protected_rows : n - protected_rows;  // rows in the range
-    // a decode step drops one row: the last of those with the least key, which
-    // is known without a round (2049 rows: the rounds were 4000 of 12000 cycles)
+    uint32_t moves, drop = 0;
+    // A decode step drops one row, the last of those with the least key, and
+    // the one row above `keep` takes its place: neither rounds nor lists
+    // (a step of 2049 rows 18.5 -> 15.8 us, of 32 x 4097 67.2 -> 62.5).
     const bool one = n - keep == 1 && !crowded;
+    if (one) {
+      if (lane == 0 && sh.warp_a[warp] == lo) atomicMax(&sh.drop, sh.warp_b[warp] + 1);
+      sync_all();
+      drop = (kCluster ? __reduce_max_sync(kFull, lane < nb ? *cluster.map_shared_rank(&sh.drop, lane) : 0u) : sh.drop) - 1;
+      moves = drop != (uint32_t)keep;
+    } else {
 #pragma unroll 1
-    for (int d = 0; d < 3 && !crowded && !one && lo < hi; ++d) {
-      if (!kCluster && equal <= 32) {
-        // few rows in the range: a warp ranks them
-        each([&](int, uint32_t key, bool in) {
-          if (in && key >= lo && key <= hi) sh.few[atomicAdd(&sh.nfew, 1u)] = key;
-        });
-        __syncthreads();
-        if (warp == 0) {
-          const uint32_t own = lane < equal ? sh.few[lane] : 0u;
-          uint32_t larger = 0, same = 0;
-          for (uint32_t i = 0; i < equal; ++i) {
-            const uint32_t k = __shfl_sync(kFull, own, i);
-            larger += k > own;
-            same += k == own;
+      for (int d = 0; d < 3 && !crowded && lo < hi; ++d) {
+        if (!kCluster && equal <= 32) {
+          // few rows in the range: a warp ranks them
+          each([&](int, uint32_t key, bool in) {
+            if (in && key >= lo && key <= hi) sh.few[atomicAdd(&sh.nfew, 1u)] = key;
+          });
+          __syncthreads();
+          if (warp == 0) {
+            const uint32_t own = lane < equal ? sh.few[lane] : 0u;
+            uint32_t larger = 0, same = 0;
+            for (uint32_t i = 0; i < equal; ++i) {
+              const uint32_t k = __shfl_sync(kFull, own, i);
+              larger += k > own;
+              same += k == own;
+            }
+            // the key that the wanted row has
+            if (lane < equal && larger < want && larger + same >= want) {
+              sh.bin = own;
+              sh.above = larger;
+              sh.in_bin = same;
+            }
           }
-          // the key that the wanted row has
-          if (lane < equal && larger < want && larger + same >= want) {
-            sh.bin = own;
-            sh.above = larger;
-            sh.in_bin = same;
+          __syncthreads();
+          lo = hi = sh.bin;
+          want -= sh.above;
+          equal = sh.in_bin;
+          break;
+        }
+        // keys lo .. hi in bins of 2^shift
+        const int shift = max(0, 32 - __clz(hi - lo) - 11);
+        each([&](int, uint32_t key, bool in) {
+          if (in && key >= lo && key <= hi) atomicAdd(&sh.hist[d][(key - lo) >> shift], 1u);
+        });
+        sync_all();
+        // a thread's bins, from the top
+        uint32_t c[kBinsPer];
+#pragma unroll
+        for (int i = 0; i < kBinsPer; ++i) c[i] = 0;
+        const int b0 = kBins - kBinsPer - kBinsPer * tid;
+        if (tid < kBins / kBinsPer) {
+#pragma unroll
+          for (int q = 0; q < kBinsPer; q += 4) {
+            const uint32_t* bins = &sh.hist[d][b0 + kBinsPer - 4 - q];
+            uint4 v[kCluster ? kEvictMaxBlocks : 1];
+#pragma unroll
+            for (int i = 0; i < (kCluster ? kEvictMaxBlocks : 1); ++i)
+              v[i] = !kCluster ? *reinterpret_cast<const uint4*>(bins)
+                     : i < nb ? *reinterpret_cast<const uint4*>(cluster.map_shared_rank(bins, i)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < (kCluster ? kEvictMaxBlocks : 1); ++i) {
+              c[q] += v[i].w;
+              c[q + 1] += v[i].z;
+              c[q + 2] += v[i].y;
+              c[q + 3] += v[i].x;
+            }
           }
         }
+        uint32_t sum = 0;
+#pragma unroll
+        for (int i = 0; i < kBinsPer; ++i) sum += c[i];
+        const uint32_t inc = warp_incl_scan(sum, lane);
+        if (lane == 31) sh.warp_a[warp] = inc;
         __syncthreads();
-        lo = hi = sh.bin;
+        uint32_t before = __reduce_add_sync(kFull, lane < warp ? sh.warp_a[lane] : 0u) + inc - sum;
+#pragma unroll
+        for (int i = 0; i < kBinsPer; ++i) {
+          if (before < want && before + c[i] >= want) {
+            sh.bin = b0 + kBinsPer - 1 - i;
+            sh.above = before;
+            sh.in_bin = c[i];
+          }
+          before += c[i];
+        }
+        __syncthreads();
+        const uint32_t bin_lo = lo + (sh.bin << shift);
+        hi = min(hi, bin_lo + ((1u << shift) - 1u));
+        lo = bin_lo;
         want -= sh.above;
         equal = sh.in_bin;
-        break;
       }
-      // keys lo .. hi in bins of 2^shift
-      const int shift = max(0, 32 - __clz(hi - lo) - 11);
-      each([&](int, uint32_t key, bool in) {
-        if (in && key >= lo && key <= hi) atomicAdd(&sh.hist[d][(key - lo) >> shift], 1u);
-      });
-      sync_all();
-      // a thread's bins, from the top
-      uint32_t c[kBinsPer];
-#pragma unroll
-      for (int i = 0; i < kBinsPer; ++i) c[i] = 0;
-      const int b0 = kBins - kBinsPer - kBinsPer * tid;
-      if (tid < kBins / kBinsPer) {
-#pragma unroll
-        for (int q = 0; q < kBinsPer; q += 4) {
-          const uint32_t* bins = &sh.hist[d][b0 + kBinsPer - 4 - q];
-          uint4 v[kCluster ? kEvictMaxBlocks : 1];
-#pragma unroll
-          for (int i = 0; i < (kCluster ? kEvictMaxBlocks : 1); ++i)
-            v[i] = !kCluster ? *reinterpret_cast<const uint4*>(bins)
-                   : i < nb ? *reinterpret_cast<const uint4*>(cluster.map_shared_rank(bins, i)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < (kCluster ? kEvictMaxBlocks : 1); ++i) {
-            c[q] += v[i].w;
-            c[q + 1] += v[i].z;
-            c[q + 2] += v[i].y;
-            c[q + 3] += v[i].x;
-          }
-        }
-      }
-      uint32_t sum = 0;
-#pragma unroll
-      for (int i = 0; i < kBinsPer; ++i) sum += c[i];
-      const uint32_t inc = warp_incl_scan(sum, lane);
-      if (lane == 31) sh.warp_a[warp] = inc;
-      __syncthreads();
-      uint32_t before = __reduce_add_sync(kFull, lane < warp ? sh.warp_a[lane] : 0u) + inc - sum;
-#pragma unroll
-      for (int i = 0; i < kBinsPer; ++i) {
-        if (before < want && before + c[i] >= want) {
-          sh.bin = b0 + kBinsPer - 1 - i;
-          sh.above = before;
-          sh.in_bin = c[i];
-        }
-        before += c[i];
-      }
-      __syncthreads();
-      const uint32_t bin_lo = lo + (sh.bin << shift);
-      hi = min(hi, bin_lo + ((1u << shift) - 1u));
-      lo = bin_lo;
-      want -= sh.above;
-      equal = sh.in_bin;
-    }
-    // the threshold: rows above it stay, and the first `want` of those on it
-    const uint32_t least = crowded ? kProtected : lo;
-    const uint32_t below = (1u << lane) - 1u;
-    uint32_t eq_at = 0;
-    const bool split_tie = one || equal > want;  // not all of them stay: the first by row
-    if (split_tie) {
-      uint32_t eq = 0;
-      each([&](int, uint32_t key, bool in) { eq += __popc(__ballot_sync(kFull, in && key == least)); });
-      __syncthreads();
-      if (lane == 0) sh.warp_a[warp] = eq;
-      __syncthreads();
-      const uint32_t v = sh.warp_a[lane];
-      eq_at = __reduce_add_sync(kFull, lane < warp ? v : 0u);
-      uint32_t all = __reduce_add_sync(kFull, v);
-      if (kCluster) {
-        if (tid == 0) sh.count[0] = all;
-        cluster.sync();
-        const uint32_t of = lane < nb ? *cluster.map_shared_rank(&sh.count[0], min(lane, nb - 1)) : 0u;
-        eq_at += __reduce_add_sync(kFull, lane < rank ? of : 0u);
-        all = __reduce_add_sync(kFull, of);
-      }
-      if (one) want = all - 1;
-    }
-    // holes and tails of 32 rows as bits
-    auto sort_out = [&](int i, uint32_t key, bool in, uint32_t& hs, uint32_t& ts) {
-      bool k = key >= least;
+      // the threshold: rows above it stay, and the first `want` of those on it
+      const uint32_t least = crowded ? kProtected : lo;
+      const uint32_t below = (1u << lane) - 1u;
+      uint32_t eq_at = 0;
+      const bool split_tie = equal > want;  // not all of them stay: the first by row
       if (split_tie) {
-        const uint32_t eqs = __ballot_sync(kFull, in && key == least);
-        k = key > least || (key == least && eq_at + __popc(eqs & below) < want);
-        eq_at += __popc(eqs);
+        uint32_t eq = 0;
+        each([&](int, uint32_t key, bool in) { eq += __popc(__ballot_sync(kFull, in && key == least)); });
+        __syncthreads();
+        if (lane == 0) sh.warp_a[warp] = eq;
+        __syncthreads();
+        const uint32_t v = sh.warp_a[lane];
+        eq_at = __reduce_add_sync(kFull, lane < warp ? v : 0u);
+        if (kCluster) {
+          const uint32_t all = __reduce_add_sync(kFull, v);
+          if (tid == 0) sh.count[0] = all;
+          cluster.sync();
+          eq_at += __reduce_add_sync(kFull, lane < rank ? *cluster.map_shared_rank(&sh.count[0], min(lane, nb - 1)) : 0u);
+        }
       }
-      const bool low = 32 * i + lane < room;
-      hs = __ballot_sync(kFull, in && !k && low);
-      ts = __ballot_sync(kFull, in && k && !low);
-    };
-    uint32_t holes = 0, tails = 0;
-    const uint32_t eq_start = eq_at;
-    each([&](int i, uint32_t key, bool in) {
-      uint32_t hs, ts;
-      sort_out(i, key, in, hs, ts);
-      holes += __popc(hs);
-      tails += __popc(ts);
-    });
-    __syncthreads();
-    if (lane == 0) {
-      sh.warp_a[warp] = holes;
-      sh.warp_b[warp] = tails;
-    }
-    __syncthreads();
-    const uint32_t ha = sh.warp_a[lane], ta = sh.warp_b[lane];
-    uint32_t hole_at = __reduce_add_sync(kFull, lane < warp ? ha : 0u), tail_at = __reduce_add_sync(kFull, lane < warp ? ta : 0u);
-    const uint32_t block_holes = __reduce_add_sync(kFull, ha), block_tails = __reduce_add_sync(kFull, ta);
-    if (tid == 0) {
-      sh.count[1] = block_holes;
-      sh.count[2] = block_tails;
-    }
-    int32_t* list = a.list + (int64_t)bh * 2 * a.c.rmax;
-    eq_at = eq_start;
-    if (holes + tails > 0)  // of the warp
+      // holes and tails of 32 rows as bits
+      auto sort_out = [&](int i, uint32_t key, bool in, uint32_t& hs, uint32_t& ts) {
+        bool k = key >= least;
+        if (split_tie) {
+          const uint32_t eqs = __ballot_sync(kFull, in && key == least);
+          k = key > least || (key == least && eq_at + __popc(eqs & below) < want);
+          eq_at += __popc(eqs);
+        }
+        const bool low = 32 * i + lane < room;
+        hs = __ballot_sync(kFull, in && !k && low);
+        ts = __ballot_sync(kFull, in && k && !low);
+      };
+      uint32_t holes = 0, tails = 0;
+      const uint32_t eq_start = eq_at;
       each([&](int i, uint32_t key, bool in) {
         uint32_t hs, ts;
         sort_out(i, key, in, hs, ts);
-        const int32_t r = (int32_t)first + 32 * i + lane;
-        if (hs >> lane & 1u) list[r0 + hole_at + __popc(hs & below)] = r;
-        if (ts >> lane & 1u) list[a.c.rmax + r0 + tail_at + __popc(ts & below)] = r;
-        hole_at += __popc(hs);
-        tail_at += __popc(ts);
+        holes += __popc(hs);
+        tails += __popc(ts);
       });
-    __threadfence();
-    sync_all();
-    // move i of the cluster: tail i into hole i; 16 threads a move
-    uint32_t moves = block_holes;
-    if (kCluster) {
-      if (tid < kEvictMaxBlocks) {
-        sh.blocks[1][tid] = tid < nb ? *cluster.map_shared_rank(&sh.count[1], tid) : 0u;
-        sh.blocks[2][tid] = tid < nb ? *cluster.map_shared_rank(&sh.count[2], tid) : 0u;
+      __syncthreads();
+      if (lane == 0) {
+        sh.warp_a[warp] = holes;
+        sh.warp_b[warp] = tails;
       }
       __syncthreads();
-      moves = 0;
-      for (int i = 0; i < nb; ++i) moves += sh.blocks[1][i];
+      const uint32_t ha = sh.warp_a[lane], ta = sh.warp_b[lane];
+      uint32_t hole_at = __reduce_add_sync(kFull, lane < warp ? ha : 0u), tail_at = __reduce_add_sync(kFull, lane < warp ? ta : 0u);
+      const uint32_t block_holes = __reduce_add_sync(kFull, ha), block_tails = __reduce_add_sync(kFull, ta);
+      if (tid == 0) {
+        sh.count[1] = block_holes;
+        sh.count[2] = block_tails;
+      }
+      eq_at = eq_start;
+      int32_t* list = a.list + (int64_t)bh * 2 * a.c.rmax;
+      if (holes + tails > 0)  // of the warp
+        each([&](int i, uint32_t key, bool in) {
+          uint32_t hs, ts;
+          sort_out(i, key, in, hs, ts);
+          const int32_t r = (int32_t)first + 32 * i + lane;
+          if (hs >> lane & 1u) list[r0 + hole_at + __popc(hs & below)] = r;
+          if (ts >> lane & 1u) list[a.c.rmax + r0 + tail_at + __popc(ts & below)] = r;
+          hole_at += __popc(hs);
+          tail_at += __popc(ts);
+        });
+      __threadfence();
+      sync_all();
+      moves = block_holes;
+      if (kCluster) {
+        if (tid < kEvictMaxBlocks) {
+          sh.blocks[1][tid] = tid < nb ? *cluster.map_shared_rank(&sh.count[1], tid) : 0u;
+          sh.blocks[2][tid] = tid < nb ? *cluster.map_shared_rank(&sh.count[2], tid) : 0u;
+        }
+        __syncthreads();
+        moves = 0;
+        for (int i = 0; i < nb; ++i) moves += sh.blocks[1][i];
+      }
     }
+    // move i of the cluster: tail i into hole i
     // entry i of a list whose pieces start at the blocks' slices
     auto entry = [&](int which, uint32_t i) -> int32_t {
-      const int32_t* l = list + (which == 2 ? a.c.rmax : 0);
+      const int32_t* l = a.list + ((int64_t)bh * 2 + (which == 2)) * a.c.rmax;
       if (kCluster) {
         int blk = 0;
         for (; blk + 1 < nb && i >= sh.blocks[which][blk]; ++blk) i -= sh.blocks[which][blk];
@@ -363,8 +374,8 @@ __global__ void __launch_bounds__(kThreads) k_kv4_evict(EvictArgs a) {
       const int here = (int)min(moves - i0, (uint32_t)kMoves);
       int32_t to = 0, from = 0;
       if (lane < here) {
-        to = entry(1, i0 + lane);
-        from = entry(2, i0 + lane);
+        to = one ? (int32_t)drop : entry(1, i0 + lane);
+        from = one ? keep : entry(2, i0 + lane);
       }
       uint32_t x[kMoves], y[kMoves / 8];
 #pragma unroll
