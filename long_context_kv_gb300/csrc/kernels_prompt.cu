@@ -135,7 +135,7 @@ constexpr int kItems = 4;
 
 struct PromptShared {
   uint64_t q_full, q_empty, full[kStages], empty[kStages], s_full[kTiles], p_full[2 * kTiles], o_full[kTiles], o_empty[kTiles];
-  uint64_t item_full[kItems], item_empty[kItems];
+  uint64_t item_full[kItems], item_empty[kItems], drained;
   PromptItem items[kItems];  // s < 0: no more
   uint32_t tmem;
   uint32_t gave_up;
@@ -300,6 +300,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       bar_init(o_full + 8 * i, 1);
       bar_init(o_empty + 8 * i, kTile);
     }
+    bar_init(smem_u32(&sh.drained), 1);
     for (int i = 0; i < kItems; ++i) {
       bar_init(item_full + 8 * i, 1);
       bar_init(item_empty + 8 * i, 9);  // the issuing warp and eight softmax warps
@@ -479,8 +480,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           x += 2;
         }
       }
-      // the last products and their signals have arrived before the block ends
-      if (ok && x > 0) wait(empty + 8 * ((x - 1) % kStages), ((x - 1) / kStages) & 1);
+      mma_drain(smem_u32(&sh.drained));
     }
   } else {
     // ---- softmax of tile i, a row per thread

@@ -32,7 +32,7 @@ constexpr int kQHalf = kWRows * 128;   // 64 channels of a chunk
 constexpr size_t kWSmem = (size_t)kWStages * kKeyBytes + 2 * kQHalf + 1024;
 
 struct WeightShared {
-  uint64_t q_full, q_empty, k_full[kWStages], k_empty[kWStages], s_full[2], s_empty[2], part_full[4];
+  uint64_t q_full, q_empty, k_full[kWStages], k_empty[kWStages], s_full[2], s_empty[2], part_full[4], drained;
   uint32_t tmem, gave_up;
   float part[4][kTile];  // the second group's sums
   __align__(16) float lse[kWRows];  // base 2, negative
@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     sh.gave_up = 0;
     bar_init(q_full, 1);
     bar_init(q_empty, 1);
+    bar_init(smem_u32(&sh.drained), 1);
     for (int i = 0; i < kWStages; ++i) {
       bar_init(k_full + 8 * i, 1);
       bar_init(k_empty + 8 * i, 1);
@@ -150,8 +151,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       }
       __syncwarp();
     }
-    // the last signals have arrived before the block ends
-    if (ok) wait(q_empty, (nchunk - 1) & 1);
+    mma_drain(smem_u32(&sh.drained));
   } else if (warp < 8) {
     const int grp = warp >> 2, row = tid & (kTile - 1);
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;

@@ -24,7 +24,9 @@ paris_status fail(paris_status st, const char* fmt, ...) {
 }
 
 paris_status launched(cudaError_t e, const char* what) {
-  return e == cudaSuccess ? PARIS_OK : fail(PARIS_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+  if (e == cudaSuccess) return PARIS_OK;
+  cudaGetLastError();  // reported here, not by the caller's next call
+  return fail(PARIS_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

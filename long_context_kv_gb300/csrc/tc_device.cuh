@@ -100,6 +100,14 @@ __device__ __forceinline__ bool elect() {
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
 }
+// A whole warp: the products that it issued are over, and their signals have
+// arrived, before the block ends (also after a wait that gave up).
+__device__ __forceinline__ void mma_drain(uint32_t bar) {
+  if (elect()) mma_commit(bar);
+  __syncwarp();
+  const uint64_t t0 = now_ns();
+  while (!bar_try(bar, 0) && now_ns() - t0 < kWaitNs) {}
+}
 __device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
