@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -299,26 +300,44 @@ class Context:
 # checked with as few calls into torch as it takes, and pointers go to the
 # library as plain integers.
 HEAD_DIM = 128
+_torch = None  # torch, from the first call that needs it on
+_codes = {}    # its dtypes' codes
+# paris_prompt and paris_strides: packing is quicker than filling a ctypes structure
+_PROMPT, _STRIDES = struct.Struct("4i2q2P2q12q"), struct.Struct("3q")
+
+
+def _with_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _codes.update({torch.float32: PARIS_F32, torch.bfloat16: PARIS_BF16})
+        _torch = torch
+    return _torch
+
+
+def _code(t):
+    """The code of a tensor's dtype, when torch is there already."""
+    c = _codes.get(t.dtype)
+    return _dtype_code(t) if c is None else c
 
 
 def _on(index, *tensors):
     """Every tensor on CUDA device `index`, and that the current one."""
-    import torch
     for t in tensors:
         if t is not None and t.get_device() != index:
             raise ValueError(f"tensors on different devices: {t.device} and cuda:{index}")
     if index < 0:
         raise ValueError("tensors must be on a CUDA device")
-    if torch._C._cuda_getDevice() != index:
-        raise ValueError(f"the tensors are on cuda:{index}, the current device is cuda:{torch._C._cuda_getDevice()}")
+    now = (_torch or _with_torch())._C._cuda_getDevice()
+    if now != index:
+        raise ValueError(f"the tensors are on cuda:{index}, the current device is cuda:{now}")
 
 
 def _raw_stream(index, stream):
     """The stream's handle: the one given, or the device's current one."""
     if stream is not None:
         return stream.cuda_stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(index)
+    return (_torch or _with_torch())._C._cuda_getCurrentRawStream(index)
 
 
 def _flat(t):
@@ -353,7 +372,7 @@ def _heads(t, name, packed):
 
 def _scratch(nbytes, device, stream):
     """Scratch of one call, from the caching allocator of the call's stream."""
-    import torch
+    torch = _torch or _with_torch()
     if stream is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     with torch.cuda.stream(stream):
@@ -361,7 +380,8 @@ def _scratch(nbytes, device, stream):
 
 
 def _prompt(q, k, cu_q, cu_k, max_q, max_k, v=None, out=None):
-    import torch
+    """A checked paris_prompt, its query heads, query rows, KV heads and key rows, and whether it is packed."""
+    torch = _torch or _with_torch()
     bf16 = torch.bfloat16
     if (cu_q is None) != (cu_k is None):
         raise ValueError("cu_q and cu_k must both be given or both be None")
@@ -374,10 +394,10 @@ def _prompt(q, k, cu_q, cu_k, max_q, max_k, v=None, out=None):
     rows_k, hkv, k_seqs, ks = _heads(k, "k", packed)
     if k_seqs != seqs:
         raise ValueError(f"q and k: batches of {seqs} and {k_seqs}")
-    starts_q = starts_k = None
+    starts_q = starts_k = 0
     if packed:
         for c, name in ((cu_q, "cu_q"), (cu_k, "cu_k")):
-            if c.dtype != torch.int32 or c.dim() != 1 or not c.is_contiguous() or c.shape != cu_q.shape or not c.numel():
+            if c.dtype is not torch.int32 or c.dim() != 1 or not c.is_contiguous() or c.shape != cu_q.shape or not c.numel():
                 raise ValueError(f"{name}: a contiguous int32 tensor of n + 1 starts, as many for q as for k")
         seqs, starts_q, starts_k = cu_q.numel() - 1, cu_q.data_ptr(), cu_k.data_ptr()
     vs = os_ = (0, 0, 0)
@@ -389,8 +409,8 @@ def _prompt(q, k, cu_q, cu_k, max_q, max_k, v=None, out=None):
         if out.shape != q.shape:
             raise ValueError(f"out: shape {tuple(out.shape)}, expected {tuple(q.shape)}")
         os_ = _heads(out, "out", packed)[3]
-    return paris_prompt(seqs, hq, hkv, HEAD_DIM, rows_q, rows_k, starts_q, starts_k,
-                        rows_q if max_q is None else max_q, rows_k if max_k is None else max_k, qs, ks, vs, os_), packed
+    return _PROMPT.pack(seqs, hq, hkv, HEAD_DIM, rows_q, rows_k, starts_q, starts_k, rows_q if max_q is None else max_q,
+                        rows_k if max_k is None else max_k, *qs, *ks, *vs, *os_), hq, rows_q, hkv, rows_k, packed
 
 
 def _raw(t):
@@ -405,18 +425,18 @@ def paris_prompt_attend(q, k, v, out, cu_q=None, cu_k=None, max_q=None, max_k=No
     Any strides with a contiguous last dimension and 16-byte aligned rows.  lse: float32 [Hq, rows_q] or
     [batch, Hq, T], or None.
     """
-    import torch
-    p, packed = _prompt(q, k, cu_q, cu_k, max_q, max_k, v, out)
+    p, hq, rows_q, _, _, packed = _prompt(q, k, cu_q, cu_k, max_q, max_k, v, out)
     index = q.get_device()
     if lse is not None:
-        _on(index, lse)
-        _shaped(lse, "lse", (p.n_q_heads, p.rows_q) if packed else q.shape[:3], torch.float32)
+        if lse.get_device() != index:
+            _on(index, lse)
+        _shaped(lse, "lse", (hq, rows_q) if packed else q.shape[:3], _torch.float32)
     lib = _lib or load()
-    ref = ctypes.byref(p)
     n = ctypes.c_size_t()
-    _check(lib.paris_prompt_workspace(ref, ctypes.byref(n)))
-    ws = _scratch(n.value, q.device, stream) if n.value else None
-    _check(lib.paris_prompt_attend(ref, _raw(q), _raw(k), _raw(v), PARIS_BF16, _raw(out), _flat(lse), _raw(ws), n.value,
+    _check(lib.paris_prompt_workspace(p, ctypes.byref(n)))
+    need = n.value
+    ws = _scratch(need, q.device, stream) if need else None
+    _check(lib.paris_prompt_attend(p, _raw(q), _raw(k), _raw(v), PARIS_BF16, _raw(out), _flat(lse), _raw(ws), need,
                                    _raw_stream(index, stream)))
 
 
@@ -429,13 +449,12 @@ def paris_prompt_weights(q, k, lse, weights, window, cu_q=None, cu_k=None, max_k
     """weights[h, j]: the softmax weights that each sequence's last `window` queries give to its key j, added up over
     them and over the query heads of KV head h.  lse as paris_prompt_attend gives it; weights: float32 [Hkv, rows_k]
     (packed) or [batch, Hkv, T]."""
-    import torch
-    p, packed = _prompt(q, k, cu_q, cu_k, None, max_k)
+    p, hq, rows_q, hkv, rows_k, packed = _prompt(q, k, cu_q, cu_k, None, max_k)
     index = q.get_device()
     _on(index, lse, weights)
-    _shaped(lse, "lse", (p.n_q_heads, p.rows_q) if packed else q.shape[:3], torch.float32)
-    _shaped(weights, "weights", (p.n_kv_heads, p.rows_k) if packed else k.shape[:3], torch.float32)
-    _check((_lib or load()).paris_prompt_weights(ctypes.byref(p), _raw(q), _raw(k), PARIS_BF16, _flat(lse), int(window),
+    _shaped(lse, "lse", (hq, rows_q) if packed else q.shape[:3], _torch.float32)
+    _shaped(weights, "weights", (hkv, rows_k) if packed else k.shape[:3], _torch.float32)
+    _check((_lib or load()).paris_prompt_weights(p, _raw(q), _raw(k), PARIS_BF16, _flat(lse), int(window),
                                                  _flat(weights), _raw_stream(index, stream)))
 
 
@@ -447,7 +466,7 @@ class KV4Cache:
     """
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, weights, positions, lens, next_pos):
-        import torch
+        torch = _with_torch()
         if k_codes.dim() != 4 or k_codes.shape[3] != HEAD_DIM // 2:
             raise ValueError(f"k_codes: shape {tuple(k_codes.shape)}, expected [batch, heads, max_rows, 64]")
         b, h, r = k_codes.shape[:3]
@@ -495,12 +514,11 @@ class KV4Cache:
     def _space(self, nbytes, stream, handle):
         """Address of the workspace of a call: kept for each stream, whose calls take turns with it; during a capture
         one of the graph's own."""
-        import torch
         if stream is None:
-            capturing = torch.cuda.is_current_stream_capturing()
+            capturing = _torch._C._cuda_isCurrentStreamCapturing()
         else:
-            with torch.cuda.stream(stream):
-                capturing = torch.cuda.is_current_stream_capturing()
+            with _torch.cuda.stream(stream):
+                capturing = _torch._C._cuda_isCurrentStreamCapturing()
         if capturing:
             return _scratch(nbytes, self.device, stream).data_ptr()
         t = self._spaces.get(handle)
@@ -511,7 +529,6 @@ class KV4Cache:
     def paris_kv4_store(self, k, v, cu=None, max_new=None, weights=None, stream=None):
         """Add tokens: packed [rows, Hkv, 128] with int32 starts cu [batch + 1] (max_new: at least the most tokens of
         a sequence, default all rows), or [batch, Hkv, T, 128].  weights: float32 [Hkv, rows] or [batch, Hkv, T]."""
-        import torch
         packed = cu is not None
         rows, heads, seqs, ks = _heads(k, "k", packed)
         vs = _heads(v, "v", packed)[3]
@@ -520,12 +537,12 @@ class KV4Cache:
         if heads != self.n_kv_heads or (not packed and seqs != self.batch):
             raise ValueError(f"k: shape {tuple(k.shape)} for a cache of {self.batch} sequences, {self.n_kv_heads} heads")
         _on(self._index, k, v, cu, weights)
-        if packed and (cu.dtype != torch.int32 or cu.shape != (self.batch + 1,) or not cu.is_contiguous()):
+        if packed and (cu.dtype is not _torch.int32 or cu.shape != (self.batch + 1,) or not cu.is_contiguous()):
             raise ValueError("cu: a contiguous int32 tensor of batch + 1 starts")
         if weights is not None:
-            _shaped(weights, "weights", (heads, rows) if packed else k.shape[:3], torch.float32)
+            _shaped(weights, "weights", (heads, rows) if packed else k.shape[:3], _torch.float32)
         _check((_lib or load()).paris_kv4_store(
-            self._ref, _raw(k), _raw(v), _dtype_code(k), ctypes.byref(paris_strides(*ks)), ctypes.byref(paris_strides(*vs)),
+            self._ref, _raw(k), _raw(v), _code(k), _STRIDES.pack(*ks), _STRIDES.pack(*vs),
             rows, _raw(cu), rows if max_new is None else int(max_new), _flat(weights), _raw_stream(self._index, stream)))
 
     def paris_kv4_append(self, k, v, stream=None):
@@ -533,22 +550,21 @@ class KV4Cache:
         _shaped(k, "k", self._token_shape, k.dtype)
         _shaped(v, "v", self._token_shape, k.dtype)
         _on(self._index, k, v)
-        _check((_lib or load()).paris_kv4_append(self._ref, _flat(k), _flat(v), _dtype_code(k),
+        _check((_lib or load()).paris_kv4_append(self._ref, _flat(k), _flat(v), _code(k),
                                                  _raw_stream(self._index, stream)))
 
     def paris_kv4_attend(self, q, out, accumulate=False, stream=None):
         """out = softmax(K q / sqrt(d)) V over the rows in use: q, out [batch, Hq, 128]; accumulate: add each row's
         softmax weights, over its query heads, to `weights`."""
-        import torch
         shape = q.shape
         if len(shape) != 3 or shape[0] != self.batch or shape[2] != HEAD_DIM:
             raise ValueError(f"q: shape {tuple(shape)}, expected [{self.batch}, heads, 128]")
-        _shaped(out, "out", shape, torch.bfloat16)
+        _shaped(out, "out", shape, _torch.bfloat16)
         _on(self._index, q, out)
         lib, hq, acc = _lib or load(), shape[1], 1 if accumulate else 0
         n = self._ws.get((hq, acc)) or self._bytes((hq, acc), lambda b: lib.paris_kv4_workspace(self._ref, hq, acc, b))
         handle = _raw_stream(self._index, stream)
-        _check(lib.paris_kv4_attend(self._ref, _flat(q), _dtype_code(q), hq, acc, _flat(out),
+        _check(lib.paris_kv4_attend(self._ref, _flat(q), _code(q), hq, acc, _flat(out),
                                     self._space(n, stream, handle), n, handle))
 
     def paris_kv4_evict(self, keep, sink=0, recent=0, stream=None):
@@ -561,11 +577,10 @@ class KV4Cache:
 
     def paris_kv4_read(self, k_out, v_out, stream=None):
         """The values of the first rows: k_out, v_out bfloat16 [batch, Hkv, rows, 128]."""
-        import torch
         if k_out.dim() != 4:
             raise ValueError(f"k_out: shape {tuple(k_out.shape)}, expected [batch, heads, rows, 128]")
         for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-            _shaped(t, name, (self.batch, self.n_kv_heads, k_out.shape[2], HEAD_DIM), torch.bfloat16)
+            _shaped(t, name, (self.batch, self.n_kv_heads, k_out.shape[2], HEAD_DIM), _torch.bfloat16)
         _on(self._index, k_out, v_out)
         _check((_lib or load()).paris_kv4_read(self._ref, _flat(k_out), _flat(v_out), k_out.shape[2],
                                                _raw_stream(self._index, stream)))

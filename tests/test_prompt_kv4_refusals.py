@@ -155,3 +155,13 @@ def test_binding_checks_shapes_types_and_devices(lib):
         P.KV4Cache(z[..., :32], z, z, z, z, z, z, z)
     with pytest.raises((ValueError, TypeError)):
         P.KV4Cache(z, z, z, z, z, z, z, z)
+
+
+def test_packed_descriptions_are_the_structures():
+    assert P._PROMPT.size == ctypes.sizeof(P.paris_prompt)
+    assert P._STRIDES.size == ctypes.sizeof(P.paris_strides)
+    p = P.paris_prompt.from_buffer_copy(P._PROMPT.pack(*range(1, 23)))
+    got = [p.n_seqs, p.n_q_heads, p.n_kv_heads, p.head_dim, p.rows_q, p.rows_k, p.cu_q, p.cu_k, p.max_q, p.max_k]
+    for x in (p.q, p.k, p.v, p.out):
+        got += [x.token, x.head, x.seq]
+    assert got == list(range(1, 23))
