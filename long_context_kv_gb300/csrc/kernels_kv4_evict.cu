@@ -126,9 +126,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 1) k_kv4_evict
           take(key, (uint32_t)first + 32 * (i0 + u) + lane);
         }
     }
-    auto each = [&](auto&& f) {  // f(i, key, whether the row is there): whole warps, rows ascending
+    auto some = [&](int i0, int i1, auto&& f) {  // f(i, key, whether the row is there): whole warps, rows ascending
 #pragma unroll 1
-      for (int i = 0; i < mine; ++i) {
+      for (int i = i0; i < i1; ++i) {
         const int x = 32 * i + lane;
         const bool in = x < end;
         uint32_t key = 0;
@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 1) k_kv4_evict
         f(i, key, in);
       }
     };
+    auto each = [&](auto&& f) { some(0, mine, f); };
 #pragma unroll 1
     for (int i = heldi; i < mine; ++i) {
       const int x = 32 * i + lane;
@@ -294,26 +295,36 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 1) k_kv4_evict
           eq_at += __reduce_add_sync(kFull, lane < rank ? *cluster.map_shared_rank(&sh.count[0], min(lane, nb - 1)) : 0u);
         }
       }
-      // holes and tails of 32 rows as bits
-      auto sort_out = [&](int i, uint32_t key, bool in, uint32_t& hs, uint32_t& ts) {
-        bool k = key >= least;
-        if (split_tie) {
-          const uint32_t eqs = __ballot_sync(kFull, in && key == least);
-          k = key > least || (key == least && eq_at + __popc(eqs & below) < want);
-          eq_at += __popc(eqs);
-        }
-        const bool low = 32 * i + lane < room;
-        hs = __ballot_sync(kFull, in && !k && low);
-        ts = __ballot_sync(kFull, in && k && !low);
+      // Holes and tails of 32 x 32 rows as bits, those of 32 rows in a lane;
+      // then each lane lists its own, of up to 32 x 32 rows a warp without
+      // sorting them out again (512 of 8704 rows dropped, with the store and the
+      // read: 57.0 -> 55.4 us).
+      uint32_t hs = 0, ts = 0;
+      auto sort_out = [&](int i0) {
+        hs = ts = 0;
+        some(i0, min(mine, i0 + 32), [&](int i, uint32_t key, bool in) {
+          bool k = key >= least;
+          if (split_tie) {
+            const uint32_t eqs = __ballot_sync(kFull, in && key == least);
+            k = key > least || (key == least && eq_at + __popc(eqs & below) < want);
+            eq_at += __popc(eqs);
+          }
+          const bool low = 32 * i + lane < room;
+          const uint32_t h = __ballot_sync(kFull, in && !k && low), t = __ballot_sync(kFull, in && k && !low);
+          if (lane == i - i0) {
+            hs = h;
+            ts = t;
+          }
+        });
       };
       uint32_t holes = 0, tails = 0;
       const uint32_t eq_start = eq_at;
-      each([&](int i, uint32_t key, bool in) {
-        uint32_t hs, ts;
-        sort_out(i, key, in, hs, ts);
-        holes += __popc(hs);
-        tails += __popc(ts);
-      });
+#pragma unroll 1
+      for (int i0 = 0; i0 < mine; i0 += 32) {
+        sort_out(i0);
+        holes += __reduce_add_sync(kFull, __popc(hs));
+        tails += __reduce_add_sync(kFull, __popc(ts));
+      }
       __syncthreads();
       if (lane == 0) {
         sh.warp_a[warp] = holes;
@@ -329,16 +340,20 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 1) k_kv4_evict
       }
       eq_at = eq_start;
       int32_t* list = a.list + (int64_t)bh * 2 * a.c.rmax;
-      if (holes + tails > 0)  // of the warp
-        each([&](int i, uint32_t key, bool in) {
-          uint32_t hs, ts;
-          sort_out(i, key, in, hs, ts);
-          const int32_t r = (int32_t)first + 32 * i + lane;
-          if (hs >> lane & 1u) list[r0 + hole_at + __popc(hs & below)] = r;
-          if (ts >> lane & 1u) list[a.c.rmax + r0 + tail_at + __popc(ts & below)] = r;
-          hole_at += __popc(hs);
-          tail_at += __popc(ts);
-        });
+      if (holes + tails > 0) {  // of the warp
+#pragma unroll 1
+        for (int i0 = 0; i0 < mine; i0 += 32) {
+          if (mine > 32) sort_out(i0);
+          auto put = [&](uint32_t bits, uint32_t& at, int32_t* to) {
+            const uint32_t inc = warp_incl_scan((uint32_t)__popc(bits), lane);
+            int32_t* p = to + (at + inc - __popc(bits));
+            for (; bits != 0; bits &= bits - 1) *p++ = (int32_t)first + 32 * (i0 + lane) + __ffs(bits) - 1;
+            at += __shfl_sync(kFull, inc, 31);
+          };
+          put(hs, hole_at, list + r0);
+          put(ts, tail_at, list + a.c.rmax + r0);
+        }
+      }
       __threadfence();
       sync_all();
       moves = block_holes;

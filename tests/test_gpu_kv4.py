@@ -323,6 +323,18 @@ def test_eviction_of_one_row_among_equal_ones(rows):
     check_evict(c, rows - 1, 1 if rows > 2 else 0, 0)
 
 
+@pytest.mark.parametrize("ties", [False, True])
+def test_eviction_of_more_rows_than_a_cluster_holds(ties):
+    rows = 300001
+    c = filled([rows], 1, rows, seed=76)
+    w = torch.rand(1, 1, rows, generator=torch.Generator(device="cuda").manual_seed(77), device="cuda")
+    c.weights.copy_(torch.floor(w * 3) if ties else w)
+    check_evict(c, rows - 1, 16, 100)
+    check_evict(c, 270000, 16, 100)
+    check_evict(c, 100000, 16, 100)
+    check_evict(c, 99999, 0, 0)
+
+
 def test_eviction_with_odd_weights_and_many_protected_rows():
     c = filled([100], 1, 100, seed=73)
     c.weights.copy_(torch.randn(1, 1, 100, device="cuda"))
