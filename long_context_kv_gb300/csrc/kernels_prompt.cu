@@ -704,38 +704,57 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
 }
 
-// A warp per query row: join the partials.
+// A warp per query row: join the partials.  Bound by latency: the first four
+// parts are on their way, from places that are there whether they are used or
+// not, before the row's number of parts and its sequence's length are known
+// (512 queries over 32768 keys, 3 to 4 parts a row: 18.5 -> 11.0 us).
 __global__ void __launch_bounds__(32 * kRowWarps) k_prompt_join(PromptArgs a, int nqb) {
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.y, s = blockIdx.z, kvh = h / a.g;
-  int64_t q0, lq, k0, lk;
-  seq_rows(a.cu_q, s, a.rows_q, q0, lq);
-  seq_rows(a.cu_k, s, a.rows_k, k0, lk);
   const int64_t tok = (int64_t)blockIdx.x * kRowWarps + warp;
-  if (tok >= min64(lq, a.max_q)) return;
+  if (tok >= a.max_q) return;
   const int tq = kTile / a.g;
   const int64_t qb = tok / (kTiles * tq);
   const int in = (int)(tok - qb * kTiles * tq), row = in / tq * kTile + in % tq * a.g + h % a.g;
   const float* part = a.ws + ((((int64_t)s * a.hkv + kvh) * nqb + qb) * a.nsplit * (kTiles * kTile) + row) * kPartRow;
   const int64_t step = (int64_t)(kTiles * kTile) * kPartRow;
+  constexpr int kAhead = 4;
+  float2 ml[kAhead];
+  float4 v[kAhead];
+#pragma unroll
+  for (int x = 0; x < kAhead; ++x)
+    if (x < a.nsplit) {
+      ml[x] = *reinterpret_cast<const float2*>(part + x * step);
+      v[x] = *reinterpret_cast<const float4*>(part + x * step + 4 + 4 * lane);
+    }
   const int parts = __float_as_int(part[2]);  // at most nsplit
+  int64_t q0, lq, k0, lk;
+  seq_rows(a.cu_q, s, a.rows_q, q0, lq);
+  seq_rows(a.cu_k, s, a.rows_k, k0, lk);
+  if (tok >= lq) return;
   float M = -INFINITY;
-  for (int x = 0; x < parts; ++x) M = fmaxf(M, part[x * step]);
+#pragma unroll
+  for (int x = 0; x < kAhead; ++x)
+    if (x < parts) M = fmaxf(M, ml[x].x);
+  for (int x = kAhead; x < parts; ++x) M = fmaxf(M, part[x * step]);
   float L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int x = 0; x < parts; ++x) {
-    const float4 v = *reinterpret_cast<const float4*>(part + x * step + 4 + 4 * lane);
-    const float2 ml = *reinterpret_cast<const float2*>(part + x * step);
-    const float f = ml.y == 0.f ? 0.f : ml.x == M ? 1.f : exp2f(ml.x - M);
-    if (ml.y == 0.f) continue;
+  auto add = [&](const float2& ml, const float4& v) {
+    if (ml.y == 0.f) return;  // no weight at all, and M may be -inf
+    const float f = ml.x == M ? 1.f : exp2f(ml.x - M);
     L += ml.y * f;
     o[0] = fmaf(v.x, f, o[0]);
     o[1] = fmaf(v.y, f, o[1]);
     o[2] = fmaf(v.z, f, o[2]);
     o[3] = fmaf(v.w, f, o[3]);
-  }
+  };
+#pragma unroll
+  for (int x = 0; x < kAhead; ++x)
+    if (x < parts) add(ml[x], v[x]);
+#pragma unroll 4
+  for (int x = kAhead; x < parts; ++x)
+    add(*reinterpret_cast<const float2*>(part + x * step), *reinterpret_cast<const float4*>(part + x * step + 4 + 4 * lane));
   const float inv = L != 0.f ? 1.f / L : 0.f;
   bool finite = true;
 #pragma unroll
