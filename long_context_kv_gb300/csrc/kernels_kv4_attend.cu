@@ -29,7 +29,7 @@
 // by k_kv4_finish, which also turns the scores into weights.  More than eight
 // query heads per KV head are two blocks, each reading the rows.
 //
-// At 131072 rows of 8 KV heads, 4 query heads each (142.6 MB): 37.6 us with the
+// At 131072 rows of 8 KV heads, 4 query heads each (142.6 MB): 35.8 us with the
 // merge.  The copies alone, with nothing computed, take 30.6: 23.5 at 6 TB/s and
 // 7 for the start, the first rows' way and the end.  Fewer instructions no
 // longer tell (HFMA2 halved by keys as subnormals: the same), nor do more or
@@ -145,17 +145,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // The rows of a batch are cut into chunks, a block each (per KV head and head
 // group), a sequence's into equal ones.  Their size comes from the lengths as
 // they are on the device, so that nblocks chunks hold every row however the
-// lengths differ: C tiles, C = ceil(sum of tiles / (nblocks - batch)), leaves
-// sum of ceil(tiles / C) <= nblocks.  Batches of more than 128 sequences (a
-// thread each) fill the GPU anyway, and are cut evenly.
-struct ChunkShared {
-  uint32_t warp_sum[4], warp_n[4];
-  int b, first, n;
-};
+// lengths differ.  Batches of more than 128 sequences (four a lane) fill the
+// GPU anyway, and are cut evenly.
+constexpr int kCutSeqs = 128;
 
 // The block's sequence (-1: none), the first of its chunks and their number.
-__device__ __forceinline__ int3 chunk_of(const Attend4Args& a, ChunkShared& sh, int x) {
-  if (a.c.batch > 128) {
+__device__ __forceinline__ int3 chunk_of(const Attend4Args& a, int x) {
+  if (a.c.batch > kCutSeqs) {
     const int n = a.nblocks / a.c.batch;
     return make_int3(x / n, x / n * n, n);
   }
@@ -165,36 +161,18 @@ __device__ __forceinline__ int3 chunk_of(const Attend4Args& a, ChunkShared& sh, 
     const uint32_t size = max(1u, (all + a.nblocks - 1) / a.nblocks), n = (all + size - 1) / size;
     return make_int3((uint32_t)x < n ? 0 : -1, 0, n);
   }
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const uint32_t tiles = t < a.c.batch ? ((uint32_t)kv4_len(a.c, t) + kTile4 - 1) / kTile4 : 0u;
-  const uint32_t sum = __reduce_add_sync(kFull, tiles);
-  if (lane == 0) sh.warp_sum[warp] = sum;
-  if (t == 0) sh.b = -1;
-  __syncthreads();
-  const uint32_t all = sh.warp_sum[0] + sh.warp_sum[1] + sh.warp_sum[2] + sh.warp_sum[3];
-  const uint32_t spare = (uint32_t)(a.nblocks - a.c.batch);
-  const uint32_t size = max(1u, (all + spare - 1) / spare), n = (tiles + size - 1) / size;
-  const uint32_t inc = warp_incl_scan(n, lane);
-  if (lane == 31) sh.warp_n[warp] = inc;
-  __syncthreads();
-  uint32_t first = inc - n;
+  const int lane = threadIdx.x & 31;
+  uint32_t tiles[kCutSeqs / 32];
 #pragma unroll
-  for (int w = 0; w < 3; ++w)
-    if (w < warp) first += sh.warp_n[w];
-  if ((uint32_t)x >= first && (uint32_t)x < first + n) {
-    sh.b = t;
-    sh.first = (int)first;
-    sh.n = (int)n;
-  }
-  __syncthreads();
-  return make_int3(sh.b, sh.first, sh.n);
+  for (int i = 0; i < kCutSeqs / 32; ++i)
+    tiles[i] = 32 * i + lane < a.c.batch ? ((uint32_t)kv4_len(a.c, 32 * i + lane) + kTile4 - 1) / kTile4 : 0u;
+  return cut_tiles(tiles, a.nblocks, x);
 }
 
 struct Shared4 {
   uint2 q[8][2][32];           // query fragments: step, column tile, lane
   float qscale[kHeads4];
   float ml[kWarps4][kHeads4][2];
-  ChunkShared chunks;
 };
 
 // NT column tiles: 1 for up to four query heads (columns 0-3 their upper,
@@ -209,7 +187,7 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int warp = __shfl_sync(kFull, tid >> 5, 0);
   const int kvh = blockIdx.y, h0 = blockIdx.z * kHeads;
-  int3 chunk = chunk_of(a, sh.chunks, blockIdx.x);
+  int3 chunk = chunk_of(a, blockIdx.x);
   // the same in every lane: a reduction tells the compiler, and the addresses
   // stay in uniform registers (36.4 against 33.4 us at 128K rows)
   chunk = make_int3(__reduce_max_sync(kFull, chunk.x), __reduce_max_sync(kFull, chunk.y), __reduce_max_sync(kFull, chunk.z));

@@ -28,6 +28,9 @@ namespace {
 constexpr int kWStages = 4;
 constexpr int kWRows = 256;            // window rows of a chunk
 constexpr int kWThreads = 384;
+// Up to this many sequences' tiles are cut by their lengths; more of them, or
+// more KV heads of them than SMs, are a block each (and KV head).
+constexpr int kCutSeqs = 160;
 constexpr int kKeyBytes = kTile * kDim * 2;
 constexpr int kQHalf = kWRows * 128;   // 64 channels of a chunk
 constexpr size_t kWSmem = (size_t)kWStages * kKeyBytes + 2 * kQHalf + 1024;
@@ -45,20 +48,40 @@ struct WeightMaps {
 };
 
 __global__ void __launch_bounds__(kWThreads, 1)
-    k_prompt_weights(const __grid_constant__ PromptWeightArgs wa, const __grid_constant__ WeightMaps maps, int blocks_per_unit, int tiles_per_block) {
+    k_prompt_weights(const __grid_constant__ PromptWeightArgs wa, const __grid_constant__ WeightMaps maps, int chunks) {
   extern __shared__ uint8_t dyn[];
   __shared__ __align__(16) WeightShared sh;
   pdl_wait();
   pdl_trigger();
   const PromptArgs& a = wa.p;
-  const int unit = blockIdx.x / blocks_per_unit, part = blockIdx.x - unit * blocks_per_unit;
-  const int s = unit / a.hkv, kvh = unit - s * a.hkv;
+  // the block's part of a sequence's key tiles
+  const int place = blockIdx.x / a.hkv, kvh = blockIdx.x - place * a.hkv;
+  int s = place, part = 0, parts = 1;
+  if (chunks > 0 && a.n_seqs == 1) {
+    s = 0;
+    part = place;
+    parts = chunks;
+  } else if (chunks > 0) {
+    const int lane = threadIdx.x & 31;
+    uint32_t tiles[kCutSeqs / 32];
+#pragma unroll
+    for (int i = 0; i < kCutSeqs / 32; ++i) {
+      int64_t start = 0, len = 0;
+      if (32 * i + lane < a.n_seqs) seq_rows(a.cu_k, 32 * i + lane, a.rows_k, start, len);
+      tiles[i] = (uint32_t)((min64(len, a.max_k) + kTile - 1) / kTile);
+    }
+    const int3 cut = cut_tiles(tiles, (uint32_t)chunks, (uint32_t)place);
+    if (cut.x < 0) return;
+    s = cut.x;
+    part = place - cut.y;
+    parts = cut.z;
+  }
   int64_t q0, lq, k0, lk;
   seq_rows(a.cu_q, s, a.rows_q, q0, lq);
   seq_rows(a.cu_k, s, a.rows_k, k0, lk);
   const int64_t lkm = min64(lk, a.max_k);
-  const int tile0 = part * tiles_per_block;
-  const int ntile = (int)min64(tiles_per_block, (lkm + kTile - 1) / kTile - tile0);
+  const int all_tiles = (int)((lkm + kTile - 1) / kTile), per = (all_tiles + parts - 1) / parts;
+  const int tile0 = part * per, ntile = min(per, all_tiles - tile0);
   if (ntile <= 0) return;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(kFull, tid >> 5, 0);
@@ -277,14 +300,16 @@ cudaError_t launch_prompt_weights(const PromptWeightArgs& w, int sm_count, cudaS
     return cudaErrorInvalidValue;
   cudaError_t e = raise_smem();
   if (e != cudaSuccess) return e;
-  // a block per SM, each with an even share of the tiles
+  // A block per SM, and for each KV head as many chunks of the sequences' tiles
+  // (six sequences of 7422 tokens in all: 10.0 -> 9.0 us against chunks cut by
+  // the longest one's); a block for each sequence and KV head where those are
+  // more.
   const int64_t units = (int64_t)a.n_seqs * a.hkv, tiles = (a.max_k + kTile - 1) / kTile;
-  const int64_t per = std::max<int64_t>(1, (units * tiles + sm_count - 1) / sm_count);
+  const bool cut = units <= sm_count && a.n_seqs <= kCutSeqs;
+  const int64_t most = cut ? std::min<int64_t>(sm_count / a.hkv, a.n_seqs * tiles) : 0;
   const int64_t chunk = kWRows / a.g, chunks = (std::min<int64_t>(w.window, a.rows_q) + chunk - 1) / chunk;
-  if (chunks * per > 0x7fffffff) return cudaErrorInvalidValue;
-  const int64_t blocks = (tiles + per - 1) / per;
-  if (blocks * units > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_pdl(k_prompt_weights, dim3((unsigned)(blocks * units)), dim3(kWThreads), kWSmem, st, w, m, (int)blocks, (int)per);
+  if (chunks * tiles > 0x7fffffff) return cudaErrorInvalidValue;
+  return launch_pdl(k_prompt_weights, dim3((unsigned)(cut ? most * a.hkv : units)), dim3(kWThreads), kWSmem, st, w, m, (int)most);
 }
 
 }  // namespace paris

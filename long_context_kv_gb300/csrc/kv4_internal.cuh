@@ -42,6 +42,55 @@ __device__ __forceinline__ void seq_rows(const int32_t* cu, int s, int64_t rows,
   len = min64(max64(cu[s + 1], start), rows) - start;
 }
 
+// 32 N sequences (N a lane) of so many tiles each are cut into chunks of as
+// few tiles as `most` chunks allow: chunk x's sequence (-1: there is no such
+// chunk), the first of that sequence's chunks and their number.  A whole warp;
+// `most` is at least the number of sequences that have tiles, and all tiles
+// together are below 2^32.
+template <int N>
+__device__ __forceinline__ int3 cut_tiles(const uint32_t (&tiles)[N], uint32_t most, uint32_t x) {
+  const int lane = threadIdx.x & 31;
+  uint32_t all = 0, longest = 0, seqs = 0, used = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    all += tiles[i];
+    longest = max(longest, tiles[i]);
+    const uint32_t has = __ballot_sync(kFull, tiles[i] > 0);
+    seqs += __popc(has);
+    if (has != 0) used |= 1u << i;
+  }
+  all = __reduce_add_sync(kFull, all);
+  longest = __reduce_max_sync(kFull, longest);
+  // an even share may be too little, as every sequence has a chunk that is not
+  // full; the longest sequence's tiles, or an even share of the other chunks,
+  // are enough
+  uint32_t lo = max(1u, (all + most - 1) / most), hi = max(lo, longest);
+  if (most > seqs) hi = max(lo, min(hi, (all + most - seqs - 1) / (most - seqs)));
+  while (lo < hi) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (used >> i & 1u) n += (tiles[i] + mid - 1) / mid;
+    if (__reduce_add_sync(kFull, n) <= most) hi = mid;
+    else lo = mid + 1;
+  }
+  uint32_t before = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if ((used >> i & 1u) == 0) continue;
+    const uint32_t n = (tiles[i] + lo - 1) / lo;
+    const uint32_t inc = warp_incl_scan(n, lane) + before;
+    const uint32_t in = __ballot_sync(kFull, x >= inc - n && x < inc);
+    if (in != 0) {
+      const int src = __ffs(in) - 1;
+      return make_int3(32 * i + src, (int)__shfl_sync(kFull, inc - n, src), (int)__shfl_sync(kFull, n, src));
+    }
+    before = __shfl_sync(kFull, inc, 31);
+  }
+  return make_int3(-1, 0, 0);
+}
+
 struct StoreArgs {
   Kv4 c;
   const void *k, *v;

@@ -192,6 +192,16 @@ def test_attention_over_the_rows_in_use(g, lens):
     check_attend(c, q, out2, before)
 
 
+@pytest.mark.parametrize("lens", [[300 if b in (0, 40, 99) else 0 for b in range(100)],
+                                  [3000 if b == 70 else b % 5 for b in range(128)], [b % 300 for b in range(131)]])
+def test_attention_over_many_sequences(lens):
+    c = filled(lens, 2, max(lens) + 4, seed=33)
+    q = rand(len(lens), 6, R.D, seed=34, amp=2.0).to(BF)
+    before, out = c.weights.clone(), torch.full_like(q, 9.0)
+    c.paris_kv4_attend(q, out, accumulate=True)
+    check_attend(c, q, out, before)
+
+
 @pytest.mark.parametrize("rows", [1, 5, 130, 20000])
 def test_attention_with_float32_queries_and_full_caches(rows):
     c = filled([rows], 1, rows, seed=50, garbage=False)

@@ -313,6 +313,21 @@ def test_window_weights_of_many_query_heads_and_sequences():
             a += n
 
 
+@pytest.mark.parametrize("lens,hkv", [([0, 3] * 45 + [200], 2), ([300] + [0] * 60 + [2, 700], 2), ([260, 1], 80)])
+def test_window_weights_of_uneven_sequences(lens, hkv):
+    q, k, v = make(lens, lens, hkv, hkv, seed=22)
+    cu = R.starts(lens)
+    lse = torch.zeros(hkv, q.shape[0], device="cuda")
+    P.paris_prompt_attend(q, k, v, torch.empty_like(q), cu_q=cu, cu_k=cu, lse=lse)
+    got = torch.full((hkv, k.shape[0]), 9.0, device="cuda")
+    P.paris_prompt_weights(q, k, lse, got, window=6, cu_q=cu, cu_k=cu, max_k=max(lens))
+    a = 0
+    for n in lens:
+        want, tol = weights_ref(q[a:a + n], k[a:a + n], lse[:, a:a + n], 1, 6)
+        assert torch.all((got[:, a:a + n].double() - want).abs() <= tol + 1e-30)
+        a += n
+
+
 def test_window_weights_do_not_see_other_rows():
     q, k, v = make([100], [100], 4, 2, seed=15)
     cu = torch.tensor([0, 60], dtype=torch.int32, device="cuda")
