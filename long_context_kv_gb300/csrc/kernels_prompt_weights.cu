@@ -51,48 +51,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
     k_prompt_weights(const __grid_constant__ PromptWeightArgs wa, const __grid_constant__ WeightMaps maps, int chunks) {
   extern __shared__ uint8_t dyn[];
   __shared__ __align__(16) WeightShared sh;
-  pdl_wait();
-  pdl_trigger();
-  const PromptArgs& a = wa.p;
-  // the block's part of a sequence's key tiles
-  const int place = blockIdx.x / a.hkv, kvh = blockIdx.x - place * a.hkv;
-  int s = place, part = 0, parts = 1;
-  if (chunks > 0 && a.n_seqs == 1) {
-    s = 0;
-    part = place;
-    parts = chunks;
-  } else if (chunks > 0) {
-    const int lane = threadIdx.x & 31;
-    uint32_t tiles[kCutSeqs / 32];
-#pragma unroll
-    for (int i = 0; i < kCutSeqs / 32; ++i) {
-      int64_t start = 0, len = 0;
-      if (32 * i + lane < a.n_seqs) seq_rows(a.cu_k, 32 * i + lane, a.rows_k, start, len);
-      tiles[i] = (uint32_t)((min64(len, a.max_k) + kTile - 1) / kTile);
-    }
-    const int3 cut = cut_tiles(tiles, (uint32_t)chunks, (uint32_t)place);
-    if (cut.x < 0) return;
-    s = cut.x;
-    part = place - cut.y;
-    parts = cut.z;
-  }
-  int64_t q0, lq, k0, lk;
-  seq_rows(a.cu_q, s, a.rows_q, q0, lq);
-  seq_rows(a.cu_k, s, a.rows_k, k0, lk);
-  const int64_t lkm = min64(lk, a.max_k);
-  const int all_tiles = (int)((lkm + kTile - 1) / kTile), per = (all_tiles + parts - 1) / parts;
-  const int tile0 = part * per, ntile = min(per, all_tiles - tile0);
-  if (ntile <= 0) return;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(kFull, tid >> 5, 0);
-  const int win = (int)min64(wa.window, lq);      // queries of the window
-  const int tq = kWRows / a.g;                    // of a chunk
-  const int nchunk = (win + tq - 1) / tq;
-  float* out = wa.weights + ((int64_t)(a.cu_k ? 0 : s) * a.hkv + kvh) * a.rows_k + k0;
-  if (nchunk == 0) {
-    for (int64_t j = (int64_t)tile0 * kTile + tid; j < min64(lkm, (int64_t)(tile0 + ntile) * kTile); j += kWThreads) out[j] = 0.f;
-    return;
-  }
   const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u, qb = base + kWStages * kKeyBytes;
   const uint32_t q_full = smem_u32(&sh.q_full), q_empty = smem_u32(&sh.q_empty), k_full = smem_u32(&sh.k_full[0]),
                  k_empty = smem_u32(&sh.k_empty[0]), s_full = smem_u32(&sh.s_full[0]), s_empty = smem_u32(&sh.s_empty[0]), part_full = smem_u32(&sh.part_full[0]);
@@ -121,6 +81,55 @@ __global__ void __launch_bounds__(kWThreads, 1)
   tm_fence_after();
   const uint32_t tmem = __shfl_sync(kFull, *(volatile uint32_t*)&sh.tmem, 0);
   volatile uint32_t* gave_up = &sh.gave_up;
+  auto free_tmem = [&]() {
+    if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
+  };
+  pdl_wait();
+  pdl_trigger();
+  const PromptArgs& a = wa.p;
+  // the block's part of a sequence's key tiles
+  const int place = blockIdx.x / a.hkv, kvh = blockIdx.x - place * a.hkv;
+  int s = place, part = 0, parts = 1;
+  if (chunks > 0 && a.n_seqs == 1) {
+    s = 0;
+    part = place;
+    parts = chunks;
+  } else if (chunks > 0) {
+    uint32_t tiles[kCutSeqs / 32];
+#pragma unroll
+    for (int i = 0; i < kCutSeqs / 32; ++i) {
+      int64_t start = 0, len = 0;
+      if (32 * i + lane < a.n_seqs) seq_rows(a.cu_k, 32 * i + lane, a.rows_k, start, len);
+      tiles[i] = (uint32_t)((min64(len, a.max_k) + kTile - 1) / kTile);
+    }
+    const int3 cut = cut_tiles(tiles, (uint32_t)chunks, (uint32_t)place);
+    if (cut.x < 0) {
+      free_tmem();
+      return;
+    }
+    s = cut.x;
+    part = place - cut.y;
+    parts = cut.z;
+  }
+  int64_t q0, lq, k0, lk;
+  seq_rows(a.cu_q, s, a.rows_q, q0, lq);
+  seq_rows(a.cu_k, s, a.rows_k, k0, lk);
+  const int64_t lkm = min64(lk, a.max_k);
+  const int all_tiles = (int)((lkm + kTile - 1) / kTile), per = (all_tiles + parts - 1) / parts;
+  const int tile0 = part * per, ntile = min(per, all_tiles - tile0);
+  if (ntile <= 0) {
+    free_tmem();
+    return;
+  }
+  const int win = (int)min64(wa.window, lq);      // queries of the window
+  const int tq = kWRows / a.g;                    // of a chunk
+  const int nchunk = (win + tq - 1) / tq;
+  float* out = wa.weights + ((int64_t)(a.cu_k ? 0 : s) * a.hkv + kvh) * a.rows_k + k0;
+  if (nchunk == 0) {
+    for (int64_t j = (int64_t)tile0 * kTile + tid; j < min64(lkm, (int64_t)(tile0 + ntile) * kTile); j += kWThreads) out[j] = 0.f;
+    free_tmem();
+    return;
+  }
   const int64_t first = lq - win;                 // first query of the window
   const int total = nchunk * ntile;               // products, chunk by chunk (the launch keeps it below 2^31)
   // rows of chunk c, and the product's N
@@ -270,10 +279,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
     tm_fence_before();
   }
   __syncthreads();
-  if (warp == 8) {
-    tm_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
-  }
+  tm_fence_after();
+  free_tmem();
 }
 
 cudaError_t raise_smem() {
