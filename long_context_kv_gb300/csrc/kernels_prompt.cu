@@ -28,7 +28,9 @@
 // 2048; it takes 2900 to 3050 (32768 tokens of 8 query heads: 1.34 ms,
 // 1643 TFLOP/s, 0.84 of the measured bf16 rate).  What the steps measured:
 // operands kept in uniform registers by electing the issuing lane, 2474 ->
-// 1446 us there; a block per item instead of per SM, 1468 against 1364 us.  An
+// 1446 us there; a block per item instead of per SM, 1468 against 1364 us; an
+// eighth of the exponentials by a polynomial in the FMA units, 1406 against
+// 1331 us: the special-function units are not what a step waits for.  An
 // item's result takes 4000 cycles more, in which its tile's group does nothing
 // else; that is 15 % of a batch of short prompts.
 //
