@@ -25,8 +25,8 @@
 // Bound by the tensor cores (4 d flops a visible pair), and right under them
 // by shared memory: a step of both tiles and 128 keys is 2048 cycles of
 // products, whose operands and copies are 256 KB at 128 bytes a cycle, again
-// 2048; it takes 2900 to 3050 (32768 tokens of 8 query heads: 1.34 ms,
-// 1643 TFLOP/s, 0.84 of the measured bf16 rate).  What the steps measured:
+// 2048; it takes 2900 to 3050 (32768 tokens of 8 query heads: 1.31 ms,
+// 1679 TFLOP/s, 0.86 of the measured bf16 rate).  What the steps measured:
 // operands kept in uniform registers by electing the issuing lane, 2474 ->
 // 1446 us there; a block per item instead of per SM, 1468 against 1364 us; an
 // eighth of the exponentials by a polynomial in the FMA units, 1406 against
@@ -525,18 +525,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tm_fence_after();
         uint32_t s[kTile];
         tm_ld32(s, 0, ts);
+        tm_wait_ld();
         tm_ld32(s, 32, ts + 32);
         tm_ld32(s, 64, ts + 64);
         tm_ld32(s, 96, ts + 96);
-        tm_wait_ld();
-        if ((j + 1) * kTile - 1 > tile_key) {
-          const int left = last_key - j * kTile;  // last visible column
+        const bool cut = (j + 1) * kTile - 1 > tile_key;
+        const int left = last_key - j * kTile;  // last visible column
+        if (cut) {
 #pragma unroll
-          for (int c = 0; c < kTile; ++c)
+          for (int c = 0; c < 32; ++c)
             if (c > left) s[c] = 0xff800000u;  // -inf
         }
-        // The first weights are taken with the maximum so far while the block's
-        // own is found; only a row that grew past kGrowth does them again.
+        // The first weights are taken with the maximum so far, while the other
+        // scores are on their way and before the block's own maximum is found;
+        // only a row that grew past kGrowth does them again.
         const uint64_t c2 = pair2(kScaleLog2, kScaleLog2);
         uint64_t sum0 = 0, sum1 = 0;
         auto four = [&](int c, uint64_t n2, uint32_t& lo, uint32_t& hi) {
@@ -558,10 +560,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
           four(c, pair2(neg, neg), first[c / 2], first[c / 2 + 1]);
-#pragma unroll
-          for (int u = 0; u < 8; ++u)
-            mx[u & 3] = fmaxf(mx[u & 3], fmaxf(__uint_as_float(s[4 * c + 2 * u]), __uint_as_float(s[4 * c + 2 * u + 1])));
+          mx[0] = fmaxf(mx[0], fmaxf(__uint_as_float(s[c]), __uint_as_float(s[c + 1])));
+          mx[1] = fmaxf(mx[1], fmaxf(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])));
         }
+        tm_wait_ld();
+        hold32(s, 32);
+        hold32(s, 64);
+        hold32(s, 96);
+        if (cut) {
+#pragma unroll
+          for (int c = 32; c < kTile; ++c)
+            if (c > left) s[c] = 0xff800000u;
+        }
+#pragma unroll
+        for (int u = 16; u < 64; ++u)
+          mx[u & 3] = fmaxf(mx[u & 3], fmaxf(__uint_as_float(s[2 * u]), __uint_as_float(s[2 * u + 1])));
         const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kScaleLog2;
         const bool grew = mt > m + kGrowth;
         if (__any_sync(kFull, grew)) {

@@ -135,6 +135,12 @@ template <int N>
 __device__ __forceinline__ void tm_ld32(uint32_t (&r)[N], int o, uint32_t addr) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 " TM32S ", [%32];\n" : TM32O(r, o) : "r"(addr) : "memory");
 }
+// What follows uses the registers as they are here, not before.
+template <int N>
+__device__ __forceinline__ void hold32(uint32_t (&r)[N], int o) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) asm volatile("" : "+r"(r[o + i]), "+r"(r[o + i + 1]), "+r"(r[o + i + 2]), "+r"(r[o + i + 3]));
+}
 template <int N>
 __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[N], int o) {
   asm volatile(
