@@ -359,15 +359,20 @@ def _shaped(t, name, shape, dtype):
 
 def _heads(t, name, packed):
     """A tensor of heads as (rows, heads, sequence axis, strides): [rows, H, d] packed, [batch, H, T, d] otherwise."""
-    shape, st = t.shape, t.stride()
+    shape = t.shape
     if len(shape) != (3 if packed else 4) or shape[-1] != HEAD_DIM:
         want = "[rows, heads, 128]" if packed else "[batch, heads, T, 128]"
         raise ValueError(f"{name}: shape {tuple(shape)}, expected {want}")
+    if packed:
+        return shape[0], shape[1], 1, _strides(t, name, packed)
+    return shape[2], shape[1], shape[0], _strides(t, name, packed)
+
+
+def _strides(t, name, packed):
+    st = t.stride()
     if st[-1] != 1 and t.numel():
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    if packed:
-        return shape[0], shape[1], 1, (st[0], st[1], 0)
-    return shape[2], shape[1], shape[0], (st[2], st[1], st[0])
+    return (st[0], st[1], 0) if packed else (st[2], st[1], st[0])
 
 
 def _scratch(nbytes, device, stream):
@@ -396,19 +401,20 @@ def _prompt(q, k, cu_q, cu_k, max_q, max_k, v=None, out=None):
         raise ValueError(f"q and k: batches of {seqs} and {k_seqs}")
     starts_q = starts_k = 0
     if packed:
+        n = cu_q.shape
         for c, name in ((cu_q, "cu_q"), (cu_k, "cu_k")):
-            if c.dtype is not torch.int32 or c.dim() != 1 or not c.is_contiguous() or c.shape != cu_q.shape or not c.numel():
+            if c.dtype is not torch.int32 or not c.is_contiguous() or c.shape != n or len(n) != 1 or n[0] == 0:
                 raise ValueError(f"{name}: a contiguous int32 tensor of n + 1 starts, as many for q as for k")
-        seqs, starts_q, starts_k = cu_q.numel() - 1, cu_q.data_ptr(), cu_k.data_ptr()
+        seqs, starts_q, starts_k = n[0] - 1, cu_q.data_ptr(), cu_k.data_ptr()
     vs = os_ = (0, 0, 0)
     if v is not None:
         if v.shape != k.shape:
             raise ValueError(f"v: shape {tuple(v.shape)}, expected {tuple(k.shape)}")
-        vs = _heads(v, "v", packed)[3]
+        vs = _strides(v, "v", packed)
     if out is not None:
         if out.shape != q.shape:
             raise ValueError(f"out: shape {tuple(out.shape)}, expected {tuple(q.shape)}")
-        os_ = _heads(out, "out", packed)[3]
+        os_ = _strides(out, "out", packed)
     return _PROMPT.pack(seqs, hq, hkv, HEAD_DIM, rows_q, rows_k, starts_q, starts_k, rows_q if max_q is None else max_q,
                         rows_k if max_k is None else max_k, *qs, *ks, *vs, *os_), hq, rows_q, hkv, rows_k, packed
 
@@ -531,9 +537,9 @@ class KV4Cache:
         a sequence, default all rows), or [batch, Hkv, T, 128].  weights: float32 [Hkv, rows] or [batch, Hkv, T]."""
         packed = cu is not None
         rows, heads, seqs, ks = _heads(k, "k", packed)
-        vs = _heads(v, "v", packed)[3]
-        if v.shape != k.shape or v.dtype != k.dtype:
+        if v.shape != k.shape or v.dtype is not k.dtype:
             raise ValueError("k and v must have the same shape and dtype")
+        vs = _strides(v, "v", packed)
         if heads != self.n_kv_heads or (not packed and seqs != self.batch):
             raise ValueError(f"k: shape {tuple(k.shape)} for a cache of {self.batch} sequences, {self.n_kv_heads} heads")
         _on(self._index, k, v, cu, weights)
