@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
   for (int j = 0; j < 8; ++j)
 #pragma unroll
     for (int c = 0; c < NT; ++c) o[j][c][0] = o[j][c][1] = o[j][c][2] = o[j][c][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // m: a product, before its scale qs
   float* sc = a.accumulate ? a.scores + ((int64_t)b * a.hq + qh0 + hc) * a.c.rmax + r_begin : nullptr;
 
   // Index 2x + y of an 8-row product stands for row 2x + (y ^ (x & 1)): the
@@ -412,17 +412,17 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
     }
     float mx[2];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) mx[c] = fmaxf(fmaxf(p[0][0][c], p[0][1][c]), fmaxf(p[1][0][c], p[1][1][c])) * qs[c];
+    for (int c = 0; c < 2; ++c) mx[c] = fmaxf(fmaxf(p[0][0][c], p[0][1][c]), fmaxf(p[1][0][c], p[1][1][c]));
     // a maximum may lag by kGrowth4: weights stay below 2^8, and the sums are
     // scaled again a few times at most
-    if (__any_sync(kFull, mx[0] > m[0] + kGrowth4 || mx[1] > m[1] + kGrowth4)) {
+    if (__any_sync(kFull, (mx[0] - m[0]) * qs[0] > kGrowth4 || (mx[1] - m[1]) * qs[1] > kGrowth4)) {
       float f[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(kFull, mx[c], off));
         const float mn = fmaxf(m[c], mx[c]);
-        f[c] = mn == -INFINITY ? 1.f : exp2_fast(m[c] - mn);
+        f[c] = mn == -INFINITY ? 1.f : exp2_fast((m[c] - mn) * qs[c]);
         m[c] = mn;
         l[c] *= f[c];
       }
@@ -434,15 +434,18 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[j][c][i] *= f[i & 1];
     }
-    // weights are kept 2^kUp4 up, at most 2^15: down to 2^-32 of the largest
-    // they still count in a half's subnormals
-    const float neg[2] = {kUp4 - m[0], kUp4 - m[1]};
+    // Weights are kept 2^kUp4 up, at most 2^15: down to 2^-32 of the largest
+    // they still count in a half's subnormals.  The maximum is subtracted
+    // before the scale: it is one of the products, so the largest weight is
+    // 2^kUp4 at any size of the scores.  Taken off the scaled score in one fma,
+    // its own rounding, 2^-24 of it, is left over in the exponent, and from
+    // scores of 2^24 on takes weights past a half's range.
     uint32_t pb[2][2][NT];  // rows 8 r + 16 u, column tile
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float p0 = exp2_fast(fmaf(p[u][r][0], qs[0], neg[0])), p1 = exp2_fast(fmaf(p[u][r][1], qs[1], neg[1]));
+        const float p0 = exp2_fast(fmaf(p[u][r][0] - m[0], qs[0], kUp4)), p1 = exp2_fast(fmaf(p[u][r][1] - m[1], qs[1], kUp4));
         l[0] += p0;
         l[1] += p1;
         const __half2 hi = __floats2half2_rn(p0, p1);
@@ -486,7 +489,7 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) l[c] += __shfl_xor_sync(kFull, l[c], off);
     if (g == 0 && (NT == 2 || t < 2)) {
-      sh.ml[warp][hc + c][0] = m[c];
+      sh.ml[warp][hc + c][0] = m[c] * qs[c];  // qs > 0
       sh.ml[warp][hc + c][1] = l[c] * kDown4;
     }
   }

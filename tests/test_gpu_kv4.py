@@ -221,6 +221,37 @@ def test_queries_of_any_size(amp):
     check_attend(c, q, out)
 
 
+def one_hot_case(amp, g, rows, seed):
+    """Scores so far apart that each head's softmax is one row: (k, v, q) and each head's row, made on the CPU."""
+    gen = torch.Generator().manual_seed(seed)
+    k, v = (torch.randn(rows, 1, R.D, generator=gen).to(BF) for _ in range(2))
+    q = (torch.randn(1, g, R.D, generator=gen) * amp).to(BF)
+    s = q[0].double() @ R.values(*R.quantise(k))[:, 0].T / math.sqrt(R.D)
+    top = s.topk(2, dim=-1)
+    size = (q[0].double().abs() @ R.values(*R.quantise(k))[:, 0].abs().T).amax(-1) / math.sqrt(R.D)
+    # 128 float32 products of any order and two half parts of 2^-22 put a score off by less than 2^-16 of its terms; a
+    # weight of 2^-150 is 0
+    assert torch.all(top.values[:, 0] - top.values[:, 1] > 2.0 ** -15 * size + 150 * math.log(2))
+    return k, v, q, top.indices[:, 0]
+
+
+def check_one_hot(amp, dtype, g, rows):
+    k, v, q, at = (t.cuda() for t in one_hot_case(amp, g, rows, seed=500 + g))
+    c = P.KV4Cache.create(1, 1, rows)
+    c.paris_kv4_store(k, v, cu=R.starts([rows]))
+    out = torch.full((1, g, R.D), 9.0, dtype=BF, device="cuda")
+    c.paris_kv4_attend(q.to(dtype), out, accumulate=True)
+    assert torch.equal(out[0].double(), R.values(c.v_codes, c.v_scales)[0, 0][at])
+    assert torch.equal(c.weights[0, 0], torch.bincount(at, minlength=rows).float())
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("g", [2, 8])
+@pytest.mark.parametrize("amp,rows", [(1e7, 300), (1e9, 9000), (1e20, 300), (1e28, 300), (1e28, 9000)])
+def test_scores_far_apart_leave_one_row(amp, rows, g, dtype):
+    check_one_hot(amp, dtype, g, rows)
+
+
 @pytest.mark.parametrize("batch", [2, 33, 128, 129, 300])
 def test_batches_of_very_different_lengths(batch):
     gen = torch.Generator().manual_seed(batch)
