@@ -269,9 +269,11 @@ __global__ void __launch_bounds__(kThreads4, NT == 1 ? 4 : 3) k_kv4_attend(Atten
     }
     amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
-    // 2^(e + 1) > amax; exponents beyond +-100 are left to overflow to the
-    // infinities that such queries' scores are anyway
-    const int e = min(max((int)((__float_as_uint(amax) >> 23) & 255u) - 126, -100), 100);
+    // 2^e > amax for every finite query but those of 2^126 and more, which come
+    // out below 4 (64 in even channels); queries below 2^-101 are scaled by
+    // less than their size asks for, and their scores are nothing in float32
+    // all the same
+    const int e = min(max((int)((__float_as_uint(amax) >> 23) & 255u) - 126, -100), 126);
     const float down = __uint_as_float((uint32_t)(127 - e) << 23);
     if (warp == 0 && t == 0) sh.qscale[h] = __uint_as_float((uint32_t)(127 + e) << 23) * (1.4426950408889634f * 0.08838834764831845f);
 #pragma unroll

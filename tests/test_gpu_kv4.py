@@ -252,6 +252,22 @@ def test_scores_far_apart_leave_one_row(amp, rows, g, dtype):
     check_one_hot(amp, dtype, g, rows)
 
 
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("g", [2, 8])
+@pytest.mark.parametrize("amp,rows", [(1e32, 300), (1e36, 300), (1e36, 9000), (4e37, 300)])
+def test_the_largest_finite_queries(amp, rows, g, dtype):
+    check_one_hot(amp, dtype, g, rows)
+
+
+@pytest.mark.parametrize("amp", [1e-28, 1e-34, 1e-38])
+def test_the_smallest_queries(amp):
+    c = filled([300], 1, 512, seed=52)
+    q = (rand(1, 8, R.D, seed=53) * amp)
+    out = torch.zeros(1, 8, R.D, dtype=BF, device="cuda")
+    c.paris_kv4_attend(q, out)
+    check_attend(c, q, out)
+
+
 @pytest.mark.parametrize("batch", [2, 33, 128, 129, 300])
 def test_batches_of_very_different_lengths(batch):
     gen = torch.Generator().manual_seed(batch)
