@@ -36,8 +36,8 @@
 //
 // What a row does not see has weight 0, but 0 times an infinity or NaN in V
 // is NaN: value rows past the end of a sequence are cleared in shared memory,
-// and a row whose result is not finite is computed again by prompt_row, which
-// reads only what the row sees.
+// and a row whose result is not finite is computed again, when the block's
+// items are done, by prompt_row, which reads only what the row sees.
 #include <atomic>
 #include <algorithm>
 
@@ -167,6 +167,23 @@ __device__ __forceinline__ int seq_blocks(const PromptArgs& a, int s, int tokens
   return blocks_of(min64(lq, a.max_q), tokens);
 }
 
+__device__ __forceinline__ PromptCursor first_cursor(const PromptArgs& a) {
+  const int lane = threadIdx.x & 31, tokens = kTiles * (kTile / a.g);
+  PromptCursor cur{};
+  if (a.cu_q == nullptr) {
+    cur.units = (int64_t)blocks_of(a.max_q, tokens) * a.n_seqs;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kFewSeqs / 32; ++i) {
+      cur.few[i] = seq_blocks(a, 32 * i + lane, tokens);
+      cur.units += __reduce_add_sync(kFull, (uint32_t)cur.few[i]);
+    }
+    for (int s0 = kFewSeqs; s0 < a.n_seqs; s0 += 32) cur.units += __reduce_add_sync(kFull, (uint32_t)seq_blocks(a, s0 + lane, tokens));
+  }
+  cur.units *= a.hkv;
+  return cur;
+}
+
 // Item `it` of this block (a warp computes it).  False: there is no such item.
 //
 // Units are numbered by query block in descending order, so that those that
@@ -277,6 +294,31 @@ __device__ __forceinline__ bool prompt_item(const PromptArgs& a, int it, PromptC
   return true;
 }
 
+// A softmax warp's rows of all the block's items once more: those whose result
+// is not finite are computed again.  That takes as long as there are keys
+// (32 rows of each of eight warps that see 65536 keys: 0.35 s), so it waits
+// until every item is done and no role waits for another: what is in V decides
+// how long it takes, and no wait's limit may depend on that.
+__device__ __noinline__ void prompt_again(const PromptArgs& a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tq = kTile / a.g, first = (warp & 3) * 32;
+  PromptCursor cur = first_cursor(a);
+  PromptItem w;
+  __syncwarp();  // a row was stored by several lanes, and is read by all
+  for (int it = 0; prompt_item(a, it, cur, w); ++it) {
+    const int n = (int)min64(w.lq, a.max_q);
+    for (int r = first; r < min(first + 32, tq * a.g); ++r) {
+      const int tok = w.t0 + (warp >> 2) * tq + r / a.g, h = w.kvh * a.g + r % a.g;
+      if (tok >= n) break;
+      const __nv_bfloat16* out = a.out + (a.cu_q ? 0 : w.s * a.so.seq) + (int64_t)(w.q0 + tok) * a.so.token + h * a.so.head;
+      const uint2 y = *reinterpret_cast<const uint2*>(out + 4 * lane);
+      const uint32_t x = y.x & 0x7f807f80u, z = y.y & 0x7f807f80u;  // exponents; all ones: infinities and NaN
+      const bool bad = (x & 0xffffu) == 0x7f80u || x >> 16 == 0x7f80u || (z & 0xffffu) == 0x7f80u || z >> 16 == 0x7f80u;
+      if (__any_sync(kFull, bad)) prompt_row(a, w.s, h, w.q0, tok, w.k0, min(w.lk, tok + w.lk - w.lq + 1));
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kPromptThreads, 1)
     k_prompt_attend(const __grid_constant__ PromptArgs a, const __grid_constant__ PromptMaps maps) {
   extern __shared__ uint8_t dyn[];
@@ -330,19 +372,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int tq = kTile / a.g;
       int nq = 0, x = 0;  // query loads, ring loads so far
       bool ok = true;
-      PromptCursor cur{};
-      const int tokens = kTiles * tq;
-      if (a.cu_q == nullptr) {
-        cur.units = (int64_t)blocks_of(a.max_q, tokens) * a.n_seqs;
-      } else {
-#pragma unroll
-        for (int i = 0; i < kFewSeqs / 32; ++i) {
-          cur.few[i] = seq_blocks(a, 32 * i + lane, tokens);
-          cur.units += __reduce_add_sync(kFull, (uint32_t)cur.few[i]);
-        }
-        for (int s0 = kFewSeqs; s0 < a.n_seqs; s0 += 32) cur.units += __reduce_add_sync(kFull, (uint32_t)seq_blocks(a, s0 + lane, tokens));
-      }
-      cur.units *= a.hkv;
+      PromptCursor cur = first_cursor(a);
       auto item = [&](int it, PromptItem& w) { return prompt_item(a, it, cur, w); };
       PromptItem w, next;
       bool more = item(0, next);
@@ -492,7 +522,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int row_tok = row / a.g, row_head = row % a.g;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + i * kTile, to = tmem + lanes + (2 + i) * kTile;
-    bool ok = true;
+    bool ok = true, again = false;  // again: a row's result is not finite
     uint32_t ns = 0, no = 0;  // steps and results of the tile so far
     for (int it = 0; ok; ++it) {
       ok = __all_sync(kFull, bar_wait(item_full + 8 * (it % kItems), (it / kItems) & 1, gave_up));
@@ -513,7 +543,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int64_t nqb = (a.max_q + kTiles * tq - 1) / (kTiles * tq);
         part = a.ws + (((((int64_t)ws * a.hkv + w.kvh) * nqb + w.qb) * a.nsplit + w.part) * (kTiles * kTile) + i * kTile + row) * kPartRow;
       }
-      const int k0 = w.k0;
       if (part != nullptr && live) part[2] = __int_as_float(w.parts);
       __syncwarp();
       if (lane == 0) bar_arrive(item_empty + 8 * (it % kItems));
@@ -703,13 +732,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           a.lse[((int64_t)(a.cu_q ? 0 : ws) * a.hq + h) * a.rows_q + q0 + tok] = last_key >= 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
         float z0, z1;
         unpair2(none, z0, z1);
-        for (uint32_t again = __ballot_sync(kFull, live && !(z0 + z1 == 0.f)); again; again &= again - 1) {
-          const int src = __ffs(again) - 1;
-          const int t = __shfl_sync(kFull, tok, src);
-          prompt_row(a, ws, __shfl_sync(kFull, h, src), q0, t, k0, min(lk, t + lk - lq + 1));
-        }
+        again = again || (live && !(z0 + z1 == 0.f));
       }
     }
+    if (ok && __any_sync(kFull, again)) prompt_again(a);
     tm_fence_before();
   }
   __syncthreads();

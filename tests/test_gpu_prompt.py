@@ -176,6 +176,56 @@ def test_non_finite_values_that_a_query_sees_reach_it():
     assert not torch.isnan(out[:, :, 6:]).any()
 
 
+@pytest.mark.parametrize("hq,hkv,n", [(4, 2, 90), (8, 1, 30)])
+def test_not_finite_values_of_one_sequence_leave_the_others_alone(hq, hkv, n):
+    # blocks that walk several sequences, clean ones in front of the others and behind them
+    gen = torch.Generator().manual_seed(23)
+    lens = torch.randint(1, 200, (n,), generator=gen).tolist()
+    bad = n // 2
+    lens[bad] = 333
+    g = hq // hkv
+    q, k, v = make(lens, lens, hq, hkv, seed=23)
+    a = sum(lens[:bad])
+    v[a + 300, 0, 9] = math.nan
+    v[a + 200, hkv - 1, 5] = math.inf
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((hq, q.shape[0]), 7.0, device="cuda")
+    cu = R.starts(lens)
+    P.paris_prompt_attend(q, k, v, out, cu_q=cu, cu_k=cu, max_q=max(lens), max_k=max(lens), lse=lse)
+    P.paris_prompt_check()
+    at = 0
+    for i, m in enumerate(lens):
+        s = slice(at, at + m if i != bad else at + 200)
+        check_seq(q[s], k[s], v[s], out[s], lse[:, s], g)
+        at += m
+    rows = out[a:a + 333]
+    assert torch.isnan(rows[300:, :g, 9]).all() and not torch.isnan(rows[:300, :g, 9]).any()
+    assert torch.all(rows[200:, hq - g:, 5] == math.inf) and torch.isfinite(rows[:200, hq - g:, 5]).all()
+    v0 = v[a:a + 333].clone()
+    v0[:, :, [5, 9]] = 0
+    got = rows.clone()
+    got[:, :, [5, 9]] = 0
+    check_seq(q[a:a + 333], k[a:a + 333], v0, got, lse[:, a:a + 333], g)
+
+
+def test_a_not_finite_value_that_long_rows_see_costs_no_other_sequence():
+    # 256 rows that see a NaN over 800000 keys take seconds to compute again; the blocks walk other sequences too
+    n, others = 800000, 400
+    gen = torch.Generator(device="cuda").manual_seed(24)
+    rand = lambda rows: torch.randn(rows, 1, R.D, generator=gen, device="cuda").to(BF)  # noqa: E731
+    q, k, v = rand(256 + others), rand(n + others), rand(n + others)
+    v[3, 0, 7] = math.nan
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((1, q.shape[0]), 7.0, device="cuda")
+    P.paris_prompt_attend(q, k, v, out, cu_q=R.starts([256] + [1] * others), cu_k=R.starts([n] + [1] * others), max_q=256,
+                          max_k=n, lse=lse)
+    P.paris_prompt_check()
+    assert torch.equal(out[256:], v[n:])  # one key each
+    assert torch.isnan(out[:256, 0, 7]).all() and torch.isfinite(out[:256, 0, 8:]).all()
+    v[3, 0, 7] = out[252:256, 0, 7] = 0
+    check_seq(q[252:256], k[:n], v[:n], out[252:256], lse[:, 252:256], 1)
+
+
 def test_rows_that_no_sequence_owns_are_left_alone():
     q, k, v = make([300], [300], 2, 2, seed=9)
     cu = torch.tensor([20, 90, 90, 250], dtype=torch.int32, device="cuda")
