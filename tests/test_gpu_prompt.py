@@ -348,6 +348,24 @@ def test_window_weights_of_chunks_padded_layout_and_queries_that_see_nothing():
         assert torch.all((got[i].double() - want).abs() <= tol + 1e-30)
 
 
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("hq,hkv,n,window", [(4, 2, 300, 32), (8, 2, 400, 64), (1, 1, 400, 32), (4, 1, 700, 200)])
+def test_queries_whose_lse_says_so_add_nothing(hq, hkv, n, window, bad):
+    # padding at the end of a batch's prompts: lse = -inf there, and anything in q
+    q, k, v = make([n], [n], hq, hkv, seed=25)
+    cu = R.starts([n])
+    lse = torch.zeros(hq, n, device="cuda")
+    P.paris_prompt_attend(q, k, v, torch.empty_like(q), cu_q=cu, cu_k=cu, lse=lse)
+    lse[:, n - 5:] = -math.inf
+    lse[0, n - window] = -math.inf
+    want, tol = weights_ref(q, k, lse, hq // hkv, window)
+    q[n - 5:] = bad
+    q[n - window, 0] = bad
+    got = torch.full((hkv, n), 9.0, device="cuda")
+    P.paris_prompt_weights(q, k, lse, got, window=window, cu_q=cu, cu_k=cu)
+    assert torch.all((got.double() - want).abs() <= tol + 1e-30)
+
+
 def test_window_weights_of_many_query_heads_and_sequences():
     for lens, hq, hkv, window in (([40, 300], 128, 1, 7), ([5] * 70 + [400], 6, 2, 4)):
         q, k, v = make(lens, lens, hq, hkv, seed=21)
