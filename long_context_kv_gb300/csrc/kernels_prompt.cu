@@ -58,6 +58,13 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b, float acc) {
   return acc;
 }
 
+// A weight's exponent is one fma of the product, the scale and the maximum, in
+// which the maximum's own rounding, 2^-24 of it, is left over.  It does no harm
+// while weights stay within float32 and bf16, as a row's sum and result are off
+// by the same factor; from a maximum of 2^31 on they would not, and rows past
+// 2^29 are left to prompt_row, whose largest weight is 1 at any size.
+__device__ __forceinline__ bool too_far(float m) { return fabsf(m) > 536870912.f && m != -INFINITY; }
+
 // One query row by one warp: its visible keys 32 at a time, a lane per key
 // for the scores, four channels per lane for the weighted sum.  Only rows
 // that the query sees are read.
@@ -657,7 +664,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         ++no;
         tm_fence_after();
       }
-      const float inv = l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing: 0
+      const float inv = too_far(m) ? NAN : l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing: 0
       // 0 times every value, added up: 0 but for infinities and NaN
       uint64_t none = 0;
       const uint64_t inv2 = pair2(inv, inv);
@@ -803,6 +810,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_prompt_join(PromptArgs a, in
     o[c] *= inv;
     finite = finite && fabsf(o[c]) < INFINITY;
   }
+  finite = finite && !too_far(M);
   const int64_t visible = max64(0, min64(lk, tok + lk - lq + 1));
   if (!__all_sync(kFull, finite)) {
     prompt_row(a, s, h, q0, tok, k0, visible);

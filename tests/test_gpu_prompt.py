@@ -83,6 +83,46 @@ def test_flat_and_very_peaked_scores(amp):
     check([700], [700], 4, 2, seed=4, amp=amp)
 
 
+def one_hot_prompt(lens_q, lens_k, hq, hkv, amp, seed):
+    """Scores so far apart that each row's softmax is one key: q, k, v, each row's key, its score and how far float32
+    puts that off, on the CPU."""
+    gen = torch.Generator().manual_seed(seed)
+    q, k, v = (torch.randn(sum(n), h, R.D, generator=gen) for n, h in ((lens_q, hq), (lens_k, hkv), (lens_k, hkv)))
+    q, k, v = (q * amp).to(BF), (k * amp).to(BF), v.to(BF)
+    best = torch.zeros(hq, sum(lens_q), dtype=torch.int64)
+    top, off = torch.zeros(2, hq, sum(lens_q), dtype=torch.float64)
+    a = b = 0
+    for lq, lk in zip(lens_q, lens_k):
+        seen = torch.arange(lk)[None] <= torch.arange(lq)[:, None] + (lk - lq)
+        for h in range(hq):
+            x, y = q[a:a + lq, h].double(), k[b:b + lk, h * hkv // hq].double()
+            s = (x @ y.T / math.sqrt(R.D)).masked_fill(~seen, -math.inf)
+            t = s.topk(min(2, lk), dim=-1)
+            # 128 float32 products and the scale put a score off by less than 2^-16 of its terms; weights of 2^-150 are 0
+            off[h, a:a + lq] = 2.0 ** -16 * (x.abs() @ y.abs().T).amax(-1) / math.sqrt(R.D)
+            if lk > 1:
+                assert torch.all(t.values[:, 0] - t.values[:, 1] > 2 * off[h, a:a + lq] + 150 * math.log(2))
+            best[h, a:a + lq], top[h, a:a + lq] = b + t.indices[:, 0], t.values[:, 0]
+        a, b = a + lq, b + lk
+    return q, k, v, best, top, off
+
+
+@pytest.mark.parametrize("amp", [1e3, 3e4, 1e5, 1e15])
+@pytest.mark.parametrize("lens_q,lens_k,hq,hkv,seed", [([3, 40, 7], [3, 40, 7], 4, 2, 1), ([4], [3000], 2, 1, 2),
+                                                       ([1, 2] * 80, [1, 30] * 80, 2, 1, 2)])
+def test_scores_far_apart_leave_one_key(lens_q, lens_k, hq, hkv, seed, amp):
+    q, k, v, best, top, off = one_hot_prompt(lens_q, lens_k, hq, hkv, amp, seed)
+    out = torch.full_like(q, 7.0, device="cuda")
+    lse = torch.full((hq, q.shape[0]), 7.0, device="cuda")
+    P.paris_prompt_attend(q.cuda(), k.cuda(), v.cuda(), out, cu_q=R.starts(lens_q), cu_k=R.starts(lens_k), max_q=max(lens_q),
+                          max_k=max(lens_k), lse=lse)
+    for h in range(hq):
+        want = v[best[h], h * hkv // hq].double()
+        # the weight's rounding and the result's
+        assert torch.all((out[:, h].cpu().double() - want).abs() <= 2.01 * R.HALF_BF16 * want.abs())
+    assert torch.all((lse.cpu().double() - top).abs() <= off)
+
+
 def test_a_longer_prompt_with_a_running_maximum_that_grows():
     lens = [2500]
     q, k, v = make(lens, lens, 4, 1, seed=5)
