@@ -67,7 +67,8 @@ __device__ __forceinline__ bool too_far(float m) { return fabsf(m) > 536870912.f
 
 // One query row by one warp: its visible keys 32 at a time, a lane per key
 // for the scores, four channels per lane for the weighted sum.  Only rows
-// that the query sees are read.
+// that the query sees are read.  The sum is held as the mean so far, which
+// stays within the values' range where the plain sum may not.
 __device__ __noinline__ void prompt_row(const PromptArgs& a, int s, int h, int64_t q0, int64_t i, int64_t k0, int64_t visible) {
   const int lane = threadIdx.x & 31;
   const int kvh = h / a.g;
@@ -95,20 +96,21 @@ __device__ __noinline__ void prompt_row(const PromptArgs& a, int s, int h, int64
     float ps = p;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) ps += __shfl_xor_sync(kFull, ps, off);
-    l = l * f + ps;
+    const float before = l * f;
+    l = before + ps;
+    const float share = p / l, old = before / l;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) o[c] *= f;
+    for (int c = 0; c < 4; ++c) o[c] *= old;
     for (int j = 0; j < n; ++j) {
-      const float pj = __shfl_sync(kFull, p, j);
+      const float pj = __shfl_sync(kFull, share, j);
       float vy[4];
       load4(v + (j0 + j) * a.sv.token, 1, 4 * lane, vy);
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[c] = fmaf(pj, vy[c], o[c]);
     }
   }
-  const float inv = visible > 0 ? 1.f / l : 0.f;
   __nv_bfloat16* out = a.out + (a.cu_q ? 0 : s * a.so.seq) + (q0 + i) * a.so.token + h * a.so.head;
-  *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+  *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
   if (a.lse != nullptr && lane == 0)
     a.lse[((int64_t)(a.cu_q ? 0 : s) * a.hq + h) * a.rows_q + q0 + i] = visible > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
 }

@@ -266,6 +266,23 @@ def test_a_not_finite_value_that_long_rows_see_costs_no_other_sequence():
     check_seq(q[252:256], k[:n], v[:n], out[252:256], lse[:, 252:256], 1)
 
 
+@pytest.mark.parametrize("lens_q,lens_k", [([200], [200]), ([9], [3000]), ([3, 70] * 80, [3, 90] * 80)])
+def test_the_largest_finite_values(lens_q, lens_k):
+    # sums of two such values pass float32's range, their mean does not
+    hq, hkv = 2, 1
+    q, k, v = make(lens_q, lens_k, hq, hkv, seed=26, amp=0.3)
+    v = (3e38 * torch.sign(v) - 1e38 * (v > 1)).to(BF)
+    v[:, :, ::4] = 3.3e38
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((hq, q.shape[0]), 7.0, device="cuda")
+    P.paris_prompt_attend(q, k, v, out, cu_q=R.starts(lens_q), cu_k=R.starts(lens_k), max_q=max(lens_q),
+                          max_k=max(lens_k), lse=lse)
+    a = b = 0
+    for lq, lk in zip(lens_q, lens_k):
+        check_seq(q[a:a + lq], k[b:b + lk], v[b:b + lk], out[a:a + lq], lse[:, a:a + lq], hq // hkv)
+        a, b = a + lq, b + lk
+
+
 def test_rows_that_no_sequence_owns_are_left_alone():
     q, k, v = make([300], [300], 2, 2, seed=9)
     cu = torch.tensor([20, 90, 90, 250], dtype=torch.int32, device="cuda")
