@@ -426,10 +426,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
       }
       if (!ok && lane == 0) {  // given up: what was issued lands before the block ends
-        const uint64_t t0 = now_ns();
-        while (nq > 0 && !bar_try(q_full, (nq - 1) & 1) && now_ns() - t0 < kWaitNs) {}
+        WaitLimit limit(now_ns());
+        while (nq > 0 && !bar_try(q_full, (nq - 1) & 1) && !limit.over(now_ns())) {}
         for (int y = max(0, x - kStages); y < x; ++y)
-          while (!bar_try(full + 8 * (y % kStages), (y / kStages) & 1) && now_ns() - t0 < kWaitNs) {}
+          while (!bar_try(full + 8 * (y % kStages), (y / kStages) & 1) && !limit.over(now_ns())) {}
       }
     } else if (warp == 8) {
       // ---- products (the whole warp walks; one lane issues)

@@ -159,10 +159,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
                    k_full + 8 * st);
       }
       if (x < total) {  // given up: what was issued lands before the block ends
-        const uint64_t t0 = now_ns();
+        WaitLimit limit(now_ns());
         for (int y = max(0, x - kWStages); y < x; ++y)
-          while (!bar_try(k_full + 8 * (y % kWStages), (y / kWStages) & 1) && now_ns() - t0 < kWaitNs) {}
-        while (x > 0 && !bar_try(q_full, ((x - 1) / ntile) & 1) && now_ns() - t0 < kWaitNs) {}
+          while (!bar_try(k_full + 8 * (y % kWStages), (y / kWStages) & 1) && !limit.over(now_ns())) {}
+        while (x > 0 && !bar_try(q_full, ((x - 1) / ntile) & 1) && !limit.over(now_ns())) {}
       }
     }
   } else if (warp == 8) {

@@ -5,6 +5,7 @@
 #include <cuda.h>
 
 #include "kv4_internal.cuh"
+#include "wait_limit.h"
 
 namespace paris {
 namespace {
@@ -13,7 +14,6 @@ constexpr int kTile = 128;  // rows of a product: query rows, or keys
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kScaleLog2 = kLog2e * 0.08838834764831845f;  // log2(e) / sqrt(128)
-constexpr uint64_t kWaitNs = 4000000000ull;  // a wait that takes this long gives up
 
 static __device__ uint32_t g_gave_up;  // set when a wait gave up; one word per translation unit
 
@@ -37,17 +37,17 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ uint64_t now_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;\n" : "=l"(t));
+__device__ __forceinline__ uint32_t now_ns() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;\n" : "=r"(t));
   return t;
 }
 // Wait for a phase; false when it, or another wait of the block, gave up.
 __device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
-  const uint64_t t0 = now_ns();
+  WaitLimit limit(now_ns());
   while (!bar_try(bar, parity)) {
     if (*gave_up) return false;
-    if (now_ns() - t0 > kWaitNs) {
+    if (limit.over(now_ns())) {
       *gave_up = 1;
       atomicOr(&g_gave_up, 1u);
       return false;
@@ -105,8 +105,8 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 __device__ __forceinline__ void mma_drain(uint32_t bar) {
   if (elect()) mma_commit(bar);
   __syncwarp();
-  const uint64_t t0 = now_ns();
-  while (!bar_try(bar, 0) && now_ns() - t0 < kWaitNs) {}
+  WaitLimit limit(now_ns());
+  while (!bar_try(bar, 0) && !limit.over(now_ns())) {}
 }
 __device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
