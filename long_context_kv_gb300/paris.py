@@ -468,7 +468,8 @@ class KV4Cache:
     """A cache in 4 bits (paris_kv4): its arrays are torch tensors, given by the caller or made by `create`.
 
     k_codes, v_codes uint8 [batch, Hkv, max_rows, 64]; k_scales, v_scales uint8 [batch, Hkv, max_rows, 4];
-    weights float32 and positions int32 [batch, Hkv, max_rows]; lens and next_pos int32 [batch].
+    weights float32 and positions int32 [batch, Hkv, max_rows]; lens and next_pos int32 [batch].  As with any tensor, a
+    cache that another stream than its own still uses is dropped only after `record_stream`.
     """
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, weights, positions, lens, next_pos):
@@ -509,6 +510,13 @@ class KV4Cache:
                    v_codes=z(*n, 64, dtype=torch.uint8), v_scales=z(*n, 4, dtype=torch.uint8),
                    weights=z(*n, dtype=torch.float32), positions=z(*n, dtype=torch.int32),
                    lens=z(batch, dtype=torch.int32), next_pos=z(batch, dtype=torch.int32))
+
+    def record_stream(self, stream):
+        """torch.Tensor.record_stream for all of the cache's memory, also for what only the cache knows of: once it is
+        dropped, none of it is given away before what `stream` has been given until then is done."""
+        for t in (self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.weights, self.positions, self.lens,
+                  self.next_pos, self._words):
+            t.record_stream(stream)
 
     def _bytes(self, key, call):
         """Workspace bytes of a call, asked once per kind of call."""

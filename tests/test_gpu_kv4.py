@@ -333,6 +333,10 @@ def snapshot(c):
     return {n: getattr(c, n).clone() for n in ("k_codes", "v_codes", "k_scales", "v_scales", "weights", "positions")}
 
 
+def snapshot_tensors(c):
+    return c.k_codes, c.v_codes, c.k_scales, c.v_scales, c.weights, c.positions, c.lens, c.next_pos
+
+
 def check_evict(c, keep, sink, recent):
     before, lens = snapshot(c), c.lens.tolist()
     nxt = c.next_pos.tolist()
@@ -450,6 +454,23 @@ def test_from_a_prompt_to_decode_steps_under_a_budget():
         check_attend(c, qd, od, before)
         check_evict(c, keep, sink, recent)
     assert c.lens.tolist() == [128, 95, 128] and c.next_pos.tolist() == [m + 5 for m in lens]
+
+
+def test_a_dropped_cache_is_kept_for_the_streams_that_use_it():
+    x = rand(1, 1, R.D, seed=310).to(BF)
+    s = torch.cuda.Stream()
+    c = P.KV4Cache.create(1, 1, 64)
+    own = {t.data_ptr() for t in (*snapshot_tensors(c), c._words)}
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(4 * 10 ** 9)  # two seconds: the append runs after them
+        c.paris_kv4_append(x, x)
+    c.record_stream(s)
+    del c
+    new = [torch.empty(2, dtype=torch.int32, device="cuda") for _ in range(5000)]
+    assert not s.query()
+    assert own.isdisjoint(t.data_ptr() for t in new)
+    torch.cuda.synchronize()
 
 
 def test_steps_in_a_replayed_graph_walk_on():
