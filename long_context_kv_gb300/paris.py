@@ -333,6 +333,14 @@ def _on(index, *tensors):
         raise ValueError(f"the tensors are on cuda:{index}, the current device is cuda:{now}")
 
 
+def _number(x, name, bits=64):
+    """An integer for a C argument of so many bits: ctypes would keep only the lower ones of a larger one."""
+    x = int(x)
+    if x.bit_length() >= bits:
+        raise ValueError(f"{name}: {x} is out of range")
+    return x
+
+
 def _raw_stream(index, stream):
     """The stream's handle: the one given, or the device's current one."""
     if stream is not None:
@@ -455,12 +463,13 @@ def paris_prompt_weights(q, k, lse, weights, window, cu_q=None, cu_k=None, max_k
     """weights[h, j]: the softmax weights that each sequence's last `window` queries give to its key j, added up over
     them and over the query heads of KV head h.  lse as paris_prompt_attend gives it; weights: float32 [Hkv, rows_k]
     (packed) or [batch, Hkv, T]."""
+    window = _number(window, "window", 32)
     p, hq, rows_q, hkv, rows_k, packed = _prompt(q, k, cu_q, cu_k, None, max_k)
     index = q.get_device()
     _on(index, lse, weights)
     _shaped(lse, "lse", (hq, rows_q) if packed else q.shape[:3], _torch.float32)
     _shaped(weights, "weights", (hkv, rows_k) if packed else k.shape[:3], _torch.float32)
-    _check((_lib or load()).paris_prompt_weights(p, _raw(q), _raw(k), PARIS_BF16, _flat(lse), int(window),
+    _check((_lib or load()).paris_prompt_weights(p, _raw(q), _raw(k), PARIS_BF16, _flat(lse), window,
                                                  _flat(weights), _raw_stream(index, stream)))
 
 
@@ -544,6 +553,8 @@ class KV4Cache:
         """Add tokens: packed [rows, Hkv, 128] with int32 starts cu [batch + 1] (max_new: at least the most tokens of
         a sequence, default all rows), or [batch, Hkv, T, 128].  weights: float32 [Hkv, rows] or [batch, Hkv, T]."""
         packed = cu is not None
+        if max_new is not None:
+            max_new = _number(max_new, "max_new")
         rows, heads, seqs, ks = _heads(k, "k", packed)
         if v.shape != k.shape or v.dtype is not k.dtype:
             raise ValueError("k and v must have the same shape and dtype")
@@ -557,7 +568,7 @@ class KV4Cache:
             _shaped(weights, "weights", (heads, rows) if packed else k.shape[:3], _torch.float32)
         _check((_lib or load()).paris_kv4_store(
             self._ref, _raw(k), _raw(v), _code(k), _STRIDES.pack(*ks), _STRIDES.pack(*vs),
-            rows, _raw(cu), rows if max_new is None else int(max_new), _flat(weights), _raw_stream(self._index, stream)))
+            rows, _raw(cu), rows if max_new is None else max_new, _flat(weights), _raw_stream(self._index, stream)))
 
     def paris_kv4_append(self, k, v, stream=None):
         """Add one token to every sequence: k, v [batch, Hkv, 128]."""
@@ -583,11 +594,12 @@ class KV4Cache:
 
     def paris_kv4_evict(self, keep, sink=0, recent=0, stream=None):
         """At most `keep` rows for each sequence: protected ones and the heaviest others."""
+        keep, sink, recent = _number(keep, "keep"), _number(sink, "sink"), _number(recent, "recent")
         _on(self._index)
         lib = _lib or load()
         n = self._ws.get("evict") or self._bytes("evict", lambda b: lib.paris_kv4_evict_workspace(self._ref, b))
         handle = _raw_stream(self._index, stream)
-        _check(lib.paris_kv4_evict(self._ref, int(keep), int(sink), int(recent), self._space(n, stream, handle), n, handle))
+        _check(lib.paris_kv4_evict(self._ref, keep, sink, recent, self._space(n, stream, handle), n, handle))
 
     def paris_kv4_read(self, k_out, v_out, stream=None):
         """The values of the first rows: k_out, v_out bfloat16 [batch, Hkv, rows, 128]."""

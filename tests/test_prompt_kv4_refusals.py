@@ -157,6 +157,21 @@ def test_binding_checks_shapes_types_and_devices(lib):
         P.KV4Cache(z, z, z, z, z, z, z, z)
 
 
+def test_numbers_that_a_c_argument_does_not_hold(lib):
+    # ctypes would take 2^32 + 4 for 4, and 2^64 + 1 for 1
+    q, k = torch.zeros(10, 4, 128, dtype=BF), torch.zeros(10, 2, 128, dtype=BF)
+    c = object.__new__(P.KV4Cache)
+    for window in (1 << 31, (1 << 32) + 4, -(1 << 32) + 4):
+        with pytest.raises(ValueError, match="window.*out of range"):
+            P.paris_prompt_weights(q, k, None, None, window=window)
+    for big in ((1 << 64) + 1, 1 << 63, -(1 << 64) + 1):
+        with pytest.raises(ValueError, match="max_new.*out of range"):
+            c.paris_kv4_store(k, k, cu=k, max_new=big)
+        for args, name in (((big, 0, 0), "keep"), ((4, big, 0), "sink"), ((4, 0, big), "recent")):
+            with pytest.raises(ValueError, match=name + ".*out of range"):
+                c.paris_kv4_evict(*args)
+
+
 def test_packed_descriptions_are_the_structures():
     assert P._PROMPT.size == ctypes.sizeof(P.paris_prompt)
     assert P._STRIDES.size == ctypes.sizeof(P.paris_strides)
