@@ -473,6 +473,39 @@ def test_a_dropped_cache_is_kept_for_the_streams_that_use_it():
     torch.cuda.synchronize()
 
 
+def test_steps_of_a_cache_made_for_far_longer_sequences():
+    # the capacity asks for clusters in the eviction, the lengths for a few tiles
+    lens, hq, hkv, keep = [1000, 37, 4000], 8, 2, 900
+    c = filled(lens, hkv, 140000, seed=320)
+    gen = torch.Generator(device="cuda").manual_seed(321)
+    for b, n in enumerate(lens):
+        c.weights[b, :, :n] = torch.rand(hkv, n, generator=gen, device="cuda")
+    check_evict(c, keep, 4, 100)
+    for step in range(3):
+        x = rand(2, len(lens), hkv, R.D, seed=330 + step).to(BF)
+        q = rand(len(lens), hq, R.D, seed=340 + step, amp=2.0).to(BF)
+        out = torch.full_like(q, 9.0)
+        c.paris_kv4_append(x[0], x[1])
+        before = c.weights.clone()
+        c.paris_kv4_attend(q, out, accumulate=True)
+        check_attend(c, q, out, before)
+        check_evict(c, keep, 4, 100)
+    assert c.lens.tolist() == [900, 40, 900]
+
+
+def test_a_long_prompt_is_evicted_down_to_its_budget():
+    n, hkv = 33000, 2
+    c = filled([n, n // 2], hkv, n, seed=350)
+    gen = torch.Generator(device="cuda").manual_seed(351)
+    c.weights[0] = torch.rand(hkv, n, generator=gen, device="cuda") ** 8  # a prompt's: most of them small
+    c.weights[1, :, :n // 2] = torch.rand(hkv, n // 2, generator=gen, device="cuda") ** 8
+    check_evict(c, 4096, 16, 512)
+    q = rand(2, 8, R.D, seed=352, amp=2.0).to(BF)
+    before, out = c.weights.clone(), torch.full_like(q, 9.0)
+    c.paris_kv4_attend(q, out, accumulate=True)
+    check_attend(c, q, out, before)
+
+
 def test_steps_in_a_replayed_graph_walk_on():
     lens, hq, hkv, keep = [100, 37], 4, 2, 64
     mk = lambda: filled(lens, hkv, 128, seed=300, garbage=False)  # noqa: E731

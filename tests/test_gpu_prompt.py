@@ -283,6 +283,47 @@ def test_the_largest_finite_values(lens_q, lens_k):
         a, b = a + lq, b + lk
 
 
+def walked(lens_q, hq, hkv):
+    """Items that the fullest of 152 blocks walks: 256 rows of a KV head each."""
+    tokens = 2 * (128 // (hq // hkv))
+    return sum(-(-n // tokens) for n in lens_q) * hkv / 152
+
+
+@pytest.mark.parametrize("n,top,hq,hkv", [(40, 650, 32, 2), (200, 280, 16, 2), (64, 200, 24, 24), (65, 200, 24, 24)])
+def test_blocks_that_walk_many_items(n, top, hq, hkv):
+    # by query block (up to 64 sequences) and one sequence after the other; some empty, some whose queries see nothing
+    gen = torch.Generator().manual_seed(27 + n)
+    lens_k = torch.randint(1, top, (n,), generator=gen).tolist()
+    lens_q = [m if i % 4 else max(1, m // 3) for i, m in enumerate(lens_k)]
+    lens_k[3], lens_q[5], lens_k[7] = 0, 0, max(1, lens_q[7] // 2)
+    assert walked(lens_q, hq, hkv) > 8
+    check(lens_q, lens_k, hq, hkv, seed=28)
+
+
+def test_blocks_that_walk_many_items_of_a_padded_batch():
+    b, hq, hkv, t = 21, 16, 2, 1200
+    gen = torch.Generator(device="cuda").manual_seed(29)
+    q, k, v = (torch.randn(b, h, t, R.D, generator=gen, device="cuda").to(BF) for h in (hq, hkv, hkv))
+    assert walked([t] * b, hq, hkv) > 10
+    out, lse = torch.full_like(q, 7.0), torch.zeros(b, hq, t, device="cuda")
+    P.paris_prompt_attend(q, k, v, out, lse=lse)
+    for i in range(b):
+        check_seq(q[i].transpose(0, 1), k[i].transpose(0, 1), v[i].transpose(0, 1), out[i].transpose(0, 1), lse[i], hq // hkv)
+    P.paris_prompt_check()
+
+
+@pytest.mark.parametrize("lq", [32768, 300])
+def test_prompts_of_32768_keys(lq):
+    lk, hq, hkv = 32768, 4, 2
+    q, k, v = make([lq], [lk], hq, hkv, seed=30)
+    out, lse = torch.full_like(q, 7.0), torch.zeros(hq, lq, device="cuda")
+    P.paris_prompt_attend(q, k, v, out, cu_q=R.starts([lq]), cu_k=R.starts([lk]), lse=lse)
+    rows = sorted({*range(0, lq, max(1, lq // 40)), 1, 127, 128, 129, 255, 256, lq - 2, lq - 1})
+    for i in rows:
+        n = i + 1 + lk - lq
+        check_seq(q[i:i + 1], k[:n], v[:n], out[i:i + 1], lse[:, i:i + 1], hq // hkv)
+
+
 def test_rows_that_no_sequence_owns_are_left_alone():
     q, k, v = make([300], [300], 2, 2, seed=9)
     cu = torch.tensor([20, 90, 90, 250], dtype=torch.int32, device="cuda")
@@ -451,6 +492,30 @@ def test_window_weights_of_uneven_sequences(lens, hkv):
         want, tol = weights_ref(q[a:a + n], k[a:a + n], lse[:, a:a + n], 1, 6)
         assert torch.all((got[:, a:a + n].double() - want).abs() <= tol + 1e-30)
         a += n
+
+
+def test_window_weights_in_a_captured_graph_with_new_starts():
+    hq, hkv, total = 8, 2, 700
+    q, k, v = make([total], [total], hq, hkv, seed=31)
+    cu = torch.tensor([0, 300, total], dtype=torch.int32, device="cuda")
+    lse = torch.zeros(hq, total, device="cuda")
+    got = torch.zeros(hkv, total, device="cuda")
+    out = torch.empty_like(q)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        P.paris_prompt_attend(q, k, v, out, cu_q=cu, cu_k=cu, lse=lse)
+        P.paris_prompt_weights(q, k, lse, got, window=40, cu_q=cu, cu_k=cu)
+    for ends in ((300, 700), (1, 129), (0, 512)):
+        cu.copy_(torch.tensor([0, *ends]))
+        got.fill_(9.0)
+        graph.replay()
+        a = 0
+        for e in ends:
+            want, tol = weights_ref(q[a:e], k[a:e], lse[:, a:e], hq // hkv, 40)
+            assert torch.all((got[:, a:e].double() - want).abs() <= tol + 1e-30)
+            a = e
+        assert torch.all(got[:, ends[-1]:] == 9.0)
 
 
 def test_window_weights_do_not_see_other_rows():
