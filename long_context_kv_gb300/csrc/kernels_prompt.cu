@@ -92,13 +92,13 @@ __device__ __noinline__ void prompt_row(const PromptArgs& a, int s, int h, int64
     const float mn = fmaxf(m, mx);
     const float f = m == mn ? 1.f : exp2f(m - mn);
     m = mn;
-    const float p = lane < n ? exp2f(sc - m) : 0.f;
+    const float p = sc == -INFINITY ? 0.f : exp2f(sc - m);  // no weight, and m may be -inf too
     float ps = p;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) ps += __shfl_xor_sync(kFull, ps, off);
     const float before = l * f;
     l = before + ps;
-    const float share = p / l, old = before / l;
+    const float per = l != 0.f ? 1.f / l : 0.f, share = p * per, old = before * per;  // l is 1 at least, or 0
 #pragma unroll
     for (int c = 0; c < 4; ++c) o[c] *= old;
     for (int j = 0; j < n; ++j) {

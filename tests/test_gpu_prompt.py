@@ -324,6 +324,34 @@ def test_prompts_of_32768_keys(lq):
         check_seq(q[i:i + 1], k[:n], v[:n], out[i:i + 1], lse[:, i:i + 1], hq // hkv)
 
 
+@pytest.mark.parametrize("lens_q,lens_k", [([200], [200]), ([9], [3000]), ([3, 70] * 80, [3, 90] * 80)])
+def test_scores_of_minus_infinity_have_no_weight(lens_q, lens_k):
+    # the first keys of each sequence, and NaN values that the last query alone sees: the rows before it are computed twice
+    hq, hkv = 2, 1
+    q, k, v = make(lens_q, lens_k, hq, hkv, seed=32)
+    q[:, :, 0] = 1.0
+    a = b = 0
+    for lq, lk in zip(lens_q, lens_k):
+        k[b:b + lk // 2, :, 0] = -math.inf
+        v[b + lk - 1] = math.nan
+        b += lk
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((hq, q.shape[0]), 7.0, device="cuda")
+    P.paris_prompt_attend(q, k, v, out, cu_q=R.starts(lens_q), cu_k=R.starts(lens_k), max_q=max(lens_q),
+                          max_k=max(lens_k), lse=lse)
+    b = 0
+    for lq, lk in zip(lens_q, lens_k):
+        none = lk // 2  # left out: the result is that of the other keys, and 0 for queries that see no other
+        see = lk - lq
+        if lq > 1:
+            first = max(0, none - see)  # the first query that sees a key with a weight
+            assert torch.all(out[a:a + first] == 0) and torch.all(lse[:, a:a + first] == -math.inf)
+            check_seq(q[a + first:a + lq - 1], k[b + none:b + lk - 1], v[b + none:b + lk - 1], out[a + first:a + lq - 1],
+                      lse[:, a + first:a + lq - 1], hq // hkv)
+        assert torch.isnan(out[a + lq - 1]).all()
+        a, b = a + lq, b + lk
+
+
 def test_rows_that_no_sequence_owns_are_left_alone():
     q, k, v = make([300], [300], 2, 2, seed=9)
     cu = torch.tensor([20, 90, 90, 250], dtype=torch.int32, device="cuda")
