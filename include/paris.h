@@ -339,8 +339,10 @@ typedef struct {
  * [cu_q[s], cu_q[s + 1]) of rows_q and the key rows [cu_k[s], cu_k[s + 1])
  * of rows_k, and the seq strides are not used.  Without (both NULL), entry s
  * of the sequence axis holds rows_q query rows and rows_k key rows.
- * Starts are clamped to [0, rows] and to the start before them; rows that no
- * sequence owns are neither read nor written.  max_q and max_k: at least
+ * Starts ascend.  A start outside [0, rows] counts as the nearest of the two,
+ * and a sequence whose end lies before its start is empty; rows that no
+ * sequence owns are neither read nor written, and of rows that two of them
+ * own, as starts that do not ascend make possible, the results are either's.  max_q and max_k: at least
  * the longest sequence's rows (they size the launch; query rows past max_q
  * are left unwritten).                                                      */
 typedef struct {
@@ -363,6 +365,11 @@ paris_status paris_prompt_workspace(const paris_prompt* p, size_t* bytes);
  * query head h with KV head h / (Hq / Hkv).  A query before the first key
  * (len_q > len_k) sees nothing: o_i = 0, lse_i = -inf.  What lies in rows
  * that a query does not see, infinities and NaN included, does not reach it.
+ * Keys with a score of -inf have no weight, and a query that sees no others
+ * has o_i = 0 as well.  Scores past float32's range are infinities; within it
+ * they may be of any size, and so may values.  (Rows whose result is not finite,
+ * or with a score past 2^29, are computed a second time, key by key: 256 such
+ * rows over 65536 keys take 0.35 s.)  out and lse do not overlap q, k and v.
  * q, k, v: device, bf16 (PARIS_F32 is not supported); out: device bf16;
  * lse: device float32 [sequence axis][Hq][rows_q] (one entry of the sequence
  * axis when packed), or NULL.  Scores, maxima and sums are float32; the
@@ -375,7 +382,8 @@ paris_status paris_prompt_attend(const paris_prompt* p, const void* q, const voi
 
 /* Synchronise the device and report whether a prompt call on it gave up a
  * wait since the last check (PARIS_EDEVICE, then cleared): every wait inside
- * the kernel has a limit of seconds, past which its results are not valid.   */
+ * the kernels has a limit of four seconds, time off the GPU not counted, past
+ * which the call's results are not valid.  No input makes a wait that long.   */
 paris_status paris_prompt_check(void);
 
 /* The weights that the last `window` queries of each sequence give to its
@@ -435,6 +443,7 @@ paris_status paris_kv4_workspace(const paris_kv4* c, int n_q_heads, int accumula
 /* Decode attention over the rows in use: p = softmax(K q / sqrt(d)),
  * out = p V (zeros for an empty sequence), float32 throughout (queries,
  * and softmax weights, enter the products as two half-precision parts; the rows are exact).
+ * Scores past float32's range give NaN; within it queries may be of any size.
  * With accumulate, weights[row] += the sum of p over the query heads of the
  * row's KV head.  q: device, dtype, [batch][Hq][d]; out: device bf16
  * [batch][Hq][d]; at most 16 query heads per KV head.                        */

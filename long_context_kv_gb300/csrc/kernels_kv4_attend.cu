@@ -20,6 +20,8 @@
 //   O^T = V^T P^T, so that the eight columns are what there are few of: for up
 //   to four query heads their upper and lower half-precision parts (22 bits
 //   of a query or weight for the cost of 11), for up to eight two products.
+//   (A bf16 query's eight bits fit the upper part and its lower one is 0; the
+//   products are the same for both types.)
 //   The weights go from the one's result to the other's operand by 8x8
 //   transposes in registers.
 //
@@ -29,9 +31,9 @@
 // by k_kv4_finish, which also turns the scores into weights.  More than eight
 // query heads per KV head are two blocks, each reading the rows.
 //
-// At 131072 rows of 8 KV heads, 4 query heads each (142.6 MB): 35.8 us with the
-// merge.  The copies alone, with nothing computed, take 30.6: 23.5 at 6 TB/s and
-// 7 for the start, the first rows' way and the end.  Fewer instructions no
+// At 131072 rows of 8 KV heads, 4 query heads each (142.6 MB): 35.6 us with the
+// merge.  The copies alone in this form, with nothing computed, take 30.6: 23.5
+// at 6 TB/s and 7 for the start, the first rows' way and the end.  Fewer instructions no
 // longer tell (HFMA2 halved by keys as subnormals: the same), nor do more or
 // fewer warps (12, 16, 20 an SM: within 2 us).
 #include <atomic>
@@ -685,7 +687,8 @@ __global__ void __launch_bounds__(kFinishThreads, kFinishThreads == 256 ? 4 : 1)
 
 int kv4_blocks(int batch, int hkv, int g, int64_t rmax, int sm_count) {
   // one wave of blocks for each KV head and head group, of one tile at least (a
-  // step of 2049 rows: 14.4 us, 15.8 with two); a batch that is cut by its
+  // step of 2049 rows, append and eviction with it, on the GPU alone: 14.4 us,
+  // 15.8 with two); a batch that is cut by its
   // lengths needs more blocks than sequences, and one that is cut evenly a
   // multiple of its sequences
   const int64_t wave = std::max<int64_t>(1, (g <= 4 ? 4 : 3) * (int64_t)sm_count / ((int64_t)hkv * ((g + 7) / 8)));

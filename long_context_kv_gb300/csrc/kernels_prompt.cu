@@ -25,14 +25,21 @@
 // Bound by the tensor cores (4 d flops a visible pair), and right under them
 // by shared memory: a step of both tiles and 128 keys is 2048 cycles of
 // products, whose operands and copies are 256 KB at 128 bytes a cycle, again
-// 2048; it takes 2900 to 3050 (32768 tokens of 8 query heads: 1.31 ms,
-// 1679 TFLOP/s, 0.86 of the measured bf16 rate).  What the steps measured:
+// 2048; it takes 2900 to 3300 (32768 tokens of 8 query heads: 1.39 ms among
+// other passes, 1584 TFLOP/s, 0.81 of the measured bf16 rate in bursts and 0.93
+// of the sustained one).  What the steps measured:
 // operands kept in uniform registers by electing the issuing lane, 2474 ->
 // 1446 us there; a block per item instead of per SM, 1468 against 1364 us; an
 // eighth of the exponentials by a polynomial in the FMA units, 1406 against
 // 1331 us: the special-function units are not what a step waits for.  An
 // item's result takes 4000 cycles more, in which its tile's group does nothing
 // else; that is 15 % of a batch of short prompts.
+//
+// The weights enter P V as bf16, their sum as float32: both operands of a
+// product are of one type, V's, and a second product for what the rounding
+// leaves would be half as many operations again on what bounds the kernel.  The
+// largest error against 64 bits is 2.1e-3 to 2.3e-3 of the result's size, and
+// 1.6e-3 with float32 weights, nearly all of it the result's own rounding.
 //
 // What a row does not see has weight 0, but 0 times an infinity or NaN in V
 // is NaN: value rows past the end of a sequence are cleared in shared memory,
