@@ -52,7 +52,8 @@ typedef enum {
   PARIS_EDEVICE = -7    /* a kernel reported a fault through the status word */
 } paris_status;
 
-typedef enum { PARIS_F32 = 0, PARIS_BF16 = 1 } paris_dtype;
+/* PARIS_E4M3 is a form of a paged cache's rows only. */
+typedef enum { PARIS_F32 = 0, PARIS_BF16 = 1, PARIS_E4M3 = 2 } paris_dtype;
 
 typedef enum {
   PARIS_VOTE_RANK = 0, /* rank r of the query's top-rho centroids gives rho - r votes */
@@ -472,6 +473,136 @@ paris_status paris_kv4_read(const paris_kv4* c, void* k_out, void* v_out, int64_
 /* Synchronise the device and report the status word, then clear it:
  * PARIS_OK, or PARIS_EDEVICE if a store found no room.                       */
 paris_status paris_kv4_check(const paris_kv4* c);
+
+/* ------------------------------------------------------------------------
+ * A cache of pages.
+ *
+ * A pool of n_pages pages of page_rows rows each (a row: the key or value of
+ * one token and KV head), and for every sequence a row of the table that
+ * lists its pages: row r of sequence s is row r % page_rows of page
+ * table[s][r / page_rows].  Sequences may share pages; refs counts the
+ * sequences that hold a page, and a page without any has its bit set in
+ * free_bits.  A page that is not full has one holder.  n_layers layers have
+ * pools of the same form and share the table: pages are taken, shared and
+ * given back for all of them at once.
+ *
+ * As with the 4-bit cache, the calls need no context, every buffer is the
+ * caller's device memory, sizes that vary are read on the device, and
+ * nothing is kept, so calls may be captured into a graph and replayed as the
+ * sequences grow.  Pages are taken in a fixed way, so that results do not
+ * depend on timing: the free pages of the lowest numbers, in the order of the
+ * sequences (or of a call's list).  Calls that change a cache are ordered by
+ * the caller against all others on it; calls that only read it
+ * (paris_paged_attend, paris_paged_read) may run at the same time.
+ *
+ * Rows are bf16 (PARIS_BF16) or 8 bits wide (PARIS_E4M3): e4m3 codes c and a
+ * scale S = 2^e a row, the smallest with max|x| <= 448 S, -60 <= e <= 52,
+ * held as the byte e + 127; the row stands for c S, which is exact in bf16.
+ * Values past +-2^60 become +-2^60 and NaN becomes 0.
+ *
+ * An array's address is 16-byte aligned.  k_pages and v_pages have strides
+ * in elements: positive multiples of 16 bytes, a row's of at least 128
+ * elements, below 2^38; rows of 128 are contiguous.  Lengths outside
+ * [0, max_pages * page_rows] count as the nearest of the two, and so do
+ * entries of the table outside [0, n_pages).                                  */
+typedef struct {
+  int64_t layer, page, head, row;
+} paris_page_strides;
+
+typedef struct {
+  int n_seqs, n_layers, n_kv_heads, head_dim; /* n_seqs <= 4096; n_seqs * n_kv_heads <= 65535; head_dim 128 */
+  int page_rows;                    /* a power of two from 16 to 256                      */
+  int dtype;                        /* PARIS_BF16 or PARIS_E4M3                           */
+  int64_t n_pages, max_pages;       /* pages of a layer's pool (<= 2^21), of a sequence   */
+  void *k_pages, *v_pages;          /* [n_layers][n_pages][Hkv][page_rows][d], any order  */
+  paris_page_strides k, v;
+  uint8_t *k_scales, *v_scales;     /* PARIS_E4M3: [n_layers][n_pages][Hkv][page_rows]    */
+  int32_t* table;                   /* [n_seqs][max_pages]                                */
+  int32_t *lens, *starts;           /* [n_seqs] rows in use; rows before the last growth  */
+  int32_t* refs;                    /* [n_pages]                                          */
+  uint32_t* free_bits;              /* [(n_pages + 31) / 32]; none past n_pages is set    */
+  int32_t* n_used;                  /* [1] pages with a holder                            */
+  uint32_t* status;                 /* [1] bits set by kernels: bit 0: no room; bit 1: a
+                                       number of a sequence outside [0, n_seqs)           */
+} paris_paged;
+
+/* Make room for tokens[s] more rows of every sequence (device int32
+ * [n_seqs]; what is negative counts as 0): pages are taken, starts becomes
+ * the length before and lens the length after.  Where pages or the table do
+ * not suffice, a sequence grows by what there is room for and status bit 0 is
+ * set.  What the new rows hold is what their pages held.                      */
+paris_status paris_paged_grow(const paris_paged* c, const int32_t* tokens, void* stream);
+
+/* Write one layer's keys and values of the rows that the last growth added:
+ * token i of sequence s goes to row starts[s] + i, if that is below lens[s].
+ * k, v: device, PARIS_F32 or PARIS_BF16, rows packed by cu (device,
+ * n_seqs + 1 starts within [0, rows], as in paris_prompt) or, with cu = NULL,
+ * `rows` tokens for every sequence along the seq stride; max_new: at least the
+ * most tokens of a sequence (tokens past it are left out).                    */
+paris_status paris_paged_store(const paris_paged* c, int layer, const void* k, const void* v, paris_dtype dtype,
+                               const paris_strides* ks, const paris_strides* vs, int64_t rows, const int32_t* cu,
+                               int64_t max_new, void* stream);
+
+/* Bytes of the two workspaces of paris_paged_attend.  Host only.             */
+paris_status paris_paged_attend_workspace(const paris_paged* c, int n_q_heads, size_t* bytes, size_t* counter_bytes);
+
+/* Attention of one new token of every sequence over the rows in use of one
+ * layer, or over the last `window` of them (window > 0):
+ *   s_j = <q, k_j> / sqrt(d), lse = log sum_j exp(s_j), out = sum_j exp(s_j - lse) v_j,
+ * query head h with KV head h / (Hq / Hkv).  A sequence without rows, and a
+ * query all of whose scores are -inf, has out = 0 and lse = -inf.  What lies in
+ * rows that are not in use (or outside the window) does not reach the result,
+ * NaN included.  Scores, maxima and sums are float32; scores past
+ * float32's range give NaN.  q: device bf16 [n_seqs][Hq][d]; out: device bf16,
+ * the same; lse: device float32 [n_seqs][Hq], or NULL.  At most 128 query heads
+ * per KV head.  workspace and counters: device, 16-byte aligned, used only by
+ * this call; counters are zeros, and zeros again after it.                    */
+paris_status paris_paged_attend(const paris_paged* c, int layer, const void* q, int n_q_heads, int64_t window,
+                                void* out_bf16, float* lse, void* workspace, size_t workspace_bytes, uint32_t* counters,
+                                size_t counter_bytes, void* stream);
+
+/* One layer's values of the first rows of every sequence, as bf16: k_out and
+ * v_out have their sequences packed by cu, or along the seq stride, as k and v
+ * of paris_paged_store have.  Rows past a sequence's length are left as they
+ * were; max_rows: at least the most rows asked of a sequence.                 */
+paris_status paris_paged_read(const paris_paged* c, int layer, void* k_out, void* v_out, const paris_strides* ks,
+                              const paris_strides* vs, int64_t rows, const int32_t* cu, int64_t max_rows, void* stream);
+
+/* Bytes of workspace of paris_paged_fork with n entries.  Host only.         */
+paris_status paris_paged_fork_workspace(const paris_paged* c, int n, size_t* bytes);
+
+/* Sequence dst[i] becomes the first rows[i] rows (rows = NULL: all; at most
+ * those there are) of sequence src[i], for all i < n <= n_seqs at once: a src
+ * is taken as it was before the call, so that entries may exchange sequences.
+ * Pages that are full are shared.  Of the page that is not, the rows in use are
+ * copied, in all layers, into a page of the destination's own, unless
+ * src[i] = dst[i] and no other sequence holds it.  New pages come from those
+ * that were free before the call; an entry that finds none keeps its full
+ * pages, and status bit 0 is set.  Then what dst held before is given back.
+ * starts of a dst becomes its length.  rows of zeros and src = dst end
+ * sequences, a length below the present one takes rows back.  src, dst, rows:
+ * device int32 [n].  Of entries with the same dst the first counts; one with
+ * src or dst outside [0, n_seqs) is left out and status bit 1 is set.          */
+paris_status paris_paged_fork(const paris_paged* c, const int32_t* src, const int32_t* dst, const int32_t* rows, int n,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* End the n listed sequences (rows = NULL), or cut them to rows[i] rows:
+ * paris_paged_fork with src = dst.                                           */
+paris_status paris_paged_free(const paris_paged* c, const int32_t* seqs, const int32_t* rows, int n, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of paris_paged_compact.  Host only.                     */
+paris_status paris_paged_compact_workspace(const paris_paged* c, size_t* bytes);
+
+/* Close up the pool: the pages in use whose number is n_used or above move,
+ * in ascending order, to the free ones below it, in all layers, and the table
+ * follows.  Then the pages in use are the first n_used.                       */
+paris_status paris_paged_compact(const paris_paged* c, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Synchronise the device and report the status word, then clear it:
+ * PARIS_OK, or PARIS_EDEVICE if a call found no room or a wrong sequence, or if
+ * paris_paged_attend gave up a wait (as paris_prompt_check).                  */
+paris_status paris_paged_check(const paris_paged* c);
 
 /* Host only, no device work: the RSQ-IP magnitude levels for subspace width
  * m, computed by float64 Lloyd-Max on the density of |x_j| for x uniform on

@@ -17,7 +17,8 @@ OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libparis.so")
 SOURCES = ["paris_api.cu", "kernels_cache.cu", "kernels_decode.cu", "kernels_attend.cu", "kernels_dense.cu",
            "paris_prompt_api.cu", "kernels_prompt.cu", "kernels_prompt_weights.cu", "kernels_kv4.cu",
-           "kernels_kv4_attend.cu", "kernels_kv4_evict.cu"]
+           "kernels_kv4_attend.cu", "kernels_kv4_evict.cu", "paris_paged_api.cu", "kernels_paged.cu",
+           "kernels_paged_fork.cu", "kernels_paged_attend.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
 

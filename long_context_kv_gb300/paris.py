@@ -17,7 +17,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libparis.so")
 
 PARIS_OK, PARIS_EINVAL, PARIS_ENOMEM, PARIS_ECUDA, PARIS_ESTATE, PARIS_ECAPACITY, PARIS_EDEVICE = 0, -1, -2, -3, -4, -6, -7
-PARIS_F32, PARIS_BF16 = 0, 1
+PARIS_F32, PARIS_BF16, PARIS_E4M3 = 0, 1, 2
 PARIS_VOTE_RANK, PARIS_VOTE_FLAT = 0, 1
 PARIS_TOPK_BY_SCORE, PARIS_TOPK_BY_POSITION = 0, 1
 (DUMP_IDS, DUMP_CODES, DUMP_W, DUMP_VOTES, DUMP_CANDS, DUMP_CAND_EST, DUMP_QT, DUMP_QNORM, DUMP_HOT,
@@ -76,6 +76,26 @@ _SIGNATURES = {
     "paris_kv4_read": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
                                       ctypes.c_void_p]),
     "paris_kv4_check": (ctypes.c_int, [ctypes.c_void_p]),
+    "paris_paged_grow": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "paris_paged_store": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                         ctypes.c_int64, ctypes.c_void_p]),
+    "paris_paged_attend_workspace": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t),
+                                                    ctypes.POINTER(ctypes.c_size_t)]),
+    "paris_paged_attend": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                          ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "paris_paged_read": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                        ctypes.c_void_p]),
+    "paris_paged_fork_workspace": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
+    "paris_paged_fork": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "paris_paged_free": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                                        ctypes.c_size_t, ctypes.c_void_p]),
+    "paris_paged_compact_workspace": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t)]),
+    "paris_paged_compact": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "paris_paged_check": (ctypes.c_int, [ctypes.c_void_p]),
 }
 
 KERNELS = ["place_kv", "encode", "build_index", "append", "decode", "attend", "fill", "dense", "union"]
@@ -107,6 +127,18 @@ class paris_kv4(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int) for n in ("batch", "n_kv_heads", "head_dim")] + [("max_rows", ctypes.c_int64)]
                 + [(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scales", "v_scales", "weights", "positions",
                                                   "lens", "next_pos", "counters", "status")])
+
+
+class paris_page_strides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("layer", "page", "head", "row")]
+
+
+class paris_paged(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("n_seqs", "n_layers", "n_kv_heads", "head_dim", "page_rows", "dtype")]
+                + [(n, ctypes.c_int64) for n in ("n_pages", "max_pages")]
+                + [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages")] + [(n, paris_page_strides) for n in ("k", "v")]
+                + [(n, ctypes.c_void_p) for n in ("k_scales", "v_scales", "table", "lens", "starts", "refs", "free_bits",
+                                                  "n_used", "status")])
 
 
 _lib = None
@@ -614,3 +646,214 @@ class KV4Cache:
     def paris_kv4_check(self):
         """Synchronise; raise if a store found no room."""
         _check(load().paris_kv4_check(self._ref))
+
+
+class PagedCache:
+    """A cache of pages that sequences share (paris_paged): its arrays are torch tensors, given by the caller or made by
+    `create`.
+
+    k_pages, v_pages bfloat16 or float8_e4m3fn [layers, n_pages, Hkv, page_rows, 128], in any order of the first four
+    dimensions in memory; with float8_e4m3fn k_scales, v_scales uint8 [layers, n_pages, Hkv, page_rows]; table int32
+    [sequences, max_pages]; lens and starts int32 [sequences]; refs int32 [n_pages]; free_bits int32
+    [(n_pages + 31) // 32]; n_used int32 [1].  As with any tensor, a cache that another stream than its own still uses is
+    dropped only after `record_stream`.
+    """
+
+    def __init__(self, k_pages, v_pages, table, lens, starts, refs, free_bits, n_used, k_scales=None, v_scales=None):
+        torch = _with_torch()
+        if k_pages.dim() != 5 or k_pages.shape[4] != HEAD_DIM:
+            raise ValueError(f"k_pages: shape {tuple(k_pages.shape)}, expected [layers, n_pages, heads, page_rows, 128]")
+        if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise TypeError(f"k_pages: dtype {k_pages.dtype}, expected bfloat16 or float8_e4m3fn")
+        if table.dim() != 2:
+            raise ValueError(f"table: shape {tuple(table.shape)}, expected [sequences, max_pages]")
+        layers, n_pages, hkv, rows = k_pages.shape[:4]
+        n, width = table.shape
+        i32, e4m3 = torch.int32, k_pages.dtype is torch.float8_e4m3fn
+        if (k_scales is None) == e4m3 or (v_scales is None) == e4m3:
+            raise ValueError("k_scales and v_scales belong to float8_e4m3fn pages")
+        want = dict(k_pages=(k_pages.shape, k_pages.dtype), v_pages=(k_pages.shape, k_pages.dtype),
+                    table=((n, width), i32), lens=((n,), i32), starts=((n,), i32), refs=((n_pages,), i32),
+                    free_bits=(((n_pages + 31) // 32,), i32), n_used=((1,), i32))
+        given = dict(k_pages=k_pages, v_pages=v_pages, table=table, lens=lens, starts=starts, refs=refs, free_bits=free_bits,
+                     n_used=n_used)
+        if e4m3:
+            want.update(k_scales=(k_pages.shape[:4], torch.uint8), v_scales=(k_pages.shape[:4], torch.uint8))
+            given.update(k_scales=k_scales, v_scales=v_scales)
+        for name, (shape, dtype) in want.items():
+            _shaped(given[name], name, shape, dtype)
+        for name, t in given.items():
+            if t.device != k_pages.device or k_pages.device.type != "cuda":
+                raise ValueError(f"{name}: on {t.device}; a cache is on one CUDA device")
+            if name in ("k_pages", "v_pages"):
+                if t.numel() and t.stride(4) != 1:
+                    raise ValueError(f"{name}: the last dimension must be contiguous")
+            elif not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        self.__dict__.update(given)
+        self.n_seqs, self.n_layers, self.n_pages, self.n_kv_heads, self.page_rows = n, layers, n_pages, hkv, rows
+        self.max_pages, self.device, self._index = width, k_pages.device, k_pages.get_device()
+        self._tensors = tuple(given.values())
+        self._status = torch.zeros(1, dtype=i32, device=self.device)
+        strides = lambda t: paris_page_strides(*t.stride()[:4])  # noqa: E731
+        self._c = paris_paged(n_seqs=n, n_layers=layers, n_kv_heads=hkv, head_dim=HEAD_DIM, page_rows=rows,
+                              dtype=PARIS_E4M3 if e4m3 else PARIS_BF16, n_pages=n_pages, max_pages=width,
+                              k=strides(k_pages), v=strides(v_pages), status=self._status.data_ptr(),
+                              **{name: t.data_ptr() for name, t in given.items()})
+        self._ref = ctypes.byref(self._c)
+        self._token_shape, self._ws, self._spaces = (n, hkv, HEAD_DIM), {}, {}
+
+    @classmethod
+    def create(cls, n_seqs, n_kv_heads, n_pages, max_pages, page_rows=16, n_layers=1, dtype=None, device="cuda"):
+        """An empty cache; dtype: bfloat16 (the default) or float8_e4m3fn."""
+        torch = _with_torch()
+        dtype = torch.bfloat16 if dtype is None else dtype
+        z = lambda *s, dtype=torch.int32: torch.zeros(*s, dtype=dtype, device=device)  # noqa: E731
+        size = (n_layers, n_pages, n_kv_heads, page_rows)
+        bits = torch.full(((n_pages + 31) // 32,), -1, dtype=torch.int32)
+        if n_pages % 32:
+            bits[-1] = (1 << n_pages % 32) - 1
+        more = {}
+        if dtype is torch.float8_e4m3fn:
+            more = dict(k_scales=z(*size, dtype=torch.uint8), v_scales=z(*size, dtype=torch.uint8))
+        pages = lambda: z(*size, HEAD_DIM, dtype=torch.uint8 if more else dtype).view(dtype)  # noqa: E731
+        return cls(pages(), pages(), table=z(n_seqs, max_pages), lens=z(n_seqs), starts=z(n_seqs), refs=z(n_pages),
+                   free_bits=bits.to(device), n_used=z(1), **more)
+
+    def record_stream(self, stream):
+        """torch.Tensor.record_stream for all of the cache's memory, also for what only the cache knows of: once it is
+        dropped, none of it is given away before what `stream` has been given until then is done."""
+        for t in (*self._tensors, self._status):
+            t.record_stream(stream)
+
+    def _space(self, nbytes, stream, handle, zeros=False):
+        """Address of the workspace of a call, or of its counters: kept for each stream, whose calls take turns with it;
+        during a capture one of the graph's own."""
+        if stream is None:
+            capturing = _torch._C._cuda_isCurrentStreamCapturing()
+        else:
+            with _torch.cuda.stream(stream):
+                capturing = _torch._C._cuda_isCurrentStreamCapturing()
+        t = None if capturing else self._spaces.get((handle, zeros))
+        if t is None or t.numel() < nbytes:
+            t = _scratch(nbytes, self.device, stream)
+            if zeros:
+                with _torch.cuda.stream(stream or _torch.cuda.current_stream()):
+                    t.zero_()
+            if not capturing:
+                self._spaces[handle, zeros] = t
+        return t.data_ptr()
+
+    def _sizes(self, key, call, count):
+        """Workspace bytes of a call, asked once per kind of call."""
+        ns = [ctypes.c_size_t() for _ in range(count)]
+        _check(call(*[ctypes.byref(n) for n in ns]))
+        self._ws[key] = [n.value for n in ns]
+        return self._ws[key]
+
+    def _list(self, t, name, n=None):
+        if t.dtype is not _torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+            raise ValueError(f"{name}: a contiguous int32 tensor of {'one dimension' if n is None else n}")
+        return t.data_ptr() or None
+
+    def _rows(self, k, v, cu, longest, name):
+        """The checked tensors of a store or read call: rows, strides, the most rows of a sequence."""
+        packed = cu is not None
+        if longest is not None:
+            longest = _number(longest, name)
+        rows, heads, seqs, ks = _heads(k, "k", packed)
+        if v.shape != k.shape or v.dtype is not k.dtype:
+            raise ValueError("k and v must have the same shape and dtype")
+        vs = _strides(v, "v", packed)
+        if heads != self.n_kv_heads or (not packed and seqs != self.n_seqs):
+            raise ValueError(f"k: shape {tuple(k.shape)} for a cache of {self.n_seqs} sequences, {self.n_kv_heads} heads")
+        _on(self._index, k, v, cu)
+        if packed and (cu.dtype is not _torch.int32 or cu.shape != (self.n_seqs + 1,) or not cu.is_contiguous()):
+            raise ValueError("cu: a contiguous int32 tensor of n_seqs + 1 starts")
+        return rows, _STRIDES.pack(*ks), _STRIDES.pack(*vs), rows if longest is None else longest
+
+    def paris_paged_grow(self, tokens, stream=None):
+        """Room for tokens[s] more rows of every sequence: tokens int32 [n_seqs]."""
+        p = self._list(tokens, "tokens", self.n_seqs)
+        _on(self._index, tokens)
+        _check((_lib or load()).paris_paged_grow(self._ref, p, _raw_stream(self._index, stream)))
+
+    def paris_paged_store(self, k, v, cu=None, max_new=None, layer=0, stream=None):
+        """Write a layer's rows that the last growth added: packed [rows, Hkv, 128] with int32 starts cu [n_seqs + 1]
+        (max_new: at least the most tokens of a sequence, default all rows), or [n_seqs, Hkv, T, 128]."""
+        rows, ks, vs, longest = self._rows(k, v, cu, max_new, "max_new")
+        _check((_lib or load()).paris_paged_store(self._ref, _number(layer, "layer", 32), _raw(k), _raw(v), _code(k), ks, vs,
+                                                  rows, _raw(cu), longest, _raw_stream(self._index, stream)))
+
+    def paris_paged_append(self, k, v, layer=0, stream=None):
+        """Write a layer's row of the one token that the last growth added to every sequence: k, v [n_seqs, Hkv, 128]
+        with any strides that paris_paged_store takes.  Sequences that have not grown are left as they are."""
+        _shaped(k, "k", self._token_shape, k.dtype)
+        _shaped(v, "v", self._token_shape, k.dtype)
+        self.paris_paged_store(k.unsqueeze(2), v.unsqueeze(2), layer=layer, stream=stream)
+
+    def paris_paged_attend(self, q, out, window=0, lse=None, layer=0, stream=None):
+        """out = softmax(K q / sqrt(d)) V over a layer's rows in use, or the last `window` of them: q, out bfloat16
+        [n_seqs, Hq, 128]; lse: float32 [n_seqs, Hq], or None."""
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != self.n_seqs or shape[2] != HEAD_DIM:
+            raise ValueError(f"q: shape {tuple(shape)}, expected [{self.n_seqs}, heads, 128]")
+        _shaped(q, "q", shape, _torch.bfloat16)
+        _shaped(out, "out", shape, _torch.bfloat16)
+        if lse is not None:
+            _shaped(lse, "lse", shape[:2], _torch.float32)
+        _on(self._index, q, out, lse)
+        lib, hq, window = _lib or load(), shape[1], _number(window, "window")
+        sizes = self._ws.get(hq) or self._sizes(hq, lambda a, b: lib.paris_paged_attend_workspace(self._ref, hq, a, b), 2)
+        handle = _raw_stream(self._index, stream)
+        _check(lib.paris_paged_attend(self._ref, _number(layer, "layer", 32), _flat(q), hq, window, _flat(out), _flat(lse),
+                                      self._space(sizes[0], stream, handle), sizes[0],
+                                      self._space(sizes[1], stream, handle, True), sizes[1], handle))
+
+    def paris_paged_read(self, k_out, v_out, cu=None, max_rows=None, layer=0, stream=None):
+        """A layer's values of the first rows: bfloat16 [rows, Hkv, 128] with int32 starts cu [n_seqs + 1] (max_rows: at
+        least the most rows of a sequence), or [n_seqs, Hkv, T, 128].  Rows past a sequence's end stay as they were."""
+        rows, ks, vs, longest = self._rows(k_out, v_out, cu, max_rows, "max_rows")
+        if k_out.dtype is not _torch.bfloat16:
+            raise TypeError(f"k_out: dtype {k_out.dtype}, expected {_torch.bfloat16}")
+        _check((_lib or load()).paris_paged_read(self._ref, _number(layer, "layer", 32), _raw(k_out), _raw(v_out), ks, vs, rows,
+                                                 _raw(cu), longest, _raw_stream(self._index, stream)))
+
+    def _fork_space(self, n, stream, handle):
+        key = ("fork", n)
+        lib = _lib or load()
+        sizes = self._ws.get(key) or self._sizes(key, lambda b: lib.paris_paged_fork_workspace(self._ref, n, b), 1)
+        return self._space(sizes[0], stream, handle), sizes[0]
+
+    def paris_paged_fork(self, src, dst, rows=None, stream=None):
+        """Sequence dst[i] becomes the first rows[i] rows (None: all) of sequence src[i] as it was before the call: full
+        pages are shared, the last one is copied.  src, dst, rows: int32 [n]."""
+        n = src.shape[0] if src.dim() else 0
+        a, b = self._list(src, "src"), self._list(dst, "dst", n)
+        r = None if rows is None else self._list(rows, "rows", n)
+        _on(self._index, src, dst, rows)
+        handle = _raw_stream(self._index, stream)
+        ws, size = self._fork_space(n, stream, handle)
+        _check((_lib or load()).paris_paged_fork(self._ref, a, b, r, n, ws, size, handle))
+
+    def paris_paged_free(self, seqs, rows=None, stream=None):
+        """End the listed sequences (rows None), or cut them to rows[i] rows: int32 [n]."""
+        n = seqs.shape[0] if seqs.dim() else 0
+        a = self._list(seqs, "seqs")
+        r = None if rows is None else self._list(rows, "rows", n)
+        _on(self._index, seqs, rows)
+        handle = _raw_stream(self._index, stream)
+        ws, size = self._fork_space(n, stream, handle)
+        _check((_lib or load()).paris_paged_free(self._ref, a, r, n, ws, size, handle))
+
+    def paris_paged_compact(self, stream=None):
+        """Move the pages in use to the front of the pool."""
+        _on(self._index)
+        lib, handle = _lib or load(), _raw_stream(self._index, stream)
+        sizes = self._ws.get("compact") or self._sizes("compact",
+                                                       lambda b: lib.paris_paged_compact_workspace(self._ref, b), 1)
+        _check(lib.paris_paged_compact(self._ref, self._space(sizes[0], stream, handle), sizes[0], handle))
+
+    def paris_paged_check(self):
+        """Synchronise; raise if a call found no room or a sequence out of range."""
+        _check(load().paris_paged_check(self._ref))
