@@ -502,7 +502,8 @@ paris_status paris_kv4_check(const paris_kv4* c);
  *
  * An array's address is 16-byte aligned.  k_pages and v_pages have strides
  * in elements: positive multiples of 16 bytes, a row's of at least 128
- * elements, below 2^38; rows of 128 are contiguous.  Lengths outside
+ * elements, below 2^38; rows of 128 are contiguous.  max_pages * page_rows
+ * is below 2^31, and n_seqs times that at most 2^37.  Lengths outside
  * [0, max_pages * page_rows] count as the nearest of the two, and so do
  * entries of the table outside [0, n_pages).                                  */
 typedef struct {

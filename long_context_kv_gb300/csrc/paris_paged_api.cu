@@ -42,6 +42,8 @@ paris_status take_paged(const paris_paged* c, Paged* k) {
     return fail(PARIS_EINVAL, "n_pages must be in [1, 2^%d]", kMaxPagesLog);
   if (c->max_pages < 1 || c->max_pages > 0x7fffffff / c->page_rows)
     return fail(PARIS_EINVAL, "max_pages must be positive, and max_pages * page_rows below 2^31");
+  if (c->n_seqs * c->max_pages * c->page_rows > (int64_t)1 << 37)
+    return fail(PARIS_EINVAL, "n_seqs * max_pages * page_rows must be at most 2^37");
   const bool e4m3 = c->dtype == PARIS_E4M3;
   if (!c->k_pages || !c->v_pages || !c->table || !c->lens || !c->starts || !c->refs || !c->free_bits || !c->n_used || !c->status ||
       (e4m3 && (!c->k_scales || !c->v_scales)))
