@@ -191,7 +191,7 @@ __device__ __forceinline__ uint4 values8(uint2 codes, uint32_t byte) {
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t h = e4m3_to_f16x2((i < 2 ? codes.x : codes.y) >> (16 * (i & 1)));
+    const uint32_t w = i < 2 ? codes.x : codes.y, h = i & 1 ? e4m3_hi(w) : e4m3_lo(w);
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
     o[i] = pack_bf16x2(f.x * S, f.y * S);
   }

@@ -4,10 +4,13 @@
 // in bf16, 258 in 8 bits.  What that asks for:
 //
 // - All SMs read to the end.  The tiles of all sequences form one line, which
-//   the blocks of a KV head cut into equal parts; a part may end one sequence
-//   and begin the next.  A sequence that several blocks share leaves partial
-//   sums (maximum, sum, unnormalised result) in the workspace, and the block
-//   that finishes last joins them, in the blocks' order.
+//   is cut into units within sequences: long ones in front, short ones in its
+//   last quarter.  Blocks take (unit, KV head, head group) jobs from a queue,
+//   since SMs differ by a third in what the memory gives them (equal parts of
+//   131072 rows ended 72 to 104 us after the start).  A sequence of one unit
+//   is done with its job; the units of others leave partial sums (maximum,
+//   sum, unnormalised result), which a second kernel joins in their order.
+//   Which block has which job changes no result.
 // - Copies are always under way.  A warp takes steps of 8 KB of its own (16
 //   bf16 rows of keys and values, or 32 in 8 bits) through a ring in shared
 //   memory that TMA fills, two steps ahead and across the ends of sequences;
@@ -46,8 +49,10 @@ constexpr int kPgStage = 8192;  // bytes of a step: half keys, half values
 constexpr int kPgScale = 64;    // a step's scale bytes: 32 of keys, 32 of values
 constexpr int kPgOut = 8192;    // bytes through which the warps' results meet
 constexpr float kPgGrowth = 8.f;
-constexpr int kPgGroups = 32;   // counters of a (sequence, KV head)
-constexpr int kPgSmem = 1024 + kPgWarps * kPgDepth * (kPgStage + kPgScale) + kPgOut;
+constexpr int kPgEntries = 512;  // of the line's table
+constexpr uint32_t kPgMinUnit = 4;  // tiles (8-bit batch of 24: 44.1 us, with 3 46.0; one sequence of 128K rows the same)
+constexpr int kPgUnknown = -1;
+constexpr int kPgSmem = 1024 + kPgWarps * kPgDepth * (kPgStage + kPgScale) + kPgOut + 16 * 16 * kPgWarps;
 
 template <bool kE4m3>
 struct Pg {
@@ -82,10 +87,10 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
 template <bool kE4m3>
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   if constexpr (kE4m3)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -118,10 +123,11 @@ __device__ __forceinline__ uint32_t pack_weights(float a, float b) {
     return pack_bf16x2(a, b);
   }
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst), "l"(src),
-               "r"(bytes), "r"(bar)
-               : "memory");
+__device__ __forceinline__ void tma_load5(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, int c4, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+      : "memory");
 }
 
 // A maximum: a row's product d and exponent e, for scores d qs + e.
@@ -130,81 +136,65 @@ struct PgMax {
 };
 // How far x lies above y.
 __device__ __forceinline__ float above(PgMax x, PgMax y, float qs) { return fmaf(x.d - y.d, qs, x.e - y.e); }
-// The larger one by k (its distance from some third one); the same on both sides of an exchange.
-__device__ __forceinline__ void keep_larger(float& k, PgMax& m, float k2, PgMax m2) {
-  if (k2 > k || (k2 == k && (m2.d > m.d || (m2.d == m.d && m2.e > m.e)))) {
-    k = k2;
-    m = m2;
+// How the line of all tiles is cut: units of at most `large` tiles in front of
+// `border`, of at most `small` behind it; sequences of at most `small` whole.
+struct PgCut {
+  uint32_t border, large, small;
+};
+// total tiles of seqs sequences, heads jobs a unit, for so many blocks.  Where
+// units of a few tiles give no more jobs than blocks, all are of that size.
+// Otherwise two large units a block, and four small ones to even out what they
+// took.  (Two or three small ones end later: a ragged batch of 24 104 -> 111
+// us.)  Of few sequences one large unit: they are cut into as many as there
+// are blocks (one sequence of 128K rows 89.4 -> 88.0 us, in 8 bits 60.9 -> 57.5; a
+// ragged batch would have blocks with two of them, 112 -> 131).
+__device__ __forceinline__ PgCut pg_cut(uint32_t total, uint32_t seqs, uint32_t heads, uint32_t blocks) {
+  PgCut c;
+  c.border = total - total / 4;
+  const uint32_t each = blocks / heads;
+  if (each > seqs) {  // a sequence's last unit may not be full
+    c.small = c.large = max(1u, (total + each - seqs - 1) / (each - seqs));
+    if (c.small <= kPgMinUnit) return c;
   }
+  const float share = (float)total * (float)heads / (float)blocks;
+  c.small = max(kPgMinUnit, (uint32_t)ceilf(share * 0.0625f));
+  c.large = max(c.small, (uint32_t)ceilf(share * (16 * seqs <= each ? 0.75f : 0.375f)));
+  return c;
+}
+// A sequence's units: in front of the border and behind it.
+struct PgUnits {
+  uint32_t front, nf, nb;  // tiles in front, units in front and behind
+};
+__device__ __forceinline__ PgUnits pg_units(const PgCut& c, uint32_t at, uint32_t tiles) {
+  PgUnits u = {tiles, tiles > 0 ? 1u : 0u, 0};
+  if (tiles > c.small) {
+    u.front = at < c.border ? min(c.border - at, tiles) : 0u;
+    u.nf = (u.front + c.large - 1) / c.large;
+    u.nb = (tiles - u.front + c.small - 1) / c.small;
+  }
+  return u;
+}
+// Units, and units of sequences with several of them in the upper half.
+__device__ __forceinline__ uint32_t pg_count(const PgUnits& u) {
+  const uint32_t n = u.nf + u.nb;
+  return n > 1 ? n | n << 16 : n;
 }
 
-// Join the partial results of blocks [xf, xl] for nh query heads: a warp a
-// head, its lanes over the partials' maxima and sums and then over the channels.
-__device__ __forceinline__ void pg_join(const PagedAttendArgs& a, int b, int qh0, int nh, int xf, int xl, bool begins) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = xl - xf + 1;
-  for (int h = warp; h < nh; h += kPgWarps) {
-    const float* part = a.part + ((int64_t)(qh0 + h) * a.nblocks + xf) * 2 * kPartStride;
-    // a block's first stretch lies in its first half; that of the block in which the sequence begins may not be it
-    auto at = [&](int i) { return part + (2 * i + (i == 0 && !begins ? 1 : 0)) * kPartStride; };
-    auto head = [&](int i) { return __ldcg(reinterpret_cast<const float4*>(at(i))); };
-    PgMax m = {0.f, 0.f};
-    float qs = 0.f, sum = 0.f;
-#pragma unroll 1
-    for (int round = 0; round < 2; ++round) {  // the second finds the largest by exact distances from about the largest
-      float k = -INFINITY;
-      PgMax best = {-INFINITY, -INFINITY};
-      for (int i = lane; i < n; i += 32) {
-        const float4 v = head(i);
-        qs = v.w;
-        if (v.z != 0.f) keep_larger(k, best, above({v.x, v.y}, m, v.w), {v.x, v.y});
-      }
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const float k2 = __shfl_xor_sync(kFull, k, off);
-        keep_larger(k, best, k2, {__shfl_xor_sync(kFull, best.d, off), __shfl_xor_sync(kFull, best.e, off)});
-      }
-      if (k > -INFINITY) m = best;
-    }
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      float f = 0.f;
-      if (i0 + lane < n) {
-        const float4 v = head(i0 + lane);
-        if (v.z != 0.f) {  // the sum 0: no rows of weight
-          f = ex2(above({v.x, v.y}, m, v.w));
-          sum += v.z * f;
-        }
-      }
-      const int most = min(32, n - i0);
-#pragma unroll 8
-      for (int i = 0; i < most; ++i) {
-        const float fi = __shfl_sync(kFull, f, i);
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(at(i0 + i) + 4) + lane);
-        o.x = fmaf(x.x, fi, o.x);
-        o.y = fmaf(x.y, fi, o.y);
-        o.z = fmaf(x.z, fi, o.z);
-        o.w = fmaf(x.w, fi, o.w);
-      }
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
-    const float inv = sum != 0.f ? 1.f / sum : 0.f;
-    const int64_t q = (int64_t)b * a.hq + qh0 + h;
-    reinterpret_cast<uint2*>(a.out + q * kDim)[lane] = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    qs = __shfl_sync(kFull, qs, 0);
-    if (a.lse != nullptr && lane == 0)
-      a.lse[q] = sum != 0.f ? kLn2 * (fmaf(m.d, qs, m.e) + log2f(sum)) : -INFINITY;
-  }
-}
+// A unit of one KV head and head group.
+struct PgJob {
+  int s, len, first, base;
+  uint32_t t0, t1;  // tiles of the sequence
+  int slot;         // of its partial sums, or -1: it is the whole sequence
+  int kvh, h0;
+};
 
 struct PgShared {
   uint64_t bar[kPgWarps][kPgDepth];
   float4 ml[kPgWarps][16];   // maximum (product, exponent), sum, scale of a head's scores
-  float f[kPgWarps][16];     // a warp's share of the block's result
-  float4 all[16];            // the block's maximum, sum and scale
+  uint2 line[kPgEntries];    // tiles and units (pg_count) in front of every `group`-th sequence
   uint32_t tmp[33];
-  uint32_t start_tile;
-  int start_seq, last;
+  int used[kPgWarps];        // sequences with rows
+  int next[2];               // the job after the present one, or kPgUnknown
   uint32_t gave_up;
 };
 
@@ -228,102 +218,163 @@ __global__ void __launch_bounds__(kPgThreads, 2)
   const uint32_t bar0 = smem_u32(&sh.bar[warp][0]);
   if (lane == 0) {
 #pragma unroll
-    for (int i = 0; i < kPgDepth; ++i) bar_init(bar0 + 8 * i, 1);
+    for (int i = 0; i < kPgDepth; ++i) bar_init(bar0 + 8 * i, kE4m3 ? 33 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (tid == 0) sh.gave_up = 0;
   volatile uint32_t* gave_up = &sh.gave_up;
-  const int kvh = blockIdx.y, h0 = blockIdx.z * kHeads, nh = min(kHeads, a.g - h0), qh0 = kvh * a.g + h0;
-  const uint32_t x = blockIdx.x;
+  const uint32_t heads = (uint32_t)(a.c.hkv * a.groups), blocks = gridDim.x;
   pdl_wait();
   pdl_trigger();
 
-  // sequences without rows: spread over the blocks
-  for (int s = x; s < a.c.n_seqs; s += a.nblocks) {
-    if (paged_len(a.c, s) > 0) continue;
-    const int64_t q = (int64_t)s * a.hq + qh0;
-    for (int i = tid; i < nh * (kDim / 8); i += kPgThreads) reinterpret_cast<uint4*>(a.out + q * kDim)[i] = make_uint4(0, 0, 0, 0);
-    if (a.lse != nullptr && tid < nh) a.lse[q + tid] = -INFINITY;
-  }
-
-  // the block's part [lo, hi) of all tiles, and the sequence in which it begins
-  uint32_t total, lo, hi, nb;
+  // the line's table: a thread has up to four entries in a row
+  const int group = (a.c.n_seqs + kPgEntries - 1) / kPgEntries, entries = (a.c.n_seqs + group - 1) / group;
+  PgCut cut;
+  uint32_t jobs;
   {
-    const int per = (a.c.n_seqs + kPgThreads - 1) / kPgThreads, s0 = tid * per, s1 = min(s0 + per, a.c.n_seqs);
-    uint32_t mine = 0;
-    for (int s = s0; s < s1; ++s) mine += pg_seq<kE4m3>(a, s).tiles;
-    uint32_t before = block_excl_scan(mine, sh.tmp, &total);
-    nb = min((uint32_t)a.nblocks, total);  // blocks with a part, of one tile at least
-    if (x >= nb) return;
-    lo = (uint32_t)((uint64_t)x * total / nb);
-    hi = (uint32_t)((uint64_t)(x + 1) * total / nb);
-    if (lo >= before && lo < before + mine) {
-      for (int s = s0; s < s1; ++s) {
-        const uint32_t n = pg_seq<kE4m3>(a, s).tiles;
-        if (lo < before + n) {
-          sh.start_seq = s;
-          sh.start_tile = before;
-          break;
-        }
-        before += n;
-      }
+    const int per = (entries + kPgThreads - 1) / kPgThreads * group;
+    const int s0 = min(tid * per, a.c.n_seqs), s1 = min(s0 + per, a.c.n_seqs);
+    const uint32_t only = s0 < s1 ? pg_seq<kE4m3>(a, s0).tiles : 0u;  // of a thread's first sequence
+    auto tiles_of = [&](int s) { return s == s0 ? only : pg_seq<kE4m3>(a, s).tiles; };
+    uint32_t mine = 0, total;
+    int used = 0;
+    for (int s = s0; s < s1; ++s) {
+      const uint32_t n = tiles_of(s);
+      mine += n;
+      used += n > 0 ? 1 : 0;
     }
+    used = __reduce_add_sync(kFull, used);
+    if (lane == 0) sh.used[warp] = used;
+    const uint32_t at0 = block_excl_scan(mine, sh.tmp, &total);
+    cut = pg_cut(total, sh.used[0] + sh.used[1] + sh.used[2] + sh.used[3], heads, blocks);
+    uint32_t at = at0, count = 0, several = 0;
+    for (int s = s0; s < s1; ++s) {
+      const uint32_t n = tiles_of(s), c = pg_count(pg_units(cut, at, n));
+      count += c;
+      several += c >> 16 != 0 ? 1u : 0u;
+      at += n;
+    }
+    uint32_t units, splits = 0, split = 0;
+    uint32_t unit = block_excl_scan(count, sh.tmp, &units);
+    jobs = (units & 0xffffu) * heads;
+    if (blockIdx.x == 0) {
+      split = block_excl_scan(several, sh.tmp, &splits);
+      if (tid == 0) a.counts[1] = splits;  // none if max_splits is 0
+    }
+    at = at0;
+    for (int s = s0; s < s1; ++s) {
+      if (s % group == 0) sh.line[s / group] = make_uint2(at, unit);
+      if (per == 1 && blockIdx.x != 0) break;
+      const uint32_t n = tiles_of(s), c = pg_count(pg_units(cut, at, n));
+      if (blockIdx.x == 0 && c >> 16 != 0) a.splits[split++] = PgSplit{s, (int)(unit >> 16), (int)(c >> 16), 0};
+      unit += c;
+      at += n;
+    }
+    if (tid == 0) sh.next[0] = sh.next[1] = kPgUnknown;
     __syncthreads();
   }
 
-  // what the warp copies next: step `ahead.tile` of the line, in sequence ahead.s
-  int c_s = sh.start_seq;
-  PgSeq c_q = pg_seq<kE4m3>(a, c_s);
-  uint32_t c_a = sh.start_tile;  // the sequence's first tile
-  int p_s = c_s;
-  PgSeq p_q = c_q;
-  uint32_t p_a = c_a, p_tile = lo, issued = 0, taken = 0;
-  uint32_t p_stage = 0, c_stage = 0, c_parity = 0;
-  auto copy_next = [&]() {
-    if (p_tile >= hi) return;
-    while (p_tile >= p_a + p_q.tiles) {
-      p_a += p_q.tiles;
-      p_q = pg_seq<kE4m3>(a, ++p_s);
+  // a job's unit: its entry of the line, and the sequence in the entry
+  auto find = [&](uint32_t job) {
+    const uint32_t unit = job / heads, head = job - unit * heads;
+    PgJob r;
+    r.kvh = (int)head / a.groups;
+    r.h0 = ((int)head - r.kvh * a.groups) * kHeads;
+    int e = -1;
+    for (int e0 = 0; e0 < entries; e0 += 32) {
+      const int n = __popc(__ballot_sync(kFull, e0 + lane < entries && (sh.line[e0 + lane].y & 0xffffu) <= unit));
+      e += n;
+      if (n < 32) break;
     }
-    const int row = p_q.base + (int)(p_tile - p_a) * G::kTile + warp * kRows;
+    uint32_t at = sh.line[e].x, begin = sh.line[e].y;
+    for (r.s = e * group;; ++r.s) {
+      const PgSeq q = pg_seq<kE4m3>(a, r.s);
+      const PgUnits u = pg_units(cut, at, q.tiles);
+      const uint32_t count = pg_count(u), i = unit - (begin & 0xffffu);  // the sequence's i-th unit
+      if (i >= (count & 0xffffu) && r.s + 1 < a.c.n_seqs) {
+        at += q.tiles;
+        begin += count;
+        continue;
+      }
+      const bool back = i >= u.nf;
+      const uint32_t size = back ? cut.small : cut.large, from = back ? u.front : 0u, to = back || u.nf + u.nb == 1 ? q.tiles : u.front;
+      r.len = q.len;
+      r.first = q.first;
+      r.base = q.base;
+      r.t0 = from + (back ? i - u.nf : i) * size;
+      r.t1 = u.nf + u.nb == 1 ? to : min(r.t0 + size, to);
+      r.slot = count >> 16 != 0 ? (int)min((begin >> 16) + i, (uint32_t)a.slots - 1u) : -1;
+      return r;
+    }
+  };
+
+  // What the warp copies next: step p_tile of the present job, or of the next
+  // one once that is known.
+  const bool busy = blockIdx.x < jobs;
+  PgJob cur = find(busy ? blockIdx.x : 0u), nxt = cur;
+  bool in_next = false;
+  // pages of 32 steps from p_from on, a lane each (in 8 bits and pages of 16 rows two)
+  uint32_t p_from = cur.t0;
+  int page0 = 0, page1 = 0;
+  auto look_up = [&](const PgJob& p) {
+    const int row = p.base + (int)(p_from + lane) * G::kTile + warp * kRows, j = row >> a.c.shift;
+    const int32_t* t = a.c.table + (int64_t)p.s * a.c.width;
+    if (p_from + lane < p.t1 && row < p.len) {
+      page0 = clamp_page(a.c, t[j]);
+      if (kE4m3 && a.c.shift == 4) page1 = row + 16 < p.len ? clamp_page(a.c, t[j + 1]) : 0;
+    }
+  };
+  int k = 0;
+  uint32_t job = blockIdx.x;
+  uint32_t p_tile = cur.t0, issued = 0, taken = 0, p_stage = 0, c_stage = 0, c_parity = 0;
+  auto copy_next = [&]() {
+    if (issued - taken >= kPgDepth) return;
+    if (!in_next && p_tile >= cur.t1) {
+      const int j = __shfl_sync(kFull, *(volatile int*)&sh.next[(k + 1) & 1], 0);
+      if (j == kPgUnknown || (uint32_t)j >= jobs) return;
+      nxt = find(j);
+      in_next = true;
+      p_tile = p_from = nxt.t0;
+      look_up(nxt);
+    }
+    if (in_next && p_tile >= nxt.t1) return;
+    const PgJob& p = in_next ? nxt : cur;
+    if (p_tile - p_from == 32) {
+      p_from = p_tile;
+      look_up(p);
+    }
+    const int row = p.base + (int)p_tile * G::kTile + warp * kRows, len = p.len, kvh = p.kvh;
+    const int page = __shfl_sync(kFull, page0, p_tile - p_from), next = __shfl_sync(kFull, page1, p_tile - p_from);
     ++p_tile;
-    if (row >= p_q.len || __any_sync(kFull, *gave_up != 0)) return;
-    const int j = row >> a.c.shift, r = row & ((1 << a.c.shift) - 1);
+    if (row >= len || __any_sync(kFull, *gave_up != 0)) return;
+    const int r = row & ((1 << a.c.shift) - 1);
     const uint32_t dst = ring + p_stage * kPgStage, bar = bar0 + 8 * p_stage;
-    if (elect()) {
-      const int page = page_at(a.c, p_s, j);
-      if constexpr (!kE4m3) {
+    if constexpr (!kE4m3) {
+      if (elect()) {
         bar_expect(bar, kPgStage);
+        tma_load5(dst, &km, 0, r, 0, kvh, page, bar);
+        tma_load5(dst + kPgStage / 2, &vm, 0, r, 0, kvh, page, bar);
+      }
+    } else {
+      // Pages of 16 rows: two, the second one if it has rows.  The scale bytes
+      // go by the lanes, four rows each: as copies of their own they took as
+      // much of the copy engine's time as the rows.
+      const bool one = a.c.shift > 4, two = !one && row + 16 < len;
+      const int r4 = 4 * (lane & 7);
+      if (lane < 16 && (one || two || r4 < 16)) {
+        const int64_t e = one || r4 < 16 ? scale_at(a.c, a.layer, page, kvh, r + r4) : scale_at(a.c, a.layer, next, kvh, r4 - 16);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(smem_u32(scales) + p_stage * kPgScale + 4 * lane),
+                     "l"((lane < 8 ? a.c.ks : a.c.vs) + e)
+                     : "memory");
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
+      if (elect()) {
+        bar_expect(bar, one || two ? kPgStage : kPgStage / 2);
         tma_load(dst, &km, 0, r, kvh, page, bar);
-        tma_load(dst + 2048, &km, 64, r, kvh, page, bar);
-        tma_load(dst + 4096, &vm, 0, r, kvh, page, bar);
-        tma_load(dst + 6144, &vm, 64, r, kvh, page, bar);
-      } else {
-        const uint32_t sc = smem_u32(scales) + p_stage * kPgScale;
-        if (a.c.shift > 4) {
-          bar_expect(bar, kPgStage + kPgScale);
-          tma_load(dst, &km, 0, r, kvh, page, bar);
-          tma_load(dst + 4096, &vm, 0, r, kvh, page, bar);
-          const int64_t e = scale_at(a.c, a.layer, page, kvh, r);
-          bulk_load(sc, a.c.ks + e, 32, bar);
-          bulk_load(sc + 32, a.c.vs + e, 32, bar);
-        } else {
-          // two pages, the second one if it has rows
-          const bool two = row + 16 < p_q.len;
-          const int next = two ? page_at(a.c, p_s, j + 1) : 0;
-          bar_expect(bar, (kPgStage + kPgScale) >> (two ? 0 : 1));
-          tma_load(dst, &km, 0, 0, kvh, page, bar);
-          tma_load(dst + 4096, &vm, 0, 0, kvh, page, bar);
-          const int64_t e = scale_at(a.c, a.layer, page, kvh, 0);
-          bulk_load(sc, a.c.ks + e, 16, bar);
-          bulk_load(sc + 32, a.c.vs + e, 16, bar);
-          if (two) {
-            tma_load(dst + 2048, &km, 0, 0, kvh, next, bar);
-            tma_load(dst + 6144, &vm, 0, 0, kvh, next, bar);
-            const int64_t f = scale_at(a.c, a.layer, next, kvh, 0);
-            bulk_load(sc + 16, a.c.ks + f, 16, bar);
-            bulk_load(sc + 48, a.c.vs + f, 16, bar);
-          }
+        tma_load(dst + kPgStage / 2, &vm, 0, r, kvh, page, bar);
+        if (two) {
+          tma_load(dst + 2048, &km, 0, 0, kvh, next, bar);
+          tma_load(dst + kPgStage / 2 + 2048, &vm, 0, 0, kvh, next, bar);
         }
       }
     }
@@ -331,44 +382,53 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     p_stage = p_stage + 1 == kPgDepth ? 0 : p_stage + 1;
     ++issued;
   };
-#pragma unroll
-  for (int i = 0; i < kPgDepth - 1; ++i) copy_next();
 
   // a lane's places in a step's boxes (128 bytes a row, 16-byte pieces swizzled by the row)
   const uint32_t lrow = lane & 15, lhi = lane >> 4, lsw = lane & 7;
 
-  uint32_t tile = lo;
-  while (tile < hi) {
-    while (tile >= c_a + c_q.tiles) {
-      c_a += c_q.tiles;
-      c_q = pg_seq<kE4m3>(a, ++c_s);
+  // the queries' words: column g's head (of four: twice)
+  uint32_t qw[kQ][8][2];
+  auto load_queries = [&](const PgJob& j) {
+    const int nh = min(kHeads, a.g - j.h0);
+#pragma unroll
+    for (int c = 0; c < kQ; ++c) {
+      const int h = 8 * c + (kHeads == 4 ? g & 3 : g);
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q + ((int64_t)j.s * a.hq + j.kvh * a.g + j.h0 + h) * kDim);
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        if constexpr (!kE4m3) {
+          qw[c][s][0] = h < nh ? __ldg(q + 8 * s + t) : 0u;
+          qw[c][s][1] = h < nh ? __ldg(q + 8 * s + 4 + t) : 0u;
+        } else {
+          const uint2 u = h < nh ? __ldg(reinterpret_cast<const uint2*>(q + 8 * s) + t) : make_uint2(0, 0);
+          qw[c][s][0] = u.x;
+          qw[c][s][1] = u.y;
+        }
+      }
     }
-    const uint32_t end = min(hi, c_a + c_q.tiles);
+  };
+  if (busy) {
+    look_up(cur);
+    load_queries(cur);
+  }
+  while (busy) {
+#pragma unroll 1
+    for (int i = 0; i < kPgDepth - 1 && !in_next && issued - taken < kPgDepth - 1; ++i) copy_next();
+    // the job after this one: on its way while the first steps are computed
+    int fetched = 0;
+    bool pending = tid == 0;
+    if (pending) fetched = (int)(a.max_splits > 0 ? blocks + atomicAdd(a.counts, 1u) : job + blocks);
+    const int kvh = cur.kvh, h0 = cur.h0, nh = min(kHeads, a.g - h0), qh0 = kvh * a.g + h0;
 
-    // the queries: column g's head (of four: twice)
     uint32_t qf[kQ][8][2];
     float qs[kQ][2];  // of a thread's columns 2 t and 2 t + 1
 #pragma unroll
     for (int c = 0; c < kQ; ++c) {
-      const int h = 8 * c + (kHeads == 4 ? g & 3 : g);
-      const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q + ((int64_t)c_s * a.hq + qh0 + h) * kDim);
-      uint32_t w[8][2];
-#pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        if constexpr (!kE4m3) {
-          w[s][0] = h < nh ? __ldg(q + 8 * s + t) : 0u;
-          w[s][1] = h < nh ? __ldg(q + 8 * s + 4 + t) : 0u;
-        } else {
-          const uint2 u = h < nh ? __ldg(reinterpret_cast<const uint2*>(q + 8 * s) + t) : make_uint2(0, 0);
-          w[s][0] = u.x;
-          w[s][1] = u.y;
-        }
-      }
       if constexpr (!kE4m3) {
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
-          qf[c][s][0] = w[s][0];
-          qf[c][s][1] = w[s][1];
+          qf[c][s][0] = qw[c][s][0];
+          qf[c][s][1] = qw[c][s][1];
         }
         qs[c][0] = qs[c][1] = kScoreScale;
       } else {
@@ -378,7 +438,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
         for (int s = 0; s < 8; ++s)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_float(w[s][i] & 0xffffu)), fabsf(__uint_as_float(w[s][i] & 0xffff0000u))));
+            amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_float(qw[c][s][i] & 0xffffu)), fabsf(__uint_as_float(qw[c][s][i] & 0xffff0000u))));
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
         const int e = min(max((int)((__float_as_uint(amax) >> 23) & 255u) - 126, -100), 126);
@@ -387,7 +447,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
         for (int s = 0; s < 8; ++s)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            qf[c][s][i] = pack_weights<true>(bf16_bits_to_float(w[s][i] & 0xffffu) * down, __uint_as_float(w[s][i] & 0xffff0000u) * down);
+            qf[c][s][i] = pack_weights<true>(bf16_bits_to_float(qw[c][s][i] & 0xffffu) * down, __uint_as_float(qw[c][s][i] & 0xffff0000u) * down);
         qs[c][0] = __shfl_sync(kFull, up, 8 * t);
         qs[c][1] = __shfl_sync(kFull, up, 8 * t + 4);
       }
@@ -411,21 +471,26 @@ __global__ void __launch_bounds__(kPgThreads, 2)
       }
 
 #pragma unroll 1
-    for (; tile < end; ++tile) {
+    for (uint32_t tile = cur.t0; tile < cur.t1; ++tile) {
+      if (pending && tile != cur.t0) {
+        *(volatile int*)&sh.next[(k + 1) & 1] = fetched;
+        pending = false;
+      }
+      __syncwarp();
       copy_next();
-      const int row0 = c_q.base + (int)(tile - c_a) * G::kTile + warp * kRows;
-      if (row0 >= c_q.len || taken == issued) continue;  // (nothing is copied any more after a wait that gave up)
+      const int row0 = cur.base + (int)tile * G::kTile + warp * kRows;
+      if (row0 >= cur.len || taken == issued) continue;  // (nothing is copied any more after a wait that gave up)
       const uint32_t kst = ring + c_stage * kPgStage, vst = kst + kPgStage / 2;
       if (!bar_wait(bar0 + 8 * c_stage, c_parity, gave_up)) {
         WaitLimit limit(now_ns());  // the copy ends before the block does
         while (!bar_try(bar0 + 8 * c_stage, c_parity) && !limit.over(now_ns())) {}
       }
       ++taken;
-      const bool edge = row0 < c_q.first || row0 + kRows > c_q.len;
+      const bool edge = row0 < cur.first || row0 + kRows > cur.len;
       if (edge) {
         // rows that do not count may hold anything, and 0 times NaN is NaN
         for (int r = lane >> 3; r < kRows; r += 4) {
-          if (row0 + r >= c_q.first && row0 + r < c_q.len) continue;
+          if (row0 + r >= cur.first && row0 + r < cur.len) continue;
           const uint32_t z = vst + r * 128 + 16 * (lane & 7);
           asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(z), "r"(0) : "memory");
           if (!kE4m3) asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(z + 2048), "r"(0) : "memory");
@@ -456,8 +521,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
             ldsm4(f, kst + (16 * u + lrow) * 128 + (((2 * s + lhi) ^ lsw) << 4));
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint32_t a0 = e4m3_to_f16x2(f[2 * i]), a1 = e4m3_to_f16x2(f[2 * i + 1]);
-              const uint32_t a2 = e4m3_to_f16x2(f[2 * i] >> 16), a3 = e4m3_to_f16x2(f[2 * i + 1] >> 16);
+              const uint32_t a0 = e4m3_lo(f[2 * i]), a1 = e4m3_lo(f[2 * i + 1]), a2 = e4m3_hi(f[2 * i]), a3 = e4m3_hi(f[2 * i + 1]);
 #pragma unroll
               for (int c = 0; c < kQ; ++c) mma16<true>(p[u][c], a0, a1, a2, a3, qf[c][2 * s + i][0], qf[c][2 * s + i][1]);
             }
@@ -467,7 +531,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
             const uint8_t* sc = scales + c_stage * kPgScale + 16 * u + 8 * r + g;
             const int kb = sc[0], vb = sc[32];
             const float S = __uint_as_float((uint32_t)kb << 23);
-            ev[u][r] = (float)(vb - 127);
+            ev[u][r] = (float)vb - (127.f - kUp);
             inv[u][r] = __uint_as_float((uint32_t)(254 - vb) << 23);
 #pragma unroll
             for (int c = 0; c < kQ; ++c) {
@@ -483,27 +547,35 @@ __global__ void __launch_bounds__(kPgThreads, 2)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const int row = row0 + 16 * u + 8 * r + g;
-            if (row >= c_q.first && row < c_q.len) continue;
-            ev[u][r] = 0.f;
+            if (row >= cur.first && row < cur.len) continue;
+            ev[u][r] = kUp;
             inv[u][r] = 1.f;
 #pragma unroll
             for (int c = 0; c < kQ; ++c) p[u][c][2 * r] = p[u][c][2 * r + 1] = -INFINITY;
           }
       }
-      auto score = [&](int u, int c, int r, int i) {
-        const float d = p[u][c][2 * r + i] - m[c][i].d;
-        return kE4m3 ? fmaf(d, qs[c][i], ev[u][r] - m[c][i].e) : d * qs[c][i];
+      // exponents of the weights, kUp up (NaN counts as no growth)
+      float sc[kU][kQ][4];
+      auto exponents = [&]() {
+#pragma unroll
+        for (int c = 0; c < kQ; ++c)
+#pragma unroll
+          for (int u = 0; u < kU; ++u)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float d = p[u][c][x] - m[c][x & 1].d;
+              sc[u][c][x] = kE4m3 ? fmaf(d, qs[c][x & 1], ev[u][x >> 1] - m[c][x & 1].e) : d * qs[c][x & 1];
+            }
       };
+      exponents();
       bool grows = false;
 #pragma unroll
       for (int u = 0; u < kU; ++u)
 #pragma unroll
         for (int c = 0; c < kQ; ++c)
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              grows |= score(u, c, r, i) > kPgGrowth || (!live[c][i] && p[u][c][2 * r + i] > -INFINITY);
+          for (int x = 0; x < 4; ++x)
+            grows |= sc[u][c][x] > kPgGrowth + kUp || (!live[c][x & 1] && p[u][c][x] > -INFINITY);
       // A maximum that is found by distances from far away may be off by their
       // rounding; the next look is from nearby.
 #pragma unroll 1
@@ -514,18 +586,25 @@ __global__ void __launch_bounds__(kPgThreads, 2)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             float k = -INFINITY;
-            PgMax best = {-INFINITY, -INFINITY};
+            PgMax best = {-INFINITY, 0.f};
 #pragma unroll
             for (int u = 0; u < kU; ++u)
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
-                const PgMax v = {p[u][c][2 * r + i], kE4m3 ? ev[u][r] : 0.f};
-                keep_larger(k, best, kE4m3 ? score(u, c, r, i) : v.d, v);
+                const float d = p[u][c][2 * r + i], k2 = kE4m3 ? sc[u][c][2 * r + i] : d;
+                const bool more = k2 > k;
+                k = more ? k2 : k;
+                best.d = more ? d : best.d;
+                if (kE4m3) best.e = more ? ev[u][r] - kUp : best.e;
               }
+            float top = k;
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) {
-              const float k2 = __shfl_xor_sync(kFull, k, off);
-              keep_larger(k, best, k2, {__shfl_xor_sync(kFull, best.d, off), __shfl_xor_sync(kFull, best.e, off)});
+            for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+            if (kE4m3) {  // that of the first of the eight lanes that have it
+              const int src = __ffs(__ballot_sync(kFull, k == top) & (0x11111111u << t)) - 1;
+              best = {__shfl_sync(kFull, best.d, src), __shfl_sync(kFull, best.e, src)};
+            } else {
+              best.d = top;
             }
             const float up = above(best, m[c][i], qs[c][i]);
             if (best.d > -INFINITY && (!live[c][i] || up > 0.f)) {
@@ -539,11 +618,14 @@ __global__ void __launch_bounds__(kPgThreads, 2)
               m[c][i] = best;
               live[c][i] = true;
             }
-#pragma unroll
-            for (int u = 0; u < kU; ++u)
-#pragma unroll
-              for (int r = 0; r < 2; ++r) grows |= score(u, c, r, i) > kPgGrowth;
           }
+        exponents();
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int c = 0; c < kQ; ++c)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) grows |= sc[u][c][x] > kPgGrowth + kUp;
       }
 
       // P^T as the second operand: rows 16 u + 8 r, a column tile's upper and lower parts
@@ -554,7 +636,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
         for (int c = 0; c < kQ; ++c)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float w0 = ex2(score(u, c, r, 0) + kUp), w1 = ex2(score(u, c, r, 1) + kUp);
+            const float w0 = ex2(sc[u][c][2 * r]), w1 = ex2(sc[u][c][2 * r + 1]);
             l[c][0] = kE4m3 ? fmaf(w0, inv[u][r], l[c][0]) : l[c][0] + w0;
             l[c][1] = kE4m3 ? fmaf(w1, inv[u][r], l[c][1]) : l[c][1] + w1;
             if constexpr (kHeads == 4) {
@@ -587,7 +669,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
           for (int u = 0; u < kU; ++u) {
             // two rows by two channels a word: even channels are the product's first eight rows, odd ones the others
             const uint32_t w0 = __byte_perm(f[2 * u], 0, 0x3120), w1 = __byte_perm(f[2 * u + 1], 0, 0x3120);
-            const uint32_t a0 = e4m3_to_f16x2(w0), a1 = e4m3_to_f16x2(w0 >> 16), a2 = e4m3_to_f16x2(w1), a3 = e4m3_to_f16x2(w1 >> 16);
+            const uint32_t a0 = e4m3_lo(w0), a1 = e4m3_hi(w0), a2 = e4m3_lo(w1), a3 = e4m3_hi(w1);
 #pragma unroll
             for (int c = 0; c < kQ; ++c) mma16<true>(o[j][c], a0, a1, a2, a3, pb[u][c][0][0], pb[u][c][0][1]);
           }
@@ -600,6 +682,9 @@ __global__ void __launch_bounds__(kPgThreads, 2)
       }
     }
 
+    if (pending) sh.next[(k + 1) & 1] = fetched;
+    // the next job's queries, on their way through what follows
+    if (in_next) load_queries(nxt);
     // the warps' sums
 #pragma unroll
     for (int c = 0; c < kQ; ++c)
@@ -610,106 +695,222 @@ __global__ void __launch_bounds__(kPgThreads, 2)
         if (g == 0 && (kHeads > 4 || t < 2)) sh.ml[warp][8 * c + 2 * t + i] = make_float4(m[c][i].d, m[c][i].e, l[c][i] * kDown, qs[c][i]);
       }
     __syncthreads();
-    if (tid < kHeads) {
-      PgMax best = {0.f, 0.f};
-      const float scale = sh.ml[0][tid].w;
+    if (tid == kPgThreads - 1) sh.next[k & 1] = kPgUnknown;  // this job's own: read by all before
+    // their results, kCh channels at a time: [warp][head][channel]
+    constexpr int kCh = kPgOut / 4 / kPgWarps / kHeads, kTiles = kCh / 16, kStride = kCh + 4;
+    const int h = tid * 4 / kCh, ch = tid * 4 % kCh;  // a thread's share of the joined result
+    PgMax best = {0.f, 0.f};
+    const float scale = sh.ml[0][h].w;
+    float share[kPgWarps], sum = 0.f;
+    {
       bool any = false;
 #pragma unroll
       for (int w = 0; w < kPgWarps; ++w) {
-        const float4 v = sh.ml[w][tid];
+        const float4 v = sh.ml[w][h];
         if (v.z != 0.f && (!any || above({v.x, v.y}, best, scale) > 0.f)) {
           best = {v.x, v.y};
           any = true;
         }
       }
-      float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kPgWarps; ++w) {
-        const float4 v = sh.ml[w][tid];
-        const float f = v.z != 0.f ? ex2(above({v.x, v.y}, best, scale)) : 0.f;
-        sh.f[w][tid] = f * kDown;
-        sum += v.z != 0.f ? v.z * f : 0.f;
+        const float4 v = sh.ml[w][h];
+        share[w] = v.z != 0.f ? ex2(above({v.x, v.y}, best, scale)) : 0.f;
+        sum += v.z != 0.f ? v.z * share[w] : 0.f;
+        share[w] *= kDown;
       }
-      sh.all[tid] = make_float4(best.d, best.e, sum, scale);
     }
-    // the blocks that share the sequence
-    const int xf = (int)(((uint64_t)(c_a + 1) * nb - 1) / total), xl = (int)(((uint64_t)(c_a + c_q.tiles) * nb - 1) / total);
-    const bool begins = (uint32_t)((uint64_t)xf * total / nb) == c_a;  // with its first block
-    const int half = (int)x == xf && !begins ? 1 : 0;
-    // their results, kCh channels at a time: [warp][head][channel]
-    constexpr int kCh = kPgOut / 4 / kPgWarps / kHeads, kTiles = kCh / 16;
 #pragma unroll
     for (int pass = 0; pass < kDim / kCh; ++pass) {
-      __syncthreads();
+      if (pass > 0) __syncthreads();
 #pragma unroll
       for (int jj = 0; jj < kTiles; ++jj) {
         const int j = pass * kTiles + jj;
 #pragma unroll
         for (int c = 0; c < kQ; ++c)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float v = o[j][c][i];
-            if constexpr (kHeads == 4) v += __shfl_xor_sync(kFull, v, 2);
-            const int ch = 16 * jj + (kE4m3 ? 2 * g + (i >> 1) : g + 8 * (i >> 1)), h = 8 * c + 2 * t + (i & 1);
-            if (kHeads > 4 || t < 2) so[(warp * kHeads + h) * kCh + ch] = v;
+          for (int i = 0; i < 2; ++i) {
+            float v0 = o[j][c][i], v1 = o[j][c][i + 2];
+            if constexpr (kHeads == 4) {
+              v0 += __shfl_xor_sync(kFull, v0, 2);
+              v1 += __shfl_xor_sync(kFull, v1, 2);
+            }
+            float* to = so + (warp * kHeads + 8 * c + 2 * t + i) * kStride + 16 * jj;
+            if (kHeads > 4 || t < 2) {
+              if constexpr (kE4m3) {
+                *reinterpret_cast<float2*>(to + 2 * g) = make_float2(v0, v1);
+              } else {
+                to[g] = v0;
+                to[g + 8] = v1;
+              }
+            }
           }
       }
       __syncthreads();
-      const int h = tid * 4 / kCh, ch = tid * 4 % kCh;
       if (h < nh) {
         float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kPgWarps; ++w) {
-          const float f = sh.f[w][h];
-          const float4 v = *reinterpret_cast<const float4*>(so + (w * kHeads + h) * kCh + ch);
+          const float f = share[w];
+          const float4 v = *reinterpret_cast<const float4*>(so + (w * kHeads + h) * kStride + ch);
           if (f == 0.f) continue;  // no rows of weight
           r.x = fmaf(v.x, f, r.x);
           r.y = fmaf(v.y, f, r.y);
           r.z = fmaf(v.z, f, r.z);
           r.w = fmaf(v.w, f, r.w);
         }
-        const float4 all = sh.all[h];
+        const float4 all = make_float4(best.d, best.e, sum, scale);
         const int channel = pass * kCh + ch;
-        if (xf == xl) {
+        if (cur.slot < 0) {
           const float inv = all.z != 0.f ? 1.f / all.z : 0.f;
-          const int64_t q = (int64_t)c_s * a.hq + qh0 + h;
+          const int64_t q = (int64_t)cur.s * a.hq + qh0 + h;
           *reinterpret_cast<uint2*>(a.out + q * kDim + channel) =
               make_uint2(pack_bf16x2(r.x * inv, r.y * inv), pack_bf16x2(r.z * inv, r.w * inv));
           if (a.lse != nullptr && channel == 0)
             a.lse[q] = all.z != 0.f ? kLn2 * (fmaf(all.x, all.w, all.y) + log2f(all.z)) : -INFINITY;
         } else {
-          float* part = a.part + (((int64_t)(qh0 + h) * a.nblocks + x) * 2 + half) * kPartStride;
+          float* part = a.part + ((int64_t)cur.slot * a.hq + qh0 + h) * kPartStride;
           *reinterpret_cast<float4*>(part + 4 + channel) = r;
           if (channel == 0) *reinterpret_cast<float4*>(part) = all;
         }
       }
     }
-    if (xf != xl) {
-      __syncthreads();
-      if (tid == 0) {
-        __threadfence();
-        const uint32_t n = (uint32_t)(xl - xf);
-        uint32_t* counter = a.counters + ((int64_t)c_s * a.c.hkv + kvh) * kPgGroups + blockIdx.z;
-        sh.last = atomicInc(counter, n) == n;
-        __threadfence();
-      }
-      __syncthreads();
-      if (sh.last) pg_join(a, c_s, qh0, nh, xf, xl, begins);
-    }
     __syncthreads();  // what the sums went through may be used again
+    job = (uint32_t)sh.next[(k + 1) & 1];
+    if (job >= jobs) break;
+    if (!in_next) {
+      nxt = find(job);
+      p_tile = p_from = nxt.t0;
+      look_up(nxt);
+      load_queries(nxt);
+    }
+    cur = nxt;
+    in_next = false;
+    ++k;
+  }
+
+  // sequences without rows: spread over the blocks
+  for (int s = blockIdx.x; s < a.c.n_seqs; s += blocks) {
+    if (paged_len(a.c, s) > 0) continue;
+    const int64_t q = (int64_t)s * a.hq;
+    for (int i = tid; i < a.hq * (kDim / 8); i += kPgThreads) reinterpret_cast<uint4*>(a.out + q * kDim)[i] = make_uint4(0, 0, 0, 0);
+    if (a.lse != nullptr)
+      for (int i = tid; i < a.hq; i += kPgThreads) a.lse[q + i] = -INFINITY;
   }
 }
 
-// box rows x 128 channels of one head and page (bf16: 64 channels, 128 bytes).
+// The units' partial sums of a sequence and query head, joined: a block an
+// item, each of its warps every kWarps-th result, kAhead of them under way
+// while the maxima are looked at, which every warp does for itself.  Bound by
+// latency: three loads that need one another.
+template <int kWarps, int kAhead>
+__global__ void __launch_bounds__(32 * kWarps) k_paged_join(PagedAttendArgs a) {
+  constexpr int kHeld = kWarps * kAhead / 32;  // maxima and sums a lane has of as many units as the results under way
+  __shared__ float4 so[kWarps][32];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (blockIdx.x == 0 && tid == 0) a.counts[0] = 0;  // the queue, for the next call
+  for (int64_t it = blockIdx.x; it < (int64_t)a.max_splits * a.hq; it += gridDim.x) {
+    const PgSplit sp = a.splits[it / a.hq];
+    if (it / a.hq >= a.counts[1]) return;
+    const int h = (int)(it - it / a.hq * a.hq), n = min(sp.units, a.slots - sp.slot);
+    const float* part = a.part + ((int64_t)sp.slot * a.hq + h) * kPartStride;
+    const int64_t step = (int64_t)a.hq * kPartStride;
+    float4 v[kHeld], x[kAhead];
+    auto load = [&](int u0) {
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);  // the sum 0: no rows of weight
+        if (u0 + 32 * k + lane < n) v[k] = *reinterpret_cast<const float4*>(part + (u0 + 32 * k + lane) * step);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (u0 + warp + i * kWarps < n) x[i] = *(reinterpret_cast<const float4*>(part + (u0 + warp + i * kWarps) * step + 4) + lane);
+    };
+    load(0);
+    const float qs = __shfl_sync(kFull, v[0].w, 0);
+    PgMax m = {0.f, 0.f};
+#pragma unroll 1
+    for (int round = 0; round < 2; ++round) {  // the second finds the largest by exact distances from about the largest
+      float far = -INFINITY;
+      PgMax best = {-INFINITY, -INFINITY};
+      auto look = [&](const float4& w) {
+        const float d = w.z != 0.f ? above({w.x, w.y}, m, qs) : -INFINITY;
+        const bool more = d > far;
+        far = more ? d : far;
+        best.d = more ? w.x : best.d;
+        best.e = more ? w.y : best.e;
+      };
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) look(v[k]);
+      for (int i = 32 * kHeld + lane; i < n; i += 32) look(*reinterpret_cast<const float4*>(part + i * step));
+      float top = far;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+      const int src = __ffs(__ballot_sync(kFull, far == top)) - 1;
+      if (top > -INFINITY) m = {__shfl_sync(kFull, best.d, src), __shfl_sync(kFull, best.e, src)};
+    }
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    for (int u0 = 0; u0 < n; u0 += 32 * kHeld) {
+      if (u0 > 0) load(u0);
+      float f[kHeld];
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        f[k] = v[k].z != 0.f ? ex2(above({v[k].x, v[k].y}, m, qs)) : 0.f;
+        if (v[k].z != 0.f) sum = fmaf(v[k].z, f[k], sum);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int u = warp + i * kWarps;
+        const float fi = __shfl_sync(kFull, f[i * kWarps / 32], u & 31);
+        if (u0 + u >= n || fi == 0.f) continue;
+        o.x = fmaf(x[i].x, fi, o.x);
+        o.y = fmaf(x[i].y, fi, o.y);
+        o.z = fmaf(x[i].z, fi, o.z);
+        o.w = fmaf(x[i].w, fi, o.w);
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
+    so[warp][lane] = o;
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) {
+        const float4 y = so[w][lane];
+        o.x += y.x;
+        o.y += y.y;
+        o.z += y.z;
+        o.w += y.w;
+      }
+      const float inv = sum != 0.f ? 1.f / sum : 0.f;
+      const int64_t q = (int64_t)sp.s * a.hq + h;
+      reinterpret_cast<uint2*>(a.out + q * kDim)[lane] = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+      if (a.lse != nullptr && lane == 0) a.lse[q] = sum != 0.f ? kLn2 * (fmaf(m.d, qs, m.e) + log2f(sum)) : -INFINITY;
+    }
+    __syncthreads();
+  }
+}
+
+// Rows of one head and page: 128 codes each, or two halves of 64 bf16 values,
+// one behind the other in shared memory; 128 bytes a row of either.
 bool encode_pages(CUtensorMap* m, const Paged& c, const uint8_t* base, const PageStrides& s, int layer) {
   EncodeTiled fn = encode_tiled();
   if (fn == nullptr) return false;
-  const int rows = 1 << c.shift;
-  const cuuint64_t dims[4] = {(cuuint64_t)kDim, (cuuint64_t)rows, (cuuint64_t)c.hkv, (cuuint64_t)c.n_pages};
-  const cuuint64_t strides[3] = {(cuuint64_t)s.row, (cuuint64_t)s.head, (cuuint64_t)s.page};
-  const cuuint32_t box[4] = {c.e4m3 ? 128u : 64u, (cuuint32_t)(c.e4m3 ? std::min(rows, 32) : 16), 1, 1}, one[4] = {1, 1, 1, 1};
-  return fn(m, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-            const_cast<uint8_t*>(base + layer * s.layer), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  const cuuint32_t rows = 1u << c.shift, hkv = c.hkv, pages = c.n_pages, one[5] = {1, 1, 1, 1, 1};
+  const cuuint64_t row = s.row, head = s.head, page = s.page;
+  void* p = const_cast<uint8_t*>(base + layer * s.layer);
+  if (c.e4m3) {
+    const cuuint64_t dims[4] = {kDim, rows, hkv, pages}, strides[3] = {row, head, page};
+    const cuuint32_t box[4] = {kDim, std::min(rows, 32u), 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
+  const cuuint64_t dims[5] = {kDim / 2, rows, 2, hkv, pages}, strides[4] = {row, kDim, head, page};
+  const cuuint32_t box[5] = {kDim / 2, 16, 2, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, p, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -725,23 +926,28 @@ cudaError_t launch_heads(const PagedAttendArgs& a, const CUtensorMap& km, const 
     if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
   }
   if (e != cudaSuccess) return e;
-  const dim3 grid(a.nblocks, a.c.hkv, (a.g + kHeads - 1) / kHeads);
-  return launch_pdl(k_paged_attend<kE4m3, kHeads>, grid, dim3(kPgThreads), kPgSmem, st, a, km, vm);
+  return launch_pdl(k_paged_attend<kE4m3, kHeads>, dim3(a.nblocks), dim3(kPgThreads), kPgSmem, st, a, km, vm);
 }
 
 }  // namespace
 
-// Blocks of a KV head and head group: a wave of two an SM, and no more than
-// there could be tiles.
-int paged_attend_blocks(const Paged& c, int g, int sm_count) {
-  const int groups = (g + heads_of(g) - 1) / heads_of(g), tile = c.e4m3 ? Pg<true>::kTile : Pg<false>::kTile;
-  const int64_t wave = std::max<int64_t>(1, 2 * (int64_t)sm_count / ((int64_t)c.hkv * groups));
-  const int64_t rows = (int64_t)c.width << c.shift;
-  return (int)std::min(wave, c.n_seqs * ((rows + tile - 1) / tile + (rows > tile ? 1 : 0)));
-}
-
-size_t paged_attend_part_bytes(const Paged&, int hq, int nblocks) {
-  return (size_t)hq * nblocks * 2 * kPartStride * sizeof(float);
+// What a call needs for its cache, heads and GPU.
+PagedAttendPlan paged_attend_plan(const Paged& c, int hq, int sm_count) {
+  PagedAttendPlan p;
+  const int g = hq / c.hkv, heads = heads_of(g);
+  p.groups = (g + heads - 1) / heads;
+  const int64_t jobs = (int64_t)c.hkv * p.groups, tile = c.e4m3 ? Pg<true>::kTile : Pg<false>::kTile;
+  const int64_t tiles = (((int64_t)c.width << c.shift) + tile - 1) / tile * c.n_seqs;
+  p.blocks = (int)std::min<int64_t>(2 * (int64_t)sm_count, tiles * jobs);  // two an SM
+  // Units of sequences that have several: with T tiles, `large` is at least
+  // 3/8 and `small` 1/16 of T jobs / blocks, so 3/4 T makes two and 1/4 T four
+  // units a block and head, at most one more each for a sequence, of which
+  // fewer than T / small have several.
+  p.max_splits = tiles == c.n_seqs ? 0 : (int)std::min<int64_t>(c.n_seqs, 16 * p.blocks / jobs + 1);
+  p.slots = (int)(6 * p.blocks / jobs + 2 * p.max_splits + 4);
+  p.part_bytes = (size_t)p.slots * hq * kPartStride * sizeof(float);
+  p.bytes = p.part_bytes + (size_t)p.max_splits * sizeof(PgSplit);
+  return p;
 }
 
 cudaError_t paged_attend_error(uint32_t* bits) { return take_gave_up(bits); }
@@ -750,9 +956,17 @@ cudaError_t launch_paged_attend(const PagedAttendArgs& a, cudaStream_t st) {
   CUtensorMap km, vm;
   if (!encode_pages(&km, a.c, a.c.k, a.c.sk, a.layer) || !encode_pages(&vm, a.c, a.c.v, a.c.sv, a.layer)) return cudaErrorInvalidValue;
   const int heads = heads_of(a.g);
+  cudaError_t e;
   if (a.c.e4m3)
-    return heads == 4 ? launch_heads<true, 4>(a, km, vm, st) : heads == 8 ? launch_heads<true, 8>(a, km, vm, st) : launch_heads<true, 16>(a, km, vm, st);
-  return heads == 4 ? launch_heads<false, 4>(a, km, vm, st) : heads == 8 ? launch_heads<false, 8>(a, km, vm, st) : launch_heads<false, 16>(a, km, vm, st);
+    e = heads == 4 ? launch_heads<true, 4>(a, km, vm, st) : heads == 8 ? launch_heads<true, 8>(a, km, vm, st) : launch_heads<true, 16>(a, km, vm, st);
+  else
+    e = heads == 4 ? launch_heads<false, 4>(a, km, vm, st) : heads == 8 ? launch_heads<false, 8>(a, km, vm, st) : launch_heads<false, 16>(a, km, vm, st);
+  if (e != cudaSuccess) return e;
+  if (a.max_splits == 0) return cudaSuccess;  // no sequence can have several units
+  // few items have many units each, and many have few
+  const int64_t items = (int64_t)a.max_splits * a.hq;
+  if (items <= a.nblocks / 2) return launch_pdl(k_paged_join<16, 16>, dim3((unsigned)items), dim3(512), 0, st, a);
+  return launch_pdl(k_paged_join<4, 8>, dim3((unsigned)std::min<int64_t>(items, 4 * a.nblocks)), dim3(128), 0, st, a);
 }
 
 }  // namespace paris

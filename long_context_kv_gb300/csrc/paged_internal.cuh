@@ -41,10 +41,16 @@ __device__ __forceinline__ int64_t scale_at(const Paged& c, int layer, int page,
   return ((((int64_t)layer * c.n_pages + page) * c.hkv + head) << c.shift) + row;
 }
 
-// Two e4m3 codes as halves; every code is exact in them.
-__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t codes) {
+// Two e4m3 codes, of a word's lower or upper half, as halves; every code is
+// exact in them.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t codes) {
   uint32_t y;
   asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}\n" : "=r"(y) : "r"(codes));
+  return y;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t codes) {
+  uint32_t y;
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, hi;\n}\n" : "=r"(y) : "r"(codes));
   return y;
 }
 
@@ -90,6 +96,16 @@ struct CompactArgs {
 };
 cudaError_t launch_paged_compact(const CompactArgs& a, int sm_count, cudaStream_t st);
 
+// A sequence whose attention is computed in several units.
+struct PgSplit {
+  int s, slot, units, pad;
+};
+struct PagedAttendPlan {
+  int groups, blocks, slots, max_splits;
+  size_t part_bytes, bytes;
+};
+PagedAttendPlan paged_attend_plan(const Paged& c, int hq, int sm_count);
+
 struct PagedAttendArgs {
   Paged c;
   int layer, hq, g;
@@ -97,12 +113,11 @@ struct PagedAttendArgs {
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
   float* lse;  // may be null
-  int nblocks;
-  float* part;
-  uint32_t* counters;
+  int groups, nblocks, slots, max_splits;
+  float* part;       // [slots][hq][kPartStride]
+  PgSplit* splits;   // [max_splits]
+  uint32_t* counts;  // the queue's next job; sequences of several units
 };
-int paged_attend_blocks(const Paged& c, int g, int sm_count);
-size_t paged_attend_part_bytes(const Paged& c, int hq, int nblocks);
 cudaError_t launch_paged_attend(const PagedAttendArgs& a, cudaStream_t st);
 cudaError_t paged_attend_error(uint32_t* bits);
 

@@ -94,8 +94,7 @@ paris_status check_paged_heads(const Paged& c, int hq) {
   return PARIS_OK;
 }
 
-// One counter for each (sequence, KV head, group of at least four query heads).
-size_t attend_counter_bytes(const Paged& c) { return ((size_t)c.n_seqs * c.hkv * 32 * sizeof(uint32_t) + 15) / 16 * 16; }
+constexpr size_t kCounterBytes = 16;
 
 size_t fork_bytes(const Paged& c, int n) { return (size_t)n * sizeof(ForkEntry) + (size_t)n * c.width * sizeof(int32_t); }
 size_t compact_bytes(const Paged& c) { return 16 + 3 * (size_t)c.n_pages * sizeof(int32_t); }
@@ -156,8 +155,8 @@ paris_status paris_paged_attend_workspace(const paris_paged* c, int n_q_heads, s
   paris_status st = take_paged(c, &k);
   if (st == PARIS_OK) st = check_paged_heads(k, n_q_heads);
   if (st != PARIS_OK) return st;
-  *bytes = paged_attend_part_bytes(k, n_q_heads, paged_attend_blocks(k, n_q_heads / k.hkv, sm_count()));
-  *counter_bytes = attend_counter_bytes(k);
+  *bytes = paged_attend_plan(k, n_q_heads, sm_count()).bytes;
+  *counter_bytes = kCounterBytes;
   return PARIS_OK;
 }
 
@@ -172,20 +171,24 @@ paris_status paris_paged_attend(const paris_paged* c, int layer, const void* q, 
   if (window < 0) return fail(PARIS_EINVAL, "window must be >= 0 (got %lld)", (long long)window);
   if (!q || !out_bf16) return fail(PARIS_EINVAL, "q and out must not be NULL");
   if (!aligned16(q) || !aligned16(out_bf16)) return fail(PARIS_EINVAL, "q and out must be 16-byte aligned");
-  a.g = n_q_heads / a.c.hkv;
-  a.nblocks = paged_attend_blocks(a.c, a.g, sm_count());
-  const size_t need = paged_attend_part_bytes(a.c, n_q_heads, a.nblocks), counts = attend_counter_bytes(a.c);
-  if (!workspace || workspace_bytes < need || !aligned16(workspace) || !counters || counter_bytes < counts || !aligned16(counters))
+  const PagedAttendPlan p = paged_attend_plan(a.c, n_q_heads, sm_count());
+  if (!workspace || workspace_bytes < p.bytes || !aligned16(workspace) || !counters || counter_bytes < kCounterBytes || !aligned16(counters))
     return fail(PARIS_EINVAL, "paris_paged_attend: needs %zu bytes of workspace and %zu of counters, 16-byte aligned (got %zu, %zu)",
-                need, counts, workspace ? workspace_bytes : (size_t)0, counters ? counter_bytes : (size_t)0);
+                p.bytes, kCounterBytes, workspace ? workspace_bytes : (size_t)0, counters ? counter_bytes : (size_t)0);
   a.layer = layer;
   a.hq = n_q_heads;
   a.window = window > 0x7fffffff ? 0 : (int)window;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.out = static_cast<__nv_bfloat16*>(out_bf16);
   a.lse = lse;
+  a.g = n_q_heads / a.c.hkv;
+  a.groups = p.groups;
+  a.nblocks = p.blocks;
+  a.slots = p.slots;
+  a.max_splits = p.max_splits;
   a.part = static_cast<float*>(workspace);
-  a.counters = counters;
+  a.splits = reinterpret_cast<PgSplit*>(static_cast<uint8_t*>(workspace) + p.part_bytes);
+  a.counts = counters;
   return launched(launch_paged_attend(a, static_cast<cudaStream_t>(stream)), "paris_paged_attend");
 }
 
