@@ -10,11 +10,15 @@ constexpr int kPlanThreads = 1024;
 
 // The `want` lowest free pages (at most those there are): f(r, page) for the
 // r-th of them, by any thread, one thread's in ascending order; their bits are
-// cleared.  The whole block; tmp: 33 words of shared memory.
+// cleared.  The whole block; tmp: 33 words of shared memory; first: the thread's
+// word of the first 1024.
+__device__ __forceinline__ uint32_t first_bits(const Paged& c) {
+  return (int)threadIdx.x < (c.n_pages + 31) / 32 ? c.bits[threadIdx.x] : 0u;
+}
 template <typename F>
-__device__ __forceinline__ void take_free(const Paged& c, uint32_t want, uint32_t* tmp, F&& f) {
+__device__ __forceinline__ void take_free(const Paged& c, uint32_t want, uint32_t first, uint32_t* tmp, F&& f) {
   const int words = (c.n_pages + 31) / 32;
-  uint32_t before = 0, next = (int)threadIdx.x < words ? c.bits[threadIdx.x] : 0u;
+  uint32_t before = 0, next = first;
   for (int w0 = 0; w0 < words && before < want; w0 += kPlanThreads) {
     const int w = w0 + threadIdx.x;
     const uint32_t word = next;
