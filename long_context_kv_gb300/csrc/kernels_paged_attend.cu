@@ -221,17 +221,39 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     for (int i = 0; i < kPgDepth; ++i) bar_init(bar0 + 8 * i, kE4m3 ? 33 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (tid == 0) sh.gave_up = 0;
+  if (tid == 0) {
+    sh.gave_up = 0;
+    sh.next[0] = sh.next[1] = kPgUnknown;
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(&km) : "memory");
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(&vm) : "memory");
+  }
   volatile uint32_t* gave_up = &sh.gave_up;
   const uint32_t heads = (uint32_t)(a.c.hkv * a.groups), blocks = gridDim.x;
   pdl_wait();
   pdl_trigger();
 
-  // the line's table: a thread has up to four entries in a row
+  // The line: up to 32 sequences are a lane each of every warp; more of them are
+  // in a table, of whose entries a thread has up to two in a row.
+  const bool few = a.c.n_seqs <= 32;
   const int group = (a.c.n_seqs + kPgEntries - 1) / kPgEntries, entries = (a.c.n_seqs + group - 1) / group;
   PgCut cut;
-  uint32_t jobs;
-  {
+  uint32_t jobs, my_at = 0, my_begin = 0;
+  PgSeq my_q = {0, 0, 0, 0};
+  if (few) {
+    if (lane < a.c.n_seqs) my_q = pg_seq<kE4m3>(a, lane);
+    __syncthreads();  // the barriers are there
+    const uint32_t seqs = __popc(__ballot_sync(kFull, my_q.tiles > 0)), end = warp_incl_scan(my_q.tiles, lane);
+    cut = pg_cut(__shfl_sync(kFull, end, 31), seqs, heads, blocks);
+    my_at = end - my_q.tiles;
+    const uint32_t c = pg_count(pg_units(cut, my_at, my_q.tiles)), units = warp_incl_scan(c, lane);
+    my_begin = units - c;
+    jobs = (__shfl_sync(kFull, units, 31) & 0xffffu) * heads;
+    if (blockIdx.x == 0 && warp == 0) {
+      const uint32_t several = __ballot_sync(kFull, c >> 16 != 0);
+      if (c >> 16 != 0) a.splits[__popc(several & ((1u << lane) - 1u))] = PgSplit{lane, (int)(my_begin >> 16), (int)(c >> 16), 0};
+      if (lane == 0) a.counts[1] = __popc(several);  // none if max_splits is 0
+    }
+  } else {
     const int per = (entries + kPgThreads - 1) / kPgThreads * group;
     const int s0 = min(tid * per, a.c.n_seqs), s1 = min(s0 + per, a.c.n_seqs);
     const uint32_t only = s0 < s1 ? pg_seq<kE4m3>(a, s0).tiles : 0u;  // of a thread's first sequence
@@ -259,7 +281,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     jobs = (units & 0xffffu) * heads;
     if (blockIdx.x == 0) {
       split = block_excl_scan(several, sh.tmp, &splits);
-      if (tid == 0) a.counts[1] = splits;  // none if max_splits is 0
+      if (tid == 0) a.counts[1] = splits;
     }
     at = at0;
     for (int s = s0; s < s1; ++s) {
@@ -270,51 +292,66 @@ __global__ void __launch_bounds__(kPgThreads, 2)
       unit += c;
       at += n;
     }
-    if (tid == 0) sh.next[0] = sh.next[1] = kPgUnknown;
     __syncthreads();
   }
 
-  // a job's unit: its entry of the line, and the sequence in the entry
+  // a job's unit and sequence
   auto find = [&](uint32_t job) {
     const uint32_t unit = job / heads, head = job - unit * heads;
     PgJob r;
     r.kvh = (int)head / a.groups;
     r.h0 = ((int)head - r.kvh * a.groups) * kHeads;
-    int e = -1;
-    for (int e0 = 0; e0 < entries; e0 += 32) {
-      const int n = __popc(__ballot_sync(kFull, e0 + lane < entries && (sh.line[e0 + lane].y & 0xffffu) <= unit));
-      e += n;
-      if (n < 32) break;
-    }
-    uint32_t at = sh.line[e].x, begin = sh.line[e].y;
-    for (r.s = e * group;; ++r.s) {
-      const PgSeq q = pg_seq<kE4m3>(a, r.s);
-      const PgUnits u = pg_units(cut, at, q.tiles);
-      const uint32_t count = pg_count(u), i = unit - (begin & 0xffffu);  // the sequence's i-th unit
-      if (i >= (count & 0xffffu) && r.s + 1 < a.c.n_seqs) {
+    PgSeq q;
+    uint32_t at, begin;
+    if (few) {  // the last lane that begins at or before the unit
+      r.s = __popc(__ballot_sync(kFull, lane < a.c.n_seqs && (my_begin & 0xffffu) <= unit)) - 1;
+      q.len = __shfl_sync(kFull, my_q.len, r.s);
+      q.first = __shfl_sync(kFull, my_q.first, r.s);
+      q.base = __shfl_sync(kFull, my_q.base, r.s);
+      q.tiles = __shfl_sync(kFull, my_q.tiles, r.s);
+      at = __shfl_sync(kFull, my_at, r.s);
+      begin = __shfl_sync(kFull, my_begin, r.s);
+    } else {  // likewise the entry, and a sequence of its `group`
+      int e = -1;
+      for (int e0 = 0; e0 < entries; e0 += 32) {
+        const int n = __popc(__ballot_sync(kFull, e0 + lane < entries && (sh.line[e0 + lane].y & 0xffffu) <= unit));
+        e += n;
+        if (n < 32) break;
+      }
+      at = sh.line[e].x;
+      begin = sh.line[e].y;
+      r.s = e * group;
+      q = pg_seq<kE4m3>(a, r.s);
+      while (r.s + 1 < a.c.n_seqs) {
+        const uint32_t count = pg_count(pg_units(cut, at, q.tiles));
+        if (unit - (begin & 0xffffu) < (count & 0xffffu)) break;
         at += q.tiles;
         begin += count;
-        continue;
+        q = pg_seq<kE4m3>(a, ++r.s);
       }
-      const bool back = i >= u.nf;
-      const uint32_t size = back ? cut.small : cut.large, from = back ? u.front : 0u, to = back || u.nf + u.nb == 1 ? q.tiles : u.front;
-      r.len = q.len;
-      r.first = q.first;
-      r.base = q.base;
-      r.t0 = from + (back ? i - u.nf : i) * size;
-      r.t1 = u.nf + u.nb == 1 ? to : min(r.t0 + size, to);
-      r.slot = count >> 16 != 0 ? (int)min((begin >> 16) + i, (uint32_t)a.slots - 1u) : -1;
-      return r;
     }
+    const PgUnits u = pg_units(cut, at, q.tiles);
+    const uint32_t i = unit - (begin & 0xffffu), n = u.nf + u.nb;  // the sequence's i-th unit
+    const bool back = i >= u.nf;
+    const uint32_t size = back ? cut.small : cut.large, from = back ? u.front : 0u, to = back || n == 1 ? q.tiles : u.front;
+    r.len = q.len;
+    r.first = q.first;
+    r.base = q.base;
+    r.t0 = from + (back ? i - u.nf : i) * size;
+    r.t1 = n == 1 ? to : min(r.t0 + size, to);
+    r.slot = n > 1 ? (int)min((begin >> 16) + i, (uint32_t)a.slots - 1u) : -1;
+    return r;
   };
 
   // What the warp copies next: step p_tile of the present job, or of the next
   // one once that is known.
   const bool busy = blockIdx.x < jobs;
-  PgJob cur = find(busy ? blockIdx.x : 0u), nxt = cur;
+  uint32_t job = blockIdx.x;
+  PgJob cur = find(busy ? job : 0u), nxt = cur;
+  int k = 0;  // jobs that the block has had
   bool in_next = false;
   // pages of 32 steps from p_from on, a lane each (in 8 bits and pages of 16 rows two)
-  uint32_t p_from = cur.t0;
+  uint32_t p_tile = cur.t0, p_from = cur.t0;
   int page0 = 0, page1 = 0;
   auto look_up = [&](const PgJob& p) {
     const int row = p.base + (int)(p_from + lane) * G::kTile + warp * kRows, j = row >> a.c.shift;
@@ -324,9 +361,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
       if (kE4m3 && a.c.shift == 4) page1 = row + 16 < p.len ? clamp_page(a.c, t[j + 1]) : 0;
     }
   };
-  int k = 0;
-  uint32_t job = blockIdx.x;
-  uint32_t p_tile = cur.t0, issued = 0, taken = 0, p_stage = 0, c_stage = 0, c_parity = 0;
+  uint32_t issued = 0, taken = 0, p_stage = 0, c_stage = 0, c_parity = 0;
   auto copy_next = [&]() {
     if (issued - taken >= kPgDepth) return;
     if (!in_next && p_tile >= cur.t1) {
@@ -344,7 +379,8 @@ __global__ void __launch_bounds__(kPgThreads, 2)
       look_up(p);
     }
     const int row = p.base + (int)p_tile * G::kTile + warp * kRows, len = p.len, kvh = p.kvh;
-    const int page = __shfl_sync(kFull, page0, p_tile - p_from), next = __shfl_sync(kFull, page1, p_tile - p_from);
+    const int page = __shfl_sync(kFull, page0, p_tile - p_from);
+    const int next = __shfl_sync(kFull, page1, p_tile - p_from);
     ++p_tile;
     if (row >= len || __any_sync(kFull, *gave_up != 0)) return;
     const int r = row & ((1 << a.c.shift) - 1);
