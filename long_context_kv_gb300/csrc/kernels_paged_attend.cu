@@ -343,47 +343,58 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     return r;
   };
 
-  // What the warp copies next: step p_tile of the present job, or of the next
-  // one once that is known.
+  // What the warp copies next: a step of the present job, or of the next one
+  // once that is known.
   const bool busy = blockIdx.x < jobs;
   uint32_t job = blockIdx.x;
   PgJob cur = find(busy ? job : 0u), nxt = cur;
   int k = 0;  // jobs that the block has had
-  bool in_next = false;
-  // pages of 32 steps from p_from on, a lane each (in 8 bits and pages of 16 rows two)
-  uint32_t p_tile = cur.t0, p_from = cur.t0;
-  int page0 = 0, page1 = 0;
+  bool in_next = false, stop = false;  // stop: a wait gave up, nothing more is copied
+  // The steps left of the job that is copied, and the place of the next one
+  // among 32 that were looked up, a lane each: its page, its first row there in
+  // 16s, whether it has rows (and, in 8 bits and pages of 16 rows, its second
+  // page if that has rows).  As little as possible is left for a step's own
+  // copy, which all of the warp waits for.
+  constexpr uint32_t kPageMask = (1u << kMaxPagesLog) - 1u, kHas = 1u << 31;
+  int p_left = 0, p_i = 0, p_row = 0;
+  uint32_t step0 = 0, step1 = 0;
+  const uint8_t* p_scales = nullptr;  // of the job's layer and head: a lane's keys' or values', four rows
+  const uint32_t p_pitch = (uint32_t)a.c.hkv << a.c.shift;
   auto look_up = [&](const PgJob& p) {
-    const int row = p.base + (int)(p_from + lane) * G::kTile + warp * kRows, j = row >> a.c.shift;
+    const int row = p_row + lane * G::kTile, j = row >> a.c.shift;
     const int32_t* t = a.c.table + (int64_t)p.s * a.c.width;
-    if (p_from + lane < p.t1 && row < p.len) {
-      page0 = clamp_page(a.c, t[j]);
-      if (kE4m3 && a.c.shift == 4) page1 = row + 16 < p.len ? clamp_page(a.c, t[j + 1]) : 0;
+    p_i = 0;
+    p_row += 32 * G::kTile;
+    step0 = step1 = 0;
+    if (lane < p_left && row < p.len) {
+      step0 = kHas | (uint32_t)(row & ((1 << a.c.shift) - 1)) >> 4 << kMaxPagesLog | (uint32_t)clamp_page(a.c, t[j]);
+      if (kE4m3 && a.c.shift == 4 && row + 16 < p.len) step1 = kHas | (uint32_t)clamp_page(a.c, t[j + 1]);
     }
   };
-  uint32_t issued = 0, taken = 0, p_stage = 0, c_stage = 0, c_parity = 0;
+  auto enter = [&](const PgJob& j) {
+    p_row = j.base + (int)j.t0 * G::kTile + warp * kRows;
+    p_left = (int)(j.t1 - j.t0);
+    if (kE4m3) p_scales = (lane < 8 ? a.c.ks : a.c.vs) + scale_at(a.c, a.layer, 0, j.kvh, 4 * (lane & 7));
+    look_up(j);
+  };
+  uint32_t ahead = 0, p_stage = 0, c_stage = 0, c_parity = 0;  // steps that are copied and not yet taken
   auto copy_next = [&]() {
-    if (issued - taken >= kPgDepth) return;
-    if (!in_next && p_tile >= cur.t1) {
+    if (ahead >= kPgDepth) return;
+    if (p_left == 0) {
+      if (in_next) return;
       const int j = __shfl_sync(kFull, *(volatile int*)&sh.next[(k + 1) & 1], 0);
       if (j == kPgUnknown || (uint32_t)j >= jobs) return;
       nxt = find(j);
       in_next = true;
-      p_tile = p_from = nxt.t0;
-      look_up(nxt);
+      enter(nxt);
     }
-    if (in_next && p_tile >= nxt.t1) return;
-    const PgJob& p = in_next ? nxt : cur;
-    if (p_tile - p_from == 32) {
-      p_from = p_tile;
-      look_up(p);
-    }
-    const int row = p.base + (int)p_tile * G::kTile + warp * kRows, len = p.len, kvh = p.kvh;
-    const int page = __shfl_sync(kFull, page0, p_tile - p_from);
-    const int next = __shfl_sync(kFull, page1, p_tile - p_from);
-    ++p_tile;
-    if (row >= len || __any_sync(kFull, *gave_up != 0)) return;
-    const int r = row & ((1 << a.c.shift) - 1);
+    if (p_i == 32) look_up(in_next ? nxt : cur);
+    const uint32_t w0 = __shfl_sync(kFull, step0, p_i), w1 = kE4m3 ? __shfl_sync(kFull, step1, p_i) : 0u;
+    const int kvh = in_next ? nxt.kvh : cur.kvh;
+    ++p_i;
+    --p_left;
+    if ((w0 & kHas) == 0 || stop) return;
+    const int page = (int)(w0 & kPageMask), r = (int)(w0 >> kMaxPagesLog & 15u) << 4;
     const uint32_t dst = ring + p_stage * kPgStage, bar = bar0 + 8 * p_stage;
     if constexpr (!kE4m3) {
       if (elect()) {
@@ -395,13 +406,11 @@ __global__ void __launch_bounds__(kPgThreads, 2)
       // Pages of 16 rows: two, the second one if it has rows.  The scale bytes
       // go by the lanes, four rows each: as copies of their own they took as
       // much of the copy engine's time as the rows.
-      const bool one = a.c.shift > 4, two = !one && row + 16 < len;
-      const int r4 = 4 * (lane & 7);
-      if (lane < 16 && (one || two || r4 < 16)) {
-        const int64_t e = one || r4 < 16 ? scale_at(a.c, a.layer, page, kvh, r + r4) : scale_at(a.c, a.layer, next, kvh, r4 - 16);
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(smem_u32(scales) + p_stage * kPgScale + 4 * lane),
-                     "l"((lane < 8 ? a.c.ks : a.c.vs) + e)
-                     : "memory");
+      const bool one = a.c.shift > 4, two = (w1 & kHas) != 0, upper = !one && (lane & 4) != 0;
+      const int next = (int)(w1 & kPageMask);
+      if (lane < 16 && (!upper || two)) {
+        const uint8_t* e = p_scales + (uint64_t)(uint32_t)(upper ? next : page) * p_pitch + (upper ? -16 : r);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(smem_u32(scales) + p_stage * kPgScale + 4 * lane), "l"(e) : "memory");
       }
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
       if (elect()) {
@@ -416,7 +425,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     }
     __syncwarp();
     p_stage = p_stage + 1 == kPgDepth ? 0 : p_stage + 1;
-    ++issued;
+    ++ahead;
   };
 
   // a lane's places in a step's boxes (128 bytes a row, 16-byte pieces swizzled by the row)
@@ -444,12 +453,12 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     }
   };
   if (busy) {
-    look_up(cur);
+    enter(cur);
     load_queries(cur);
   }
   while (busy) {
 #pragma unroll 1
-    for (int i = 0; i < kPgDepth - 1 && !in_next && issued - taken < kPgDepth - 1; ++i) copy_next();
+    for (int i = 0; i < kPgDepth - 1 && !in_next && ahead < kPgDepth - 1; ++i) copy_next();
     // the job after this one: on its way while the first steps are computed
     int fetched = 0;
     bool pending = tid == 0;
@@ -515,13 +524,14 @@ __global__ void __launch_bounds__(kPgThreads, 2)
       __syncwarp();
       copy_next();
       const int row0 = cur.base + (int)tile * G::kTile + warp * kRows;
-      if (row0 >= cur.len || taken == issued) continue;  // (nothing is copied any more after a wait that gave up)
+      if (row0 >= cur.len || ahead == 0) continue;  // (nothing is copied any more after a wait that gave up)
       const uint32_t kst = ring + c_stage * kPgStage, vst = kst + kPgStage / 2;
-      if (!bar_wait(bar0 + 8 * c_stage, c_parity, gave_up)) {
+      if (__any_sync(kFull, !bar_wait(bar0 + 8 * c_stage, c_parity, gave_up))) {
+        stop = true;
         WaitLimit limit(now_ns());  // the copy ends before the block does
         while (!bar_try(bar0 + 8 * c_stage, c_parity) && !limit.over(now_ns())) {}
       }
-      ++taken;
+      --ahead;
       const bool edge = row0 < cur.first || row0 + kRows > cur.len;
       if (edge) {
         // rows that do not count may hold anything, and 0 times NaN is NaN
@@ -536,19 +546,25 @@ __global__ void __launch_bounds__(kPgThreads, 2)
       }
 
       // S^T: p[u][c][2 r + i] of row 16 u + 8 r + g, column 2 t + i
-      float p[kU][kQ][4], ev[kU][2], inv[kU][2];
+      float p[kU][kQ][4], p2[kU][kQ][4], ev[kU][2], inv[kU][2];  // p2: every second product, as they wait for one another
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
 #pragma unroll
-        for (int c = 0; c < kQ; ++c) p[u][c][0] = p[u][c][1] = p[u][c][2] = p[u][c][3] = 0.f;
+        for (int c = 0; c < kQ; ++c)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) p[u][c][x] = p2[u][c][x] = 0.f;
         if constexpr (!kE4m3) {
 #pragma unroll
           for (int s = 0; s < 8; ++s) {
             uint32_t f[4];
             ldsm4(f, kst + (s >> 2) * 2048 + lrow * 128 + (((2 * (s & 3) + lhi) ^ lsw) << 4));
 #pragma unroll
-            for (int c = 0; c < kQ; ++c) mma16<false>(p[u][c], f[0], f[1], f[2], f[3], qf[c][s][0], qf[c][s][1]);
+            for (int c = 0; c < kQ; ++c) mma16<false>(s & 1 ? p2[u][c] : p[u][c], f[0], f[1], f[2], f[3], qf[c][s][0], qf[c][s][1]);
           }
+#pragma unroll
+          for (int c = 0; c < kQ; ++c)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) p[u][c][x] += p2[u][c][x];
         } else {
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
@@ -559,7 +575,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
             for (int i = 0; i < 2; ++i) {
               const uint32_t a0 = e4m3_lo(f[2 * i]), a1 = e4m3_lo(f[2 * i + 1]), a2 = e4m3_hi(f[2 * i]), a3 = e4m3_hi(f[2 * i + 1]);
 #pragma unroll
-              for (int c = 0; c < kQ; ++c) mma16<true>(p[u][c], a0, a1, a2, a3, qf[c][2 * s + i][0], qf[c][2 * s + i][1]);
+              for (int c = 0; c < kQ; ++c) mma16<true>(i ? p2[u][c] : p[u][c], a0, a1, a2, a3, qf[c][2 * s + i][0], qf[c][2 * s + i][1]);
             }
           }
 #pragma unroll
@@ -571,8 +587,8 @@ __global__ void __launch_bounds__(kPgThreads, 2)
             inv[u][r] = __uint_as_float((uint32_t)(254 - vb) << 23);
 #pragma unroll
             for (int c = 0; c < kQ; ++c) {
-              p[u][c][2 * r] *= S;
-              p[u][c][2 * r + 1] *= S;
+              p[u][c][2 * r] = (p[u][c][2 * r] + p2[u][c][2 * r]) * S;
+              p[u][c][2 * r + 1] = (p[u][c][2 * r + 1] + p2[u][c][2 * r + 1]) * S;
             }
           }
         }
@@ -590,6 +606,17 @@ __global__ void __launch_bounds__(kPgThreads, 2)
             for (int c = 0; c < kQ; ++c) p[u][c][2 * r] = p[u][c][2 * r + 1] = -INFINITY;
           }
       }
+      // the values' fragments are on their way while the weights are computed, where registers allow it
+      constexpr bool kEarly = kHeads < 16;
+      uint32_t vf[8][4];
+      const uint32_t vrow = (lane & 7) + ((lane >> 4) << 3), vhi = (lane >> 3) & 1;  // rows 0-7 and 8-15 by channels 16 j and 16 j + 8
+      auto load_values = [&](int j) {
+        if constexpr (kE4m3) ldsm4_t(vf[j], vst + lane * 128 + ((j ^ lsw) << 4));
+        else ldsm4_t(vf[j], vst + (j >> 2) * 2048 + vrow * 128 + (((2 * (j & 3) + vhi) ^ lsw) << 4));
+      };
+      if constexpr (kEarly)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) load_values(j);
       // exponents of the weights, kUp up (NaN counts as no growth)
       float sc[kU][kQ][4];
       auto exponents = [&]() {
@@ -689,18 +716,14 @@ __global__ void __launch_bounds__(kPgThreads, 2)
           }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
+        if constexpr (!kEarly) load_values(j);
+        const uint32_t (&f)[4] = vf[j];
         if constexpr (!kE4m3) {
-          uint32_t f[4];
-          // rows 0-7 and 8-15 by channels 16 j and 16 j + 8
-          const uint32_t vrow = (lane & 7) + ((lane >> 4) << 3), vhi = (lane >> 3) & 1;
-          ldsm4_t(f, vst + (j >> 2) * 2048 + vrow * 128 + (((2 * (j & 3) + vhi) ^ lsw) << 4));
 #pragma unroll
           for (int c = 0; c < kQ; ++c)
 #pragma unroll
             for (int s = 0; s < kParts; ++s) mma16<false>(o[j][c], f[0], f[1], f[2], f[3], pb[0][c][s][0], pb[0][c][s][1]);
         } else {
-          uint32_t f[4];
-          ldsm4_t(f, vst + lane * 128 + ((j ^ lsw) << 4));
 #pragma unroll
           for (int u = 0; u < kU; ++u) {
             // two rows by two channels a word: even channels are the product's first eight rows, odd ones the others
@@ -816,8 +839,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     if (job >= jobs) break;
     if (!in_next) {
       nxt = find(job);
-      p_tile = p_from = nxt.t0;
-      look_up(nxt);
+      enter(nxt);
       load_queries(nxt);
     }
     cur = nxt;
