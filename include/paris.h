@@ -503,7 +503,7 @@ paris_status paris_kv4_check(const paris_kv4* c);
  * An array's address is 16-byte aligned.  k_pages and v_pages have strides
  * in elements: positive multiples of 16 bytes, a row's of at least 128
  * elements, below 2^38; rows of 128 are contiguous.  max_pages * page_rows
- * is below 2^31, and n_seqs times that at most 2^37.  Lengths outside
+ * is at most 2^30, and n_seqs times that at most 2^37.  Lengths outside
  * [0, max_pages * page_rows] count as the nearest of the two, and so do
  * entries of the table outside [0, n_pages).                                  */
 typedef struct {
@@ -554,8 +554,9 @@ paris_status paris_paged_attend_workspace(const paris_paged* c, int n_q_heads, s
  * query all of whose scores are -inf, has out = 0 and lse = -inf.  What lies in
  * rows that are not in use (or outside the window) does not reach the result,
  * NaN included.  Scores, maxima and sums are float32; scores past
- * float32's range give NaN.  q: device bf16 [n_seqs][Hq][d]; out: device bf16,
- * the same; lse: device float32 [n_seqs][Hq], or NULL.  At most 128 query heads
+ * float32's range give NaN.  Softmax weights enter the product with V as two
+ * bf16 parts (8-bit rows: as halves, as the query does).  q: device bf16
+ * [n_seqs][Hq][d]; out: device bf16, the same; lse: device float32 [n_seqs][Hq], or NULL.  At most 128 query heads
  * per KV head.  workspace and counters: device, 16-byte aligned, used only by
  * this call; counters are zeros, and zeros again after it.                    */
 paris_status paris_paged_attend(const paris_paged* c, int layer, const void* q, int n_q_heads, int64_t window,

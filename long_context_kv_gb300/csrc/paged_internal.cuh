@@ -28,7 +28,7 @@ struct Paged {
   uint32_t* status;
 };
 
-__device__ __forceinline__ int paged_cap(const Paged& c) { return (int)min64((int64_t)c.width << c.shift, 0x7fffffff); }
+__device__ __forceinline__ int paged_cap(const Paged& c) { return c.width << c.shift; }
 __device__ __forceinline__ int paged_len(const Paged& c, int s) { return min(max(c.lens[s], 0), paged_cap(c)); }
 // Pages of so many rows.
 __device__ __forceinline__ int pages_of(const Paged& c, int rows) {

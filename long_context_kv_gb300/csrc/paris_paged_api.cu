@@ -40,8 +40,9 @@ paris_status take_paged(const paris_paged* c, Paged* k) {
   if (c->dtype != PARIS_BF16 && c->dtype != PARIS_E4M3) return fail(PARIS_EINVAL, "the cache's dtype must be PARIS_BF16 or PARIS_E4M3");
   if (c->n_pages < 1 || c->n_pages > (int64_t)1 << kMaxPagesLog)
     return fail(PARIS_EINVAL, "n_pages must be in [1, 2^%d]", kMaxPagesLog);
-  if (c->max_pages < 1 || c->max_pages > 0x7fffffff / c->page_rows)
-    return fail(PARIS_EINVAL, "max_pages must be positive, and max_pages * page_rows below 2^31");
+  // rows past a sequence's end, up to 32 tiles of them, still have 32-bit numbers
+  if (c->max_pages < 1 || c->max_pages > ((int64_t)1 << 30) / c->page_rows)
+    return fail(PARIS_EINVAL, "max_pages must be positive, and max_pages * page_rows at most 2^30");
   if (c->n_seqs * c->max_pages * c->page_rows > (int64_t)1 << 37)
     return fail(PARIS_EINVAL, "n_seqs * max_pages * page_rows must be at most 2^37");
   const bool e4m3 = c->dtype == PARIS_E4M3;

@@ -153,6 +153,26 @@ def test_rows_of_strided_tensors_and_batches(dtype):
             assert torch.all(out[s, :, m:] == 3.0)
 
 
+def test_starts_that_leave_rows_out_or_lie_outside():
+    c = empty(3, 2, 12, 4)
+    x = rand(50, 2, R.D, seed=5).to(BF)
+    c.paris_paged_grow(i32([20, 7, 16]))
+    cu = i32([3, 23, 30, 46])  # three rows in front and four behind are nobody's
+    c.paris_paged_store(x, x, cu=cu, max_new=20)
+    out = torch.full((50, 2, R.D), 4.0, dtype=BF, device="cuda")
+    c.paris_paged_read(out, out.clone(), cu=cu)
+    assert torch.all(out[:3] == 4.0) and torch.all(out[46:] == 4.0) and torch.equal(out[3:46], x[3:46])
+    # a start past the rows counts as their end, one before the start in front as that
+    before = R.raw(c.k_pages).clone()
+    c.paris_paged_store(x, x, cu=i32([60, 70, 10, -5]))
+    assert torch.equal(R.raw(c.k_pages), before)
+    c.paris_paged_store(-x, -x, cu=i32([-9, 4, 2, 1000]), max_new=50)
+    assert torch.equal(R.rows_of(c, "k", 0, 0)[:, :4].transpose(0, 1), -x[:4].double())
+    assert torch.equal(R.rows_of(c, "k", 0, 0)[:, 4:].transpose(0, 1), x[7:23].double())
+    assert torch.equal(R.rows_of(c, "k", 0, 1).transpose(0, 1), x[23:30].double())
+    assert torch.equal(R.rows_of(c, "v", 0, 2).transpose(0, 1), -x[2:18].double())
+
+
 def test_a_store_writes_the_last_growth_only():
     c = empty(2, 1, 8, 4)
     x = rand(40, 1, R.D, seed=4).to(BF)
@@ -652,6 +672,54 @@ def test_readers_on_two_streams_at_once():
     torch.cuda.synchronize()
     for j in range(2):
         assert torch.all(outs[j] == want[j][0])
+
+
+def test_two_graphs_and_a_stream_at_once():
+    c, _, _ = filled([7000, 300, 0, 1, 2500], 2, dtype=E4, seed=122)
+    q = rand(3, 5, 16, R.D, seed=123, amp=2.0).to(BF)
+    want = [attend(c, x)[0] for x in q]
+    outs = torch.zeros(3, 5, 16, R.D, dtype=BF, device="cuda")
+    graphs, streams = [torch.cuda.CUDAGraph() for _ in range(2)], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for g, i in zip(graphs, range(2)):
+        with torch.cuda.graph(g):
+            for _ in range(5):
+                c.paris_paged_attend(q[i], outs[i])
+    for _ in range(10):
+        outs.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        c.paris_paged_attend(q[2], outs[2])
+        torch.cuda.synchronize()
+        for i in range(3):
+            assert torch.equal(outs[i], want[i])
+    c.paris_paged_check()
+
+
+def test_attention_with_different_numbers_of_heads_in_turn():
+    c, _, _ = filled([3000, 20], 2, dtype=BF, seed=124)
+    for hq in (2, 256, 8, 64, 16, 2):
+        q = rand(2, hq, R.D, seed=125 + hq, amp=2.0).to(BF)
+        out, lse = attend(c, q)
+        check_attend(c, q, out, lse)
+
+
+def test_many_kv_heads():
+    c, _, _ = filled([40, 100], 300, dtype=E4, seed=126)
+    q = rand(2, 600, R.D, seed=127).to(BF)
+    out, lse = attend(c, q)
+    check_attend(c, q, out, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+def test_pages_of_256_rows_and_windows_that_begin_inside(dtype):
+    c, _, _ = filled([900, 256, 255, 513], 2, 256, dtype, seed=128, order="rhd")
+    q = rand(4, 32, R.D, seed=129, amp=2.0).to(BF)
+    for window in (0, 1, 100, 257, 600):
+        out, lse = attend(c, q, window)
+        check_attend(c, q, out, lse, window)
 
 
 def test_a_dropped_cache_is_kept_for_the_streams_that_use_it():

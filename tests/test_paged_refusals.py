@@ -35,7 +35,7 @@ BAD = [
     (dict(n_kv_heads=0), "n_kv_heads"), (dict(n_seqs=4096, n_kv_heads=16), "65535"), (dict(n_layers=0), "n_layers"),
     (dict(page_rows=8), "page_rows"), (dict(page_rows=48), "page_rows"), (dict(page_rows=512), "page_rows"),
     (dict(dtype=P.PARIS_F32), "dtype"), (dict(n_pages=0), "n_pages"), (dict(n_pages=(1 << 21) + 1), "n_pages"),
-    (dict(n_seqs=4096, n_kv_heads=1, max_pages=(1 << 21) + 1), "2^37"), (dict(max_pages=0), "max_pages"), (dict(max_pages=1 << 27), "max_pages"), (dict(lens=None), "NULL"),
+    (dict(n_seqs=4096, n_kv_heads=1, max_pages=(1 << 21) + 1), "2^37"), (dict(max_pages=0), "max_pages"), (dict(max_pages=(1 << 26) + 1), "max_pages"), (dict(lens=None), "NULL"),
     (dict(k_pages=None), "NULL"), (dict(status=None), "NULL"), (dict(dtype=P.PARIS_E4M3, k_scales=None), "NULL"),
     (dict(v_pages=4104), "aligned"), (dict(dtype=P.PARIS_E4M3, v_scales=4104), "aligned"),
     (dict(k=P.paris_page_strides(0, 4096, 2048, 128)), "k_pages: the layer stride"),
