@@ -51,6 +51,9 @@ constexpr int kPgOut = 8192;    // bytes through which the warps' results meet
 constexpr float kPgGrowth = 8.f;
 constexpr int kPgEntries = 512;  // of the line's table
 constexpr uint32_t kPgMinUnit = 4;  // tiles (8-bit batch of 24: 44.1 us, with 3 46.0; one sequence of 128K rows the same)
+// Where sequences can have no more tiles than this, each is one unit, and there
+// is nothing to join (four of up to 300 rows: 8.0 -> 7.2 us; one of six tiles: 6.4 -> 6.6).
+constexpr uint32_t kPgWhole = 6;
 constexpr int kPgUnknown = -1;
 constexpr int kPgSmem = 1024 + kPgWarps * kPgDepth * (kPgStage + kPgScale) + kPgOut + 16 * 16 * kPgWarps;
 
@@ -148,9 +151,11 @@ struct PgCut {
 // us.)  Of few sequences one large unit: they are cut into as many as there
 // are blocks (one sequence of 128K rows 89.4 -> 88.0 us, in 8 bits 60.9 -> 57.5; a
 // ragged batch would have blocks with two of them, 112 -> 131).
-__device__ __forceinline__ PgCut pg_cut(uint32_t total, uint32_t seqs, uint32_t heads, uint32_t blocks) {
+__device__ __forceinline__ PgCut pg_cut(uint32_t total, uint32_t seqs, uint32_t heads, uint32_t blocks, bool whole) {
   PgCut c;
   c.border = total - total / 4;
+  c.small = c.large = kPgWhole;
+  if (whole) return c;
   const uint32_t each = blocks / heads;
   if (each > seqs) {  // a sequence's last unit may not be full
     c.small = c.large = max(1u, (total + each - seqs - 1) / (each - seqs));
@@ -243,7 +248,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     if (lane < a.c.n_seqs) my_q = pg_seq<kE4m3>(a, lane);
     __syncthreads();  // the barriers are there
     const uint32_t seqs = __popc(__ballot_sync(kFull, my_q.tiles > 0)), end = warp_incl_scan(my_q.tiles, lane);
-    cut = pg_cut(__shfl_sync(kFull, end, 31), seqs, heads, blocks);
+    cut = pg_cut(__shfl_sync(kFull, end, 31), seqs, heads, blocks, a.max_splits == 0);
     my_at = end - my_q.tiles;
     const uint32_t c = pg_count(pg_units(cut, my_at, my_q.tiles)), units = warp_incl_scan(c, lane);
     my_begin = units - c;
@@ -268,7 +273,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     used = __reduce_add_sync(kFull, used);
     if (lane == 0) sh.used[warp] = used;
     const uint32_t at0 = block_excl_scan(mine, sh.tmp, &total);
-    cut = pg_cut(total, sh.used[0] + sh.used[1] + sh.used[2] + sh.used[3], heads, blocks);
+    cut = pg_cut(total, sh.used[0] + sh.used[1] + sh.used[2] + sh.used[3], heads, blocks, a.max_splits == 0);
     uint32_t at = at0, count = 0, several = 0;
     for (int s = s0; s < s1; ++s) {
       const uint32_t n = tiles_of(s), c = pg_count(pg_units(cut, at, n));
@@ -1001,7 +1006,7 @@ PagedAttendPlan paged_attend_plan(const Paged& c, int hq, int sm_count) {
   // 3/8 and `small` 1/16 of T jobs / blocks, so 3/4 T makes two and 1/4 T four
   // units a block and head, at most one more each for a sequence, of which
   // fewer than T / small have several.
-  p.max_splits = tiles == c.n_seqs ? 0 : (int)std::min<int64_t>(c.n_seqs, 16 * p.blocks / jobs + 1);
+  p.max_splits = tiles <= kPgWhole * (int64_t)c.n_seqs ? 0 : (int)std::min<int64_t>(c.n_seqs, 16 * p.blocks / jobs + 1);
   p.slots = (int)(6 * p.blocks / jobs + 2 * p.max_splits + 4);
   p.part_bytes = (size_t)p.slots * hq * kPartStride * sizeof(float);
   p.bytes = p.part_bytes + (size_t)p.max_splits * sizeof(PgSplit);

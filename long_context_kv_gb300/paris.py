@@ -701,7 +701,7 @@ class PagedCache:
                               k=strides(k_pages), v=strides(v_pages), status=self._status.data_ptr(),
                               **{name: t.data_ptr() for name, t in given.items()})
         self._ref = ctypes.byref(self._c)
-        self._token_shape, self._ws, self._spaces = (n, hkv, HEAD_DIM), {}, {}
+        self._token_shape, self._ws, self._spaces, self._ready = (n, hkv, HEAD_DIM), {}, {}, {}
 
     @classmethod
     def create(cls, n_seqs, n_kv_heads, n_pages, max_pages, page_rows=16, n_layers=1, dtype=None, device="cuda"):
@@ -726,14 +726,17 @@ class PagedCache:
         for t in (*self._tensors, self._status):
             t.record_stream(stream)
 
+    @staticmethod
+    def _capturing(stream):
+        if stream is None:
+            return _torch._C._cuda_isCurrentStreamCapturing()
+        with _torch.cuda.stream(stream):
+            return _torch._C._cuda_isCurrentStreamCapturing()
+
     def _space(self, nbytes, stream, handle, zeros=False):
         """Address of the workspace of a call, or of its counters: kept for each stream, whose calls take turns with it;
         during a capture one of the graph's own."""
-        if stream is None:
-            capturing = _torch._C._cuda_isCurrentStreamCapturing()
-        else:
-            with _torch.cuda.stream(stream):
-                capturing = _torch._C._cuda_isCurrentStreamCapturing()
+        capturing = self._capturing(stream)
         t = None if capturing else self._spaces.get((handle, zeros))
         if t is None or t.numel() < nbytes:
             t = _scratch(nbytes, self.device, stream)
@@ -742,6 +745,7 @@ class PagedCache:
                     t.zero_()
             if not capturing:
                 self._spaces[handle, zeros] = t
+                self._ready.clear()
         return t.data_ptr()
 
     def _sizes(self, key, call, count):
@@ -795,20 +799,25 @@ class PagedCache:
     def paris_paged_attend(self, q, out, window=0, lse=None, layer=0, stream=None):
         """out = softmax(K q / sqrt(d)) V over a layer's rows in use, or the last `window` of them: q, out bfloat16
         [n_seqs, Hq, 128]; lse: float32 [n_seqs, Hq], or None."""
-        shape = q.shape
+        shape, bf16 = q.shape, _torch.bfloat16
         if len(shape) != 3 or shape[0] != self.n_seqs or shape[2] != HEAD_DIM:
             raise ValueError(f"q: shape {tuple(shape)}, expected [{self.n_seqs}, heads, 128]")
-        _shaped(q, "q", shape, _torch.bfloat16)
-        _shaped(out, "out", shape, _torch.bfloat16)
+        if q.dtype is not bf16 or out.dtype is not bf16 or out.shape != shape:
+            _shaped(q, "q", shape, bf16)
+            _shaped(out, "out", shape, bf16)
         if lse is not None:
             _shaped(lse, "lse", shape[:2], _torch.float32)
         _on(self._index, q, out, lse)
-        lib, hq, window = _lib or load(), shape[1], _number(window, "window")
-        sizes = self._ws.get(hq) or self._sizes(hq, lambda a, b: lib.paris_paged_attend_workspace(self._ref, hq, a, b), 2)
-        handle = _raw_stream(self._index, stream)
-        _check(lib.paris_paged_attend(self._ref, _number(layer, "layer", 32), _flat(q), hq, window, _flat(out), _flat(lse),
-                                      self._space(sizes[0], stream, handle), sizes[0],
-                                      self._space(sizes[1], stream, handle, True), sizes[1], handle))
+        lib, hq, handle = _lib or load(), shape[1], _raw_stream(self._index, stream)
+        # both workspaces of a stream that has been here before (never one that is being captured)
+        ready = self._ready.get((handle, hq))
+        if ready is None or self._capturing(stream):
+            n, m = self._ws.get(hq) or self._sizes(hq, lambda a, b: lib.paris_paged_attend_workspace(self._ref, hq, a, b), 2)
+            ready = self._space(n, stream, handle), n, self._space(m, stream, handle, True), m
+            if not self._capturing(stream):
+                self._ready[handle, hq] = ready
+        _check(lib.paris_paged_attend(self._ref, _number(layer, "layer", 32), _flat(q), hq, _number(window, "window"), _flat(out),
+                                      _flat(lse), *ready, handle))
 
     def paris_paged_read(self, k_out, v_out, cu=None, max_rows=None, layer=0, stream=None):
         """A layer's values of the first rows: bfloat16 [rows, Hkv, 128] with int32 starts cu [n_seqs + 1] (max_rows: at
