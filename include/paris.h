@@ -588,8 +588,8 @@ paris_status paris_paged_fork_workspace(const paris_paged* c, int n, size_t* byt
 paris_status paris_paged_fork(const paris_paged* c, const int32_t* src, const int32_t* dst, const int32_t* rows, int n,
                               void* workspace, size_t workspace_bytes, void* stream);
 
-/* End the n listed sequences (rows = NULL), or cut them to rows[i] rows:
- * paris_paged_fork with src = dst.                                           */
+/* End the n listed sequences (rows = NULL; no workspace is used then), or cut
+ * them to rows[i] rows: paris_paged_fork with src = dst.                      */
 paris_status paris_paged_free(const paris_paged* c, const int32_t* seqs, const int32_t* rows, int n, void* workspace,
                               size_t workspace_bytes, void* stream);
 

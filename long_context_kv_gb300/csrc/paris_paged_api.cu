@@ -108,16 +108,18 @@ paris_status fork(const paris_paged* c, const int32_t* src, const int32_t* dst, 
   if (n < 0 || n > a.c.n_seqs) return fail(PARIS_EINVAL, "%s: n must be in [0, n_seqs] (got %d)", what, n);
   if (n == 0) return PARIS_OK;
   if (!src || !dst) return fail(PARIS_EINVAL, "%s: the sequences must not be NULL", what);
-  const size_t need = fork_bytes(a.c, n);
-  if (!workspace || workspace_bytes < need || !aligned16(workspace))
+  const size_t need = zero && !rows ? 0 : fork_bytes(a.c, n);  // sequences that end need none
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
     return fail(PARIS_EINVAL, "%s: needs %zu bytes of 16-byte aligned workspace (got %zu)", what, need, workspace ? workspace_bytes : (size_t)0);
   a.src = src;
   a.dst = dst;
   a.rows = rows;
   a.n = n;
   a.zero = zero;
-  a.plan = static_cast<ForkEntry*>(workspace);
-  a.entries = reinterpret_cast<int32_t*>(a.plan + n);
+  if (need > 0) {
+    a.plan = static_cast<ForkEntry*>(workspace);
+    a.entries = reinterpret_cast<int32_t*>(a.plan + n);
+  }
   return launched(launch_paged_fork(a, static_cast<cudaStream_t>(stream)), what);
 }
 

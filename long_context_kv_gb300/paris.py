@@ -756,7 +756,7 @@ class PagedCache:
         return self._ws[key]
 
     def _list(self, t, name, n=None):
-        if t.dtype is not _torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+        if t.dtype is not _torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and len(t) != n):
             raise ValueError(f"{name}: a contiguous int32 tensor of {'one dimension' if n is None else n}")
         return t.data_ptr() or None
 
@@ -766,7 +766,7 @@ class PagedCache:
         if longest is not None:
             longest = _number(longest, name)
         rows, heads, seqs, ks = _heads(k, "k", packed)
-        if v.shape != k.shape or v.dtype is not k.dtype:
+        if v.dtype is not k.dtype or v.shape != k.shape:
             raise ValueError("k and v must have the same shape and dtype")
         vs = _strides(v, "v", packed)
         if heads != self.n_kv_heads or (not packed and seqs != self.n_seqs):
@@ -852,7 +852,7 @@ class PagedCache:
         r = None if rows is None else self._list(rows, "rows", n)
         _on(self._index, seqs, rows)
         handle = _raw_stream(self._index, stream)
-        ws, size = self._fork_space(n, stream, handle)
+        ws, size = (None, 0) if rows is None else self._fork_space(n, stream, handle)
         _check((_lib or load()).paris_paged_free(self._ref, a, r, n, ws, size, handle))
 
     def paris_paged_compact(self, stream=None):

@@ -104,6 +104,8 @@ def test_cache_calls(lib):
                  (a, a, None, 2, odd, n.value), (a, a, None, 2, a, n.value - 1)):
         assert lib.paris_paged_fork(c, *args, None) == E
     assert lib.paris_paged_free(c, None, None, 2, a, n.value, None) == E
+    assert lib.paris_paged_free(c, a, a, 2, a, n.value - 1, None) == E
+    assert lib.paris_paged_free(c, a, a, 2, None, n.value, None) == E
     assert lib.paris_paged_compact_workspace(c, ctypes.byref(n)) == P.PARIS_OK
     assert lib.paris_paged_compact(c, a, n.value - 1, None) == E
     assert lib.paris_paged_compact(c, None, n.value, None) == E
