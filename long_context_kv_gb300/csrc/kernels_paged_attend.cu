@@ -14,9 +14,11 @@
 // - Copies are always under way.  A warp takes steps of 8 KB of its own (16
 //   bf16 rows of keys and values, or 32 in 8 bits) through a ring in shared
 //   memory that TMA fills, two steps ahead and across the ends of sequences;
-//   no warp waits for another but at those.  The tensor maps' swizzle makes
-//   the reads below free of bank conflicts, and their strides take any order
-//   of the pages' dimensions.
+//   no warp waits for another but at those.  (Twelve warps an SM with two
+//   steps each took 111.9 instead of 110.9 us for a ragged batch and 43.9
+//   instead of 41.5 in 8 bits, a warp that copies for four others 113.7 and
+//   70.)  The tensor maps' swizzle makes the reads below free of bank
+//   conflicts, and their strides take any order of the pages' dimensions.
 // - The arithmetic stays out of the way.  Both products have the cache's rows
 //   on their M side, S^T = K Q^T and O^T = V^T P^T (m16n8k16, float32 sums), so
 //   that the eight columns are what there are few of.  For up to four query
@@ -31,6 +33,11 @@
 // 2^(s + e - m), m the maximum of s + e, and the sum takes 2^-e of it.  m is kept
 // as a row's own product and e, and both are subtracted before the scale, so
 // that weights are right at any size of the scores.
+//
+// Measured, without the join (3 to 4 us more): 131072 rows of 8 KV heads in bf16
+// 82.8 us, 6.5 TB/s; 24 ragged sequences, 167K rows of 4 KV heads in 8 bits, 39
+// us, 4.4 TB/s: there a warp's own instructions (1.2 us for 32 rows, 8 warps an
+// SM) and a unit's ends (2.5 us, three a block) bound it.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -139,6 +146,7 @@ struct PgMax {
 };
 // How far x lies above y.
 __device__ __forceinline__ float above(PgMax x, PgMax y, float qs) { return fmaf(x.d - y.d, qs, x.e - y.e); }
+
 // How the line of all tiles is cut: units of at most `large` tiles in front of
 // `border`, of at most `small` behind it; sequences of at most `small` whole.
 struct PgCut {
@@ -238,7 +246,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
   pdl_trigger();
 
   // The line: up to 32 sequences are a lane each of every warp; more of them are
-  // in a table, of whose entries a thread has up to two in a row.
+  // in a table, of whose entries a thread has up to four in a row.
   const bool few = a.c.n_seqs <= 32;
   const int group = (a.c.n_seqs + kPgEntries - 1) / kPgEntries, entries = (a.c.n_seqs + group - 1) / group;
   PgCut cut;

@@ -7,8 +7,9 @@
 // their copies, the third gives back what the destinations held, writes their
 // entries and copies rows.  Counts change by sums only, so their order does not
 // matter.  All of it is bound by latency: small forks are one block that takes
-// the steps in turn, larger ones a kernel a step, and sequences that end need
-// none of the first two.
+// the steps in turn (one sequence to four: 8.3 us, 9.8 as three kernels),
+// larger ones a kernel a step (64 beams: 12.5 us), and sequences that end need
+// none of the first two (3 us).
 #include "paged_device.cuh"
 
 namespace paris {
@@ -295,6 +296,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_compact_plan(CompactArgs
   if (threadIdx.x == 0) a.moves[0] = (int)min(low, high);
 }
 
+// The moves, four rows an item of 16 threads; counts and entries follow.  Bound
+// by the bytes: 2000 pages of 64 KB in two layers (517 MB read and written)
+// 75 us, 6.9 TB/s; one row at a time 88.
 __global__ void __launch_bounds__(kForkThreads) k_paged_compact_move(CompactArgs a) {
   pdl_wait();
   pdl_trigger();
