@@ -26,7 +26,9 @@
 //   more, bf16 weights take a second product for their lower parts.  Values
 //   of 8-bit rows are converted to halves, in which they are exact, and their
 //   scales stay outside the products: a key row's multiplies its scores, a
-//   value row's joins the exponent.
+//   value row's joins the exponent.  (The tensor pipe is 8 to 11 % busy: what
+//   tcgen05 is faster at is not what is missing here, and it takes weights
+//   through memory.)
 //
 // Weights are p = 2^(s - m) of base-2 scores, m a maximum so far that may lag
 // by 2^8.  With a value row's scale 2^e, what enters the product with V is

@@ -794,7 +794,15 @@ class PagedCache:
         with any strides that paris_paged_store takes.  Sequences that have not grown are left as they are."""
         _shaped(k, "k", self._token_shape, k.dtype)
         _shaped(v, "v", self._token_shape, k.dtype)
-        self.paris_paged_store(k.unsqueeze(2), v.unsqueeze(2), layer=layer, stream=stream)
+        _on(self._index, k, v)
+        strides = []
+        for t, name in ((k, "k"), (v, "v")):
+            seq, head, channel = t.stride()
+            if channel != 1 and t.numel():
+                raise ValueError(f"{name}: the last dimension must be contiguous")
+            strides.append(_STRIDES.pack(HEAD_DIM, head, seq))
+        _check((_lib or load()).paris_paged_store(self._ref, _number(layer, "layer", 32), _raw(k), _raw(v), _code(k), *strides,
+                                                  1, None, 1, _raw_stream(self._index, stream)))
 
     def paris_paged_attend(self, q, out, window=0, lse=None, layer=0, stream=None):
         """out = softmax(K q / sqrt(d)) V over a layer's rows in use, or the last `window` of them: q, out bfloat16

@@ -545,19 +545,53 @@ def test_layers_are_apart(dtype):
     assert not torch.equal(outs[0], outs[1])
 
 
-def test_a_pool_past_four_gigabytes():
-    n_pages = 70000  # 8 heads of 16 rows: 4.6 GB of keys
-    c = empty(1, 8, n_pages, 40, garbage=False)
+def test_appended_rows_of_strided_tensors():
+    c = empty(3, 2, 6, 2)
+    both = rand(3, 4, 2, 2, R.D, seed=81).to(BF)  # keys and values of several layers side by side
+    for layer in range(1, 3):
+        c.paris_paged_grow(i32([1, 0, 1]))
+        c.paris_paged_append(both[:, layer, 0], both[:, layer, 1])
+    f = rand(3, 2, R.D, seed=82)
+    c.paris_paged_grow(i32([0, 1, 1]))
+    c.paris_paged_append(f, f.to(torch.float32))
+    assert c.lens.tolist() == [2, 1, 3]
+    for i, name in enumerate(("k", "v")):
+        for s, rows in ((0, [both[0, 1, i], both[0, 2, i]]), (1, [f[1]]), (2, [both[2, 1, i], both[2, 2, i], f[2]])):
+            assert torch.equal(R.rows_of(c, name, 0, s).transpose(0, 1), torch.stack([x.to(BF) for x in rows]).double())
+    with pytest.raises(ValueError, match="contiguous"):
+        c.paris_paged_append(both[:, 1, 0].transpose(1, 2).contiguous().transpose(1, 2), both[:, 1, 1])
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+def test_a_pool_past_four_gigabytes(dtype):
+    n_pages = 140000 if dtype is BF else 280000  # 8 heads of 16 rows: 4.6 GB of keys
+    c = empty(1, 8, n_pages, 40, garbage=False, dtype=dtype)
     c.table[0, :40] = torch.arange(n_pages - 40, n_pages, dtype=torch.int32, device="cuda").flip(0)
     c.lens.fill_(600)
-    c.k_pages[0, n_pages - 40:] = rand(40, 8, 16, R.D, seed=78).to(BF)
-    c.v_pages[0, n_pages - 40:] = rand(40, 8, 16, R.D, seed=79).to(BF)
+    k, v = rand(600, 8, R.D, seed=78).to(BF), rand(600, 8, R.D, seed=79).to(BF)
+    c.paris_paged_store(k, v, cu=K4.starts([600]))  # starts is 0
+    assert torch.any(R.raw(c.k_pages)[0, n_pages - 1]) and not torch.any(R.raw(c.k_pages)[0, :n_pages - 40][::7])
     q = rand(1, 16, R.D, seed=80).to(BF)
     out, lse = attend(c, q)
     check_attend(c, q, out, lse)
     ko, vo = torch.zeros(600, 8, R.D, dtype=BF, device="cuda"), torch.zeros(600, 8, R.D, dtype=BF, device="cuda")
     c.paris_paged_read(ko, vo, cu=K4.starts([600]))
     assert torch.equal(ko.double().transpose(0, 1), R.rows_of(c, "k", 0, 0))
+    # and copied there and back: the last 38 pages move to the front
+    c.refs[n_pages - 38:] = 1
+    c.free_bits.copy_(pack_bits(c.refs == 0))
+    c.n_used.fill_(38)
+    c.paris_paged_compact()
+    assert c.table[0, :38].max() < 38
+    got, _ = attend(c, q)
+    assert torch.equal(got, out)
+
+
+def pack_bits(flags):
+    w = torch.zeros(-(-flags.numel() // 32) * 32, dtype=torch.int64, device=flags.device)
+    w[:flags.numel()] = flags
+    w = (w.reshape(-1, 32) << torch.arange(32, device=flags.device)).sum(-1)
+    return torch.where(w >= 1 << 31, w - (1 << 32), w).to(torch.int32)
 
 
 # --------------------------------------------------------------- together
