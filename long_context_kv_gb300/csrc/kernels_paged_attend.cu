@@ -9,8 +9,9 @@
 //   since SMs differ by a third in what the memory gives them (equal parts of
 //   131072 rows ended 72 to 104 us after the start).  A sequence of one unit
 //   is done with its job; the units of others leave partial sums (maximum,
-//   sum, unnormalised result), which a second kernel joins in their order.
-//   Which block has which job changes no result.
+//   sum, unnormalised result), which a second kernel joins in their order
+//   (k_paged_join, k_paged_join_many).  Which block has which job changes no
+//   result.
 // - Copies are always under way.  A warp takes steps of 8 KB of its own (16
 //   bf16 rows of keys and values, or 32 in 8 bits) through a ring in shared
 //   memory that TMA fills, two steps ahead and across the ends of sequences;
@@ -36,10 +37,14 @@
 // as a row's own product and e, and both are subtracted before the scale, so
 // that weights are right at any size of the scores.
 //
-// Measured, without the join (3 to 4 us more): 131072 rows of 8 KV heads in bf16
-// 82.8 us, 6.5 TB/s; 24 ragged sequences, 167K rows of 4 KV heads in 8 bits, 39
-// us, 4.4 TB/s: there a warp's own instructions (1.2 us for 32 rows, 8 warps an
-// SM) and a unit's ends (2.5 us, three a block) bound it.
+// Measured: 131072 rows of 8 KV heads in bf16 84.9 us, 6.3 TB/s; 24 ragged
+// sequences, 167K rows of 4 KV heads in 8 bits, 39.1 us, 4.4 TB/s.  Of those 39
+// the rows take 24 at the memory's rate; the first of them are there after 3 to
+// 5.5 us (lengths, pages, rows: one round trip after another), blocks end up to
+// 3 us apart (a unit of four tiles takes 4), and joining takes 5 with its launch.
+// A step of 32 8-bit rows is 0.9 us of a warp's time, hidden behind the copies
+// but for the last one.  (Four more warps a block that do the copying, with
+// registers moved from them to the others: 8-bit batch 38.2, long sequence 88.)
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -895,11 +900,12 @@ __global__ void __launch_bounds__(kPgThreads, 2)
 }
 
 // The units' partial sums of a sequence and query head, joined: a block an
-// item, each of its warps every kWarps-th result, kAhead of them under way
+// item, each of its warps every fourth result, eight of them under way
 // while the maxima are looked at, which every warp does for itself.  Bound by
 // latency: three loads that need one another.
-template <int kWarps, int kAhead>
-__global__ void __launch_bounds__(32 * kWarps) k_paged_join(PagedAttendArgs a) {
+constexpr int kPgJoin = 4;
+__global__ void __launch_bounds__(32 * kPgJoin) k_paged_join(PagedAttendArgs a) {
+  constexpr int kWarps = kPgJoin, kAhead = 8;
   constexpr int kHeld = kWarps * kAhead / 32;  // maxima and sums a lane has of as many units as the results under way
   __shared__ float4 so[kWarps][32];
   pdl_wait();
@@ -989,6 +995,134 @@ __global__ void __launch_bounds__(32 * kWarps) k_paged_join(PagedAttendArgs a) {
   }
 }
 
+// The same for sequences of many units (few KV heads or sequences), with more
+// threads an item: kParts blocks, each for its part of the channels, whose
+// threads share the maxima and leave the units' weights in shared memory.  In
+// place of 16 of the other's warps: 131072 rows of one KV head and 8 query heads
+// 32.6 -> 24.3 us, 400000 69.1 -> 48.8, 30000 of 8 KV heads 28.6 -> 27.9.
+constexpr int kPgManyUnits = 2048;
+template <int kWarps, int kParts>
+__global__ void __launch_bounds__(32 * kWarps) k_paged_join_many(PagedAttendArgs a) {
+  constexpr int kThreads = 32 * kWarps, kLanes = 32 / kParts, kEach = kThreads / kLanes, kAhead = 4;  // lanes of a result, results at once
+  __shared__ float2 top[kPgManyUnits];      // a unit's maximum
+  __shared__ float weight[kPgManyUnits];    // its sum, then its share
+  __shared__ float4 far[2][kWarps], so[kWarps][kLanes];
+  __shared__ float sums[kWarps];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, mine = tid / kLanes;
+  if (blockIdx.x == 0 && tid == 0) a.counts[0] = 0;  // the queue, for the next call
+  for (int64_t b = blockIdx.x; b < (int64_t)a.max_splits * a.hq * kParts; b += gridDim.x) {
+    const int64_t it = b / kParts;
+    const int channel = ((int)(b - it * kParts) * kLanes + lane % kLanes) * 4;
+    const PgSplit sp = a.splits[it / a.hq];
+    if (it / a.hq >= a.counts[1]) return;
+    const int h = (int)(it - it / a.hq * a.hq), n = min(min(sp.units, a.slots - sp.slot), kPgManyUnits);
+    const float* part = a.part + ((int64_t)sp.slot * a.hq + h) * kPartStride;
+    const int64_t step = (int64_t)a.hq * kPartStride;
+    float4 x[kAhead];
+    PgMax m = {0.f, 0.f};
+    float qs = 0.f, d0 = -INFINITY;
+    PgMax best = {-INFINITY, -INFINITY};
+    auto look = [&](float d, float e, float z) {
+      const float up = z != 0.f ? above({d, e}, m, qs) : -INFINITY;
+      const bool more = up > d0;
+      d0 = more ? up : d0;
+      best.d = more ? d : best.d;
+      best.e = more ? e : best.e;
+    };
+    auto meet = [&](int round) {  // the block's largest, the first one of several
+      float t = d0;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, off));
+      const int src = __ffs(__ballot_sync(kFull, d0 == t)) - 1;
+      const float d = __shfl_sync(kFull, best.d, src), e = __shfl_sync(kFull, best.e, src);
+      if (lane == 0) far[round][warp] = make_float4(t, d, e, qs);
+      __syncthreads();
+      qs = far[round][0].w;
+      t = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 v = far[round][w];
+        if (v.x > t) {
+          t = v.x;
+          m = {v.y, v.z};
+        }
+      }
+    };
+#pragma unroll 4
+    for (int u = tid; u < n; u += kThreads) {
+      const float4 v = *reinterpret_cast<const float4*>(part + u * step);
+      top[u] = make_float2(v.x, v.y);
+      weight[u] = v.z;
+      qs = v.w;
+      look(v.x, v.y, v.z);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (mine + i * kEach < n) x[i] = *reinterpret_cast<const float4*>(part + (mine + i * kEach) * step + 4 + channel);
+    meet(0);
+    d0 = -INFINITY;  // by exact distances from about the largest
+    best = {-INFINITY, -INFINITY};
+    for (int u = tid; u < n; u += kThreads) look(top[u].x, top[u].y, weight[u]);
+    meet(1);
+    float sum = 0.f;
+    for (int u = tid; u < n; u += kThreads) {
+      const float z = weight[u], f = z != 0.f ? ex2(above({top[u].x, top[u].y}, m, qs)) : 0.f;
+      if (z != 0.f) sum = fmaf(z, f, sum);
+      weight[u] = f;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
+    if (lane == 0) sums[warp] = sum;
+    __syncthreads();
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int u0 = mine; u0 < n; u0 += kAhead * kEach) {
+      float f[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int u = u0 + i * kEach;
+        f[i] = u < n ? weight[u] : 0.f;
+        if (u0 != mine && u < n) x[i] = *reinterpret_cast<const float4*>(part + u * step + 4 + channel);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (f[i] == 0.f) continue;
+        o.x = fmaf(x[i].x, f[i], o.x);
+        o.y = fmaf(x[i].y, f[i], o.y);
+        o.z = fmaf(x[i].z, f[i], o.z);
+        o.w = fmaf(x[i].w, f[i], o.w);
+      }
+    }
+#pragma unroll
+    for (int off = 16; off >= kLanes; off >>= 1) {
+      o.x += __shfl_xor_sync(kFull, o.x, off);
+      o.y += __shfl_xor_sync(kFull, o.y, off);
+      o.z += __shfl_xor_sync(kFull, o.z, off);
+      o.w += __shfl_xor_sync(kFull, o.w, off);
+    }
+    if (lane < kLanes) so[warp][lane] = o;
+    __syncthreads();
+    if (tid < kLanes) {
+      sum = sums[0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) {
+        const float4 y = so[w][lane];
+        o.x += y.x;
+        o.y += y.y;
+        o.z += y.z;
+        o.w += y.w;
+        sum += sums[w];
+      }
+      const float inv = sum != 0.f ? 1.f / sum : 0.f;
+      const int64_t q = (int64_t)sp.s * a.hq + h;
+      *reinterpret_cast<uint2*>(a.out + q * kDim + channel) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+      if (a.lse != nullptr && channel == 0) a.lse[q] = sum != 0.f ? kLn2 * (fmaf(m.d, qs, m.e) + log2f(sum)) : -INFINITY;
+    }
+    __syncthreads();  // what was shared may be used again
+  }
+}
+
 // Rows of one head and page: 128 codes each, or two halves of 64 bf16 values,
 // one behind the other in shared memory; 128 bytes a row of either.
 bool encode_pages(CUtensorMap* m, const Paged& c, const uint8_t* base, const PageStrides& s, int layer) {
@@ -1058,10 +1192,18 @@ cudaError_t launch_paged_attend(const PagedAttendArgs& a, cudaStream_t st) {
     e = heads == 4 ? launch_heads<false, 4>(a, km, vm, st) : heads == 8 ? launch_heads<false, 8>(a, km, vm, st) : launch_heads<false, 16>(a, km, vm, st);
   if (e != cudaSuccess) return e;
   if (a.max_splits == 0) return cudaSuccess;  // no sequence can have several units
-  // few items have many units each, and many have few
   const int64_t items = (int64_t)a.max_splits * a.hq;
-  if (items <= a.nblocks / 2) return launch_pdl(k_paged_join<16, 16>, dim3((unsigned)items), dim3(512), 0, st, a);
-  return launch_pdl(k_paged_join<4, 8>, dim3((unsigned)std::min<int64_t>(items, 4 * a.nblocks)), dim3(128), 0, st, a);
+  // Few items have many units each, and many have few; eight parts of the
+  // channels where that leaves no block without an SM (one sequence 48.8 us, four
+  // parts 50.6; 128 items 41.7, four 39.0).
+  if (items <= a.nblocks / 2) {
+    constexpr int kWarps = 8;
+    if (6 * a.nblocks / (a.c.hkv * a.groups) + 2 > kPgManyUnits) return cudaErrorInvalidConfiguration;
+    if (8 * items <= 2 * a.nblocks)
+      return launch_pdl(k_paged_join_many<kWarps, 8>, dim3((unsigned)(8 * items)), dim3(32 * kWarps), 0, st, a);
+    return launch_pdl(k_paged_join_many<kWarps, 4>, dim3((unsigned)std::min<int64_t>(4 * items, 4 * a.nblocks)), dim3(32 * kWarps), 0, st, a);
+  }
+  return launch_pdl(k_paged_join, dim3((unsigned)std::min<int64_t>(items, 4 * a.nblocks)), dim3(32 * kPgJoin), 0, st, a);
 }
 
 }  // namespace paris

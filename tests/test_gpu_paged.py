@@ -756,6 +756,19 @@ def test_pages_of_256_rows_and_windows_that_begin_inside(dtype):
         check_attend(c, q, out, lse, window)
 
 
+@pytest.mark.parametrize("dtype", [BF, E4])
+@pytest.mark.parametrize("n,hq", [(150000, 4), (400000, 2), (150000, 128)])
+def test_one_kv_head_over_hundreds_of_units(n, hq, dtype):
+    """Partial sums of up to 680 units a sequence, and (128 query heads) of many sequences' worth of heads."""
+    c, _, _ = filled([n, 0, 700], 1, 64, dtype, seed=131)
+    q = rand(3, hq, R.D, seed=132, amp=2.0).to(BF)
+    out, lse = attend(c, q)
+    check_attend(c, q, out, lse)
+    again, lse2 = attend(c, q)
+    assert torch.equal(again, out) and torch.equal(lse2, lse)
+    c.paris_paged_check()
+
+
 def test_a_dropped_cache_is_kept_for_the_streams_that_use_it():
     x = rand(1, 1, R.D, seed=130).to(BF)
     s = torch.cuda.Stream()
