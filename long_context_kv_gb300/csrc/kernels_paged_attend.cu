@@ -5,7 +5,7 @@
 //
 // - All SMs read to the end.  The tiles of all sequences form one line, which
 //   is cut into units within sequences: long ones in front, short ones in its
-//   last quarter.  Blocks take (unit, KV head, head group) jobs from a queue,
+//   last quarter or third.  Blocks take (unit, KV head, head group) jobs from a queue,
 //   since SMs differ by a third in what the memory gives them (equal parts of
 //   131072 rows ended 72 to 104 us after the start).  A sequence of one unit
 //   is done with its job; the units of others leave partial sums (maximum,
@@ -184,10 +184,15 @@ struct PgCut {
 // units of a few tiles give no more jobs than blocks, all are of that size.
 // Otherwise two large units a block, and four small ones to even out what they
 // took.  (Two or three small ones end later: a ragged batch of 24 104 -> 111
-// us.)  Of few sequences one large unit: they are cut into as many as there
-// are blocks (one sequence of 128K rows 89.4 -> 88.0 us, in 8 bits 60.9 -> 57.5; a
-// ragged batch would have blocks with two of them, 112 -> 131).
-__device__ __forceinline__ PgCut pg_cut(uint32_t total, uint32_t seqs, uint32_t heads, uint32_t blocks, bool whole) {
+// us.)  Where the memory alone bounds the call, SMs differ most in what they
+// get, and the large units leave a third to the small ones instead of a quarter:
+// the same batch 109.5 -> 106.7 us, twice its rows 220 -> 210, a decode step of
+// 30 sequences 59.7 -> 57.8; but with 16 heads 41.0 -> 43.9 and in 8 bits 39.4
+// -> 41.1, where small units cost a warp's time.  Of few sequences one large
+// unit: they are cut into as many as there are blocks (one sequence of 128K rows
+// 89.4 -> 88.0 us, in 8 bits 60.9 -> 57.5; a ragged batch would have blocks with
+// two of them, 112 -> 131).
+__device__ __forceinline__ PgCut pg_cut(uint32_t total, uint32_t seqs, uint32_t heads, uint32_t blocks, bool whole, bool memory) {
   PgCut c;
   c.border = total - total / 4;
   c.small = c.large = kPgWhole;
@@ -198,8 +203,11 @@ __device__ __forceinline__ PgCut pg_cut(uint32_t total, uint32_t seqs, uint32_t 
     if (c.small <= kPgMinUnit) return c;
   }
   const float share = (float)total * (float)heads / (float)blocks;
-  c.small = max(kPgMinUnit, (uint32_t)ceilf(share * 0.0625f));
-  c.large = max(c.small, (uint32_t)ceilf(share * (16 * seqs <= each ? 0.75f : 0.375f)));
+  const bool few = 16 * seqs <= each;
+  memory &= !few;
+  if (memory) c.border = (uint32_t)((float)total * 0.66f);
+  c.small = max(kPgMinUnit, (uint32_t)ceilf(share * (memory ? 0.085f : 0.0625f)));
+  c.large = max(c.small, (uint32_t)ceilf(share * (few ? 0.75f : memory ? 0.33f : 0.375f)));
   return c;
 }
 // A sequence's units: in front of the border and behind it.
@@ -284,7 +292,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     if (lane < a.c.n_seqs) my_q = pg_seq<kE4m3>(a, lane);
     __syncthreads();  // the barriers are there
     const uint32_t seqs = __popc(__ballot_sync(kFull, my_q.tiles > 0)), end = warp_incl_scan(my_q.tiles, lane);
-    cut = pg_cut(__shfl_sync(kFull, end, 31), seqs, heads, blocks, a.max_splits == 0);
+    cut = pg_cut(__shfl_sync(kFull, end, 31), seqs, heads, blocks, a.max_splits == 0, !kE4m3 && kHeads < 16);
     my_at = end - my_q.tiles;
     const uint32_t c = pg_count(pg_units(cut, my_at, my_q.tiles)), units = warp_incl_scan(c, lane);
     my_begin = units - c;
@@ -309,7 +317,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     used = __reduce_add_sync(kFull, used);
     if (lane == 0) sh.used[warp] = used;
     const uint32_t at0 = block_excl_scan(mine, sh.tmp, &total);
-    cut = pg_cut(total, sh.used[0] + sh.used[1] + sh.used[2] + sh.used[3], heads, blocks, a.max_splits == 0);
+    cut = pg_cut(total, sh.used[0] + sh.used[1] + sh.used[2] + sh.used[3], heads, blocks, a.max_splits == 0, !kE4m3 && kHeads < 16);
     uint32_t at = at0, count = 0, several = 0;
     for (int s = s0; s < s1; ++s) {
       const uint32_t n = tiles_of(s), c = pg_count(pg_units(cut, at, n));
@@ -1170,8 +1178,8 @@ PagedAttendPlan paged_attend_plan(const Paged& c, int hq, int sm_count) {
   p.blocks = (int)std::min<int64_t>(2 * (int64_t)sm_count, tiles * jobs);  // two an SM
   // Units of sequences that have several: with T tiles, `large` is at least
   // 3/8 and `small` 1/16 of T jobs / blocks, so 3/4 T makes two and 1/4 T four
-  // units a block and head, at most one more each for a sequence, of which
-  // fewer than T / small have several.
+  // units a block and head (as 0.66 T and 0.34 T of 0.33 and 0.085 do), at most
+  // one more each for a sequence, of which fewer than T / small have several.
   p.max_splits = tiles <= kPgWhole * (int64_t)c.n_seqs ? 0 : (int)std::min<int64_t>(c.n_seqs, 16 * p.blocks / jobs + 1);
   p.slots = (int)(6 * p.blocks / jobs + 2 * p.max_splits + 4);
   p.part_bytes = (size_t)p.slots * hq * kPartStride * sizeof(float);
