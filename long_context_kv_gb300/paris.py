@@ -701,7 +701,12 @@ class PagedCache:
                               k=strides(k_pages), v=strides(v_pages), status=self._status.data_ptr(),
                               **{name: t.data_ptr() for name, t in given.items()})
         self._ref = ctypes.byref(self._c)
-        self._token_shape, self._ws, self._spaces, self._ready = (n, hkv, HEAD_DIM), {}, {}, {}
+        self._token_shape = (n, hkv, HEAD_DIM)
+        self._begin()
+
+    def _begin(self):
+        """What calls keep for the ones after them: sizes, workspaces and, of attention, a stream's arguments."""
+        self._ws, self._spaces, self._ready = {}, {}, {}
 
     @classmethod
     def create(cls, n_seqs, n_kv_heads, n_pages, max_pages, page_rows=16, n_layers=1, dtype=None, device="cuda"):
@@ -733,20 +738,24 @@ class PagedCache:
         with _torch.cuda.stream(stream):
             return _torch._C._cuda_isCurrentStreamCapturing()
 
-    def _space(self, nbytes, stream, handle, zeros=False):
-        """Address of the workspace of a call, or of its counters: kept for each stream, whose calls take turns with it;
-        during a capture one of the graph's own."""
+    def _space(self, nbytes, stream, handle, counters=0):
+        """The workspace of a call, behind `counters` bytes that are zeros at first (both 16-byte aligned): one tensor,
+        which the caller holds until its call is made, since both are taken from what is free.  It is kept for each
+        stream, whose calls take turns with it; during a capture it is the graph's own."""
         capturing = self._capturing(stream)
-        t = None if capturing else self._spaces.get((handle, zeros))
-        if t is None or t.numel() < nbytes:
-            t = _scratch(nbytes, self.device, stream)
-            if zeros:
-                with _torch.cuda.stream(stream or _torch.cuda.current_stream()):
-                    t.zero_()
+        front = -(-counters // 16) * 16
+        t = None if capturing else self._spaces.get((handle, front))
+        if t is None or t.numel() < front + nbytes:
+            t = _scratch(front + nbytes, self.device, stream)
+            if front and stream is None:
+                t[:front].zero_()
+            elif front:
+                with _torch.cuda.stream(stream):
+                    t[:front].zero_()
             if not capturing:
-                self._spaces[handle, zeros] = t
+                self._spaces[handle, front] = t
                 self._ready.clear()
-        return t.data_ptr()
+        return t, t.data_ptr() + front
 
     def _sizes(self, key, call, count):
         """Workspace bytes of a call, asked once per kind of call."""
@@ -821,11 +830,12 @@ class PagedCache:
         ready = self._ready.get((handle, hq))
         if ready is None or self._capturing(stream):
             n, m = self._ws.get(hq) or self._sizes(hq, lambda a, b: lib.paris_paged_attend_workspace(self._ref, hq, a, b), 2)
-            ready = self._space(n, stream, handle), n, self._space(m, stream, handle, True), m
+            space, ws = self._space(n, stream, handle, m)
+            ready = space, (ws, n, space.data_ptr(), m)
             if not self._capturing(stream):
                 self._ready[handle, hq] = ready
         _check(lib.paris_paged_attend(self._ref, _number(layer, "layer", 32), _flat(q), hq, _number(window, "window"), _flat(out),
-                                      _flat(lse), *ready, handle))
+                                      _flat(lse), *ready[1], handle))
 
     def paris_paged_read(self, k_out, v_out, cu=None, max_rows=None, layer=0, stream=None):
         """A layer's values of the first rows: bfloat16 [rows, Hkv, 128] with int32 starts cu [n_seqs + 1] (max_rows: at
@@ -840,7 +850,7 @@ class PagedCache:
         key = ("fork", n)
         lib = _lib or load()
         sizes = self._ws.get(key) or self._sizes(key, lambda b: lib.paris_paged_fork_workspace(self._ref, n, b), 1)
-        return self._space(sizes[0], stream, handle), sizes[0]
+        return *self._space(sizes[0], stream, handle), sizes[0]
 
     def paris_paged_fork(self, src, dst, rows=None, stream=None):
         """Sequence dst[i] becomes the first rows[i] rows (None: all) of sequence src[i] as it was before the call: full
@@ -850,7 +860,7 @@ class PagedCache:
         r = None if rows is None else self._list(rows, "rows", n)
         _on(self._index, src, dst, rows)
         handle = _raw_stream(self._index, stream)
-        ws, size = self._fork_space(n, stream, handle)
+        space, ws, size = self._fork_space(n, stream, handle)
         _check((_lib or load()).paris_paged_fork(self._ref, a, b, r, n, ws, size, handle))
 
     def paris_paged_free(self, seqs, rows=None, stream=None):
@@ -860,7 +870,7 @@ class PagedCache:
         r = None if rows is None else self._list(rows, "rows", n)
         _on(self._index, seqs, rows)
         handle = _raw_stream(self._index, stream)
-        ws, size = (None, 0) if rows is None else self._fork_space(n, stream, handle)
+        space, ws, size = (None, None, 0) if rows is None else self._fork_space(n, stream, handle)
         _check((_lib or load()).paris_paged_free(self._ref, a, r, n, ws, size, handle))
 
     def paris_paged_compact(self, stream=None):
@@ -869,7 +879,8 @@ class PagedCache:
         lib, handle = _lib or load(), _raw_stream(self._index, stream)
         sizes = self._ws.get("compact") or self._sizes("compact",
                                                        lambda b: lib.paris_paged_compact_workspace(self._ref, b), 1)
-        _check(lib.paris_paged_compact(self._ref, self._space(sizes[0], stream, handle), sizes[0], handle))
+        space, ws = self._space(sizes[0], stream, handle)
+        _check(lib.paris_paged_compact(self._ref, ws, sizes[0], handle))
 
     def paris_paged_check(self):
         """Synchronise; raise if a call found no room or a sequence out of range."""

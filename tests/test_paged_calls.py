@@ -1,0 +1,144 @@
+"""How the binding's paged calls hand out what a call needs, without a GPU: memory that lasts as long as its address is
+used, the same on threads, limits and devices."""
+import contextlib
+import ctypes
+import time
+
+import pytest
+import torch
+
+from long_context_kv_gb300 import build as B
+from long_context_kv_gb300 import paris as P
+
+BF = torch.bfloat16
+WORKSPACE, COUNTERS = 5000, 16
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    return P.load()
+
+
+class Heap:
+    """Memory whose lowest free bytes go first, and that takes back what is dropped: an allocator with small blocks."""
+
+    def __init__(self):
+        self.held, self.made, self.written = {}, 0, []
+
+    def take(self, n):
+        n, at = max(-(-n // 512) * 512, 512), 1 << 20
+        for a, b in sorted(self.held.values()):
+            if at + n <= a:
+                break
+            at = b
+        self.made += 1
+        self.held[self.made] = (at, at + n)
+        return Block(self, self.made, at, n)
+
+
+class Block:
+    def __init__(self, heap, number, at, n):
+        self.heap, self.number, self.at, self.n = heap, number, at, n
+
+    def __del__(self):
+        if self.number is not None:
+            del self.heap.held[self.number]
+
+    def data_ptr(self):
+        return self.at
+
+    def numel(self):
+        return self.n
+
+    def __getitem__(self, s):
+        a, b, _ = s.indices(self.n)
+        part = Block(self.heap, None, self.at + a, b - a)
+        part.whole = self  # a view keeps its memory
+        return part
+
+    def zero_(self):
+        self.heap.written.append((self.at, self.at + self.n))
+        return self
+
+
+class Calls:
+    """In place of the library: what the attention is handed, and how many calls of it are under way."""
+
+    def __init__(self, heap, pause=0.0):
+        self.heap, self.pause, self.now, self.most, self.seen = heap, pause, 0, 0, []
+
+    def paris_paged_attend_workspace(self, cache, hq, n, m):
+        time.sleep(self.pause)
+        ctypes.cast(n, ctypes.POINTER(ctypes.c_size_t))[0] = WORKSPACE * hq
+        ctypes.cast(m, ctypes.POINTER(ctypes.c_size_t))[0] = COUNTERS
+        return P.PARIS_OK
+
+    def paris_paged_attend(self, cache, layer, q, hq, window, out, lse, ws, n, counters, m, stream):
+        self.now += 1
+        self.most = max(self.most, self.now)
+        time.sleep(self.pause)
+        for a, size in ((ws, n), (counters, m)):
+            assert a % 16 == 0 and any(x <= a and a + size <= y for x, y in self.heap.held.values()), "memory given back"
+        self.seen.append(((ws, ws + n), (counters, counters + m)))
+        self.now -= 1
+        return P.PARIS_OK
+
+
+@pytest.fixture
+def cache(monkeypatch):
+    c = object.__new__(P.PagedCache)
+    c.n_seqs, c.n_kv_heads, c._index, c.device, c._ref = 2, 2, 0, "cuda:0", None
+    c._begin()
+    heap = Heap()
+    c.heap, c.calls, c.capturing = heap, Calls(heap), False
+
+    def scratch(n, device, stream):
+        time.sleep(c.calls.pause)
+        return heap.take(n)
+
+    monkeypatch.setattr(P, "_torch", torch)
+    monkeypatch.setattr(torch.cuda, "stream", lambda stream: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: None)
+    monkeypatch.setattr(P, "_scratch", scratch)
+    monkeypatch.setattr(P, "_on", lambda *a: None)
+    monkeypatch.setattr(P, "_raw_stream", lambda index, stream: 7)
+    monkeypatch.setattr(P.PagedCache, "_capturing", staticmethod(lambda stream: c.capturing))
+    monkeypatch.setattr(P, "_lib", c.calls)
+    return c
+
+
+def attend(c, hq=4):
+    q = torch.zeros(2, hq, 128, dtype=BF)
+    c.paris_paged_attend(q, q)
+
+
+def apart(x, y):
+    return x[1] <= y[0] or y[1] <= x[0]
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+def test_workspace_and_counters_do_not_meet(cache, capturing):
+    cache.capturing = capturing
+    for hq in (4, 8, 4, 2):
+        before = len(cache.heap.written)
+        attend(cache, hq)
+        ws, counters = cache.calls.seen[-1]
+        assert apart(ws, counters)
+        assert ws[1] - ws[0] == WORKSPACE * hq
+        zeroed = cache.heap.written[before:]
+        assert all(apart(z, ws) for z in zeroed)  # nothing that a call under way may use
+        if capturing:
+            assert counters in zeroed  # a graph's counters are its own, zero before each replay's first use
+    if capturing:
+        assert not cache.heap.held  # nothing of a graph is kept, and outside of one
+        cache.capturing = False
+        attend(cache)
+        assert cache.calls.seen[-1][1] in cache.heap.written
+
+
+def test_counters_are_zeros_once_and_stay_the_stream_s_own(cache):
+    for hq in (2, 4, 2, 4):
+        attend(cache, hq)
+    used = [counters for _, counters in cache.calls.seen]
+    assert cache.heap.written == list(dict.fromkeys(used)) and used[1:] == [used[1]] * 3
