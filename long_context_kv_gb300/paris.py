@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import threading
 
 import numpy as np
 
@@ -655,8 +656,9 @@ class PagedCache:
     k_pages, v_pages bfloat16 or float8_e4m3fn [layers, n_pages, Hkv, page_rows, 128], in any order of the first four
     dimensions in memory; with float8_e4m3fn k_scales, v_scales uint8 [layers, n_pages, Hkv, page_rows]; table int32
     [sequences, max_pages]; lens and starts int32 [sequences]; refs int32 [n_pages]; free_bits int32
-    [(n_pages + 31) // 32]; n_used int32 [1].  As with any tensor, a cache that another stream than its own still uses is
-    dropped only after `record_stream`.
+    [(n_pages + 31) // 32]; n_used int32 [1].  paris_paged_attend and paris_paged_read may be called from several threads
+    at once; calls that change the cache are ordered by the caller against all others.  As with any tensor, a cache that
+    another stream than its own still uses is dropped only after `record_stream`.
     """
 
     def __init__(self, k_pages, v_pages, table, lens, starts, refs, free_bits, n_used, k_scales=None, v_scales=None):
@@ -706,7 +708,7 @@ class PagedCache:
 
     def _begin(self):
         """What calls keep for the ones after them: sizes, workspaces and, of attention, a stream's arguments."""
-        self._ws, self._spaces, self._ready = {}, {}, {}
+        self._ws, self._spaces, self._ready, self._lock = {}, {}, {}, threading.Lock()
 
     @classmethod
     def create(cls, n_seqs, n_kv_heads, n_pages, max_pages, page_rows=16, n_layers=1, dtype=None, device="cuda"):
@@ -826,16 +828,17 @@ class PagedCache:
             _shaped(lse, "lse", shape[:2], _torch.float32)
         _on(self._index, q, out, lse)
         lib, hq, handle = _lib or load(), shape[1], _raw_stream(self._index, stream)
-        # both workspaces of a stream that has been here before (never one that is being captured)
-        ready = self._ready.get((handle, hq))
-        if ready is None or self._capturing(stream):
-            n, m = self._ws.get(hq) or self._sizes(hq, lambda a, b: lib.paris_paged_attend_workspace(self._ref, hq, a, b), 2)
-            space, ws = self._space(n, stream, handle, m)
-            ready = space, (ws, n, space.data_ptr(), m)
-            if not self._capturing(stream):
-                self._ready[handle, hq] = ready
-        _check(lib.paris_paged_attend(self._ref, _number(layer, "layer", 32), _flat(q), hq, _number(window, "window"), _flat(out),
-                                      _flat(lse), *ready[1], handle))
+        args = _number(layer, "layer", 32), _flat(q), hq, _number(window, "window"), _flat(out), _flat(lse)
+        with self._lock:  # a call is several launches with its stream's workspace: threads take turns
+            # both workspaces of a stream that has been here before (never one that is being captured)
+            ready = self._ready.get((handle, hq))
+            if ready is None or self._capturing(stream):
+                n, m = self._ws.get(hq) or self._sizes(hq, lambda a, b: lib.paris_paged_attend_workspace(self._ref, hq, a, b), 2)
+                space, ws = self._space(n, stream, handle, m)
+                ready = space, (ws, n, space.data_ptr(), m)
+                if not self._capturing(stream):
+                    self._ready[handle, hq] = ready
+            _check(lib.paris_paged_attend(self._ref, *args, *ready[1], handle))
 
     def paris_paged_read(self, k_out, v_out, cu=None, max_rows=None, layer=0, stream=None):
         """A layer's values of the first rows: bfloat16 [rows, Hkv, 128] with int32 starts cu [n_seqs + 1] (max_rows: at

@@ -1,6 +1,7 @@
 """The paged cache's calls in the ways in which programs make them: captured, on threads, with limits, with arrays that
 do not agree, with values that are not finite.  Against the direct call, lists, or the definition in 64 bits."""
 import math
+import threading
 
 import pytest
 import torch
@@ -61,4 +62,35 @@ def test_captured_attention_is_the_direct_call_s(hq, hkv, lens, dtype):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(outs, want[0]) and torch.equal(lses, want[1])
+    c.paris_paged_check()
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+def test_threads_that_attend_on_one_stream(dtype):
+    c = filled([5000, 1, 900], 2, dtype=dtype, seed=3)
+    q = (2 * rand(4, 3, 8, R.D, seed=4)).to(BF)
+    want, outs = torch.zeros_like(q), torch.zeros(4, 50, 3, 8, R.D, dtype=BF, device="cuda")
+    for i in range(4):
+        c.paris_paged_attend(q[i], want[i])
+    c = P.PagedCache(c.k_pages, c.v_pages, c.table, c.lens, c.starts, c.refs, c.free_bits, c.n_used,
+                     *((c.k_scales, c.v_scales) if dtype is E4 else ()))  # without what calls keep
+    errors, start = [], threading.Barrier(4)
+
+    def work(i):
+        try:
+            start.wait()
+            for n in range(50):
+                c.paris_paged_attend(q[i], outs[i, n])
+        except BaseException as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for i in range(4):
+        assert torch.all(outs[i] == want[i])
     c.paris_paged_check()

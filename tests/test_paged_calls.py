@@ -2,6 +2,7 @@
 used, the same on threads, limits and devices."""
 import contextlib
 import ctypes
+import threading
 import time
 
 import pytest
@@ -142,3 +143,34 @@ def test_counters_are_zeros_once_and_stay_the_stream_s_own(cache):
         attend(cache, hq)
     used = [counters for _, counters in cache.calls.seen]
     assert cache.heap.written == list(dict.fromkeys(used)) and used[1:] == [used[1]] * 3
+
+
+def test_two_threads_take_turns_on_a_stream(cache):
+    """A call is two launches with one workspace: they stay together, and first calls make one workspace."""
+    cache.calls.pause, errors = 0.01, []
+    start = threading.Barrier(4)
+
+    def work():
+        try:
+            start.wait()
+            for _ in range(5):
+                attend(cache)
+        except BaseException as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    assert len(cache.calls.seen) == 20 and cache.calls.most == 1 and cache.heap.made == 1
+
+
+def test_a_call_that_fails_leaves_the_others_their_turn(cache):
+    q = torch.zeros(2, 4, 128, dtype=BF)
+    for kw in (dict(layer=1 << 40), dict(window=1 << 70)):
+        with pytest.raises(ValueError, match="out of range"):
+            cache.paris_paged_attend(q, q, **kw)
+    attend(cache)
+    assert len(cache.calls.seen) == 1
