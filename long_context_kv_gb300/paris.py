@@ -815,6 +815,15 @@ class PagedCache:
         _check((_lib or load()).paris_paged_store(self._ref, _number(layer, "layer", 32), _raw(k), _raw(v), _code(k), *strides,
                                                   1, None, 1, _raw_stream(self._index, stream)))
 
+    def _attend_space(self, lib, hq, stream, handle):
+        """The tensor of both workspaces of an attention call, and its arguments."""
+        n, m = self._ws.get(hq) or self._sizes(hq, lambda a, b: lib.paris_paged_attend_workspace(self._ref, hq, a, b), 2)
+        space, ws = self._space(n, stream, handle, m)
+        ready = ws, n, space.data_ptr(), m
+        if not self._capturing(stream):
+            self._ready[handle, hq] = ready
+        return space, ready
+
     def paris_paged_attend(self, q, out, window=0, lse=None, layer=0, stream=None):
         """out = softmax(K q / sqrt(d)) V over a layer's rows in use, or the last `window` of them: q, out bfloat16
         [n_seqs, Hq, 128]; lse: float32 [n_seqs, Hq], or None."""
@@ -828,17 +837,13 @@ class PagedCache:
             _shaped(lse, "lse", shape[:2], _torch.float32)
         _on(self._index, q, out, lse)
         lib, hq, handle = _lib or load(), shape[1], _raw_stream(self._index, stream)
-        args = _number(layer, "layer", 32), _flat(q), hq, _number(window, "window"), _flat(out), _flat(lse)
         with self._lock:  # a call is several launches with its stream's workspace: threads take turns
-            # both workspaces of a stream that has been here before (never one that is being captured)
+            # those of a stream that has been here before (never one that is being captured)
             ready = self._ready.get((handle, hq))
             if ready is None or self._capturing(stream):
-                n, m = self._ws.get(hq) or self._sizes(hq, lambda a, b: lib.paris_paged_attend_workspace(self._ref, hq, a, b), 2)
-                space, ws = self._space(n, stream, handle, m)
-                ready = space, (ws, n, space.data_ptr(), m)
-                if not self._capturing(stream):
-                    self._ready[handle, hq] = ready
-            _check(lib.paris_paged_attend(self._ref, *args, *ready[1], handle))
+                space, ready = self._attend_space(lib, hq, stream, handle)
+            _check(lib.paris_paged_attend(self._ref, _number(layer, "layer", 32), _flat(q), hq, _number(window, "window"),
+                                          _flat(out), _flat(lse), *ready, handle))
 
     def paris_paged_read(self, k_out, v_out, cu=None, max_rows=None, layer=0, stream=None):
         """A layer's values of the first rows: bfloat16 [rows, Hkv, 128] with int32 starts cu [n_seqs + 1] (max_rows: at
