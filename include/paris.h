@@ -505,7 +505,9 @@ paris_status paris_kv4_check(const paris_kv4* c);
  * elements, below 2^38; rows of 128 are contiguous.  max_pages * page_rows
  * is at most 2^30, and n_seqs times that at most 2^37.  Lengths outside
  * [0, max_pages * page_rows] count as the nearest of the two, and so do
- * entries of the table outside [0, n_pages).                                  */
+ * entries of the table outside [0, n_pages).  Pages are taken as free_bits
+ * has them: where n_used says that more are free, those are not there, and
+ * bits past n_pages are no pages.                                             */
 typedef struct {
   int64_t layer, page, head, row;
 } paris_page_strides;

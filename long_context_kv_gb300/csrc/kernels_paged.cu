@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_grow(Paged c, const int3
   if (taken == 0) return;
   __syncthreads();
   int s = -1;
-  take_free(c, taken, bits, tmp, [&](uint32_t r, int page) {
+  const uint32_t found = take_free(c, taken, bits, tmp, [&](uint32_t r, int page) {
     if (s < 0) {  // the last sequence that begins at or before r, of those with a page
       int lo = 0, hi = c.n_seqs - 1;
       while (lo < hi) {
@@ -69,7 +69,14 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_grow(Paged c, const int3
     c.table[(int64_t)s * c.width + pages[s] + (r - first[s])] = page;
     c.refs[page] = 1;
   });
-  if (tid == 0) c.n_used[0] = c.n_pages - (int)(n_free - taken);
+  if (found < taken) {  // n_used and free_bits do not agree: rows without a page are not there
+    for (int i = tid; i < c.n_seqs; i += kPlanThreads) {
+      const int most = (int)min64((int64_t)(pages[i] + (int)(min(first[i + 1], found) - min(first[i], found))) << c.shift, cap);
+      if (c.lens[i] > most) c.lens[i] = most;
+    }
+    if (tid == 0) atomicOr(c.status, kStatusNoRoom);
+  }
+  if (tid == 0) c.n_used[0] = c.n_pages - (int)(n_free - found);
 }
 
 constexpr int kRowThreads = 256;

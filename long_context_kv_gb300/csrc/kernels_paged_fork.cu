@@ -194,13 +194,25 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_fork_plan(ForkArgs a) {
   }
   if (wrong) atomicOr(a.c.status, kStatusWrongSeq);
   if (short_of) atomicOr(a.c.status, kStatusNoRoom);
-  const uint32_t taken = min(copies, n_free);
-  if (taken != 0) {
+  const uint32_t wanted = min(copies, n_free);
+  uint32_t taken = 0;
+  if (wanted != 0) {
     __syncthreads();
-    take_free(a.c, taken, bits, tmp, [&](uint32_t r, int page) {
+    taken = take_free(a.c, wanted, bits, tmp, [&](uint32_t r, int page) {
       a.plan[owner[r]].last = page;
       a.c.refs[page] = 1;
     });
+  }
+  if (taken < wanted) {  // n_used and free_bits do not agree: the entries that got no page keep their full ones
+#pragma unroll
+    for (int u = 0; u < kMaxPagedSeqs / kPlanThreads; ++u) {
+      const int i = u * kPlanThreads + tid;
+      if (i >= a.n) break;
+      if (takes[u] < (int)taken) continue;
+      a.plan[i].rows = 0;
+      a.c.lens[a.plan[i].dst] = a.c.starts[a.plan[i].dst] = a.plan[i].full << a.c.shift;
+    }
+    if (tid == 0) atomicOr(a.c.status, kStatusNoRoom);
   }
   if constexpr (!kAll) {
     if (tid == 0 && taken != 0) a.c.n_used[0] = max(a.c.n_used[0], 0) + (int)taken;
@@ -244,7 +256,7 @@ __global__ void __launch_bounds__(kForkThreads) k_paged_fork_apply(ForkArgs a, i
   }
   const int x = blockIdx.x - a.n * segs, il = x / per, i = il / a.c.layers;
   const ForkEntry e = a.plan[i];
-  if (e.dst < 0 || e.rows == 0 || e.last < 0) return;
+  if (e.dst < 0 || e.rows == 0) return;
   copy_rows(a, e, il - i * a.c.layers, (x - il * per) * (kForkThreads / 16) + (tid >> 4), per * (kForkThreads / 16));
 }
 

@@ -94,3 +94,67 @@ def test_threads_that_attend_on_one_stream(dtype):
     for i in range(4):
         assert torch.all(outs[i] == want[i])
     c.paris_paged_check()
+
+
+def state(c):
+    return {n: getattr(c, n).tolist() for n in ("table", "lens", "starts", "refs", "n_used")}
+
+
+# The pages that are free (by free_bits), and what n_used claims: as many as are wanted.
+@pytest.mark.parametrize("free", [0, 1, 2])
+@pytest.mark.parametrize("stray", [False, True])
+@pytest.mark.parametrize("dtype", [BF, E4])
+def test_a_fork_with_fewer_free_pages_than_n_used_says(dtype, stray, free):
+    """Entries that get no page keep their full ones, in the small fork and the large one, and no row is written
+    outside of the pages that were found."""
+    made = []
+    for max_pages in (4, 4096):  # one block; a kernel a step
+        lens = [20, 33, 5, 0, 0]
+        c = filled(lens, 2, dtype=dtype, seed=5, spare=free, max_pages=max_pages)
+        guard = [torch.cat([R.raw(t)[:, :1], R.raw(t), R.raw(t)[:, :1]], 1).fill_(77) for t in (c.k_pages, c.v_pages)]
+        pools = [g[:, 1:-1].view(t.dtype) for g, t in zip(guard, (c.k_pages, c.v_pages))]
+        for pool, t in zip(pools, (c.k_pages, c.v_pages)):
+            R.raw(pool).copy_(R.raw(t))
+        if stray:
+            c.free_bits[-1] |= -1 << (c.n_pages % 32)
+        n_used = int(c.n_used)
+        c = P.PagedCache(*pools, c.table, c.lens, c.starts, c.refs, c.free_bits, c.n_used - 4,
+                         *((c.k_scales, c.v_scales) if dtype is E4 else ()))
+        bytes_before = [g.clone() for g in guard]
+        c.paris_paged_fork(i32([0, 1, 2]), i32([3, 4, 0]))
+        got = [3, 4, 0][:free]
+        with pytest.raises(P.ParisError, match="no room"):
+            c.paris_paged_check()
+        want = {3: 20, 4: 33, 0: 5}
+        assert c.lens.tolist() == [want[s] if s in got else want[s] // 16 * 16 if s in want else lens[s] for s in range(5)]
+        assert c.starts.tolist() == [c.lens[s].item() if s in want else 0 for s in range(5)]
+        # what the first sequence held of its own is given back
+        assert int(c.n_used) == n_used - 4 + len(got) - 1
+        held = [p for s, n in enumerate(c.lens.tolist()) for p in c.table[s, :-(-n // 16)].tolist()]
+        assert c.refs.tolist() == [held.count(p) for p in range(c.n_pages)]
+        new = [int(c.table[s, want[s] // 16]) for s in got]
+        for g, b in zip(guard, bytes_before):
+            same = torch.ones(g.shape[1], dtype=torch.bool, device="cuda")
+            same[[p + 1 for p in new]] = False
+            assert torch.equal(g[:, same], b[:, same])
+        made.append({n: [x[:4] for x in v] if n == "table" else v for n, v in state(c).items()})
+    assert made[0] == made[1]
+
+
+def test_growing_with_fewer_free_pages_than_n_used_says():
+    for stray in (False, True):
+        c = filled([20, 33, 5], 1, seed=6, spare=3, max_pages=40)
+        if stray:
+            c.free_bits[-1] |= -1 << (c.n_pages % 32)
+        c.n_used -= 5
+        c.paris_paged_grow(i32([13, 100, 1]))  # one page, six pages, none
+        with pytest.raises(P.ParisError, match="no room"):
+            c.paris_paged_check()
+        assert c.lens.tolist() == [33, 80, 6] and c.starts.tolist() == [20, 33, 5]
+        assert int(c.n_used) == c.n_pages - 5 and not torch.any(pages_free(c))
+        assert sorted(p for s, n in enumerate((3, 5, 1)) for p in c.table[s, :n].tolist()) == list(range(c.n_pages))
+
+
+def pages_free(c):
+    at = torch.arange(c.n_pages, device="cuda")
+    return c.free_bits[at // 32] >> at % 32 & 1
