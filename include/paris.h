@@ -541,7 +541,7 @@ paris_status paris_paged_grow(const paris_paged* c, const int32_t* tokens, void*
  * k, v: device, PARIS_F32 or PARIS_BF16, rows packed by cu (device,
  * n_seqs + 1 starts within [0, rows], as in paris_prompt) or, with cu = NULL,
  * `rows` tokens for every sequence along the seq stride; max_new: at least the
- * most tokens of a sequence (tokens past it are left out).                    */
+ * most tokens of a sequence (in both forms tokens past it are left out).      */
 paris_status paris_paged_store(const paris_paged* c, int layer, const void* k, const void* v, paris_dtype dtype,
                                const paris_strides* ks, const paris_strides* vs, int64_t rows, const int32_t* cu,
                                int64_t max_new, void* stream);
@@ -570,7 +570,8 @@ paris_status paris_paged_attend(const paris_paged* c, int layer, const void* q, 
 /* One layer's values of the first rows of every sequence, as bf16: k_out and
  * v_out have their sequences packed by cu, or along the seq stride, as k and v
  * of paris_paged_store have.  Rows past a sequence's length are left as they
- * were; max_rows: at least the most rows asked of a sequence.                 */
+ * were; max_rows: at least the most rows asked of a sequence (in both forms
+ * rows past it are left as they were, too).                                   */
 paris_status paris_paged_read(const paris_paged* c, int layer, void* k_out, void* v_out, const paris_strides* ks,
                               const paris_strides* vs, int64_t rows, const int32_t* cu, int64_t max_rows, void* stream);
 

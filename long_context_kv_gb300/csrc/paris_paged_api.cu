@@ -79,7 +79,7 @@ paris_status take_rows(const paris_paged* c, int layer, const void* k, const voi
   a->layer = layer;
   a->dtype = dtype;
   a->rows = rows;
-  a->max_rows = cu ? std::min(max_rows, rows) : rows;
+  a->max_rows = std::min(max_rows, rows);
   a->cu = cu;
   if (a->max_rows == 0) return PARIS_OK;
   if (!k || !v) return fail(PARIS_EINVAL, "k and v must not be NULL");

@@ -158,3 +158,31 @@ def test_growing_with_fewer_free_pages_than_n_used_says():
 def pages_free(c):
     at = torch.arange(c.n_pages, device="cuda")
     return c.free_bits[at // 32] >> at % 32 & 1
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+@pytest.mark.parametrize("limit", [0, 1, 7, 16, 37, 1000, 1 << 40])
+def test_limits_hold_for_batches_as_for_packed_rows(limit, dtype):
+    T, grown = 37, [37, 5, 0]
+    k, v = (rand(3, 2, T, R.D, seed=7 + i).to(BF) for i in range(2))
+    fresh = lambda: P.PagedCache.create(3, 2, 12, 4, dtype=dtype)  # noqa: E731
+    c, want = fresh(), fresh()
+    for x in (c, want):
+        x.paris_paged_grow(i32(grown))
+    c.paris_paged_store(k, v, max_new=limit)
+    rows = [x.transpose(1, 2).reshape(3 * T, 2, R.D) for x in (k, v)]
+    want.paris_paged_store(*rows, cu=i32([0, T, 2 * T, 3 * T]), max_new=limit)
+    for name in ("k_pages", "v_pages"):
+        assert torch.equal(R.raw(getattr(c, name)), R.raw(getattr(want, name)))
+    for s, n in enumerate(grown):
+        assert torch.all(R.rows_of(c, "k", 0, s)[:, min(n, limit):] == 0)
+        if dtype is BF:
+            assert torch.equal(R.rows_of(c, "k", 0, s)[:, :min(n, limit)], k[s, :, :min(n, limit)].double())
+    c.paris_paged_store(k, v)
+    out = torch.full((2, 3, 2, T, R.D), 6.0, dtype=BF, device="cuda")
+    c.paris_paged_read(*out, max_rows=limit)
+    for i, name in enumerate(("k", "v")):
+        for s, n in enumerate(grown):
+            n = min(n, limit)
+            assert torch.all(out[i, s, :, n:] == 6.0)
+            assert torch.equal(out[i, s, :, :n].double(), R.rows_of(c, name, 0, s)[:, :n])

@@ -174,3 +174,17 @@ def test_a_call_that_fails_leaves_the_others_their_turn(cache):
             cache.paris_paged_attend(q, q, **kw)
     attend(cache)
     assert len(cache.calls.seen) == 1
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_a_limit_of_no_rows_leaves_nothing_to_do(lib, packed):
+    """Also without starts: nothing is launched, nothing refused."""
+    arrays = ("k_pages", "v_pages", "k_scales", "v_scales", "table", "lens", "starts", "refs", "free_bits", "n_used", "status")
+    st = P.paris_page_strides(1 << 20, 4096, 2048, 128)
+    c = ctypes.byref(P.paris_paged(n_seqs=2, n_layers=2, n_kv_heads=2, head_dim=128, page_rows=16, dtype=P.PARIS_BF16, n_pages=40,
+                                   max_pages=8, k=st, v=st, **{n: 4096 for n in arrays}))
+    s, cu = ctypes.byref(P.paris_strides(256, 128, 1024)), ctypes.c_void_p(4096) if packed else None
+    assert lib.paris_paged_store(c, 0, None, None, P.PARIS_BF16, s, s, 4, cu, 0, None) == P.PARIS_OK
+    assert lib.paris_paged_read(c, 0, None, None, s, s, 4, cu, 0, None) == P.PARIS_OK
+    assert lib.paris_paged_store(c, 0, None, None, P.PARIS_BF16, s, s, 4, cu, 1, None) == P.PARIS_EINVAL
+    assert lib.paris_paged_read(c, 0, None, None, s, s, 4, cu, 1, None) == P.PARIS_EINVAL
