@@ -891,5 +891,6 @@ class PagedCache:
         _check(lib.paris_paged_compact(self._ref, ws, sizes[0], handle))
 
     def paris_paged_check(self):
-        """Synchronise; raise if a call found no room or a sequence out of range."""
+        """Synchronise; raise if a call found no room or a sequence out of range, or if attention gave up a wait."""
+        _on(self._index)  # the library waits for the current device, and asks that one
         _check(load().paris_paged_check(self._ref))

@@ -188,3 +188,24 @@ def test_a_limit_of_no_rows_leaves_nothing_to_do(lib, packed):
     assert lib.paris_paged_read(c, 0, None, None, s, s, 4, cu, 0, None) == P.PARIS_OK
     assert lib.paris_paged_store(c, 0, None, None, P.PARIS_BF16, s, s, 4, cu, 1, None) == P.PARIS_EINVAL
     assert lib.paris_paged_read(c, 0, None, None, s, s, 4, cu, 1, None) == P.PARIS_EINVAL
+
+
+class OtherDevice:
+    """torch with cuda:0 as the current device."""
+
+    class _C:
+        _cuda_getDevice = staticmethod(lambda: 0)
+
+
+def test_a_check_is_made_on_the_cache_s_device(monkeypatch):
+    asked = []
+    monkeypatch.setattr(P, "_torch", OtherDevice)
+    monkeypatch.setattr(P, "load", lambda: type("Lib", (), {"paris_paged_check": lambda self, c: asked.append(c) or P.PARIS_OK})())
+    c = object.__new__(P.PagedCache)
+    c._index, c._ref = 1, "the cache"
+    with pytest.raises(ValueError, match="cuda:1, the current device is cuda:0"):
+        c.paris_paged_check()
+    assert not asked
+    c._index = 0
+    c.paris_paged_check()
+    assert asked == ["the cache"]
