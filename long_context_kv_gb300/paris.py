@@ -646,6 +646,7 @@ class KV4Cache:
 
     def paris_kv4_check(self):
         """Synchronise; raise if a store found no room."""
+        _on(self._index)  # the library waits for the current device
         _check(load().paris_kv4_check(self._ref))
 
 

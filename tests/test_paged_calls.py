@@ -197,15 +197,16 @@ class OtherDevice:
         _cuda_getDevice = staticmethod(lambda: 0)
 
 
-def test_a_check_is_made_on_the_cache_s_device(monkeypatch):
+@pytest.mark.parametrize("cls,call", [(P.PagedCache, "paris_paged_check"), (P.KV4Cache, "paris_kv4_check")])
+def test_a_check_is_made_on_the_cache_s_device(monkeypatch, cls, call):
     asked = []
     monkeypatch.setattr(P, "_torch", OtherDevice)
-    monkeypatch.setattr(P, "load", lambda: type("Lib", (), {"paris_paged_check": lambda self, c: asked.append(c) or P.PARIS_OK})())
-    c = object.__new__(P.PagedCache)
+    monkeypatch.setattr(P, "load", lambda: type("Lib", (), {call: lambda self, c: asked.append(c) or P.PARIS_OK})())
+    c = object.__new__(cls)
     c._index, c._ref = 1, "the cache"
     with pytest.raises(ValueError, match="cuda:1, the current device is cuda:0"):
-        c.paris_paged_check()
+        getattr(c, call)()
     assert not asked
     c._index = 0
-    c.paris_paged_check()
+    getattr(c, call)()
     assert asked == ["the cache"]
