@@ -306,8 +306,8 @@ struct RowGrid {
   uint32_t hkv_inv;  // the division by hkv is a product: exact below 2^32 / hkv items
   dim3 grid;
   bool fits;
-  explicit RowGrid(const PagedRows& a) {
-    while (tokens > 1 && a.c.n_seqs * ((a.max_rows + tokens - 1) / tokens) < 2 * 152) tokens /= 2;
+  RowGrid(const PagedRows& a, int sm_count) {
+    while (tokens > 1 && a.c.n_seqs * ((a.max_rows + tokens - 1) / tokens) < 2 * sm_count) tokens /= 2;
     while (tokens > 1 && (int64_t)tokens * a.c.hkv * a.c.hkv >= (int64_t)1 << 32) tokens /= 2;
     const int64_t n = (a.max_rows + tokens - 1) / tokens;
     fits = n * a.c.n_seqs <= 0x7fffffff;
@@ -323,8 +323,8 @@ cudaError_t launch_paged_grow(const Paged& c, const int32_t* tokens, cudaStream_
   return launch_pdl(k_paged_grow, dim3(1), dim3(kPlanThreads), 0, st, c, tokens);
 }
 
-cudaError_t launch_paged_store(const PagedRows& a, cudaStream_t st) {
-  const RowGrid g(a);
+cudaError_t launch_paged_store(const PagedRows& a, int sm_count, cudaStream_t st) {
+  const RowGrid g(a, sm_count);
   if (!g.fits) return cudaErrorInvalidValue;
   const dim3 block(kRowThreads);
   if (a.dtype == 1)
@@ -334,8 +334,8 @@ cudaError_t launch_paged_store(const PagedRows& a, cudaStream_t st) {
                   : launch_pdl(k_paged_store<true, false>, g.grid, block, 0, st, a, g.nblk, g.tokens, g.hkv_inv);
 }
 
-cudaError_t launch_paged_read(const PagedRows& a, cudaStream_t st) {
-  const RowGrid g(a);
+cudaError_t launch_paged_read(const PagedRows& a, int sm_count, cudaStream_t st) {
+  const RowGrid g(a, sm_count);
   if (!g.fits) return cudaErrorInvalidValue;
   const dim3 block(kRowThreads);
   return a.c.e4m3 ? launch_pdl(k_paged_read<true>, g.grid, block, 0, st, a, g.nblk, g.tokens, g.hkv_inv)

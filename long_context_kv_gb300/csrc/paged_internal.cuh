@@ -65,8 +65,8 @@ struct PagedRows {
   int64_t rows, max_rows;
   const int32_t* cu;
 };
-cudaError_t launch_paged_store(const PagedRows& a, cudaStream_t st);
-cudaError_t launch_paged_read(const PagedRows& a, cudaStream_t st);
+cudaError_t launch_paged_store(const PagedRows& a, int sm_count, cudaStream_t st);
+cudaError_t launch_paged_read(const PagedRows& a, int sm_count, cudaStream_t st);
 
 // An entry of a fork: what the planning kernel tells the applying one.
 struct ForkEntry {

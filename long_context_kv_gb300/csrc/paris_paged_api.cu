@@ -141,7 +141,7 @@ paris_status paris_paged_store(const paris_paged* c, int layer, const void* k, c
   PagedRows a{};
   const paris_status st = take_rows(c, layer, k, v, dtype, ks, vs, rows, cu, max_new, &a);
   if (st != PARIS_OK || a.max_rows == 0) return st;
-  return launched(launch_paged_store(a, static_cast<cudaStream_t>(stream)), "paris_paged_store");
+  return launched(launch_paged_store(a, sm_count(), static_cast<cudaStream_t>(stream)), "paris_paged_store");
 }
 
 paris_status paris_paged_read(const paris_paged* c, int layer, void* k_out, void* v_out, const paris_strides* ks,
@@ -149,7 +149,7 @@ paris_status paris_paged_read(const paris_paged* c, int layer, void* k_out, void
   PagedRows a{};
   const paris_status st = take_rows(c, layer, k_out, v_out, PARIS_BF16, ks, vs, rows, cu, max_rows, &a);
   if (st != PARIS_OK || a.max_rows == 0) return st;
-  return launched(launch_paged_read(a, static_cast<cudaStream_t>(stream)), "paris_paged_read");
+  return launched(launch_paged_read(a, sm_count(), static_cast<cudaStream_t>(stream)), "paris_paged_read");
 }
 
 paris_status paris_paged_attend_workspace(const paris_paged* c, int n_q_heads, size_t* bytes, size_t* counter_bytes) {
