@@ -186,3 +186,32 @@ def test_limits_hold_for_batches_as_for_packed_rows(limit, dtype):
             n = min(n, limit)
             assert torch.all(out[i, s, :, n:] == 6.0)
             assert torch.equal(out[i, s, :, :n].double(), R.rows_of(c, name, 0, s)[:, :n])
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+def test_packed_rows_of_many_sequences_without_a_better_limit(dtype):
+    """The most rows that a call can name, for 4096 sequences: what it does goes by the starts."""
+    n, hkv, page = 4096, 2, 256
+    c = P.PagedCache.create(n, hkv, 200, 1 << 15, page_rows=page, dtype=dtype)
+    lens = [0] * n
+    lens[0], lens[70], lens[4000], lens[4095] = 20000, 3, 9000, 8193
+    c.paris_paged_grow(i32(lens))
+    total = sum(lens)
+    k, v = (rand(total, hkv, R.D, seed=8 + i).to(BF) for i in range(2))
+    cu, st, ref = K4.starts(lens), P._STRIDES.pack(hkv * R.D, R.D, 0), c._ref
+    out = torch.full((2, total, hkv, R.D), 6.0, dtype=BF, device="cuda")
+    most, lib, stream = (1 << 31) - 1, P.load(), torch.cuda.current_stream().cuda_stream
+    for limit in (most, 1 << 40):
+        P._check(lib.paris_paged_store(ref, 0, k.data_ptr(), v.data_ptr(), P.PARIS_BF16, st, st, most, cu.data_ptr(), limit, stream))
+        P._check(lib.paris_paged_read(ref, 0, out[0].data_ptr(), out[1].data_ptr(), st, st, most, cu.data_ptr(), limit, stream))
+    c.paris_paged_check()
+    at = 0
+    for s in (0, 70, 4000, 4095):
+        for i, (name, x) in enumerate((("k", k), ("v", v))):
+            rows = x[at:at + lens[s]]
+            if dtype is E4:
+                codes, byte = R.quantise(rows)
+                rows = codes * R.powers("cuda")[byte.long()][..., None]
+            assert torch.equal(R.rows_of(c, name, 0, s).transpose(0, 1), rows.double())
+            assert torch.equal(out[i, at:at + lens[s]].double(), rows.double())
+        at += lens[s]
