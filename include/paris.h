@@ -556,7 +556,10 @@ paris_status paris_paged_attend_workspace(const paris_paged* c, int n_q_heads, s
  * query all of whose scores are -inf, has out = 0 and lse = -inf.  What lies in
  * rows that are not in use (or outside the window) does not reach the result,
  * NaN included.  Scores, maxima and sums are float32; scores past
- * float32's range give NaN, and weighted sums of values past it infinities.
+ * float32's range give NaN.  Values may be of any size, infinities and NaN
+ * included: rows whose result is not finite are computed a second time, row by
+ * row, where one whose weight is below 2^-118 of the largest adds nothing (1.5
+ * ms for 4096 rows of a sequence, 87 ms for 131072).
  * Softmax weights enter the product with V as two
  * bf16 parts (8-bit rows: as halves, as the query does).  q: device bf16
  * [n_seqs][Hq][d]; out: device bf16, the same; lse: device float32 [n_seqs][Hq], or NULL.  At most 128 query heads

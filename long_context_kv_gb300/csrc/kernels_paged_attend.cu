@@ -175,6 +175,121 @@ struct PgMax {
 // How far x lies above y.
 __device__ __forceinline__ float above(PgMax x, PgMax y, float qs) { return fmaf(x.d - y.d, qs, x.e - y.e); }
 
+// Sums of bf16 rows that are not finite though the weights are: a value is not
+// finite, also where the lower part of its weight is 0 and their product NaN, or
+// the sum of large values passes float32's range before it is divided by the
+// weights' sum.  (8-bit rows are at most 2^60.)
+__device__ __forceinline__ bool not_finite(const float4& o, float sum) {
+  return fmaf(o.x, 0.f, fmaf(o.y, 0.f, fmaf(o.z, 0.f, o.w * 0.f))) != 0.f && fabsf(sum) < INFINITY;
+}
+// Such a query head again by one warp, channels [c0, c1) of its result: 32 rows at
+// a time, a lane a row for the scores, four channels a lane for the mean, to which
+// every row adds its own weight of the whole: nothing passes the range that the
+// mean does not.  A row whose weight is below 2^-118 of the largest adds nothing,
+// whatever it holds: as where units and warps are joined, whose weights of up to
+// 2^8 meet factors that are 0 below 2^-126.  Bound by latency: 4096 rows take 1.5
+// ms, 131072 87.
+__device__ __forceinline__ void paged_row(const PagedAttendArgs& a, int s, int h, int c0, int c1) {
+  const int lane = threadIdx.x & 31, kvh = h / a.g, mask = (1 << a.c.shift) - 1, channel = 4 * lane;
+  const int len = paged_len(a.c, s), first = a.window > 0 ? max(len - a.window, 0) : 0;
+  const uint4* q = reinterpret_cast<const uint4*>(a.q + ((int64_t)s * a.hq + h) * kDim);
+  const uint8_t* kp = a.c.k + a.layer * a.c.sk.layer + kvh * a.c.sk.head;
+  const uint8_t* vp = a.c.v + a.layer * a.c.sv.layer + kvh * a.c.sv.head;
+  auto score = [&](int r) {
+    const uint4* row = reinterpret_cast<const uint4*>(kp + page_at(a.c, s, r >> a.c.shift) * a.c.sk.page + (r & mask) * a.c.sk.row);
+    float d = 0.f;
+#pragma unroll 2
+    for (int i = 0; i < kDim / 8; ++i) {
+      const uint4 x = row[i], y = __ldg(q + i);
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        d = fmaf(bf16_bits_to_float(xs[j] & 0xffffu), bf16_bits_to_float(ys[j] & 0xffffu), d);
+        d = fmaf(__uint_as_float(xs[j] & 0xffff0000u), __uint_as_float(ys[j] & 0xffff0000u), d);
+      }
+    }
+    return d;
+  };
+  float m = -INFINITY, l = 0.f;
+  for (int r = first + lane; r < len; r += 32) {
+    const float d = score(r), top = fmaxf(m, d);
+    if (top == -INFINITY) continue;
+    l = l * ex2((m - top) * kScaleLog2) + ex2((d - top) * kScaleLog2);
+    m = top;
+  }
+  float top = m;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+  l = m > -INFINITY ? l * ex2((m - top) * kScaleLog2) : 0.f;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) l += __shfl_xor_sync(kFull, l, off);
+  const float inv = 1.f / l;
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int r0 = first; r0 < len; r0 += 32) {
+    const float w = r0 + lane < len ? ex2((score(r0 + lane) - top) * kScaleLog2) : 0.f;
+    for (uint32_t some = __ballot_sync(kFull, !(w < 0x1p-118f)); some != 0; some &= some - 1) {
+      const int j = __ffs(some) - 1, r = r0 + j;
+      const float p = __shfl_sync(kFull, w, j) * inv;
+      float v[4];
+      load4(vp + page_at(a.c, s, r >> a.c.shift) * a.c.sv.page + (r & mask) * a.c.sv.row, 1, channel, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = fmaf(p, v[i], o[i]);
+    }
+  }
+  if (channel >= c0 && channel < c1)
+    *reinterpret_cast<uint2*>(a.out + ((int64_t)s * a.hq + h) * kDim + channel) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+}
+
+// The same if what is there, in those channels, is not finite.  A whole warp.
+__device__ __forceinline__ void row_again(const PagedAttendArgs& a, int s, int h, int c0, int c1) {
+  const int channel = 4 * (threadIdx.x & 31);
+  const uint2 y = *reinterpret_cast<const uint2*>(a.out + ((int64_t)s * a.hq + h) * kDim + channel);
+  auto special = [](uint32_t x) { return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u; };
+  if (__any_sync(kFull, channel >= c0 && channel < c1 && (special(y.x) || special(y.y)))) paged_row(a, s, h, c0, c1);
+}
+// At the end of a joining kernel, whose blocks each had every gridDim.x-th of the
+// (split sequence, head, part of the channels): its own results that are not
+// finite, and (once the kernel in front has left word in counts[2], which the last
+// block that is done takes back) those of sequences of one unit, spread over the
+// blocks.
+__device__ __forceinline__ void rows_again(const PagedAttendArgs& a, int parts, bool mine, bool others) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, splits = (int)min(a.counts[1], (uint32_t)a.max_splits);
+  if (mine) {
+    __syncthreads();
+    for (int64_t b = blockIdx.x + (int64_t)warp * gridDim.x; b < (int64_t)splits * a.hq * parts; b += (int64_t)warps * gridDim.x) {
+      const int64_t it = b / parts;
+      const int u = (int)(it / a.hq), c0 = (int)(b - it * parts) * (kDim / parts);
+      row_again(a, a.splits[u].s, (int)(it - (int64_t)u * a.hq), c0, c0 + kDim / parts);
+    }
+  }
+  if (!others) return;
+  for (int64_t it = (int64_t)blockIdx.x * warps + warp; it < (int64_t)a.c.n_seqs * a.hq; it += (int64_t)gridDim.x * warps) {
+    const int s = (int)(it / a.hq);
+    bool split = false;  // not those: their blocks have written them, or will
+    for (int i = lane; i < splits; i += 32) split |= a.splits[i].s == s;
+    if (!__any_sync(kFull, split)) row_again(a, s, (int)(it - (int64_t)s * a.hq), 0, kDim);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && atomicAdd(&a.counts[3], 1u) == gridDim.x - 1) a.counts[2] = a.counts[3] = 0;
+}
+
+// What a joining block has to look at again, in shared memory: a register more in
+// its loop, or a call there, cost 2% of the whole attention.
+struct AgainFlags {
+  uint32_t mine, others;
+  template <bool kE4m3>
+  static __device__ __forceinline__ void start(AgainFlags& f, const PagedAttendArgs& a) {
+    if (kE4m3 || threadIdx.x != 0) return;
+    f.mine = 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(smem_u32(&f.others)), "l"(a.counts + 2) : "memory");
+  }
+  __device__ __forceinline__ void finish(const PagedAttendArgs& a, int parts) {
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+    __syncthreads();
+    if ((mine | others) != 0) rows_again(a, parts, mine != 0, others != 0);
+  }
+};
+
 // How the line of all tiles is cut: units of at most `large` tiles in front of
 // `border`, of at most `small` behind it; sequences of at most `small` whole.
 struct PgCut {
@@ -247,9 +362,11 @@ struct PgShared {
   uint32_t gave_up;
 };
 
-template <bool kE4m3, int kHeads>
+// kWhole: no sequence can have several units, the jobs are gridDim.x apart and no
+// kernel follows (of its own, four sequences of up to 300 rows 7.4 -> 7.0 us).
+template <bool kE4m3, int kHeads, bool kWhole>
 __global__ void __launch_bounds__(kPgThreads, 2)
-    k_paged_attend(PagedAttendArgs a, const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm) {
+    k_paged_attend(const __grid_constant__ PagedAttendArgs a, const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm) {
   using G = Pg<kE4m3>;
   constexpr int kRows = G::kRows, kU = G::kU;
   constexpr int kQ = kHeads == 16 ? 2 : 1;                       // column tiles of queries
@@ -292,15 +409,15 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     if (lane < a.c.n_seqs) my_q = pg_seq<kE4m3>(a, lane);
     __syncthreads();  // the barriers are there
     const uint32_t seqs = __popc(__ballot_sync(kFull, my_q.tiles > 0)), end = warp_incl_scan(my_q.tiles, lane);
-    cut = pg_cut(__shfl_sync(kFull, end, 31), seqs, heads, blocks, a.max_splits == 0, !kE4m3 && kHeads < 16);
+    cut = pg_cut(__shfl_sync(kFull, end, 31), seqs, heads, blocks, kWhole, !kE4m3 && kHeads < 16);
     my_at = end - my_q.tiles;
     const uint32_t c = pg_count(pg_units(cut, my_at, my_q.tiles)), units = warp_incl_scan(c, lane);
     my_begin = units - c;
     jobs = (__shfl_sync(kFull, units, 31) & 0xffffu) * heads;
-    if (blockIdx.x == 0 && warp == 0) {
+    if (!kWhole && blockIdx.x == 0 && warp == 0) {
       const uint32_t several = __ballot_sync(kFull, c >> 16 != 0);
       if (c >> 16 != 0) a.splits[__popc(several & ((1u << lane) - 1u))] = PgSplit{lane, (int)(my_begin >> 16), (int)(c >> 16), 0};
-      if (lane == 0) a.counts[1] = __popc(several);  // none if max_splits is 0
+      if (lane == 0) a.counts[1] = __popc(several);
     }
   } else {
     const int per = (entries + kPgThreads - 1) / kPgThreads * group;
@@ -317,7 +434,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     used = __reduce_add_sync(kFull, used);
     if (lane == 0) sh.used[warp] = used;
     const uint32_t at0 = block_excl_scan(mine, sh.tmp, &total);
-    cut = pg_cut(total, sh.used[0] + sh.used[1] + sh.used[2] + sh.used[3], heads, blocks, a.max_splits == 0, !kE4m3 && kHeads < 16);
+    cut = pg_cut(total, sh.used[0] + sh.used[1] + sh.used[2] + sh.used[3], heads, blocks, kWhole, !kE4m3 && kHeads < 16);
     uint32_t at = at0, count = 0, several = 0;
     for (int s = s0; s < s1; ++s) {
       const uint32_t n = tiles_of(s), c = pg_count(pg_units(cut, at, n));
@@ -328,7 +445,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     uint32_t units, splits = 0, split = 0;
     uint32_t unit = block_excl_scan(count, sh.tmp, &units);
     jobs = (units & 0xffffu) * heads;
-    if (blockIdx.x == 0) {
+    if (!kWhole && blockIdx.x == 0) {
       split = block_excl_scan(several, sh.tmp, &splits);
       if (tid == 0) a.counts[1] = splits;
     }
@@ -337,7 +454,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
       if (s % group == 0) sh.line[s / group] = make_uint2(at, unit);
       if (per == 1 && blockIdx.x != 0) break;
       const uint32_t n = tiles_of(s), c = pg_count(pg_units(cut, at, n));
-      if (blockIdx.x == 0 && c >> 16 != 0) a.splits[split++] = PgSplit{s, (int)(unit >> 16), (int)(c >> 16), 0};
+      if (!kWhole && blockIdx.x == 0 && c >> 16 != 0) a.splits[split++] = PgSplit{s, (int)(unit >> 16), (int)(c >> 16), 0};
       unit += c;
       at += n;
     }
@@ -506,13 +623,14 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     enter(cur);
     load_queries(cur);
   }
+  bool again = false;  // a sequence's result is not finite
   while (busy) {
 #pragma unroll 1
     for (int i = 0; i < kPgDepth - 1 && !in_next && ahead < kPgDepth - 1; ++i) copy_next();
     // the job after this one: on its way while the first steps are computed
     int fetched = 0;
     bool pending = tid == 0;
-    if (pending) fetched = (int)(a.max_splits > 0 ? blocks + atomicAdd(a.counts, 1u) : job + blocks);
+    if (pending) fetched = (int)(kWhole ? job + blocks : blocks + atomicAdd(a.counts, 1u));
     const int kvh = cur.kvh, h0 = cur.h0, nh = min(kHeads, a.g - h0), qh0 = kvh * a.g + h0;
 
     uint32_t qf[kQ][8][2];
@@ -829,6 +947,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
         share[w] *= kDown;
       }
     }
+    bool bad = false;
 #pragma unroll
     for (int pass = 0; pass < kDim / kCh; ++pass) {
       if (pass > 0) __syncthreads();
@@ -870,7 +989,8 @@ __global__ void __launch_bounds__(kPgThreads, 2)
         }
         const float4 all = make_float4(best.d, best.e, sum, scale);
         const int channel = pass * kCh + ch;
-        if (cur.slot < 0) {
+        if (kWhole || cur.slot < 0) {
+          if constexpr (!kE4m3) bad |= not_finite(r, sum);
           const float inv = all.z != 0.f ? 1.f / all.z : 0.f;
           const int64_t q = (int64_t)cur.s * a.hq + qh0 + h;
           *reinterpret_cast<uint2*>(a.out + q * kDim + channel) =
@@ -884,7 +1004,13 @@ __global__ void __launch_bounds__(kPgThreads, 2)
         }
       }
     }
-    __syncthreads();  // what the sums went through may be used again
+    // what the sums went through may be used again
+    if constexpr (kE4m3) {
+      __syncthreads();
+    } else if (__syncthreads_or(bad)) {
+      again = true;
+      if (tid == 0 && !kWhole) a.counts[2] = 1;  // the joining kernel looks for it
+    }
     job = (uint32_t)sh.next[(k + 1) & 1];
     if (job >= jobs) break;
     if (!in_next) {
@@ -905,6 +1031,15 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     if (a.lse != nullptr)
       for (int i = tid; i < a.hq; i += kPgThreads) a.lse[q + i] = -INFINITY;
   }
+
+  // Where no other kernel follows, a block's results that are not finite wait for
+  // the end of its jobs, blockIdx.x + k blocks (in the loop above, reached or not,
+  // they cost 0.7 us of a call's 7.2; here 0.2).
+  if (kE4m3 || !kWhole || !again) return;
+  for (uint32_t j = blockIdx.x; j < jobs; j += blocks) {
+    const PgJob w = find(j);
+    for (int i = warp; i < min(kHeads, a.g - w.h0); i += kPgWarps) row_again(a, w.s, w.kvh * a.g + w.h0 + i, 0, kDim);
+  }
 }
 
 // The units' partial sums of a sequence and query head, joined: a block an
@@ -912,17 +1047,20 @@ __global__ void __launch_bounds__(kPgThreads, 2)
 // while the maxima are looked at, which every warp does for itself.  Bound by
 // latency: three loads that need one another.
 constexpr int kPgJoin = 4;
-__global__ void __launch_bounds__(32 * kPgJoin) k_paged_join(PagedAttendArgs a) {
+template <bool kE4m3>
+__global__ void __launch_bounds__(32 * kPgJoin, 8) k_paged_join(const __grid_constant__ PagedAttendArgs a) {
   constexpr int kWarps = kPgJoin, kAhead = 8;
   constexpr int kHeld = kWarps * kAhead / 32;  // maxima and sums a lane has of as many units as the results under way
   __shared__ float4 so[kWarps][32];
+  __shared__ AgainFlags again;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (blockIdx.x == 0 && tid == 0) a.counts[0] = 0;  // the queue, for the next call
+  AgainFlags::start<kE4m3>(again, a);
   for (int64_t it = blockIdx.x; it < (int64_t)a.max_splits * a.hq; it += gridDim.x) {
     const PgSplit sp = a.splits[it / a.hq];
-    if (it / a.hq >= a.counts[1]) return;
+    if (it / a.hq >= a.counts[1]) break;
     const int h = (int)(it - it / a.hq * a.hq), n = min(sp.units, a.slots - sp.slot);
     const float* part = a.part + ((int64_t)sp.slot * a.hq + h) * kPartStride;
     const int64_t step = (int64_t)a.hq * kPartStride;
@@ -998,9 +1136,11 @@ __global__ void __launch_bounds__(32 * kPgJoin) k_paged_join(PagedAttendArgs a) 
       const int64_t q = (int64_t)sp.s * a.hq + h;
       reinterpret_cast<uint2*>(a.out + q * kDim)[lane] = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
       if (a.lse != nullptr && lane == 0) a.lse[q] = sum != 0.f ? kLn2 * (fmaf(m.d, qs, m.e) + log2f(sum)) : -INFINITY;
+      if (!kE4m3 && not_finite(o, sum)) again.mine = 1;
     }
     __syncthreads();
   }
+  if constexpr (!kE4m3) again.finish(a, 1);
 }
 
 // The same for sequences of many units (few KV heads or sequences), with more
@@ -1009,22 +1149,24 @@ __global__ void __launch_bounds__(32 * kPgJoin) k_paged_join(PagedAttendArgs a) 
 // place of 16 of the other's warps: 131072 rows of one KV head and 8 query heads
 // 32.6 -> 24.3 us, 400000 69.1 -> 48.8, 30000 of 8 KV heads 28.6 -> 27.9.
 constexpr int kPgManyUnits = 2048;
-template <int kWarps, int kParts>
-__global__ void __launch_bounds__(32 * kWarps) k_paged_join_many(PagedAttendArgs a) {
+template <bool kE4m3, int kWarps, int kParts>
+__global__ void __launch_bounds__(32 * kWarps) k_paged_join_many(const __grid_constant__ PagedAttendArgs a) {
   constexpr int kThreads = 32 * kWarps, kLanes = 32 / kParts, kEach = kThreads / kLanes, kAhead = 4;  // lanes of a result, results at once
   __shared__ float2 top[kPgManyUnits];      // a unit's maximum
   __shared__ float weight[kPgManyUnits];    // its sum, then its share
   __shared__ float4 far[2][kWarps], so[kWarps][kLanes];
   __shared__ float sums[kWarps];
+  __shared__ AgainFlags again;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, mine = tid / kLanes;
   if (blockIdx.x == 0 && tid == 0) a.counts[0] = 0;  // the queue, for the next call
+  AgainFlags::start<kE4m3>(again, a);
   for (int64_t b = blockIdx.x; b < (int64_t)a.max_splits * a.hq * kParts; b += gridDim.x) {
     const int64_t it = b / kParts;
     const int channel = ((int)(b - it * kParts) * kLanes + lane % kLanes) * 4;
     const PgSplit sp = a.splits[it / a.hq];
-    if (it / a.hq >= a.counts[1]) return;
+    if (it / a.hq >= a.counts[1]) break;
     const int h = (int)(it - it / a.hq * a.hq), n = min(min(sp.units, a.slots - sp.slot), kPgManyUnits);
     const float* part = a.part + ((int64_t)sp.slot * a.hq + h) * kPartStride;
     const int64_t step = (int64_t)a.hq * kPartStride;
@@ -1126,9 +1268,11 @@ __global__ void __launch_bounds__(32 * kWarps) k_paged_join_many(PagedAttendArgs
       const int64_t q = (int64_t)sp.s * a.hq + h;
       *reinterpret_cast<uint2*>(a.out + q * kDim + channel) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
       if (a.lse != nullptr && channel == 0) a.lse[q] = sum != 0.f ? kLn2 * (fmaf(m.d, qs, m.e) + log2f(sum)) : -INFINITY;
+      if (!kE4m3 && not_finite(o, sum)) again.mine = 1;
     }
     __syncthreads();  // what was shared may be used again
   }
+  if constexpr (!kE4m3) again.finish(a, kParts);
 }
 
 // Rows of one head and page: 128 codes each, or two halves of 64 bf16 values,
@@ -1153,17 +1297,39 @@ bool encode_pages(CUtensorMap* m, const Paged& c, const uint8_t* base, const Pag
 
 int heads_of(int g) { return g <= 4 ? 4 : g <= 8 ? 8 : 16; }
 
-template <bool kE4m3, int kHeads>
+template <bool kE4m3, int kHeads, bool kWhole>
 cudaError_t launch_heads(const PagedAttendArgs& a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
   static std::atomic<bool> done[64];  // the limit belongs to the device; setting it twice is harmless
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && !(dev >= 0 && dev < 64 && done[dev])) {
-    e = cudaFuncSetAttribute((const void*)k_paged_attend<kE4m3, kHeads>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPgSmem);
+    e = cudaFuncSetAttribute((const void*)k_paged_attend<kE4m3, kHeads, kWhole>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPgSmem);
     if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
   }
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_paged_attend<kE4m3, kHeads>, dim3(a.nblocks), dim3(kPgThreads), kPgSmem, st, a, km, vm);
+  return launch_pdl(k_paged_attend<kE4m3, kHeads, kWhole>, dim3(a.nblocks), dim3(kPgThreads), kPgSmem, st, a, km, vm);
+}
+
+template <bool kE4m3, bool kWhole>
+cudaError_t launch_attend(const PagedAttendArgs& a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
+  const int heads = heads_of(a.g);
+  return heads == 4   ? launch_heads<kE4m3, 4, kWhole>(a, km, vm, st)
+         : heads == 8 ? launch_heads<kE4m3, 8, kWhole>(a, km, vm, st)
+                      : launch_heads<kE4m3, 16, kWhole>(a, km, vm, st);
+}
+
+// Few items have many units each, and many have few; eight parts of the
+// channels where that leaves no block without an SM (one sequence 48.8 us, four
+// parts 50.6; 128 items 41.7, four 39.0).
+template <bool kE4m3>
+cudaError_t launch_join(const PagedAttendArgs& a, int64_t items, cudaStream_t st) {
+  if (items <= a.nblocks / 2 && 6 * a.nblocks / (a.c.hkv * a.groups) + 2 <= kPgManyUnits) {
+    constexpr int kWarps = 8;
+    if (8 * items <= 2 * a.nblocks)
+      return launch_pdl(k_paged_join_many<kE4m3, kWarps, 8>, dim3((unsigned)(8 * items)), dim3(32 * kWarps), 0, st, a);
+    return launch_pdl(k_paged_join_many<kE4m3, kWarps, 4>, dim3((unsigned)std::min<int64_t>(4 * items, 4 * a.nblocks)), dim3(32 * kWarps), 0, st, a);
+  }
+  return launch_pdl(k_paged_join<kE4m3>, dim3((unsigned)std::min<int64_t>(items, 4 * a.nblocks)), dim3(32 * kPgJoin), 0, st, a);
 }
 
 }  // namespace
@@ -1192,26 +1358,13 @@ cudaError_t paged_attend_error(uint32_t* bits) { return take_gave_up(bits); }
 cudaError_t launch_paged_attend(const PagedAttendArgs& a, cudaStream_t st) {
   CUtensorMap km, vm;
   if (!encode_pages(&km, a.c, a.c.k, a.c.sk, a.layer) || !encode_pages(&vm, a.c, a.c.v, a.c.sv, a.layer)) return cudaErrorInvalidValue;
-  const int heads = heads_of(a.g);
-  cudaError_t e;
-  if (a.c.e4m3)
-    e = heads == 4 ? launch_heads<true, 4>(a, km, vm, st) : heads == 8 ? launch_heads<true, 8>(a, km, vm, st) : launch_heads<true, 16>(a, km, vm, st);
-  else
-    e = heads == 4 ? launch_heads<false, 4>(a, km, vm, st) : heads == 8 ? launch_heads<false, 8>(a, km, vm, st) : launch_heads<false, 16>(a, km, vm, st);
-  if (e != cudaSuccess) return e;
-  if (a.max_splits == 0) return cudaSuccess;  // no sequence can have several units
+  const bool whole = a.max_splits == 0;  // no sequence can have several units
+  const cudaError_t e = a.c.e4m3 ? whole ? launch_attend<true, true>(a, km, vm, st) : launch_attend<true, false>(a, km, vm, st)
+                        : whole  ? launch_attend<false, true>(a, km, vm, st)
+                                 : launch_attend<false, false>(a, km, vm, st);
+  if (e != cudaSuccess || whole) return e;
   const int64_t items = (int64_t)a.max_splits * a.hq;
-  // Few items have many units each, and many have few; eight parts of the
-  // channels where that leaves no block without an SM (one sequence 48.8 us, four
-  // parts 50.6; 128 items 41.7, four 39.0).
-  if (items <= a.nblocks / 2) {
-    constexpr int kWarps = 8;
-    if (6 * a.nblocks / (a.c.hkv * a.groups) + 2 > kPgManyUnits) return cudaErrorInvalidConfiguration;
-    if (8 * items <= 2 * a.nblocks)
-      return launch_pdl(k_paged_join_many<kWarps, 8>, dim3((unsigned)(8 * items)), dim3(32 * kWarps), 0, st, a);
-    return launch_pdl(k_paged_join_many<kWarps, 4>, dim3((unsigned)std::min<int64_t>(4 * items, 4 * a.nblocks)), dim3(32 * kWarps), 0, st, a);
-  }
-  return launch_pdl(k_paged_join, dim3((unsigned)std::min<int64_t>(items, 4 * a.nblocks)), dim3(32 * kPgJoin), 0, st, a);
+  return a.c.e4m3 ? launch_join<true>(a, items, st) : launch_join<false>(a, items, st);
 }
 
 }  // namespace paris

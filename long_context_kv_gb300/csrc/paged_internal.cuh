@@ -116,7 +116,7 @@ struct PagedAttendArgs {
   int groups, nblocks, slots, max_splits;
   float* part;       // [slots][hq][kPartStride]
   PgSplit* splits;   // [max_splits]
-  uint32_t* counts;  // the queue's next job; sequences of several units
+  uint32_t* counts;  // the queue's next job; sequences of several units; rows to be computed again; blocks that are done with it
 };
 cudaError_t launch_paged_attend(const PagedAttendArgs& a, cudaStream_t st);
 cudaError_t paged_attend_error(uint32_t* bits);

@@ -215,3 +215,112 @@ def test_packed_rows_of_many_sequences_without_a_better_limit(dtype):
             assert torch.equal(R.rows_of(c, name, 0, s).transpose(0, 1), rows.double())
             assert torch.equal(out[i, at:at + lens[s]].double(), rows.double())
         at += lens[s]
+
+
+# Query heads, KV heads and lengths: sequences of one unit; split ones of few heads (joined by parts of the channels, an
+# eighth and a quarter each), and of many, with others of one unit beside them.
+PATHS = [(1, 1, [40]), (8, 2, [200, 1, 64]), (16, 1, [333]), (40, 2, [130, 90]), (4, 1, [3000]), (8, 1, [5000, 45, 0, 90]),
+         (128, 1, [2000]), (64, 2, [3000, 100, 2500]), (48, 16, [1500, 0, 1800, 60, 41]), (6, 3, [50 + i for i in range(60)])]
+
+
+def definition(c, q, b, window, at=None):
+    """Results of sequence b in 64 bits, what its terms add up to without their signs, and its bound of a score's error."""
+    n, hkv = int(c.lens[b]), c.n_kv_heads
+    first = max(0, n - window) if window else 0
+    g = q.shape[1] // hkv
+    ks, vs = (R.rows_of(c, name, 0, b)[:, first:] for name in ("k", "v"))
+    if at is not None:
+        ks, vs = ks[:, at], vs[:, at]
+    qs = q[b].double().reshape(hkv, g, R.D)
+    p = torch.softmax(qs @ ks.transpose(1, 2) / math.sqrt(R.D), -1)
+    size = (qs.abs() @ ks.abs().transpose(1, 2)).amax(-1)
+    return [x.reshape(-1, R.D) for x in (p @ vs, p @ vs.abs())], R.score_error(size, n).reshape(-1, 1)
+
+
+def close(got, want, mass, e):
+    """Infinities and NaN are the definition's; the rest as close as weights of two bf16 parts, scores and the
+    rounding of the result make it."""
+    got, fin = got.double(), torch.isfinite(want)
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got[torch.isinf(want)], want[torch.isinf(want)])
+    tol = R.HALF_BF16 * want.abs() + (1 + R.HALF_BF16) * (e + 2.0 ** -16) * mass
+    assert torch.all((got - want).abs()[fin] <= tol[fin])
+
+
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("hq,hkv,lens", PATHS)
+def test_values_that_are_not_finite(hq, hkv, lens, window):
+    k, v = (rand(sum(lens), hkv, R.D, seed=20 + i).to(BF) for i in range(2))
+    at = 0
+    for n in lens:
+        if n >= 40:  # within the window, but for one
+            v[at + n - 3, 0, 5] = math.inf
+            v[at + n - 33, -1, 6] = -math.inf
+            v[at + n - 20, :, 9], v[at + n - 10, :, 9] = math.inf, -math.inf
+            v[at + n - 39, 0, 127] = math.nan
+        if n >= 90:
+            v[at + n - 80, :, 40:44] = math.inf
+        at += n
+    c = filled(lens, hkv, seed=0, kv=(k, v))
+    q = (2 * rand(len(lens), hq, R.D, seed=22)).to(BF)
+    out, lse = torch.full_like(q, 9.0), torch.full((len(lens), hq), 9.0, device="cuda")
+    c.paris_paged_attend(q, out, window=window, lse=lse)
+    clean = filled(lens, hkv, kv=(k, v.nan_to_num(0.0, 0.0, 0.0)))
+    out2, lse2 = torch.full_like(q, 9.0), torch.full_like(lse, 9.0)
+    clean.paris_paged_attend(q, out2, window=window, lse=lse2)
+    assert torch.equal(lse, lse2)
+    for b, n in enumerate(lens):
+        if n == 0:
+            assert torch.all(out[b] == 0)
+            continue
+        (want, mass), e = definition(c, q, b, window)
+        close(out[b], want, mass, e)
+        if n >= 40:
+            assert torch.isinf(want).any() and torch.isnan(want).any()
+    again = torch.full_like(q, 9.0)
+    c.paris_paged_attend(q, again, window=window)
+    assert torch.equal(again.nan_to_num(7.0), out.nan_to_num(7.0))
+    queue, _, rows, blocks = next(iter(c._spaces.values()))[:16].view(torch.int32).tolist()
+    assert queue == rows == blocks == 0  # kept for the next call
+    c.paris_paged_check()
+
+
+@pytest.mark.parametrize("hq,hkv,lens", PATHS)
+def test_large_values_leave_their_mean(hq, hkv, lens):
+    """Sums past float32's range on the way to means within it."""
+    v = (3e38 * (1 + 0.1 * rand(sum(lens), hkv, R.D, seed=30).clamp(-1, 1))).to(BF)
+    v[:, :, 64:] = -v[:, :, 64:]
+    v[:, :, ::7] = rand(sum(lens), hkv, 19, seed=31).to(BF)
+    c = filled(lens, hkv, kv=(rand(sum(lens), hkv, R.D, seed=32).to(BF), v))
+    q = (2 * rand(len(lens), hq, R.D, seed=33)).to(BF)
+    out = torch.full_like(q, 9.0)
+    c.paris_paged_attend(q, out)
+    for b, n in enumerate(lens):
+        if n > 0:
+            (want, mass), e = definition(c, q, b, 0)
+            assert torch.isfinite(out[b]).all()
+            close(out[b], want, mass, e)
+
+
+@pytest.mark.parametrize("hq,hkv,lens", PATHS)
+def test_rows_without_weight_add_nothing_whatever_they_hold(hq, hkv, lens):
+    """Scores 256 below the others are weights of 2^-369: none, in float32."""
+    k, v = (rand(sum(lens), hkv, R.D, seed=40 + i) for i in range(2))
+    k[:, :, 0] = 0
+    q = rand(len(lens), hq, R.D, seed=42)
+    q[:, :, 0] = 256.0
+    light = torch.zeros(sum(lens), dtype=torch.bool, device="cuda")
+    light[::3] = True
+    light[torch.tensor([sum(lens[:i]) for i, n in enumerate(lens) if n > 0], device="cuda")] = False
+    k[light, :, 0] = -256 * math.sqrt(R.D) / 256.0 - 4.0
+    v[light, :, ::2] = math.inf
+    v[light, :, 1::4] = math.nan
+    c = filled(lens, hkv, kv=(k.to(BF), v.to(BF)))
+    out = torch.full((len(lens), hq, R.D), 9.0, dtype=BF, device="cuda")
+    c.paris_paged_attend(q.to(BF), out)
+    at = 0
+    for b, n in enumerate(lens):
+        if n > 0:
+            (want, mass), e = definition(c, q.to(BF), b, 0, at=(~light[at:at + n]).nonzero()[:, 0])
+            close(out[b], want, mass, e)
+        at += n
