@@ -324,3 +324,24 @@ def test_rows_without_weight_add_nothing_whatever_they_hold(hq, hkv, lens):
             (want, mass), e = definition(c, q.to(BF), b, 0, at=(~light[at:at + n]).nonzero()[:, 0])
             close(out[b], want, mass, e)
         at += n
+
+
+@pytest.mark.parametrize("max_pages", [4, 4096])
+@pytest.mark.parametrize("spare", [0, 1, 5])
+def test_a_fork_takes_no_page_that_it_gives_back(spare, max_pages):
+    """New pages are those that were free before the call, though it frees pages of lower numbers."""
+    lens = [20, 40, 30, 10, 50]
+    c = filled(lens, 1, seed=50, spare=spare, max_pages=max_pages)
+    refs, own = c.refs.tolist(), [c.table[s, :-(-n // 16)].tolist() for s, n in enumerate(lens)]
+    c.paris_paged_fork(i32([4, 4, 4]), i32([0, 1, 2]))  # pages 0 to 6 are given back, three pages are asked for
+    got = min(spare, 3)
+    assert c.lens.tolist() == [50 if s < got else 48 for s in range(3)] + lens[3:]
+    new = [int(c.table[s, 3]) for s in range(got)]
+    assert all(refs[p] == 0 for p in new) and new == sorted(p for p, r in enumerate(refs) if r == 0)[:got]
+    assert all(int(c.refs[p]) == 0 for s in range(3) for p in own[s])
+    for s in range(3):
+        assert c.table[s, :3].tolist() == own[4][:3]
+        n = int(c.lens[s])
+        assert torch.equal(R.rows_of(c, "v", 0, s, n), R.rows_of(c, "v", 0, 4, n))
+    c.paris_paged_grow(i32([0, 0, 0, 32, 0]))  # and now they are free
+    assert c.table[3, 1:3].tolist() == [0, 1]
