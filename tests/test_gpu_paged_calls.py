@@ -345,3 +345,58 @@ def test_a_fork_takes_no_page_that_it_gives_back(spare, max_pages):
         assert torch.equal(R.rows_of(c, "v", 0, s, n), R.rows_of(c, "v", 0, 4, n))
     c.paris_paged_grow(i32([0, 0, 0, 32, 0]))  # and now they are free
     assert c.table[3, 1:3].tolist() == [0, 1]
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+def test_two_branches_of_one_graph_attend_at_once(dtype):
+    """Layers' attention side by side: each branch's calls have workspaces of its own."""
+    c = filled([3000, 700], 8, dtype=dtype, seed=60)
+    q = (2 * rand(2, 4, 2, 8, R.D, seed=61)).to(BF)
+    want, outs = torch.zeros_like(q), torch.zeros_like(q)
+    for i in range(2):
+        for n in range(4):
+            c.paris_paged_attend(q[i, n], want[i, n])
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        for n in range(4):
+            c.paris_paged_attend(q[0, n], outs[0, n])
+            c.paris_paged_attend(q[1, n], outs[1, n], stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(20):
+        outs.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs, want)
+    c.paris_paged_check()
+
+
+@pytest.mark.parametrize("hq,hkv,lens", PATHS)
+def test_captured_attention_over_values_that_are_not_finite(hq, hkv, lens):
+    """What is computed again is found anew by each replay, and forgotten."""
+    k, v = (rand(sum(lens), hkv, R.D, seed=70 + i).to(BF) for i in range(2))
+    c = filled(lens, hkv, kv=(k, v))
+    q = (2 * rand(len(lens), hq, R.D, seed=72)).to(BF)
+    out, graph = torch.zeros_like(q), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        c.paris_paged_attend(q, out)
+    for bad in (False, True, False, True):
+        x = v.clone()
+        if bad:
+            for at in (sum(lens[:i]) for i, n in enumerate(lens) if n > 0):
+                x[at, :, 3], x[at, :, 100] = math.inf, -math.inf
+        c.starts.zero_()
+        c.paris_paged_store(k, x, cu=K4.starts(lens), max_new=max(lens))
+        want = torch.zeros_like(q)
+        c.paris_paged_attend(q, want)
+        out.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        used = [b for b, n in enumerate(lens) if n > 0]
+        for channel, value in ((3, math.inf), (100, -math.inf)):
+            assert torch.all((out[used][..., channel] == value) == bad)
+        assert torch.isfinite(out[..., 4:100]).all()
+    c.paris_paged_check()
