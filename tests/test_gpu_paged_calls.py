@@ -1,6 +1,9 @@
 """The paged cache's calls in the ways in which programs make them: captured, on threads, with limits, with arrays that
 do not agree, with values that are not finite.  Against the direct call, lists, or the definition in 64 bits."""
 import math
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -400,3 +403,38 @@ def test_captured_attention_over_values_that_are_not_finite(hq, hkv, lens):
             assert torch.all((out[used][..., channel] == value) == bad)
         assert torch.isfinite(out[..., 4:100]).all()
     c.paris_paged_check()
+
+
+FIRST = """
+import torch
+from long_context_kv_gb300 import paris as P
+P.load()
+i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+for dtype in (torch.bfloat16, torch.float8_e4m3fn):
+    for n in (100, 4000):  # one unit a sequence, several
+        c = P.PagedCache.create(2, 2, 300, n // 16 + 2, dtype=dtype)
+        k = torch.randn(2, 2, n, 128, device="cuda").to(torch.bfloat16)
+        q = torch.randn(2, 8, 128, device="cuda").to(torch.bfloat16)
+        ko, vo, out, tokens, src, dst = torch.zeros_like(k), torch.zeros_like(k), torch.zeros_like(q), i32(n, 3), i32(0), i32(1)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            c.paris_paged_grow(tokens)
+            c.paris_paged_store(k, k)
+            c.paris_paged_attend(q, out)
+            c.paris_paged_read(ko, vo)
+            c.paris_paged_fork(src, dst)
+            c.paris_paged_free(src)
+            c.paris_paged_compact()
+        graph.replay()
+        c.paris_paged_check()
+        assert c.lens.tolist() == [0, n] and (dtype is not torch.bfloat16 or torch.equal(ko[0], k[0]))
+        s = ko[0].repeat_interleave(4, 0).double() @ q[0].double()[:, :, None] / 128 ** 0.5
+        o = (torch.softmax(s, 1) * vo[0].repeat_interleave(4, 0).double()).sum(1)
+        assert (o - out[0].double()).abs().max() < 2.0 ** -6
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
