@@ -37,11 +37,12 @@
 // as a row's own product and e, and both are subtracted before the scale, so
 // that weights are right at any size of the scores.
 //
-// Measured: 131072 rows of 8 KV heads in bf16 84.9 us, 6.3 TB/s; 24 ragged
-// sequences, 167K rows of 4 KV heads in 8 bits, 39.1 us, 4.4 TB/s.  Of those 39
+// Measured: 131072 rows of 8 KV heads in bf16 82.8 us, 6.5 TB/s; 24 ragged
+// sequences, 167K rows of 4 KV heads in 8 bits, 38.9 us, 4.4 TB/s.  Of those 39
 // the rows take 24 at the memory's rate; the first of them are there after 3 to
 // 5.5 us (lengths, pages, rows: one round trip after another), blocks end up to
-// 3 us apart (a unit of four tiles takes 4), and joining takes 5 with its launch.
+// 3 us apart (a unit of four tiles takes 4), joining takes 5 with its launch, and
+// the next call starts 2.5 later.
 // A step of 32 8-bit rows is 0.9 us of a warp's time, hidden behind the copies
 // but for the last one.  (Four more warps a block that do the copying, with
 // registers moved from them to the others: 8-bit batch 38.2, long sequence 88.)
@@ -274,7 +275,8 @@ __device__ __forceinline__ void rows_again(const PagedAttendArgs& a, int parts, 
 }
 
 // What a joining block has to look at again, in shared memory: a register more in
-// its loop, or a call there, cost 2% of the whole attention.
+// its loop, or a call there, cost 2 to 3% of the whole attention (64 sequences of
+// 2000 rows 85.3 -> 87.0 us, 256 of 700 122.5 -> 126; so 84.7 and 122.1).
 struct AgainFlags {
   uint32_t mine, others;
   template <bool kE4m3>

@@ -8,7 +8,7 @@
 // entries and copies rows.  Counts change by sums only, so their order does not
 // matter.  All of it is bound by latency: small forks are one block that takes
 // the steps in turn (one sequence to four: 8.3 us, 9.8 as three kernels),
-// larger ones a kernel a step (64 beams: 12.5 us), and sequences that end need
+// larger ones a kernel a step (64 beams: 11.3 us), and sequences that end need
 // none of the first two (3 us).
 #include "paged_device.cuh"
 
