@@ -606,7 +606,8 @@ paris_status paris_paged_compact_workspace(const paris_paged* c, size_t* bytes);
 
 /* Close up the pool: the pages in use whose number is n_used or above move,
  * in ascending order, to the free ones below it, in all layers, and the table
- * follows.  Then the pages in use are the first n_used.                       */
+ * follows.  Then the pages in use are the first n_used, which becomes the
+ * number of those that free_bits does not have.                              */
 paris_status paris_paged_compact(const paris_paged* c, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Synchronise the device and report the status word, then clear it:

@@ -278,20 +278,28 @@ __global__ void __launch_bounds__(kForkThreads) k_paged_end(ForkArgs a) {
   if (tid == 0) a.c.lens[dst] = a.c.starts[dst] = 0;
 }
 
-// One block: the used pages past their number and the free ones below it, in
-// ascending order, by one scan of both counts (at most 2^15 a round, in the
-// halves of a word); the bits as they are afterwards.
+// One block: the pages in use are counted, as free_bits has them; then those past
+// their number and the free ones below it, in ascending order, by one scan of both
+// counts (at most 2^15 a round, in the halves of a word); the bits as they are
+// afterwards.
 __global__ void __launch_bounds__(kPlanThreads) k_paged_compact_plan(CompactArgs a) {
-  __shared__ uint32_t tmp[33];
+  __shared__ uint32_t tmp[33], counts[kPlanThreads / 32];
   pdl_wait();
   pdl_trigger();
-  const int used = min(max(a.c.n_used[0], 0), a.c.n_pages), words = (a.c.n_pages + 31) / 32;
+  const int words = (a.c.n_pages + 31) / 32, lane = threadIdx.x & 31;
+  const uint32_t first = first_bits(a.c);
+  uint32_t mine = __popc(first);
+  for (int w = kPlanThreads + threadIdx.x; w < words; w += kPlanThreads) mine += __popc(page_bits(a.c, w));
+  mine = __reduce_add_sync(kFull, mine);
+  if (lane == 0) counts[threadIdx.x >> 5] = mine;
+  __syncthreads();
+  const int used = a.c.n_pages - (int)__reduce_add_sync(kFull, counts[lane]);
   uint32_t low = 0, high = 0;
   for (int w0 = 0; w0 < words; w0 += kPlanThreads) {
     const int w = w0 + threadIdx.x, p0 = 32 * w;
     const uint32_t is_page = p0 + 32 <= a.c.n_pages ? kFull : p0 < a.c.n_pages ? (1u << (a.c.n_pages - p0)) - 1u : 0u;
     const uint32_t below = p0 + 32 <= used ? kFull : p0 < used ? (1u << (used - p0)) - 1u : 0u;
-    const uint32_t free = w < words ? a.c.bits[w] & is_page : 0u;
+    const uint32_t free = w0 == 0 ? first : page_bits(a.c, w);
     uint32_t l = free & below, h = ~free & is_page & ~below, total;
     const uint32_t at = block_excl_scan((uint32_t)__popc(l) | (uint32_t)__popc(h) << 16, tmp, &total);
     uint32_t rl = low + (at & 0xffffu), rh = high + (at >> 16);
@@ -305,6 +313,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_compact_plan(CompactArgs
     low += total & 0xffffu;
     high += total >> 16;
   }
+  if (threadIdx.x == 0) a.c.n_used[0] = used;
   if (threadIdx.x == 0) a.moves[0] = (int)min(low, high);
 }
 

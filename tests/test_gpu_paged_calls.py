@@ -158,6 +158,22 @@ def test_growing_with_fewer_free_pages_than_n_used_says():
         assert sorted(p for s, n in enumerate((3, 5, 1)) for p in c.table[s, :n].tolist()) == list(range(c.n_pages))
 
 
+@pytest.mark.parametrize("off", [-6, -1, 0, 2, 1000])
+@pytest.mark.parametrize("lens", [[20, 33, 5, 64, 0, 100], [500, 20000, 9000, 20000]])
+def test_closing_up_goes_by_free_bits(lens, off):
+    """A wrong n_used costs no sequence a page; the right one is there afterwards."""
+    c = filled(lens, 1, seed=9, spare=40)
+    c.paris_paged_free(i32([0, 2]))
+    b = R.Book(c)
+    if c.n_pages % 32:
+        c.free_bits[-1] |= -1 << c.n_pages % 32
+    c.n_used += off
+    c.paris_paged_compact()
+    b.compact()
+    b.check()
+    c.paris_paged_check()
+
+
 def pages_free(c):
     at = torch.arange(c.n_pages, device="cuda")
     return c.free_bits[at // 32] >> at % 32 & 1
